@@ -71,6 +71,8 @@ extern "C" {
 #define MOE_DEVERR_DUP_ID 2u   /* a caller-supplied id repeated within a token (skipped) */
 #define MOE_DEVERR_TIMEOUT 4u  /* a pipeline wait exceeded its limit; kernel returned */
 #define MOE_DEVERR_CAPACITY 8u /* tile list would exceed the planned capacity */
+#define MOE_DEVERR_BAD_PAGE 16u /* a page id or slot outside the cache (skipped) */
+#define MOE_DEVERR_NO_SPACE 32u /* free pages, table columns or token rows ran out */
 
 /* compute dtypes */
 #define MOE_DTYPE_F32 0
@@ -80,6 +82,11 @@ extern "C" {
 /* logits dtypes (moe_route_topk) */
 #define MOE_LOGITS_F32 0
 #define MOE_LOGITS_BF16 1
+
+/* key-value cache dtypes */
+#define MOE_KV_F32 0
+#define MOE_KV_BF16 1
+#define MOE_KV_E4M3 2
 
 /* scoring */
 #define MOE_SCORING_SOFTMAX 0
@@ -381,6 +388,151 @@ int moe_ep_pack(const void* x, int x_dtype, const int32_t* ids, const float* w, 
  */
 int moe_ep_combine(const float* back, const int32_t* row_of, int T, int H, int ep_size,
                    float* out, void* stream);
+
+/*
+ * A decode step around the layer: block tables and slot maps, the paged
+ * key-value cache, attention of one new token per request, and sampling.
+ * The pages have no counterpart of these calls; they are what a server that
+ * runs the layer needs next to it.  All of them are asynchronous on `stream`
+ * (moe_check_word excepted) and allocate nothing.  `err` is an optional
+ * device word (NULL: not reported) into which MOE_DEVERR_* bits are OR-ed;
+ * the caller zeroes it before its first use and moe_check_word reads it.
+ *
+ * The cache is a pool of num_pages pages of page_size tokens.  Token `pos` of
+ * request r lives in page block_table[r][pos / page_size] at row
+ * pos % page_size; slot = page * page_size + row.  Key and value vectors of
+ * head_dim contiguous elements sit at
+ *   k + page * stride_page + row * stride_token + head * stride_head
+ * (strides in elements, the same for v), so a cache may be kept token by
+ * token, head by head, or be a view into a larger tensor.
+ *   MOE_KV_F32 and MOE_KV_BF16 hold the vectors in that type; MOE_KV_E4M3
+ *   holds e4m3 codes whose value is code * k_scale[head] (v_scale[head] for
+ *   values), fp32 device arrays [kv_heads] that must be NULL for the others.
+ * q, out, and the vectors to append are f32 for a MOE_KV_F32 cache and bf16
+ * for the others.
+ * Requirements of every call: 1 <= num_pages, 1 <= page_size, num_pages *
+ * page_size < 2^31, 1 <= kv_heads <= 65535, head_dim a multiple of 16 in
+ * [16, 256] (8 for F32 and BF16), k and v 16-byte aligned, strides
+ * non-negative and a multiple of 16 bytes.  A cache's byte offsets are 64-bit.
+ */
+typedef struct moe_kv_cache {
+  int32_t kv_dtype;
+  int32_t num_pages, page_size, kv_heads, head_dim;
+  int32_t reserved0;
+  int64_t stride_page, stride_token, stride_head;
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+} moe_kv_cache_t;
+
+#define MOE_KV_MAX_REQUESTS 8192
+
+/*
+ * moe_kv_step -- grow the block tables for one step and map its new tokens.
+ * Request r has ctx_lens[r] tokens in the cache and gets new_lens[r] more
+ * (0 for a request that sits the step out; negative lengths count as 0).
+ *   ctx_lens, new_lens  device int32 [B], B <= MOE_KV_MAX_REQUESTS
+ *   block_table   device int32 [B, max_pages], rows table_stride apart.  The
+ *                 first ceil(ctx/page_size) entries of a row are read; the
+ *                 entries up to ceil((ctx+new)/page_size) are written
+ *   free_pages    device int32 [free_capacity]: the ids of the free pages are
+ *                 its first n_free entries (n_free_in, device int32 [1]).
+ *                 Pages are taken from the end, requests in order
+ *   n_free_out    device int32 [1]: the number left; may be n_free_in itself
+ *   slots         device int32 [max_tokens] out: the slot of each new token,
+ *                 requests in order; -1 past the last one (rows that pad a
+ *                 fixed-size batch) and where there is no page
+ *   positions     device int32 [max_tokens] out: each token's position in
+ *                 its request (0 past the last one)
+ *   starts        device int32 [B+1] out: request r's tokens are rows
+ *                 starts[r] .. starts[r+1]-1
+ *   seq_lens      device int32 [B] out: ctx + new
+ * A request that finds no free page, or needs more than max_pages, gets
+ * table entry -1 (within the table), slot -1 and MOE_DEVERR_NO_SPACE, as do
+ * tokens past max_tokens; a page id outside [0, num_pages) gives slot -1 and
+ * MOE_DEVERR_BAD_PAGE.  free_pages is not written: the call can be repeated
+ * with the same n_free_in and gives the same tables.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
+ */
+int moe_kv_step(const int32_t* ctx_lens, const int32_t* new_lens, int B, int32_t* block_table,
+                int max_pages, long long table_stride, const int32_t* free_pages,
+                int free_capacity, const int32_t* n_free_in, int32_t* n_free_out, int num_pages,
+                int page_size, int max_tokens, int32_t* slots, int32_t* positions,
+                int32_t* starts, int32_t* seq_lens, uint32_t* err, void* stream);
+
+/*
+ * moe_kv_release -- give back the pages of finished requests: for every row r
+ * with done[r] != 0 (device int32 [B]) the entries of its table row that lie
+ * in [0, num_pages) go to the end of free_pages, rows in order and columns in
+ * order, n_free (device int32 [1]) grows by their number, and the whole row
+ * becomes -1.  Rows must hold -1 where they hold no page.  Pages that do not
+ * fit free_capacity are dropped with MOE_DEVERR_NO_SPACE.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
+ */
+int moe_kv_release(const int32_t* done, int B, int32_t* block_table, int max_pages,
+                   long long table_stride, int32_t* free_pages, int free_capacity,
+                   int32_t* n_free, int num_pages, uint32_t* err, void* stream);
+
+/*
+ * moe_kv_append -- write N tokens' keys and values into the cache.
+ *   k, v   device [N, kv_heads, head_dim]; token and head strides in elements
+ *          (k_stride_token, ...), head_dim contiguous
+ *   slots  device int32 [N]: the slot of each token; -1 skips the token, a
+ *          slot outside the cache skips it with MOE_DEVERR_BAD_PAGE.  Slots
+ *          that are not skipped must differ
+ * F32 and BF16 caches get the vectors bit for bit; E4M3 caches get x / scale
+ * rounded to nearest even and saturated at +-448 (NaN stays NaN).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (head_dim, strides or
+ * alignment of the cache), MOE_ERR_CUDA.
+ */
+int moe_kv_append(const moe_kv_cache_t* cache, const void* k, long long k_stride_token,
+                  long long k_stride_head, const void* v, long long v_stride_token,
+                  long long v_stride_head, int N, const int32_t* slots, uint32_t* err,
+                  void* stream);
+
+/*
+ * moe_attn_decode -- attention of one new token per request over the cache:
+ *   out[b, h] = sum_t softmax_t(scale * q[b, h] . k[t, g]) v[t, g]
+ * over the tokens t of request b with max(0, len - window) <= t < len, where
+ * len = seq_lens[b] (its new token, already appended, included), g = h /
+ * (Hq / kv_heads), and window 0 stands for no window.
+ *   q            device [B, Hq, head_dim], strides in elements, Hq a multiple
+ *                of kv_heads
+ *   block_table  device int32 [B, max_pages], rows table_stride apart;
+ *                max_pages * page_size < 2^31 - 1024
+ *   seq_lens     device int32 [B]; a request with len <= 0 gets out 0 and
+ *                lse -inf; len is cut to max_pages * page_size with
+ *                MOE_DEVERR_NO_SPACE
+ *   out          device [B, Hq, head_dim], strides in elements
+ *   lse          NULL, or device f32 [B, Hq]: the natural logarithm of the
+ *                softmax's sum (with scale; -inf when no token was attended)
+ *   ws           device workspace of moe_attn_workspace(...) bytes, 256-byte
+ *                aligned; needs no initialisation and holds nothing after
+ *                the call
+ * Tokens whose page id lies outside the cache are left out and set
+ * MOE_DEVERR_BAD_PAGE.  What the cache holds beyond a request's tokens (in
+ * the rest of its last page) is never used, whatever its bits; an infinite or
+ * NaN key or value that is attended makes its rows of out infinite or NaN.
+ * q and out must be 16-byte aligned with strides of a multiple of 16 bytes.
+ * The result is the same from call to call: no atomics join the parts.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (head_dim, strides,
+ * alignment), MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
+ */
+int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stride_b,
+                    long long q_stride_h, int B, int Hq, const int32_t* block_table,
+                    int max_pages, long long table_stride, const int32_t* seq_lens, float scale,
+                    int window, void* out, long long o_stride_b, long long o_stride_h, float* lse,
+                    void* ws, size_t ws_bytes, uint32_t* err, void* stream);
+
+/* moe_attn_workspace -- bytes of workspace that moe_attn_decode needs for
+ * this cache type and head_dim on the current device, whatever B, Hq and the
+ * lengths; 0 for values outside the requirements. */
+size_t moe_attn_workspace(int kv_dtype, int head_dim);
+
+/* moe_check_word -- moe_check for a caller's error word: synchronise
+ * `stream`, read *err, clear it, and return MOE_OK or MOE_ERR_DEVICE. */
+int moe_check_word(uint32_t* err, uint32_t* bits, void* stream);
 
 /* moe_strerror -- static message for a MOE_* return code. */
 const char* moe_strerror(int code);

@@ -9,6 +9,7 @@ import os
 from . import _build
 
 c_i32, c_u32, c_u64, c_void_p = ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_void_p
+c_i64 = ctypes.c_int64
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = -1
@@ -22,15 +23,20 @@ MOE_DEVERR_BAD_ID = 1
 MOE_DEVERR_DUP_ID = 2
 MOE_DEVERR_TIMEOUT = 4
 MOE_DEVERR_CAPACITY = 8
+MOE_DEVERR_BAD_PAGE = 16
+MOE_DEVERR_NO_SPACE = 32
 
 MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_FP8_BLOCK128 = 0, 1, 2
 MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
 MOE_SCORING_SOFTMAX, MOE_SCORING_SIGMOID = 0, 1
+MOE_KV_F32, MOE_KV_BF16, MOE_KV_E4M3 = 0, 1, 2
 
 EXPORTED = ("moe_plan", "moe_plan_ep", "moe_forward", "moe_forward_timed", "moe_forward_with_ids",
             "moe_forward_noalloc", "moe_check_noalloc", "moe_route_topk", "moe_route_grouped_topk",
             "moe_plan_set_groups", "moe_check", "moe_plan_describe",
             "moe_ep_dispatch", "moe_ep_pack", "moe_ep_combine",
+            "moe_kv_step", "moe_kv_release", "moe_kv_append", "moe_attn_decode",
+            "moe_attn_workspace", "moe_check_word",
             "moe_strerror", "moe_abi_version")
 
 
@@ -51,6 +57,14 @@ class MoePlan(ctypes.Structure):
         buf = ctypes.create_string_buffer(512)
         lib().moe_plan_describe(ctypes.byref(self), buf, 512)
         return buf.value.decode()
+
+
+class MoeKvCache(ctypes.Structure):
+    """Mirror of ``moe_kv_cache_t``."""
+    _fields_ = [(n, c_i32) for n in ("kv_dtype", "num_pages", "page_size", "kv_heads", "head_dim",
+                                     "reserved0")]
+    _fields_ += [(n, c_i64) for n in ("stride_page", "stride_token", "stride_head")]
+    _fields_ += [(n, c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
 
 
 class MoeError(RuntimeError):
@@ -115,6 +129,21 @@ def lib() -> ctypes.CDLL:
     L.moe_ep_pack.restype = i
     L.moe_ep_combine.argtypes = [P, P, i, i, i, P, P]
     L.moe_ep_combine.restype = i
+    ll, f, sz = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+    cache = ctypes.POINTER(MoeKvCache)
+    L.moe_kv_step.argtypes = [P, P, i, P, i, ll, P, i, P, P, i, i, i, P, P, P, P, P, P]
+    L.moe_kv_step.restype = i
+    L.moe_kv_release.argtypes = [P, i, P, i, ll, P, i, P, i, P, P]
+    L.moe_kv_release.restype = i
+    L.moe_kv_append.argtypes = [cache, P, ll, ll, P, ll, ll, i, P, P, P]
+    L.moe_kv_append.restype = i
+    L.moe_attn_decode.argtypes = [cache, P, ll, ll, i, i, P, i, ll, P, f, i, P, ll, ll, P, P, sz, P,
+                                  P]
+    L.moe_attn_decode.restype = i
+    L.moe_attn_workspace.argtypes = [i, i]
+    L.moe_attn_workspace.restype = sz
+    L.moe_check_word.argtypes = [P, ctypes.POINTER(c_u32), P]
+    L.moe_check_word.restype = i
     if L.moe_abi_version() != 4:
         raise RuntimeError("libmoe_route ABI version mismatch")
     _lib = L
@@ -216,3 +245,43 @@ def moe_ep_pack(x, x_dtype, ids, w, T, H, k, ep_size, send_counts, send_tokens, 
 
 def moe_ep_combine(back, row_of, T, H, ep_size, out, stream):
     return lib().moe_ep_combine(back, row_of, T, H, ep_size, out, stream)
+
+
+def moe_kv_step(ctx_lens, new_lens, B, block_table, max_pages, table_stride, free_pages,
+                free_capacity, n_free_in, n_free_out, num_pages, page_size, max_tokens, slots,
+                positions, starts, seq_lens, err, stream):
+    return lib().moe_kv_step(ctx_lens, new_lens, B, block_table, max_pages, table_stride,
+                             free_pages, free_capacity, n_free_in, n_free_out, num_pages,
+                             page_size, max_tokens, slots, positions, starts, seq_lens, err,
+                             stream)
+
+
+def moe_kv_release(done, B, block_table, max_pages, table_stride, free_pages, free_capacity,
+                   n_free, num_pages, err, stream):
+    return lib().moe_kv_release(done, B, block_table, max_pages, table_stride, free_pages,
+                                free_capacity, n_free, num_pages, err, stream)
+
+
+def moe_kv_append(cache, k, k_stride_token, k_stride_head, v, v_stride_token, v_stride_head, N,
+                  slots, err, stream):
+    return lib().moe_kv_append(ctypes.byref(cache), k, k_stride_token, k_stride_head, v,
+                               v_stride_token, v_stride_head, N, slots, err, stream)
+
+
+def moe_attn_workspace(kv_dtype, head_dim):
+    return lib().moe_attn_workspace(kv_dtype, head_dim)
+
+
+def moe_attn_decode(cache, q, q_stride_b, q_stride_h, B, Hq, block_table, max_pages, table_stride,
+                    seq_lens, scale, window, out, o_stride_b, o_stride_h, lse, ws, ws_bytes, err,
+                    stream):
+    return lib().moe_attn_decode(ctypes.byref(cache), q, q_stride_b, q_stride_h, B, Hq,
+                                 block_table, max_pages, table_stride, seq_lens, scale, window,
+                                 out, o_stride_b, o_stride_h, lse, ws, ws_bytes, err, stream)
+
+
+def moe_check_word(err, stream):
+    """(rc, error bits) of a caller's device error word, which is cleared."""
+    bits = c_u32(0)
+    rc = lib().moe_check_word(err, ctypes.byref(bits), stream)
+    return rc, bits.value

@@ -1,0 +1,1040 @@
+// attn_decode.cu -- attention of one new token per request over the paged
+// key-value cache (moe_attn_decode, include/moe_route.h).
+//
+// With G = Hq / kv_heads query heads on each cached head, every cached
+// element is used by 2G flops and read once: for the G of real models (1 to
+// 16) the operator is bound by the cache's bytes, so the kernel is built to
+// keep loads in flight, and the products only have to keep out of the way.
+//
+//   work     A unit is (request, kv head, block of 16 query heads); its tokens
+//            form tiles of 16 per warp.  The tiles of all units, in order, are
+//            cut into equal contiguous ranges, one per CTA of a single wave,
+//            so ragged lengths and long single requests balance alike; a
+//            range may begin and end inside a unit.
+//   loads    Each warp has a ring of ST stages of 16 keys and 16 values and
+//            fills it with 16-byte cp.async, ST-1 stages ahead, across unit
+//            borders; page ids are fetched one stage before that.  Warps
+//            share nothing in the loop: no CTA-wide barrier, no producer.
+//   math     S = Q K^T and O += P V on m16n8k16 / m16n8k8 tensor core
+//            instructions with the 16 query heads as rows.  One pass keeps
+//            the running maximum m and sum l of each row in fp32 (base 2) and
+//            rescales O when m grows.  tcgen05 needs 128 rows on its M side
+//            and its result in tensor memory; here one operand has 16 rows
+//            or fewer, the softmax works on its rows between the two
+//            products, and the legacy instructions take under a third of the
+//            time that the tile's bytes take.
+//   joining  At a unit's end the CTA's warps join through shared memory.  A
+//            unit inside one range is written at once; parts of a unit cut by
+//            range borders go to the workspace in fp32 and the second kernel
+//            joins them in range order: no atomics, one fixed result.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/moe_route.h"
+#include "decode_internal.cuh"
+#include "moe_internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kRows = 16;  // query heads of a unit: the m of the mma instructions
+constexpr int kKeys = 16;  // keys of a warp's stage
+constexpr int kMaxLen = INT_MAX - 1024;  // a tile's end stays an int
+
+struct AttnArgs {
+  const char *k, *v;
+  long long s_page, s_token, s_head;  // bytes
+  const float *k_scale, *v_scale;
+  const void* q;
+  long long q_b, q_h;  // elements
+  void* out;
+  long long o_b, o_h;  // elements
+  float* lse;
+  const int* table;
+  long long table_stride;
+  const int* lens;
+  float* part_o;   // [2 * ctas][16][DP]
+  float2* part_ml; // [2 * ctas][16]
+  int4* info;      // [ctas] {unit's request, unit in request, parts, 0}
+  unsigned* err;
+  float scale_log2;
+  int B, Hq, heads, group, blocks;  // blocks: of 16 query heads per kv head
+  int dim, page, num_pages, max_pages, window, min_tiles;
+};
+
+// ------------------------------------------------------------ instructions
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  // a row that is not real is filled with zeros and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t tf32_rna(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+// x = hi + lo with 11 bits each: products of two such pairs without lo * lo
+// are off by 2^-22 of |x y| at most
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = tf32_rna(x);
+  const float h = __uint_as_float(hi);
+  lo = h == x ? 0u : tf32_rna(x - h);  // an infinite x has no rest
+}
+// two e4m3 codes (the low and the high byte of 16 bits) as f16: exact
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+      : "=r"(r)
+      : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ------------------------------------------------------------ configuration
+// Bytes of a warp's stage (16 keys and 16 values), warps and stages per CTA,
+// CTAs per SM: about 96 KB of ring per CTA and two CTAs per SM while a stage
+// is at most 8 KB (one CTA's joins overlap the other's loads), else one CTA.
+template <int KV, int DP>
+struct AttnCfg {
+  static constexpr int ES = kv_esize(KV);
+  static constexpr int RB = DP * ES;             // bytes of a row
+  static constexpr int SB = 2 * kKeys * RB;      // bytes of a warp's stage
+  static constexpr int NW = SB <= 16384 ? 4 : 2;
+  static constexpr int CTAS = SB <= 8192 ? 2 : 1;
+  static constexpr int ST = SB <= 2048 ? 8 : SB <= 4096 ? 6 : 3;
+  static constexpr int THREADS = 32 * NW;
+  static constexpr int TILE = NW * kKeys;
+  // Q in shared memory unless its fragments fit registers
+  static constexpr bool QREG = KV != MOE_KV_F32 && DP <= 128;
+  static constexpr int QES = KV == MOE_KV_F32 ? 4 : 2;
+  // row pitch of Q: conflict-free for ldmatrix (bf16), 8-byte (f16) and
+  // 16-byte (f32) fragment loads
+  static constexpr int QP = DP * QES + (KV == MOE_KV_F32 ? 64 : KV == MOE_KV_BF16 ? 16 : 32);
+  static constexpr int QBYTES = QREG ? 0 : kRows * QP;
+  static constexpr int RING = NW * ST * SB;
+  static constexpr int SMEM = RING + QBYTES;
+  // columns of O that fit a warp's stage as fp32 (joining the warps)
+  static constexpr int JC = SB / (kRows * 4) < DP ? SB / (kRows * 4) : DP;
+};
+
+// 16-byte chunk `c` of row `r` within a 16-row block of RB-byte rows, swizzled
+// so that the fragment loads of 8 rows hit all banks.  A warp's stage holds
+// keys and values; f32 values use another pattern than f32 keys, because the
+// value fragments take rows two apart.
+template <int RB>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c, bool odd_first) {
+  if constexpr (RB >= 128) {
+    const int f = odd_first ? (((r & 1) << 2) | ((r >> 1) & 3)) : (r & 7);
+    return r * RB + ((c ^ f) << 4);
+  } else {
+    return r * RB + ((c ^ ((r >> 1) & 3)) << 4);
+  }
+}
+
+// ------------------------------------------------------------ the work list
+__device__ __forceinline__ int2 span_of(const AttnArgs& A, int b, bool& cut) {
+  int len = max(A.lens[b], 0);
+  const long long room = static_cast<long long>(A.max_pages) * A.page;
+  if (len > room) {
+    len = static_cast<int>(room);
+    cut = true;
+  }
+  return make_int2(A.window > 0 ? max(0, len - A.window) : 0, len);
+}
+__device__ __forceinline__ int tiles_of(int2 span, int tile) {
+  return max(1, (span.y - span.x + tile - 1) / tile);
+}
+
+// A place in the CTA's range of tiles; every warp keeps one for the loads and
+// one for the products.
+struct Cursor {
+  int b, x, t, nt;  // request, unit in request, tile in unit, tiles of a unit
+  int first, len;   // the request's attended tokens
+  long long left;   // tiles of the range from here on
+};
+
+template <int TILE>
+__device__ __forceinline__ void advance(Cursor& c, const AttnArgs& A, int units) {
+  --c.left;
+  if (++c.t < c.nt) return;
+  c.t = 0;
+  if (++c.x < units) return;
+  c.x = 0;
+  ++c.b;
+  if (c.left <= 0) return;
+  bool cut = false;
+  const int2 s = span_of(A, c.b, cut);
+  c.first = s.x;
+  c.len = s.y;
+  c.nt = tiles_of(s, TILE);
+}
+
+template <int KV>
+__device__ __forceinline__ void store4(void* out, long long at, float4 v) {
+  if constexpr (KV == MOE_KV_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+  }
+}
+
+template <int KV, int DP>
+__global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTAS)
+    attn_decode_kernel(const AttnArgs A) {
+  using C = AttnCfg<KV, DP>;
+  constexpr int NW = C::NW, ST = C::ST, RB = C::RB, NT = DP / 8;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ long long s_sum[NW];
+  __shared__ int s_b;
+  __shared__ long long s_off;
+  __shared__ unsigned short s_mask[NW][ST];
+  __shared__ float s_m[NW][kRows], s_l[NW][kRows], s_q[kRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c4 = lane & 3;
+  const int units = A.heads * A.blocks;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's range of tiles
+  bool cut = false;
+  const int per = (A.B + C::THREADS - 1) / C::THREADS;
+  const int b0 = min(A.B, static_cast<int>(threadIdx.x) * per), b1 = min(A.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of(span_of(A, b, cut), C::TILE);
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  total *= units;
+  if (cut && A.err && blockIdx.x == 0) atomicOr(A.err, MOE_DEVERR_NO_SPACE);
+  const long long wide = (total + A.min_tiles - 1) / A.min_tiles;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), wide));
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) A.info[cta] = make_int4(0, 0, 0, 0);
+  if (cta >= ctas) return;
+  const long long begin = cta * total / ctas, end = (cta + 1) * total / ctas;
+  {
+    const long long lo = (before + incl - mine) * units, hi = (before + incl) * units;
+    if (begin >= lo && begin < hi) {
+      long long at = lo;
+      int b = b0;
+      for (;; ++b) {
+        const long long n = static_cast<long long>(tiles_of(span_of(A, b, cut), C::TILE)) * units;
+        if (begin < at + n) break;
+        at += n;
+      }
+      s_b = b;
+      s_off = begin - at;
+    }
+  }
+  __syncthreads();
+  Cursor cc;
+  cc.b = s_b;
+  {
+    const int2 s = span_of(A, cc.b, cut);
+    cc.first = s.x;
+    cc.len = s.y;
+    cc.nt = tiles_of(s, C::TILE);
+    cc.x = static_cast<int>(s_off / cc.nt);
+    cc.t = static_cast<int>(s_off - static_cast<long long>(cc.x) * cc.nt);
+    cc.left = end - begin;
+  }
+  Cursor lc = cc;
+  bool bad_page = false;
+
+  // ---- loads
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * ST * C::SB;
+  constexpr int CPR = RB / 16;                     // chunks of a row
+  constexpr int RPI = CPR >= 32 ? 1 : 32 / CPR;    // rows per instruction
+  constexpr int IPR = CPR > 32 ? CPR / 32 : 1;     // instructions per row
+  const int chunks = A.dim * C::ES / 16;
+  struct Want {
+    int row;   // row in the page of this lane's key (lanes 0 .. 15), -1: none
+    int page;
+  };
+  // page id of this lane's key at cursor c
+  auto want = [&](const Cursor& c) {
+    Want w = {-1, 0};
+    const int pos = c.first + c.t * C::TILE + warp * kKeys + (lane & 15);
+    if (c.left > 0 && pos < c.len) {
+      const int p = pos / A.page;
+      w.row = pos - p * A.page;
+      w.page = __ldg(A.table + c.b * A.table_stride + p);
+    }
+    return w;
+  };
+  auto load = [&](const Cursor& c, const Want& w, int stage) {
+    const bool in = w.page >= 0 && w.page < A.num_pages;
+    bad_page |= w.row >= 0 && !in;
+    const bool live = w.row >= 0 && in;
+    const unsigned mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
+    if (lane == 0) s_mask[warp][stage] = static_cast<unsigned short>(mask);
+    if (mask) {
+      const long long off = live ? w.page * A.s_page + w.row * A.s_token +
+                                       (c.x / A.blocks) * A.s_head
+                                 : 0;
+      const uint32_t base = ring + stage * C::SB;
+#pragma unroll
+      for (int i = 0; i < kKeys / RPI; ++i) {
+        const int r = i * RPI + (RPI > 1 ? lane / CPR : 0);
+        const long long o = __shfl_sync(0xffffffffu, off, r);
+        const bool row_live = (mask >> r) & 1u;
+#pragma unroll
+        for (int j = 0; j < IPR; ++j) {
+          const int ch = (RPI > 1 ? lane % CPR : lane) + 32 * j;
+          const bool real = row_live && ch < chunks;
+          const long long at = o + (ch < chunks ? ch * 16 : 0);
+          cp_async16(base + chunk_at<RB>(r, ch, true), A.k + at, real);
+          cp_async16(base + kKeys * RB + chunk_at<RB>(r, ch, KV != MOE_KV_F32), A.v + at, real);
+        }
+      }
+    }
+    cp_commit();
+  };
+
+  // the first ST - 1 stages: all their page ids are asked for before any use
+  Want next;
+  {
+    Want w[ST];
+    Cursor at[ST - 1];
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) {
+      at[s] = lc;
+      w[s] = want(lc);
+      if (lc.left > 0) advance<C::TILE>(lc, A, units);
+    }
+    next = want(lc);
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) load(at[s], w[s], s);
+  }
+
+  // ---- per-unit state
+  float acc[NT][4];
+  float m[2], l[2];
+  uint32_t qf[C::QREG ? DP / 16 : 1][4];
+  float sl = 0.0f, v_mul = 1.0f;  // logits' factor in base 2, values' factor
+  float q_mul[2] = {1.0f, 1.0f};  // E4M3: power of two taken out of a row of Q
+  int rows = 0, t_first = 0;
+  int slot = 0;                   // stage of the products' tile
+  const uint32_t qs = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + C::RING;
+
+  while (cc.left > 0) {
+    // ---- a unit (or the part of it in this range) begins: Q, m, l, O
+    const int kvh = cc.x / A.blocks, h0 = kvh * A.group + (cc.x % A.blocks) * kRows;
+    rows = min(kRows, (kvh + 1) * A.group - h0);
+    t_first = cc.t;
+    sl = A.scale_log2;
+    if constexpr (KV == MOE_KV_E4M3) {
+      sl *= A.k_scale[kvh];
+      v_mul = A.v_scale[kvh];
+    }
+    if constexpr (KV == MOE_KV_F32) {
+      const float* q = static_cast<const float*>(A.q) + cc.b * A.q_b + h0 * A.q_h;
+      for (int i = threadIdx.x; i < kRows * (DP / 4); i += C::THREADS) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && d < A.dim) v = __ldg(reinterpret_cast<const float4*>(q + r * A.q_h + d));
+        *reinterpret_cast<float4*>(smem + C::RING + r * C::QP + d * 4) = v;
+      }
+      __syncthreads();
+    } else {
+      const __nv_bfloat16* q =
+          static_cast<const __nv_bfloat16*>(A.q) + cc.b * A.q_b + h0 * A.q_h;
+      if constexpr (C::QREG) {
+        // fragment layout: rows g and g + 8; 16 columns of a step kk as
+        // {2c, 2c+1} and {2c+8, 2c+9}; E4M3 keys come as 4 neighbouring codes
+        // per lane, so there lane c's columns are 4c .. 4c+3 instead
+        float big[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = g + (j & 1) * 8;
+            const int d = 16 * kk + (KV == MOE_KV_BF16 ? 2 * c4 + (j >> 1) * 8
+                                                       : 4 * c4 + (j >> 1) * 2);
+            uint32_t v = 0;
+            if (r < rows && d < A.dim)
+              v = __ldg(reinterpret_cast<const unsigned int*>(q + r * A.q_h + d));
+            qf[kk][j] = v;
+            if constexpr (KV == MOE_KV_E4M3)
+              big[j & 1] = fmaxf(big[j & 1], fmaxf(fabsf(__uint_as_float(v << 16)),
+                                                   fabsf(__uint_as_float(v & 0xffff0000u))));
+          }
+        }
+        if constexpr (KV == MOE_KV_E4M3) {
+          // rows of Q as f16: a row is first scaled by a power of two that
+          // brings its largest value into [1, 2).  bf16 has 8 bits, f16 11:
+          // nothing is rounded but what lies below 2^-17 of that value
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            big[j] = fmaxf(big[j], __shfl_xor_sync(0xffffffffu, big[j], 1));
+            big[j] = fmaxf(big[j], __shfl_xor_sync(0xffffffffu, big[j], 2));
+            const int e = min(max(static_cast<int>(__float_as_uint(big[j]) >> 23), 1), 253);
+            q_mul[j] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          }
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float inv = __uint_as_float(
+                  (254u - (__float_as_uint(q_mul[j & 1]) >> 23)) << 23);
+              const uint32_t v = qf[kk][j];
+              qf[kk][j] = f16x2(__uint_as_float(v << 16) * inv,
+                                __uint_as_float(v & 0xffff0000u) * inv);
+            }
+        }
+      } else {
+        // rows of Q in shared memory: warp w brings rows w, w + NW, ...
+        for (int r = warp; r < kRows; r += NW) {
+          uint32_t v[DP / 64];
+          float big = 0.0f;
+#pragma unroll
+          for (int j = 0; j < DP / 64; ++j) {
+            const int d = 2 * (lane + 32 * j);
+            v[j] = 0;
+            if (r < rows && d < A.dim)
+              v[j] = __ldg(reinterpret_cast<const unsigned int*>(q + r * A.q_h + d));
+            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
+                                   fabsf(__uint_as_float(v[j] & 0xffff0000u))));
+          }
+          if constexpr (KV == MOE_KV_E4M3) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+              big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+            const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253);
+            const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+            for (int j = 0; j < DP / 64; ++j)
+              v[j] = f16x2(__uint_as_float(v[j] << 16) * inv,
+                           __uint_as_float(v[j] & 0xffff0000u) * inv);
+            if (lane == 0) s_q[r] = __uint_as_float(static_cast<uint32_t>(e) << 23);
+          }
+#pragma unroll
+          for (int j = 0; j < DP / 64; ++j)
+            *reinterpret_cast<uint32_t*>(smem + C::RING + r * C::QP + 4 * (lane + 32 * j)) = v[j];
+        }
+        __syncthreads();
+        if constexpr (KV == MOE_KV_E4M3) {
+          q_mul[0] = s_q[g];
+          q_mul[1] = s_q[g + 8];
+        }
+      }
+    }
+    const float f0 = sl * q_mul[0], f1 = sl * q_mul[1];
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+
+    // ---- the unit's tiles in this range
+    bool more = true;
+    Cursor unit = cc;
+    while (more) {
+      cp_wait<ST - 2>();
+      __syncwarp();
+      {  // refill the stage that was used last
+        const int to = slot == 0 ? ST - 1 : slot - 1;
+        const Cursor at = lc;
+        const Want w = next;
+        if (lc.left > 0) advance<C::TILE>(lc, A, units);
+        next = want(lc);
+        load(at, w, to);
+      }
+      const unsigned mask = s_mask[warp][slot];
+      if (mask) {
+        const uint32_t kb = ring + slot * C::SB, vb = kb + kKeys * RB;
+        float s[2][4];
+        if constexpr (KV == MOE_KV_F32) {
+          // 3 products of (hi, lo) pairs; hi * hi and the small ones in sums
+          // of their own, and few terms to a chain: the tensor cores cut,
+          // not round, their sums
+          float hh[2][2][4] = {}, hl[2][4] = {};
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            // lane c's columns of the two k = 8 steps: 4c, 4c+1 and 4c+2, 4c+3
+            const float4 qa = lds4(qs + g * C::QP + (4 * kk + c4) * 16);
+            const float4 qb = lds4(qs + (g + 8) * C::QP + (4 * kk + c4) * 16);
+            uint32_t ah[2][4], al[2][4];
+            split_tf32(qa.x, ah[0][0], al[0][0]);
+            split_tf32(qb.x, ah[0][1], al[0][1]);
+            split_tf32(qa.y, ah[0][2], al[0][2]);
+            split_tf32(qb.y, ah[0][3], al[0][3]);
+            split_tf32(qa.z, ah[1][0], al[1][0]);
+            split_tf32(qb.z, ah[1][1], al[1][1]);
+            split_tf32(qa.w, ah[1][2], al[1][2]);
+            split_tf32(qb.w, ah[1][3], al[1][3]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 kv = lds4(kb + chunk_at<RB>(8 * j + g, 4 * kk + c4, true));
+              uint32_t h0_, h1_, h2_, h3_, l0_, l1_, l2_, l3_;
+              split_tf32(kv.x, h0_, l0_);
+              split_tf32(kv.y, h1_, l1_);
+              split_tf32(kv.z, h2_, l2_);
+              split_tf32(kv.w, h3_, l3_);
+              mma_tf32(hh[j][0], ah[0], h0_, h1_);
+              mma_tf32(hh[j][1], ah[1], h2_, h3_);
+              mma_tf32(hl[j], al[0], h0_, h1_);
+              mma_tf32(hl[j], ah[0], l0_, l1_);
+              mma_tf32(hl[j], al[1], h2_, h3_);
+              mma_tf32(hl[j], ah[1], l2_, l3_);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = hh[j][0][e] + hh[j][1][e] + hl[j][e];
+        } else {
+          float part[2][2][4] = {};  // even and odd steps: shorter chains
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            uint32_t qa[4];
+            if constexpr (C::QREG) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) qa[j] = qf[kk][j];
+            } else if constexpr (KV == MOE_KV_BF16) {
+              ldsm4(qs + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::QP + (2 * kk + (lane >> 4)) * 16,
+                    qa);
+            } else {
+              const uint2 a = lds2(qs + g * C::QP + (4 * kk + c4) * 8);
+              const uint2 b = lds2(qs + (g + 8) * C::QP + (4 * kk + c4) * 8);
+              qa[0] = a.x;
+              qa[1] = b.x;
+              qa[2] = a.y;
+              qa[3] = b.y;
+            }
+            if constexpr (KV == MOE_KV_BF16) {
+              uint32_t r[4];
+              ldsm4(kb + chunk_at<RB>((lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1), true),
+                    r);
+              mma_bf16(part[kk & 1][0], qa, r[0], r[1]);
+              mma_bf16(part[kk & 1][1], qa, r[2], r[3]);
+            } else {
+              // one x4 load brings the 16-byte chunks kk and kk + 1 of 16 keys
+              static_assert(DP % 32 == 0, "E4M3 steps come in pairs");
+              if (kk % 2 == 0) {
+                uint32_t r[4], qn[4];
+                ldsm4(kb + chunk_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, kk + (lane >> 4), true),
+                      r);
+                mma_f16(part[0][0], qa, e4m3x2_f16x2(r[0]), e4m3x2_f16x2_hi(r[0]));
+                mma_f16(part[0][1], qa, e4m3x2_f16x2(r[1]), e4m3x2_f16x2_hi(r[1]));
+                if constexpr (C::QREG) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) qn[j] = qf[kk + 1][j];
+                } else {
+                  const uint2 a = lds2(qs + g * C::QP + (4 * kk + 4 + c4) * 8);
+                  const uint2 b = lds2(qs + (g + 8) * C::QP + (4 * kk + 4 + c4) * 8);
+                  qn[0] = a.x;
+                  qn[1] = b.x;
+                  qn[2] = a.y;
+                  qn[3] = b.y;
+                }
+                mma_f16(part[1][0], qn, e4m3x2_f16x2(r[2]), e4m3x2_f16x2_hi(r[2]));
+                mma_f16(part[1][1], qn, e4m3x2_f16x2(r[3]), e4m3x2_f16x2_hi(r[3]));
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = part[0][j][e] + part[1][j][e];
+        }
+        // masked keys out (their rows hold zeros), then the running softmax:
+        // rows g (e = 0, 1) and g + 8 (e = 2, 3), keys 8 j + 2 c + (e & 1)
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool live = (mask >> (8 * j + 2 * c4 + (e & 1))) & 1u;
+            s[j][e] = live ? s[j][e] * (e < 2 ? f0 : f1) : -INFINITY;
+            top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
+          }
+        float keep[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+          top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+          const float now = fmaxf(m[r], top[r]);
+          // a maximum of -inf (every logit is -inf so far) stands for 0
+          keep[r] = now == -INFINITY ? 1.0f : ex2(m[r] - now);
+          m[r] = now;
+        }
+        const float z0 = m[0] == -INFINITY ? 0.0f : m[0], z1 = m[1] == -INFINITY ? 0.0f : m[1];
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[j][e] = ex2(s[j][e] - (e < 2 ? z0 : z1));
+            sum[e >> 1] += s[j][e];
+          }
+        l[0] = l[0] * keep[0] + sum[0];
+        l[1] = l[1] * keep[1] + sum[1];
+        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            acc[i][0] *= keep[0];
+            acc[i][1] *= keep[0];
+            acc[i][2] *= keep[1];
+            acc[i][3] *= keep[1];
+          }
+        }
+        // ---- O += P V
+        if constexpr (KV == MOE_KV_BF16) {
+          // P as a sum of two bf16: 16 bits of it, where one would leave 8.
+          // The second product is free: the tile's bytes take longer
+          uint32_t ph[4], pl[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = s[j >> 1][(j & 1) * 2], y = s[j >> 1][(j & 1) * 2 + 1];
+            ph[j] = bf16x2(x, y);
+            pl[j] = bf16x2(x - __uint_as_float(ph[j] << 16),
+                           y - __uint_as_float(ph[j] & 0xffff0000u));
+          }
+#pragma unroll
+          for (int dd = 0; dd < DP / 16; ++dd) {
+            uint32_t r[4];
+            ldsm4t(vb + chunk_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * dd + (lane >> 4), true),
+                   r);
+            mma_bf16(acc[2 * dd], ph, r[0], r[1]);
+            mma_bf16(acc[2 * dd + 1], ph, r[2], r[3]);
+            mma_bf16(acc[2 * dd], pl, r[0], r[1]);
+            mma_bf16(acc[2 * dd + 1], pl, r[2], r[3]);
+          }
+        } else if constexpr (KV == MOE_KV_E4M3) {
+          // P rounded to f16: 2^-12 of each weight, as against the 2^-4 of
+          // the cached values themselves
+          uint32_t p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            p[j] = f16x2(s[j >> 1][(j & 1) * 2], s[j >> 1][(j & 1) * 2 + 1]);
+#pragma unroll
+          for (int dd = 0; dd < DP / 32; ++dd) {
+            // x4: keys 0..7 and 8..15 of chunks 2 dd and 2 dd + 1; a register
+            // holds codes (d, d+1) of keys 2c and 2c + 1, d = 2g: bytes 0 and
+            // 2 are column d of both keys, bytes 1 and 3 column d + 1
+            uint32_t r[4];
+            ldsm4t(vb + chunk_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * dd + (lane >> 4), true),
+                   r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = __byte_perm(r[j], 0, 0x3120);
+            mma_f16(acc[4 * dd], p, e4m3x2_f16x2(r[0]), e4m3x2_f16x2(r[1]));
+            mma_f16(acc[4 * dd + 1], p, e4m3x2_f16x2_hi(r[0]), e4m3x2_f16x2_hi(r[1]));
+            mma_f16(acc[4 * dd + 2], p, e4m3x2_f16x2(r[2]), e4m3x2_f16x2(r[3]));
+            mma_f16(acc[4 * dd + 3], p, e4m3x2_f16x2_hi(r[2]), e4m3x2_f16x2_hi(r[3]));
+          }
+        } else {
+          // step j takes keys 8 j ..: lane c's two are 8 j + 2 c and + 1, the
+          // very ones whose weights it holds
+          uint32_t ph[2][4], pl[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            split_tf32(s[j][0], ph[j][0], pl[j][0]);
+            split_tf32(s[j][2], ph[j][1], pl[j][1]);
+            split_tf32(s[j][1], ph[j][2], pl[j][2]);
+            split_tf32(s[j][3], ph[j][3], pl[j][3]);
+          }
+#pragma unroll
+          for (int dd = 0; dd < DP / 32; ++dd) {
+            float o[4][4] = {}, o2[4][4] = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 a = lds4(vb + chunk_at<RB>(8 * j + 2 * c4, 8 * dd + g, false));
+              const float4 b = lds4(vb + chunk_at<RB>(8 * j + 2 * c4 + 1, 8 * dd + g, false));
+              const float va[4] = {a.x, a.y, a.z, a.w}, vb4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                uint32_t ah, al, bh, bl;
+                split_tf32(va[t], ah, al);
+                split_tf32(vb4[t], bh, bl);
+                mma_tf32(o[t], ph[j], ah, bh);
+                mma_tf32(o2[t], pl[j], ah, bh);
+                mma_tf32(o2[t], ph[j], al, bl);
+              }
+            }
+            // the long sum over tiles in rounded fp32 additions
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[4 * dd + t][e] += o[t][e] + o2[t][e];
+          }
+        }
+      }
+      more = cc.left > 1 && cc.t + 1 < cc.nt;
+      if (more) {
+        slot = slot + 1 == ST ? 0 : slot + 1;
+        ++cc.t;
+        --cc.left;
+      }
+    }
+
+    // ---- the unit's part ends: join the warps through the stage just used
+    // (its refill comes after the barrier below)
+    const int t_last = cc.t;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (c4 == 0) {
+        s_m[warp][g + 8 * r] = m[r];
+        s_l[warp][g + 8 * r] = l[r];
+      }
+    }
+    const bool whole = t_first == 0 && t_last + 1 == unit.nt;
+    const long long part = 2ll * cta + (t_first == 0 ? 0 : 1);
+    constexpr int PASSES = DP / C::JC;
+    float* const dump = reinterpret_cast<float*>(smem + (warp * ST + slot) * C::SB);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (p > 0) __syncthreads();
+      __syncwarp();  // every lane is done with the stage
+#pragma unroll
+      for (int i = p * (NT / PASSES); i < (p + 1) * (NT / PASSES); ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int n = 2 * c4 + (e & 1);  // column of the instruction's result
+          const int d = KV == MOE_KV_BF16   ? 8 * i + n
+                        : KV == MOE_KV_E4M3 ? (i >> 1) * 16 + 2 * n + (i & 1)
+                                            : (i >> 2) * 32 + 4 * n + (i & 3);
+          dump[(g + 8 * (e >> 1)) * C::JC + d - p * C::JC] = acc[i][e];
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < rows * (C::JC / 4); i += C::THREADS) {
+        const int r = i / (C::JC / 4), d = i % (C::JC / 4) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w][r]);
+        float sum = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = top == -INFINITY ? 1.0f : ex2(s_m[w][r] - top);
+          const float4 x = *reinterpret_cast<const float4*>(
+              smem + (w * ST + slot) * C::SB + (r * C::JC + d) * 4);
+          sum += f * s_l[w][r];
+          o.x += f * x.x;
+          o.y += f * x.y;
+          o.z += f * x.z;
+          o.w += f * x.w;
+        }
+        const int dd = d + p * C::JC;
+        if (whole) {
+          const float inv = sum == 0.0f ? 0.0f : v_mul / sum;
+          if (dd < A.dim)
+            store4<KV>(A.out, cc.b * A.o_b + (h0 + r) * A.o_h + dd,
+                       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+          if (dd == 0 && A.lse)
+            A.lse[static_cast<long long>(cc.b) * A.Hq + h0 + r] =
+                sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(A.part_o + (part * kRows + r) * DP + dd) = o;
+          if (dd == 0) A.part_ml[part * kRows + r] = make_float2(top, sum);
+        }
+      }
+    }
+    if (!whole && t_first == 0 && threadIdx.x == 0) {
+      // the unit begins here and goes on in the next CTAs, up to the one
+      // whose range holds its last tile
+      const long long last = end - unit.left + unit.nt - 1;
+      const long long who = ((last + 1) * ctas - 1) / total;
+      A.info[cta] = make_int4(cc.b, cc.x, static_cast<int>(who - cta + 1), 0);
+    }
+    __syncthreads();  // the stages and s_m may be used again
+    slot = slot + 1 == ST ? 0 : slot + 1;
+    advance<C::TILE>(cc, A, units);
+  }
+  cp_wait<0>();
+  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
+}
+
+// Joins the parts of a unit that range borders cut.  Block (c, r): row r of
+// the unit that begins in CTA c and does not end there (most blocks find
+// none).  Its parts are c's first slot, then the second slots of the next
+// CTAs; the four warps take every fourth part, so the loads of a long
+// request's 300 parts overlap.
+template <int KV, int DP>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs A) {
+  constexpr int VL = DP / 32;  // columns per lane
+  __shared__ float s_o[4][DP];
+  __shared__ float s_l[4];
+  pdl_wait();
+  const int cta = blockIdx.x, r = blockIdx.y;
+  const int4 u = A.info[cta];
+  if (u.z == 0) return;
+  const int kvh = u.y / A.blocks, h0 = kvh * A.group + (u.y % A.blocks) * kRows;
+  if (h0 + r >= (kvh + 1) * A.group) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto at = [&](int i) { return (2ll * (cta + i) + (i == 0 ? 0 : 1)) * kRows + r; };
+  float top = -INFINITY;
+  for (int i = lane; i < u.z; i += 32) top = fmaxf(top, A.part_ml[at(i)].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float o[VL] = {};
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int i = warp; i < u.z; i += 4) {
+    const float2 ml = A.part_ml[at(i)];
+    const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
+    const float* x = A.part_o + at(i) * DP + lane * VL;
+    sum += f * ml.y;
+    float v[VL];
+#pragma unroll
+    for (int j = 0; j < VL; j += 2)
+      *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(x + j);
+#pragma unroll
+    for (int j = 0; j < VL; ++j) o[j] += f * v[j];
+  }
+#pragma unroll
+  for (int j = 0; j < VL; ++j) s_o[warp][lane * VL + j] = o[j];
+  if (lane == 0) s_l[warp] = sum;
+  __syncthreads();
+  sum = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
+  const float inv = sum == 0.0f ? 0.0f : mul / sum;
+  for (int d = threadIdx.x * 4; d < A.dim; d += 512) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = (s_o[0][d + j] + s_o[1][d + j] + s_o[2][d + j] + s_o[3][d + j]) * inv;
+    store4<KV>(A.out, u.x * A.o_b + (h0 + r) * A.o_h + d, make_float4(v[0], v[1], v[2], v[3]));
+  }
+  if (threadIdx.x == 0 && A.lse)
+    A.lse[static_cast<long long>(u.x) * A.Hq + h0 + r] =
+        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------ host
+static int attn_sm_count() {
+  static std::mutex mu;
+  static int count[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (count[dev] == 0 &&
+      cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return count[dev];
+}
+
+static int attn_dp(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+template <int KV, int DP>
+static cudaError_t launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
+  using C = AttnCfg<KV, DP>;
+  auto* kern = attn_decode_kernel<KV, DP>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_chained(attn_join_kernel<KV, DP>, dim3(ctas, a.group < kRows ? a.group : kRows),
+                        dim3(128), 0, st, a);
+}
+
+template <int KV>
+static int attn_ctas_per_sm(int dp) {
+  return dp == 64 ? AttnCfg<KV, 64>::CTAS : dp == 128 ? AttnCfg<KV, 128>::CTAS
+                                                      : AttnCfg<KV, 256>::CTAS;
+}
+static int ctas_per_sm(int kv, int dp) {
+  return kv == MOE_KV_F32    ? attn_ctas_per_sm<MOE_KV_F32>(dp)
+         : kv == MOE_KV_BF16 ? attn_ctas_per_sm<MOE_KV_BF16>(dp)
+                             : attn_ctas_per_sm<MOE_KV_E4M3>(dp);
+}
+
+template <int KV>
+static cudaError_t launch_kv(int dp, const AttnArgs& a, int ctas, cudaStream_t st) {
+  return dp == 64    ? launch_attn<KV, 64>(a, ctas, st)
+         : dp == 128 ? launch_attn<KV, 128>(a, ctas, st)
+                     : launch_attn<KV, 256>(a, ctas, st);
+}
+
+static size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_attn_workspace(int kv_dtype, int head_dim) {
+  if (kv_dtype < MOE_KV_F32 || kv_dtype > MOE_KV_E4M3 || head_dim < 1 || head_dim > 256) return 0;
+  const int dp = attn_dp(head_dim);
+  const size_t n = static_cast<size_t>(attn_sm_count()) * ctas_per_sm(kv_dtype, dp);
+  return up256(n * sizeof(int4)) + up256(2 * n * kRows * sizeof(float2)) +
+         2 * n * kRows * dp * sizeof(float);
+}
+
+int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stride_b,
+                    long long q_stride_h, int B, int Hq, const int32_t* block_table,
+                    int max_pages, long long table_stride, const int32_t* seq_lens, float scale,
+                    int window, void* out, long long o_stride_b, long long o_stride_h, float* lse,
+                    void* ws, size_t ws_bytes, uint32_t* err, void* stream) {
+  const int rc = kv_cache_ok(cache);
+  if (rc != MOE_OK) return rc;
+  if (B < 0 || Hq < 1 || Hq % cache->kv_heads || Hq > (1 << 20) || max_pages < 1 ||
+      table_stride < max_pages || window < 0 ||
+      static_cast<long long>(max_pages) * cache->page_size > kMaxLen || q_stride_b < 0 || q_stride_h < 0 ||
+      o_stride_b < 0 || o_stride_h < 0 || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (B == 0) return MOE_OK;
+  if (!q || !block_table || !seq_lens || !out || !ws) return MOE_ERR_INVALID_ARG;
+  const int qs = cache->kv_dtype == MOE_KV_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+       static_cast<uintptr_t>(q_stride_b * qs) | static_cast<uintptr_t>(q_stride_h * qs) |
+       static_cast<uintptr_t>(o_stride_b * qs) | static_cast<uintptr_t>(o_stride_h * qs)) &
+      15)
+    return MOE_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_attn_workspace(cache->kv_dtype, cache->head_dim);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const int sms = attn_sm_count();
+  if (sms < 1) return MOE_ERR_CUDA;
+  const int es = kv_esize(cache->kv_dtype), dp = attn_dp(cache->head_dim);
+  AttnArgs a = {};
+  a.k = static_cast<const char*>(cache->k);
+  a.v = static_cast<const char*>(cache->v);
+  a.s_page = cache->stride_page * es;
+  a.s_token = cache->stride_token * es;
+  a.s_head = cache->stride_head * es;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.q = q;
+  a.q_b = q_stride_b;
+  a.q_h = q_stride_h;
+  a.out = out;
+  a.o_b = o_stride_b;
+  a.o_h = o_stride_h;
+  a.lse = lse;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.lens = seq_lens;
+  a.err = err;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.B = B;
+  a.Hq = Hq;
+  a.heads = cache->kv_heads;
+  a.group = Hq / cache->kv_heads;
+  a.blocks = (a.group + kRows - 1) / kRows;
+  a.dim = cache->head_dim;
+  a.page = cache->page_size;
+  a.num_pages = cache->num_pages;
+  a.max_pages = max_pages;
+  a.window = window;
+  a.min_tiles = 1;
+  const int full = sms * ctas_per_sm(cache->kv_dtype, dp);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.info = reinterpret_cast<int4*>(w);
+  w += up256(full * sizeof(int4));
+  a.part_ml = reinterpret_cast<float2*>(w);
+  w += up256(2ull * full * kRows * sizeof(float2));
+  a.part_o = reinterpret_cast<float*>(w);
+  // no more CTAs than the most tiles that these sizes can hold (of 32 tokens
+  // at least; the kernel goes by the lengths themselves)
+  long long longest = static_cast<long long>(max_pages) * cache->page_size;
+  if (window > 0 && window < longest) longest = window;
+  const long long units = static_cast<long long>(B) * a.heads * a.blocks;
+  const long long per = (longest + 31) / 32;
+  const int ctas = units >= full || per >= full || units * per >= full
+                       ? full
+                       : static_cast<int>(units * per);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = cache->kv_dtype == MOE_KV_F32    ? launch_kv<MOE_KV_F32>(dp, a, ctas, st)
+                        : cache->kv_dtype == MOE_KV_BF16 ? launch_kv<MOE_KV_BF16>(dp, a, ctas, st)
+                                                         : launch_kv<MOE_KV_E4M3>(dp, a, ctas, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

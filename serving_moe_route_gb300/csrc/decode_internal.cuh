@@ -1,0 +1,43 @@
+// decode_internal.cuh -- shared by the translation units of the decode-step
+// operators (kv_cache.cu, attn_decode.cu, sample.cu).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "../../include/moe_route.h"
+
+namespace moe {
+
+// bytes of one cached element
+__host__ __device__ constexpr int kv_esize(int kv_dtype) {
+  return kv_dtype == MOE_KV_F32 ? 4 : kv_dtype == MOE_KV_BF16 ? 2 : 1;
+}
+
+// MOE_OK if the cache descriptor meets the header's requirements
+int kv_cache_ok(const moe_kv_cache_t* c);
+
+// Launch `kern` in clusters of `cluster` CTAs (1: none) such that it may
+// overlap its predecessor's tail in the stream; the kernel calls pdl_wait()
+// before it touches anything the predecessor writes or reads.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, int cluster,
+                                  size_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+}  // namespace moe
