@@ -530,6 +530,33 @@ int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stri
  * lengths; 0 for values outside the requirements. */
 size_t moe_attn_workspace(int kv_dtype, int head_dim);
 
+/*
+ * moe_sample -- the next token of each row from its logits and one uniform
+ * random number.
+ *   logits       device [B, V] (MOE_LOGITS_*), rows row_stride elements apart
+ *   u            device f32 [B], in [0, 1)
+ *   temperature  device f32 [B] or NULL (1); <= 0: greedy, the largest logit
+ *   top_k        device int32 [B] or NULL; <= 0 or >= V: off
+ *   top_p        device f32 [B] or NULL; >= 1: off
+ *   min_p        device f32 [B] or NULL; <= 0: off
+ *   ids          device int32 [B] out
+ *   probs        NULL, or device f32 [B] out: the drawn token's share of what
+ *                was kept (1 for a greedy row)
+ * Tokens are ordered by logit, descending, ties to the lower index.  NaN and
+ * -inf logits are never drawn, +inf counts as the type's largest number.  With w = exp((logit -
+ * largest) / temperature), a row keeps the first top_k tokens, of them those
+ * with w >= min_p (above 1 counts as 1), and of them the shortest prefix
+ * whose w sum reaches top_p of theirs (at least one token).  The draw is the
+ * first kept token, by index, at which the running sum of w exceeds u times
+ * the kept sum.  A row without a token to draw gets id -1 and probability 0.
+ * Sums are whole numbers of 2^-44 of the largest w, so they depend on no order
+ * of addition.  Requires 1 <= V <= 2^18, B <= 65535.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
+ */
+int moe_sample(const void* logits, int logits_dtype, int B, int V, long long row_stride,
+               const float* u, const float* temperature, const int32_t* top_k,
+               const float* top_p, const float* min_p, int32_t* ids, float* probs, void* stream);
+
 /* moe_check_word -- moe_check for a caller's error word: synchronise
  * `stream`, read *err, clear it, and return MOE_OK or MOE_ERR_DEVICE. */
 int moe_check_word(uint32_t* err, uint32_t* bits, void* stream);

@@ -7,10 +7,10 @@ in ``include/moe_route.h``.
 """
 from ._binding import MoeError, MoePlan, lib, moe_plan  # noqa: F401
 from .decode import (KVStep, attn_decode, attn_workspace, check_word, kv_append,  # noqa: F401
-                     kv_release, kv_step)
+                     kv_release, kv_step, sample_tokens)
 from .ep import ep_forward  # noqa: F401
 from .layer import BF16, F32, FP8, SIGMOID, SOFTMAX, MoELayer, route_topk  # noqa: F401
 
 __all__ = ["MoELayer", "MoePlan", "MoeError", "route_topk", "ep_forward", "moe_plan", "lib",
            "KVStep", "kv_step", "kv_release", "kv_append", "attn_decode", "attn_workspace",
-           "check_word", "F32", "BF16", "FP8", "SOFTMAX", "SIGMOID"]
+           "sample_tokens", "check_word", "F32", "BF16", "FP8", "SOFTMAX", "SIGMOID"]

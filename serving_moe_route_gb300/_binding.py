@@ -36,7 +36,7 @@ EXPORTED = ("moe_plan", "moe_plan_ep", "moe_forward", "moe_forward_timed", "moe_
             "moe_plan_set_groups", "moe_check", "moe_plan_describe",
             "moe_ep_dispatch", "moe_ep_pack", "moe_ep_combine",
             "moe_kv_step", "moe_kv_release", "moe_kv_append", "moe_attn_decode",
-            "moe_attn_workspace", "moe_check_word",
+            "moe_attn_workspace", "moe_sample", "moe_check_word",
             "moe_strerror", "moe_abi_version")
 
 
@@ -142,6 +142,8 @@ def lib() -> ctypes.CDLL:
     L.moe_attn_decode.restype = i
     L.moe_attn_workspace.argtypes = [i, i]
     L.moe_attn_workspace.restype = sz
+    L.moe_sample.argtypes = [P, i, i, i, ll, P, P, P, P, P, P, P, P]
+    L.moe_sample.restype = i
     L.moe_check_word.argtypes = [P, ctypes.POINTER(c_u32), P]
     L.moe_check_word.restype = i
     if L.moe_abi_version() != 4:
@@ -278,6 +280,12 @@ def moe_attn_decode(cache, q, q_stride_b, q_stride_h, B, Hq, block_table, max_pa
     return lib().moe_attn_decode(ctypes.byref(cache), q, q_stride_b, q_stride_h, B, Hq,
                                  block_table, max_pages, table_stride, seq_lens, scale, window,
                                  out, o_stride_b, o_stride_h, lse, ws, ws_bytes, err, stream)
+
+
+def moe_sample(logits, logits_dtype, B, V, row_stride, u, temperature, top_k, top_p, min_p, ids,
+               probs, stream):
+    return lib().moe_sample(logits, logits_dtype, B, V, row_stride, u, temperature, top_k, top_p,
+                            min_p, ids, probs, stream)
 
 
 def moe_check_word(err, stream):

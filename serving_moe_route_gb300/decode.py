@@ -1,6 +1,6 @@
 """The rest of a decode step around the layer: block tables and slot maps of a
-paged key-value cache, the write of new keys and values, and attention of one
-new token per request over the cache.
+paged key-value cache, the write of new keys and values, attention of one new
+token per request over the cache, and sampling.
 
 A cache is two tensors ``[num_pages, page_size, kv_heads, head_dim]`` of the
 same strides, float32, bfloat16 or float8_e4m3fn (then with one float32 scale
@@ -16,6 +16,7 @@ One step of a server with its state on the GPU::
         kv_append(k, v, step.slots, k_cache, v_cache, err=err)
         out = attn_decode(q, k_cache, v_cache, block_table, step.seq_lens, err=err)
         ...
+    ids, probs = sample_tokens(logits, u, temperature=t, top_p=p)
     kv_release(done, block_table, free_pages, n_free, num_pages=P, err=err)
 
 ``err`` is an int32 tensor of one zero that collects error bits
@@ -34,6 +35,7 @@ from .layer import _p, _stream
 
 _KV_DTYPE = {torch.float32: B.MOE_KV_F32, torch.bfloat16: B.MOE_KV_BF16,
              torch.float8_e4m3fn: B.MOE_KV_E4M3}
+_LOGITS_DTYPE = {torch.float32: B.MOE_LOGITS_F32, torch.bfloat16: B.MOE_LOGITS_BF16}
 
 
 class KVStep(NamedTuple):
@@ -241,6 +243,36 @@ def attn_workspace(kv_dtype: torch.dtype, head_dim: int) -> int:
     if kv_dtype not in _KV_DTYPE:
         raise ValueError(f"no cache of {kv_dtype}")
     return B.moe_attn_workspace(_KV_DTYPE[kv_dtype], head_dim)
+
+
+def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """The next token of each row of ``logits`` [B, V] (float32 or bfloat16)
+    from one uniform random number in [0, 1) per row, ``u`` float32 [B].
+    ``temperature``, ``top_p``, ``min_p`` (float32 [B]) and ``top_k`` (int32
+    [B]) hold per row, None leaves that restriction out; temperature <= 0 is
+    greedy.  Returns (ids int32 [B], probs float32 [B]): the drawn tokens and
+    their shares of what was kept; -1 and 0 for a row without a token."""
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    ldt = _LOGITS_DTYPE.get(logits.dtype)
+    if ldt is None:
+        raise ValueError("logits must be float32 or bfloat16")
+    if logits.dim() != 2 or logits.shape[1] < 1 or logits.shape[1] > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must be [B, V] with contiguous rows")
+    n, V = logits.shape
+    dev = logits.device
+    _vec(u, torch.float32, n, "u", dev)
+    for t, dt, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
+                        (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
+        if t is not None:
+            _vec(t, dt, n, name, dev)
+    ids = torch.empty(n, dtype=torch.int32, device=dev)
+    probs = torch.empty(n, dtype=torch.float32, device=dev)
+    rc = B.moe_sample(logits.data_ptr(), ldt, n, V, logits.stride(0) if n > 1 else V, u.data_ptr(),
+                      _p(temperature), _p(top_k), _p(top_p), _p(min_p), ids.data_ptr(),
+                      probs.data_ptr(), _stream(stream))
+    B._check(rc, "moe_sample")
+    return ids, probs
 
 
 def check_word(err, stream=None):

@@ -5,7 +5,6 @@ import numpy as np
 import torch
 
 BAD_PAGE, NO_SPACE = 16, 32
-FLT_MAX = float(np.finfo(np.float32).max)
 
 
 def kv_step(ctx, new, table, free, n_free, page, num_pages, max_tokens):
@@ -108,14 +107,17 @@ def attend(q, k, v, table, lens, scale, window=0, k_scale=None, v_scale=None):
     return out, lse, pv, dot, count
 
 
-def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
-    """ids, probs of every row, and for each row how near a border the draw and
-    the top-p cut came (share of the kept sum)."""
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, largest=np.inf):
+    """ids and probs of every row (largest: what +inf counts as), how near a
+    border the draw and the top-p cut came, and how far the sums they are
+    compared with may be off: weights that are right to 2^-38 of themselves and
+    to 2^-45 of the largest one, on both sides of the border.  Both as a share
+    of the kept sum."""
     B, V = logits.shape
-    ids, probs, near = np.full(B, -1), np.zeros(B), np.ones(B)
+    ids, probs, near, off = np.full(B, -1), np.zeros(B), np.ones(B), np.zeros(B)
     for b in range(B):
         x = logits[b].astype(np.float64)
-        x = np.where(np.isnan(x), -np.inf, np.minimum(x, FLT_MAX))
+        x = np.where(np.isnan(x), -np.inf, np.minimum(x, largest))
         order = np.lexsort((np.arange(V), -x))
         order = order[x[order] > -np.inf]
         if not len(order):
@@ -136,8 +138,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
             border = float(top_p[b]) * w[kept].sum()
             inside = before < border
             inside[0] = True
-            near[b] = min(near[b], np.abs(before[1:] - border).min() / w[kept].sum()
-                          if len(kept) > 1 else 1.0)
+            if len(kept) > 1:
+                near[b] = np.abs(before[1:] - border).min() / w[kept].sum()
             kept = kept[inside]
         kept = np.sort(kept)
         sums = np.cumsum(w[kept])
@@ -145,7 +147,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
         j = min(int((sums <= border).sum()), int(np.flatnonzero(w[kept])[-1]))
         near[b] = min(near[b], np.abs(sums - border).min() / sums[-1])
         ids[b], probs[b] = kept[j], w[kept[j]] / sums[-1]
-    return ids, probs, near
+        off[b] = 2 * (2.0 ** -38 + len(order) * 2.0 ** -45 / sums[-1])
+    return ids, probs, near, off
 
 
 def f64(t):

@@ -117,6 +117,22 @@ def test_release(kw, code):
                             a["cap"], a["n"], a["pages"], 0, 0) == code
 
 
+def sample(**kw):
+    a = dict(logits=FAKE, dtype=B.MOE_LOGITS_F32, B=2, V=100, stride=100, u=FAKE, t=0, k=0, p=0,
+             m=0, ids=FAKE, probs=0)
+    a.update(kw)
+    return B.moe_sample(a["logits"], a["dtype"], a["B"], a["V"], a["stride"], a["u"], a["t"],
+                        a["k"], a["p"], a["m"], a["ids"], a["probs"], 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), BAD), (dict(B=65536), BAD), (dict(V=0), BAD), (dict(V=(1 << 18) + 1), BAD),
+    (dict(stride=-1), BAD), (dict(dtype=2), BAD), (dict(logits=0), BAD), (dict(u=0), BAD),
+    (dict(ids=0), BAD), (dict(logits=FAKE + 2), BAD), (dict(B=0, logits=0, u=0, ids=0), OK)])
+def test_sample(kw, code):
+    assert sample(**kw) == code
+
+
 def test_check_word_and_workspace():
     assert B.moe_check_word(0, 0)[0] == BAD
     assert B.moe_attn_workspace(7, 128) == 0
@@ -157,5 +173,7 @@ def test_wrappers_refuse_cpu_tensors():
         moe.kv_append(x, x, i, kc, kc)
     with pytest.raises(ValueError, match="CUDA"):
         moe.attn_decode(x, kc, kc, t, i)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.sample_tokens(torch.zeros(2, 8), torch.zeros(2))
     with pytest.raises(ValueError, match="CUDA"):
         moe.check_word(i[:1])
