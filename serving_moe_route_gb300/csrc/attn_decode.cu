@@ -914,8 +914,8 @@ template <int KV, int DP>
 static cudaError_t launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
   using C = AttnCfg<KV, DP>;
   auto* kern = attn_decode_kernel<KV, DP>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::SMEM, done);
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, st, a);
   if (e != cudaSuccess) return e;

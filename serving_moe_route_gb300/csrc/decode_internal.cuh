@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
 #include <type_traits>
 
 #include "../../include/moe_route.h"
@@ -16,6 +18,21 @@ __host__ __device__ constexpr int kv_esize(int kv_dtype) {
 
 // MOE_OK if the cache descriptor meets the header's requirements
 int kv_cache_ok(const moe_kv_cache_t* c);
+
+// Allow `kern` up to `bytes` of dynamic shared memory on the current device,
+// asking the runtime once per device (a microsecond a call otherwise).
+// `done`: the caller's static, a bit per device, for one kernel and its
+// largest size.
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch `kern` in clusters of `cluster` CTAs (1: none) such that it may
 // overlap its predecessor's tail in the stream; the kernel calls pdl_wait()

@@ -346,9 +346,10 @@ int moe_kv_step(const int32_t* ctx_lens, const int32_t* new_lens, int B, int32_t
   int ctas = 1;
   while (ctas < 8 && max_tokens > 2048ll * ctas) ctas *= 2;
   const size_t smem = static_cast<size_t>(B) * 2 * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kv_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (smem > 32 * 1024 &&
+      allow_smem(reinterpret_cast<const void*>(kv_step_kernel),
+                 MOE_KV_MAX_REQUESTS * 2 * static_cast<int>(sizeof(int)), done) != cudaSuccess)
     return MOE_ERR_CUDA;
   return launch_cluster(kv_step_kernel, dim3(ctas), dim3(kStepThreads), ctas, smem,
                         static_cast<cudaStream_t>(stream), a) == cudaSuccess

@@ -48,6 +48,8 @@ constexpr int kBins = 2048;
 constexpr int kList = kSampThreads;  // tokens that the list holds: one a thread
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 18;
+// bytes of the largest slice (f32, 2^18 tokens over 8 CTAs) and its edges
+constexpr int kMaxSlice = kMaxVocab / kMaxCluster * 4 + 32;
 
 struct SampArgs {
   const void* logits;
@@ -765,8 +767,8 @@ __global__ void __launch_bounds__(kSampThreads) sample_kernel(const SampArgs A) 
 template <typename LT>
 static cudaError_t launch_sample(const SampArgs& a, int B, int cluster, cudaStream_t st) {
   const size_t smem = (static_cast<size_t>(a.slice) * sizeof(LT) + 31) / 16 * 16;
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<LT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(sample_kernel<LT>), kMaxSlice, done);
   if (e != cudaSuccess) return e;
   return launch_cluster(sample_kernel<LT>, dim3(static_cast<unsigned>(B) * cluster),
                         dim3(kSampThreads), cluster, smem, st, a);

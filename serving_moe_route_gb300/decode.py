@@ -31,7 +31,6 @@ from typing import NamedTuple
 import torch
 
 from . import _binding as B
-from .layer import _p, _stream
 
 _KV_DTYPE = {torch.float32: B.MOE_KV_F32, torch.bfloat16: B.MOE_KV_BF16,
              torch.float8_e4m3fn: B.MOE_KV_E4M3}
@@ -47,87 +46,106 @@ class KVStep(NamedTuple):
     n_free: torch.Tensor     # [1] free pages left
 
 
-def _vec(t, dtype, n, name, device):
-    """A contiguous vector of n elements (n None: any length) on `device`."""
+# The current stream's handle for a device number: a tenth of a microsecond
+# where torch.cuda.current_stream() builds an object in three
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(t, stream):
+    """(device number, stream handle) for a call whose tensors live with t."""
+    dev = t.get_device()
+    if stream is not None:
+        return dev, stream.cuda_stream
+    return dev, _raw_stream(dev) if dev >= 0 else 0
+
+
+def _refuse(t, dtype, n, name, dev):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must have shape {'[n]' if n is None else (n,)}, "
-                         f"got {tuple(t.shape)}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _table(t, rows, device):
-    if not t.is_cuda:
-        raise ValueError("block_table must be a CUDA tensor")
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < 1:
+def _vec(t, dtype, n, name, dev):
+    """The address of a contiguous vector of n elements on device dev."""
+    if (t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or dev < 0
+            or not t.is_contiguous()):
+        _refuse(t, dtype, n, name, dev)
+    return t.data_ptr()
+
+
+def _table(t, rows, dev):
+    """(address, max_pages, stride) of a block table."""
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != rows or shape[1] < 1:
         raise ValueError(f"block_table must be int32 [{rows}, max_pages], got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    if rows and (t.shape[1] > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < t.shape[1]):
+                         f"{tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"block_table must be on cuda:{dev}, got {t.device}")
+    width = shape[1]
+    stride, inner = t.stride()
+    if rows and (width > 1 and inner != 1 or rows > 1 and stride < width):
         raise ValueError("block_table's rows must be contiguous and must not overlap")
-    if t.device != device:
-        raise ValueError(f"block_table must be on {device}, got {t.device}")
-    return max(t.stride(0), t.shape[1])
+    return t.data_ptr(), width, stride if rows > 1 else width
 
 
 def _strides(t):
-    """Strides with 0 for axes of one element (their stride has no meaning)
-    but the last."""
-    n = t.shape
-    return [s if n[i] > 1 else 0 for i, s in enumerate(t.stride()[:-1])] + [
-        t.stride(-1) if n[-1] > 1 else 1]
+    """Strides, with 0 for axes of one element (theirs have no meaning) and 1
+    for a last axis of one."""
+    st, shape = t.stride(), t.shape
+    if 1 in shape:
+        last = len(shape) - 1
+        st = tuple(x if n != 1 else int(i == last) for i, (x, n) in enumerate(zip(st, shape)))
+    return st
 
 
-def _cache(k, v, k_scale, v_scale):
+def _cache(k, v, k_scale, v_scale, dev):
     """The C descriptor of a cache."""
-    if not k.is_cuda or k.device != v.device:
-        raise ValueError("k_cache and v_cache must be CUDA tensors of one device")
-    kv = _KV_DTYPE.get(k.dtype)
+    dtype, shape = k.dtype, k.shape
+    kv = _KV_DTYPE.get(dtype)
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("the cache and what goes with it must be CUDA tensors of one device")
     if kv is None:
-        raise ValueError(f"k_cache must be float32, bfloat16 or float8_e4m3fn, got {k.dtype}")
-    shape, stride = k.shape, _strides(k)
-    if v.dtype != k.dtype or len(shape) != 4 or v.shape != shape or _strides(v) != stride:
+        raise ValueError(f"k_cache must be float32, bfloat16 or float8_e4m3fn, got {dtype}")
+    st = _strides(k)
+    if v.dtype is not dtype or len(shape) != 4 or v.shape != shape or _strides(v) != st:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, kv_heads, head_dim] "
                          "of one type and the same strides")
-    if stride[3] != 1:
+    if st[3] != 1:
         raise ValueError("a cached vector's elements must be contiguous")
     ks = vs = None
     if kv == B.MOE_KV_E4M3:
         if k_scale is None or v_scale is None:
             raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale")
-        _vec(k_scale, torch.float32, shape[2], "k_scale", k.device)
-        _vec(v_scale, torch.float32, shape[2], "v_scale", k.device)
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+        ks = _vec(k_scale, torch.float32, shape[2], "k_scale", dev)
+        vs = _vec(v_scale, torch.float32, shape[2], "v_scale", dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("scales are only used by a float8_e4m3fn cache")
-    return B.MoeKvCache(kv, shape[0], shape[1], shape[2], shape[3], 0, stride[0], stride[1],
-                        stride[2], k.data_ptr(), v.data_ptr(), ks, vs)
+    return B.MoeKvCache(kv, *shape, 0, st[0], st[1], st[2], k.data_ptr(), v.data_ptr(), ks, vs)
 
 
-def _rows3(t, dtype, shape, name, device):
+def _rows3(t, dtype, shape, name, dev):
     """The strides of a [n, heads, head_dim] tensor with contiguous vectors."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    stride = _strides(t)
-    if stride[2] != 1:
+    st = _strides(t)
+    if st[2] != 1:
         raise ValueError(f"{name}'s vectors must be contiguous")
-    return stride
+    return st
 
 
-def _err(err, device):
-    if err is None:
-        return 0
-    _vec(err, torch.int32, 1, "err", device)
-    return err.data_ptr()
+def _err(err, dev):
+    return 0 if err is None else _vec(err, torch.int32, 1, "err", dev)
 
 
 def kv_step(ctx_lens, new_lens, block_table, free_pages, n_free, *, page_size, num_pages,
@@ -140,30 +158,26 @@ def kv_step(ctx_lens, new_lens, block_table, free_pages, n_free, *, page_size, n
     place).  ``max_tokens`` is the number of token rows to map; rows past the
     last new token get slot -1.  ``n_free_out`` may be ``n_free`` itself; by
     default the number left is a new tensor and the call can be repeated."""
-    n = ctx_lens.shape[0]
-    dev = ctx_lens.device
-    _vec(ctx_lens, torch.int32, None, "ctx_lens", dev)
-    _vec(new_lens, torch.int32, n, "new_lens", dev)
-    stride = _table(block_table, n, dev)
-    _vec(free_pages, torch.int32, None, "free_pages", dev)
-    _vec(n_free, torch.int32, 1, "n_free", dev)
-    if n_free_out is not None:
-        _vec(n_free_out, torch.int32, 1, "n_free_out", dev)
+    n = len(ctx_lens)
+    dev, st = _on(ctx_lens, stream)
+    ctx = _vec(ctx_lens, torch.int32, n, "ctx_lens", dev)
+    new = _vec(new_lens, torch.int32, n, "new_lens", dev)
+    table, width, stride = _table(block_table, n, dev)
+    free = _vec(free_pages, torch.int32, len(free_pages), "free_pages", dev)
+    left = _vec(n_free, torch.int32, 1, "n_free", dev)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    # one allocation, cut so that every output is 16-byte aligned
-    pad_t, pad_b = (max_tokens + 3) & ~3, (n + 4) & ~3
-    buf = torch.empty(2 * pad_t + 2 * pad_b + 4, dtype=torch.int32, device=dev)
-    slots, positions = buf[:max_tokens], buf[pad_t:pad_t + max_tokens]
-    at = 2 * pad_t
-    starts, seq_lens = buf[at:at + n + 1], buf[at + pad_b:at + pad_b + n]
+    # one allocation for all outputs
+    slots, positions, starts, seq_lens, left_out = torch.empty(
+        2 * max_tokens + 2 * n + 2, dtype=torch.int32, device=ctx_lens.device).split_with_sizes(
+            (max_tokens, max_tokens, n + 1, n, 1))
     if n_free_out is None:
-        n_free_out = buf[at + 2 * pad_b:at + 2 * pad_b + 1]
-    base = buf.data_ptr()
-    rc = B.moe_kv_step(_p(ctx_lens), _p(new_lens), n, _p(block_table), block_table.shape[1],
-                       stride, _p(free_pages), free_pages.shape[0], _p(n_free), _p(n_free_out),
-                       num_pages, page_size, max_tokens, base, base + 4 * pad_t, base + 4 * at,
-                       base + 4 * (at + pad_b), _err(err, dev), _stream(stream))
+        n_free_out = left_out
+    rc = B.lib().moe_kv_step(
+        ctx, new, n, table, width, stride, free, len(free_pages), left,
+        _vec(n_free_out, torch.int32, 1, "n_free_out", dev), num_pages, page_size, max_tokens,
+        slots.data_ptr(), positions.data_ptr(), starts.data_ptr(), seq_lens.data_ptr(),
+        _err(err, dev), st)
     B._check(rc, "moe_kv_step")
     return KVStep(slots, positions, starts, seq_lens, n_free_out)
 
@@ -173,14 +187,14 @@ def kv_release(done, block_table, free_pages, n_free, *, num_pages, err=None, st
     the end of ``free_pages[:n_free]``, ``n_free`` grows, and their rows of
     ``block_table`` become -1 (all in place).  A row must hold -1 where it
     holds no page."""
-    n, dev = done.shape[0], done.device
-    _vec(done, torch.int32, None, "done", dev)
-    stride = _table(block_table, n, dev)
-    _vec(free_pages, torch.int32, None, "free_pages", dev)
-    _vec(n_free, torch.int32, 1, "n_free", dev)
-    rc = B.moe_kv_release(_p(done), n, _p(block_table), block_table.shape[1], stride,
-                          _p(free_pages), free_pages.shape[0], _p(n_free), num_pages,
-                          _err(err, dev), _stream(stream))
+    n = len(done)
+    dev, st = _on(done, stream)
+    at = _vec(done, torch.int32, n, "done", dev)
+    table, width, stride = _table(block_table, n, dev)
+    free = _vec(free_pages, torch.int32, len(free_pages), "free_pages", dev)
+    rc = B.lib().moe_kv_release(at, n, table, width, stride, free, len(free_pages),
+                                _vec(n_free, torch.int32, 1, "n_free", dev), num_pages,
+                                _err(err, dev), st)
     B._check(rc, "moe_kv_release")
 
 
@@ -188,14 +202,14 @@ def kv_append(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=None, err=
     """Write N tokens' keys and values ``[N, kv_heads, head_dim]`` (float32 for
     a float32 cache, else bfloat16) into the cache at ``slots`` (int32 [N], -1
     skips).  A float8 cache gets ``x / scale``, rounded and saturated."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    n = slots.shape[0]
+    dev, st = _on(k_cache, stream)
+    c = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    n = len(slots)
     dt = torch.float32 if c.kv_dtype == B.MOE_KV_F32 else torch.bfloat16
     shape = (n, c.kv_heads, c.head_dim)
     ks, vs = _rows3(k, dt, shape, "k", dev), _rows3(v, dt, shape, "v", dev)
-    _vec(slots, torch.int32, n, "slots", dev)
-    rc = B.moe_kv_append(c, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], n, slots.data_ptr(), _err(err, dev), _stream(stream))
+    rc = B.lib().moe_kv_append(c, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], n,
+                               _vec(slots, torch.int32, n, "slots", dev), _err(err, dev), st)
     B._check(rc, "moe_kv_append")
 
 
@@ -208,34 +222,47 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, windo
     softmax's log-sum-exp ``[B, Hq]`` in float32; a request without tokens
     gets zeros and -inf.  ``workspace`` is a uint8 tensor of
     ``attn_workspace(...)`` bytes (by default one is allocated)."""
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
+    dev, st = _on(k_cache, stream)
+    c = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, head_dim]")
-    n, hq = q.shape[0], q.shape[1]
+    shape = q.shape
+    n, hq, dim = shape
+    if dim != c.head_dim:
+        raise ValueError(f"q must have shape {(n, hq, c.head_dim)}, got {tuple(shape)}")
     dt = torch.float32 if c.kv_dtype == B.MOE_KV_F32 else torch.bfloat16
-    qs = _rows3(q, dt, (n, hq, c.head_dim), "q", dev)
+    qs = _rows3(q, dt, shape, "q", dev)
     if hq < 1 or hq % c.kv_heads:
         raise ValueError(f"Hq={hq} is not a multiple of kv_heads={c.kv_heads}")
-    stride = _table(block_table, n, dev)
-    _vec(seq_lens, torch.int32, n, "seq_lens", dev)
+    table, width, stride = _table(block_table, n, dev)
+    lens = _vec(seq_lens, torch.int32, n, "seq_lens", dev)
+    device = k_cache.device
     if out is None:
-        out = torch.empty(n, hq, c.head_dim, dtype=dt, device=dev)
-    os = _rows3(out, dt, (n, hq, c.head_dim), "out", dev)
-    lse = torch.empty(n, hq, dtype=torch.float32, device=dev) if return_lse else None
-    if workspace is None:
-        workspace = torch.empty(attn_workspace(k_cache.dtype, c.head_dim), dtype=torch.uint8,
-                                device=dev)
+        out = torch.empty(shape, dtype=dt, device=device)
+        os = (hq * dim, dim)
     else:
-        _vec(workspace, torch.uint8, None, "workspace", dev)
-    if scale is None:
-        scale = c.head_dim ** -0.5
-    rc = B.moe_attn_decode(c, q.data_ptr(), qs[0], qs[1], n, hq, block_table.data_ptr(),
-                           block_table.shape[1], stride, seq_lens.data_ptr(), scale, window,
-                           out.data_ptr(), os[0], os[1], _p(lse), workspace.data_ptr(), workspace.numel(),
-                           _err(err, dev), _stream(stream))
+        os = _rows3(out, dt, shape, "out", dev)
+    lse = torch.empty((n, hq), dtype=torch.float32, device=device) if return_lse else None
+    if workspace is None:
+        size = _WORKSPACE.get((dev, k_cache.dtype, dim))
+        if size is None:
+            with torch.cuda.device(dev):
+                size = attn_workspace(k_cache.dtype, dim)
+            _WORKSPACE[dev, k_cache.dtype, dim] = size
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        ws = workspace.data_ptr()
+    else:
+        size = len(workspace)
+        ws = _vec(workspace, torch.uint8, size, "workspace", dev)
+    rc = B.lib().moe_attn_decode(c, q.data_ptr(), qs[0], qs[1], n, hq, table, width, stride, lens,
+                                 dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                 os[0], os[1], 0 if lse is None else lse.data_ptr(), ws, size,
+                                 _err(err, dev), st)
     B._check(rc, "moe_attn_decode")
     return (out, lse) if return_lse else out
+
+
+_WORKSPACE = {}  # bytes by (device, cache type, head_dim)
 
 
 def attn_workspace(kv_dtype: torch.dtype, head_dim: int) -> int:
@@ -252,7 +279,8 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     [B]) hold per row, None leaves that restriction out; temperature <= 0 is
     greedy.  Returns (ids int32 [B], probs float32 [B]): the drawn tokens and
     their shares of what was kept; -1 and 0 for a row without a token."""
-    if not logits.is_cuda:
+    dev, st = _on(logits, stream)
+    if dev < 0:
         raise ValueError("logits must be a CUDA tensor")
     ldt = _LOGITS_DTYPE.get(logits.dtype)
     if ldt is None:
@@ -260,22 +288,21 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     if logits.dim() != 2 or logits.shape[1] < 1 or logits.shape[1] > 1 and logits.stride(1) != 1:
         raise ValueError("logits must be [B, V] with contiguous rows")
     n, V = logits.shape
-    dev = logits.device
-    _vec(u, torch.float32, n, "u", dev)
-    for t, dt, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
-                        (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
-        if t is not None:
-            _vec(t, dt, n, name, dev)
-    ids = torch.empty(n, dtype=torch.int32, device=dev)
-    probs = torch.empty(n, dtype=torch.float32, device=dev)
-    rc = B.moe_sample(logits.data_ptr(), ldt, n, V, logits.stride(0) if n > 1 else V, u.data_ptr(),
-                      _p(temperature), _p(top_k), _p(top_p), _p(min_p), ids.data_ptr(),
-                      probs.data_ptr(), _stream(stream))
+    f32 = torch.float32
+    at = _vec(u, f32, n, "u", dev)
+    t = 0 if temperature is None else _vec(temperature, f32, n, "temperature", dev)
+    k = 0 if top_k is None else _vec(top_k, torch.int32, n, "top_k", dev)
+    p = 0 if top_p is None else _vec(top_p, f32, n, "top_p", dev)
+    m = 0 if min_p is None else _vec(min_p, f32, n, "min_p", dev)
+    ids = torch.empty(n, dtype=torch.int32, device=logits.device)
+    probs = torch.empty(n, dtype=f32, device=logits.device)
+    rc = B.lib().moe_sample(logits.data_ptr(), ldt, n, V, logits.stride(0) if n > 1 else V, at, t,
+                            k, p, m, ids.data_ptr(), probs.data_ptr(), st)
     B._check(rc, "moe_sample")
     return ids, probs
 
 
 def check_word(err, stream=None):
     """Synchronise, read and clear an error word: (rc, device error bits)."""
-    _vec(err, torch.int32, 1, "err", err.device)
-    return B.moe_check_word(err.data_ptr(), _stream(stream))
+    dev, st = _on(err, stream)
+    return B.moe_check_word(_vec(err, torch.int32, 1, "err", dev), st)
