@@ -8,25 +8,28 @@
 // 64-bit integers.  A vocabulary of 2^18 stays below 2^63, and no order of
 // additions, of CTAs or of atomics changes a sum.
 //
-// One cluster of C CTAs works on a row; each CTA reads its slice of the row
-// once, into shared memory, and all further passes read it there:
+// One cluster of C CTAs works on a row, each on a slice that it sweeps two or
+// three times, the first from HBM and the others out of L2 (rows in flight
+// are few enough to stay there); four CTAs share an SM, so one's waiting is
+// another's work:
 //   A  the largest logit (and its lowest index where the row is greedy)
-//   B  with top-k or top-p: token counts by bins of width t / 128 below the
-//      largest logit.  For a small top-k only every thread's largest logit is
-//      counted: k of those in the bins down to one bound the k-th token.  For
-//      top-p the counts times the bins' weights say where the border lies,
-//      nearly; a window of bins around it with at most 512 tokens is chosen.
-//   C  one pass puts the window's tokens on a list and, where they are needed,
+//   B  with top-k or top-p: token counts by bins of width t / 256 below the
+//      largest logit.  For a small top-k only the largest logits of groups of
+//      tokens are counted, without a sweep: k of those in the bins down to one
+//      bound the k-th token.  For top-p the counts times the bins' weights say
+//      where the border lies, nearly; a window of bins around it with at most
+//      256 tokens is chosen.
+//   C  one sweep puts the window's tokens on a list and, where they are needed,
 //      adds up the weights of all tokens and of those above the window.  The
-//      first CTA ranks the list's tokens against each other, one a thread, and
-//      so finds the last kept token exactly; the draw is among the list when
-//      nothing lies above it, else it goes by the warps' sums, and the warp
-//      whose tokens it falls on walks through them once more.
-//   D  where the window does not hold the border (a bin with more than 512
-//      tokens, a border the counts misjudged, top-p among more than 512 that
+//      first CTA sorts the list, one token a thread, and so finds the last kept
+//      token exactly; the draw is among the list when nothing lies above it,
+//      else it goes by the warps' sums, and the warp whose tokens it falls on
+//      walks through them once more.
+//   D  where the window does not hold the border (a bin with more than 256
+//      tokens, a border the counts misjudged, top-p among the many that a large
 //      top-k left): the border is narrowed to one logit value by histograms
 //      over order keys (at most three), and ties are counted in index order.
-// Rows without top-k and top-p only need C's sums.  Bound by the row's bytes
+// Rows without top-k and top-p only need their sums.  Bound by the row's bytes
 // where top-k is small; where the whole vocabulary has to be weighed, by the
 // weights' instructions (about 50 a token, once).
 #include <cooperative_groups.h>
@@ -47,17 +50,30 @@ namespace moe {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSampThreads = 512;
+constexpr int kSampThreads = 256;
+constexpr int kSampCtas = 4;    // per SM
 constexpr int kSampWarps = kSampThreads / 32;
-constexpr int kBins = 4096;     // of counts; half as many of weights
+constexpr int kBins = 8192;     // of counts
+constexpr int kPer = kBins / kSampThreads;            // a thread's: a coarse bin
+constexpr int kCounts = kPer * (kSampThreads + 1);    // words that hold them
+constexpr int kBand = 512;      // bins of each of the two best bands (2 t wide)
+constexpr int kCoarse = 16;     // bins in one where groups are counted
+constexpr int kNear = 3 * kPer; // bins around the border among which the window lies
 constexpr int kKeyBins = 2048;  // of D's histograms
-constexpr float kBinsPerT = 128.0f;
+constexpr float kBinsPerT = 256.0f;
+constexpr float kBinStep = 0.99610137f;  // exp(-1 / kBinsPerT)
 constexpr int kList = kSampThreads;  // tokens that the list holds: one a thread
-constexpr int kSmallK = kList / 2;   // top-k that starts from the threads' largest
-constexpr int kMaxCluster = 8;
+constexpr int kGroups = 4;           // groups of tokens per thread
+constexpr int kSmallK = 96;          // the largest top-k that starts from them
+constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 1 << 18;
-// bytes of the largest slice (f32, 2^18 tokens over 8 CTAs) and its edges
-constexpr int kMaxSlice = kMaxVocab / kMaxCluster * 4 + 32;
+
+// Where bin b's count lies: a thread's kPer neighbouring bins a row apart, so
+// that threads read theirs, and tokens of neighbouring bins add to them,
+// without bank conflicts
+__device__ __forceinline__ int count_at(int b) {
+  return b / kPer + (b % kPer) * (kSampThreads + 1);
+}
 
 struct SampArgs {
   const void* logits;
@@ -100,31 +116,29 @@ __device__ __forceinline__ float key_value(uint32_t u) {
 struct Weigher {
   float top, ch, cl;    // c = log2(e) / t as a pair
   float tg, tl;         // top c as a multiple of 2^-10 and the rest
-  uint32_t t_hi, t_lo;  // T[lane] >> 14, and its low 14 bits
+  uint32_t t_hi, t_lo;  // T[lane], 45 bits
   bool near;            // |top c| < 2^12: l c itself is a float pair near tg
 
   __device__ __forceinline__ void set(float top_, float ch_, float cl_, unsigned long long T) {
     top = top_;
     ch = ch_;
     cl = cl_;
-    t_hi = static_cast<uint32_t>(T >> 14);
-    t_lo = static_cast<uint32_t>(T & 16383);
+    t_hi = static_cast<uint32_t>(T >> 32);
+    t_lo = static_cast<uint32_t>(T);
     const float p = top * ch;
     near = fabsf(p) < 4096.0f;
     tg = rintf(p * 1024.0f) * 0.0009765625f;
     tl = (p - tg) + fmaf(top, cl, fmaf(top, ch, -p));
   }
-  // l is a number (not NaN), at most top
+  // l is at most top; -inf and NaN, and all below 2^-45, get 0: their k is -1504
+  // and the shift leaves nothing, whatever the fraction's bits
   __device__ __forceinline__ unsigned long long operator()(float l) const {
     constexpr float kRound = 12582912.0f;  // 1.5 2^23: x + kRound - kRound rounds x
     float rh, small, z;  // r = rh + small, rh exact; z: k as the low bits of a float
-    bool live;           // below x = -46 the weight rounds to 0
     if (near) {
       const float p = l * ch;
       const float e = fmaf(l, ch, -p);  // exact
-      const float d = fmaxf(p - tg, -47.0f);
-      live = d > -46.0f;
-      z = fmaf(d, 32.0f, kRound);
+      z = fmaf(fmaxf(p - tg, -47.0f), 32.0f, kRound);
       rh = p - fmaf(z - kRound, 0.03125f, tg);  // the fma is exact: a multiple of 2^-10
       small = fmaf(l, cl, e - tl);
     } else {
@@ -133,11 +147,9 @@ struct Weigher {
       const float b = dh - l;
       const float dl = (l - (dh - b)) - (top + b);
       const float ph = dh * ch;
-      live = ph > -46.0f;
-      const float at = live ? ph : 0.0f;
-      z = fmaf(at, 32.0f, kRound);
-      rh = fmaf(z - kRound, -0.03125f, at);
-      small = live ? fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch) : 0.0f;
+      z = fmaf(fmaxf(ph, -47.0f), 32.0f, kRound);
+      rh = fmaf(z - kRound, -0.03125f, ph);
+      small = fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch);
     }
     const int k = __float_as_int(z) - 0x4b400000;
     // 2^r - 1 in units of 2^-37: ln 2 as a pair, degrees 2 to 4 in floats
@@ -150,16 +162,31 @@ struct Weigher {
     const int E = __float2int_rn(a) + __float2int_rn(fmaf(q, r * r, rest));
     const uint32_t hi = __shfl_sync(0xffffffffu, t_hi, k);
     const uint32_t lo = __shfl_sync(0xffffffffu, t_lo, k);
-    const long long T = (static_cast<long long>(hi) << 14) | lo;
-    const unsigned long long w = static_cast<unsigned long long>(
-        T + ((static_cast<long long>(static_cast<int>(hi)) * E) >> 23));
-    const unsigned long long v = ((w >> ((-(k >> 5)) & 63)) + 1ull) & ~1ull;
-    return live ? v : 0ull;
+    const long long T = static_cast<long long>((static_cast<unsigned long long>(hi) << 32) | lo);
+    const int t31 = static_cast<int>(__funnelshift_r(lo, hi, 14));
+    const unsigned long long w =
+        static_cast<unsigned long long>(T + ((static_cast<long long>(t31) * E) >> 23));
+    return ((w >> ((-(k >> 5)) & 63)) + 1ull) & ~1ull;
   }
 };
 
 // The same, called and not copied into the code: for passes that few rows take
 __device__ __noinline__ unsigned long long weigh_call(const Weigher& w, float l) { return w(l); }
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// adds to shared memory where `on`: a predicate, not a branch
+__device__ __forceinline__ void red_add(uint32_t* p, uint32_t v, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "@q red.shared.add.u32 [%0], %1;\n\t}" ::"r"(smem_u32(p)),
+      "r"(v), "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
 
 // floor(f n) for 0 <= f <= 1, and whether that is less than f n
 __device__ __forceinline__ unsigned long long share_of(float f, unsigned long long n, bool& more) {
@@ -178,25 +205,43 @@ __device__ __forceinline__ unsigned long long share_of(float f, unsigned long lo
   return hi >> s2;
 }
 
+// What is kept (of the tokens that min-p keeps): order keys above one, and
+// those equal to it up to an index
+struct Cut {
+  uint32_t key;
+  int idx;
+  __device__ __forceinline__ bool keeps(uint32_t k, int i) const {
+    return k > key || (k == key && i <= idx);
+  }
+};
+
 // What the first CTA finds, written into every CTA of the cluster
 struct Result {
-  int state;                  // 0 drawn already, 1 walk through warp `who`, 2 go to D
+  int state;                  // 0 drawn already, 1 walk through warp `who`, 2 go to D,
+                              // 3 another window, the border at `need`
   int who;
-  uint32_t cut_key;           // kept: order key above it, or equal and idx <= idx_cut
+  uint32_t cut_key;
   int idx_cut;
+  float need;
   unsigned long long before, total, to;
 };
 
 struct SampShared {
   union {
-    alignas(16) uint32_t cnt[kBins];
+    alignas(16) uint32_t cnt[kCounts];
     struct {
       uint32_t lo[kKeyBins], hi[kKeyBins];  // 64-bit sums of weights
     };
+    unsigned long long list_w[kList];  // once all CTAs have read the counts
   };
+  float band[2][kSampWarps];  // what the bands' tokens weigh more than their bins
+  uint32_t coarse_n[kSampThreads];
+  float coarse_w[kSampThreads];
+  int near_n[kNear];  // the row's counts and weights around the border
+  float near_w[kNear];
   uint32_t list_key[kList];
   uint32_t list_pos[kList];  // warp of the row << 18 | index: ordered by index
-  unsigned long long all[kList], list_w[kList];  // the row's list (first CTA)
+  unsigned long long all[kList];  // the row's list (first CTA)
   int list_n, list_at, all_n;
   int next_kept[kSampWarps];
   // by warp of the row, written by all CTAs into every one (tie, top) or the
@@ -205,15 +250,14 @@ struct SampShared {
   int warp_tie[kMaxCluster * kSampWarps];
   unsigned long long warp_mass[kMaxCluster * kSampWarps];
   unsigned long long warp_all[kMaxCluster * kSampWarps];
-  uint32_t cut_pos;  // written by one CTA into every one
+  unsigned long long part_mass[kSampWarps];
+  int cut_idx;  // written by one CTA into every one
   Result result;
   long long scan[2 * kSampWarps];
-  float fscan[kSampWarps];
-  int at_bin, at_count, at_in, win_lo, win_hi, above_n;
+  int at_bin, at_count, win_lo, win_hi, above_n;
+  int near_above;
+  float near_w_above, win_w;
   unsigned long long at_mass;
-  float ch, cl, l_min, u, p, t;
-  double d_min;
-  int k, min_on;
 };
 
 __device__ __forceinline__ int cut_to_int(long long v) {
@@ -314,39 +358,82 @@ __device__ __forceinline__ unsigned long long group_scan(unsigned long long x, i
   return before + incl - x;
 }
 
+// A CTA's slice of the row as 16-byte chunks; a warp works on a run of them
 template <typename LT>
 struct Slice {
-  static constexpr int VE = 16 / sizeof(LT);  // logits of a 16-byte chunk
-  const uint4* chunk;  // in shared memory
-  int chunks;
-  int first;           // index of chunk 0's first element (may lie before the slice)
-  int begin, end;      // this warp's chunks
+  static constexpr int VE = 16 / sizeof(LT);  // logits of a chunk
+  const LT* base;  // chunk 0: 16-byte aligned, may begin before the slice
+  int skip, stop;  // elements of the slice: skip <= i < stop, counted from base
+  int first;       // index in the row of base's element
+  int begin, end;  // this warp's chunks
+  bool has_inf;    // +inf counts as the largest number
 
-  __device__ __forceinline__ void get(int c, float (&v)[VE]) const {
-    if (c >= end) {
-#pragma unroll
-      for (int j = 0; j < VE; ++j) v[j] = -INFINITY;
-      return;
-    }
-    const uint4 raw = chunk[c];
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(LT) == 4) {
-        v[j] = __uint_as_float(w[j]);
+  // What does not belong to the slice reads as -inf, and nothing outside it is
+  // touched
+  __device__ __forceinline__ uint4 load(int c) const {
+    constexpr uint32_t kNone = sizeof(LT) == 4 ? 0xff800000u : 0xff80ff80u;
+    uint4 raw = make_uint4(kNone, kNone, kNone, kNone);
+    if (c < end) {
+      const int i = c * VE;
+      if (i >= skip && i + VE <= stop) {
+        raw = __ldg(reinterpret_cast<const uint4*>(base + i));
       } else {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        uint32_t w[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (i + j >= skip && i + j < stop) {
+            if constexpr (sizeof(LT) == 4) {
+              w[j] = __float_as_uint(base[i + j]);
+            } else {
+              const uint32_t x = __bfloat16_as_ushort(base[i + j]);
+              w[j / 2] = j % 2 ? (w[j / 2] & 0xffffu) | (x << 16) : (w[j / 2] & 0xffff0000u) | x;
+            }
+          }
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    return raw;
+  }
+
+  // f(values, index of the first, number of the batch) for every chunk of this
+  // warp, U loads at a time; all lanes stay together
+  template <int U, typename F>
+  __device__ __forceinline__ void sweep(F f) const {
+    const int lane = threadIdx.x & 31;
+    for (int c0 = begin; c0 < end; c0 += 32 * U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) raw[i] = load(c0 + 32 * i + lane);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        float v[VE];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(LT) == 4) {
+            v[j] = __uint_as_float(w[j]);
+          } else {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+          }
+        }
+        if (has_inf) {
+          const float big = __uint_as_float(sizeof(LT) == 4 ? 0x7f7fffffu : 0x7f7f0000u);
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (v[j] == INFINITY) v[j] = big;
+        }
+        f(v, first + (c0 + 32 * i + lane) * VE, i);
       }
     }
   }
 };
 
 template <typename LT>
-__global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs A) {
+__global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const SampArgs A) {
   constexpr int VE = Slice<LT>::VE;
   constexpr int ES = sizeof(LT);
-  extern __shared__ __align__(16) uint8_t slice_smem[];
+  constexpr int kFew = ES == 4 ? 2 : 1;  // chunks at a time where their tokens are weighed
   __shared__ SampShared S;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
@@ -355,86 +442,67 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int my_warp = rank * kSampWarps + warp, warps = C * kSampWarps;  // of the row
   const bool lead = rank == 0;
+  auto everyone = [&]() {  // all threads of the row
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
   const unsigned long long table = kPow2[lane];
-  cluster.barrier_arrive();  // waited for before the first write into another CTA
+  if (C > 1) cluster.barrier_arrive();  // waited for before the first write into another CTA
   pdl_wait();
 
-  // ---- the slice: 16-byte chunks of the row; the elements of the first and
-  // the last chunk that lie outside the slice become -inf.  A warp brings the
-  // chunks that it works on
-  const int e0 = min(A.V, rank * A.slice), n = min(A.slice, A.V - e0);
-  const LT* src = static_cast<const LT*>(A.logits) + row * A.row_stride + e0;
-  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / ES);
+  // ---- the row's settings, and the slice
+  const float t = A.temperature ? A.temperature[row] : 1.0f;
+  const int k_in = A.top_k ? A.top_k[row] : 0;
+  const float p_in = A.top_p ? A.top_p[row] : 1.0f;
+  const float min_p = A.min_p ? A.min_p[row] : 0.0f;
+  const float u = fminf(fmaxf(A.u[row], 0.0f), 1.0f);  // NaN: 0
+  const int k = k_in > 0 && k_in < A.V ? k_in : 0;
+  const bool p_on = p_in < 1.0f;
+  const float share = fmaxf(p_in, 0.0f);
+  const bool min_on = t > 0.0f && min_p > 0.0f;
   Slice<LT> sl;
-  sl.chunk = reinterpret_cast<const uint4*>(slice_smem);
-  sl.chunks = n > 0 ? (mis + n + VE - 1) / VE : 0;
-  sl.first = e0 - mis;
-  const int per_warp = (sl.chunks + kSampWarps - 1) / kSampWarps;
-  sl.begin = min(sl.chunks, warp * per_warp);
-  sl.end = min(sl.chunks, sl.begin + per_warp);
-  for (int c = sl.begin + lane; c < sl.end; c += 32) {
-    LT* dst = reinterpret_cast<LT*>(slice_smem) + c * VE;
-    const int at = c * VE - mis;  // in the slice
-    if (at >= 0 && at + VE <= n) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src + at)
-                   : "memory");
-    } else {
-      for (int j = 0; j < VE; ++j) {
-        LT v;
-        if (at + j >= 0 && at + j < n) {
-          v = src[at + j];
-        } else if constexpr (ES == 4) {
-          v = -INFINITY;
-        } else {
-          v = __ushort_as_bfloat16(0xff80);
-        }
-        dst[j] = v;
-      }
-    }
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  if (tid == 0) {  // the row's settings, while its logits are on their way
-    const float t = A.temperature ? A.temperature[row] : 1.0f;
-    const int k = A.top_k ? A.top_k[row] : 0;
-    const float p = A.top_p ? A.top_p[row] : 1.0f;
-    const float m = A.min_p ? A.min_p[row] : 0.0f;
-    S.t = t;
-    S.k = k > 0 && k < A.V ? k : 0;
-    S.p = p;
-    S.u = A.u[row];
-    S.list_n = S.all_n = 0;
-    S.min_on = 0;
-    if (t > 0.0f) {
-      // log2(e) / t to 2^-46: quotient, and the remainder's quotient
-      constexpr float kE = 1.44269502f, kEl = 1.92596299e-8f;  // log2(e)
-      const float c = kE / t;
-      S.ch = c < 1e30f ? c : 1e30f;
-      S.cl = c < 1e30f ? (fmaf(-c, t, kE) + kEl) / t : 0.0f;
-      S.min_on = m > 0.0f;
-      if (m > 0.0f) S.d_min = static_cast<double>(t) * log(fmin(static_cast<double>(m), 1.0));
-    }
-  }
-  for (int i = tid; i < kBins; i += kSampThreads) S.cnt[i] = 0;
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncwarp();
-
-  // ---- A: the largest logit (NaN is passed over; it never counts as >= any)
-  float mine = -INFINITY;
-  for (int c = sl.begin + lane; c < sl.end; c += 32) {
-    float v[VE];
-    sl.get(c, v);
-#pragma unroll
-    for (int j = 0; j < VE; ++j) mine = fmaxf(mine, v[j]);
-  }
+  int chunks, per_warp;  // of the slice
   {
-    float m = mine;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    cluster.barrier_wait();
-    if (lane < C) cluster.map_shared_rank(S.warp_top, lane)[my_warp] = m;
+    const int e0 = min(A.V, rank * A.slice), n = min(A.slice, A.V - e0);
+    const LT* src = static_cast<const LT*>(A.logits) + row * A.row_stride + e0;
+    sl.skip = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / ES);
+    sl.base = src - sl.skip;
+    sl.stop = sl.skip + n;
+    sl.first = e0 - sl.skip;
+    chunks = n > 0 ? (sl.stop + VE - 1) / VE : 0;
+    per_warp = (chunks + kSampWarps - 1) / kSampWarps;
+    sl.begin = min(chunks, warp * per_warp);
+    sl.end = min(chunks, sl.begin + per_warp);
+    sl.has_inf = false;
   }
-  cluster.sync();
-  float top = -INFINITY;
+  if (k || p_on)
+    for (int i = tid; i < kCounts; i += kSampThreads) S.cnt[i] = 0;
+  if (tid == 0) {
+    S.list_n = S.all_n = 0;
+    S.at_bin = INT_MAX;
+  }
+
+  // ---- A: the largest logit (NaN is passed over; it never counts as >= any),
+  // also of each of the thread's groups of tokens
+  float group[kGroups];
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) group[i] = -INFINITY;
+  sl.template sweep<8>([&](const float (&v)[VE], int, int i) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) group[i % kGroups] = fmaxf(group[i % kGroups], v[j]);
+  });
+  float top = group[0];
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) top = fmaxf(top, group[i]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (C > 1) {
+    cluster.barrier_wait();
+    if (lane < C) cluster.map_shared_rank(S.warp_top, lane)[my_warp] = top;
+  } else if (lane == 0) {
+    S.warp_top[my_warp] = top;
+  }
+  everyone();
   for (int i = lane; i < warps; i += 32) top = fmaxf(top, S.warp_top[i]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -445,34 +513,22 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
     }
     return;
   }
-  if (top == INFINITY) {  // +inf counts as the largest number
-    const float big = ES == 4 ? FLT_MAX : __uint_as_float(0x7f7f0000u);
-    for (int c = sl.begin + lane; c < sl.end; c += 32) {
-      float v[VE];
-      sl.get(c, v);
+  if (top == INFINITY) {
+    sl.has_inf = true;
+    top = __uint_as_float(ES == 4 ? 0x7f7fffffu : 0x7f7f0000u);
 #pragma unroll
-      for (int j = 0; j < VE; ++j)
-        if (v[j] == INFINITY) {
-          if constexpr (ES == 4) reinterpret_cast<float*>(slice_smem)[c * VE + j] = big;
-          else reinterpret_cast<uint16_t*>(slice_smem)[c * VE + j] = 0x7f7f;
-        }
-    }
-    __syncwarp();
-    mine = fminf(mine, big);
-    top = big;
+    for (int i = 0; i < kGroups; ++i) group[i] = fminf(group[i], top);
   }
-  if (!(S.t > 0.0f)) {  // greedy: the lowest index of the largest logit
+  if (!(t > 0.0f)) {  // greedy: the lowest index of the largest logit
     int idx = INT_MAX;
-    for (int c = sl.begin + lane; c < sl.end; c += 32) {
-      float v[VE];
-      sl.get(c, v);
+    sl.template sweep<4>([&](const float (&v)[VE], int at, int) {
 #pragma unroll
       for (int j = VE - 1; j >= 0; --j)
-        if (v[j] == top) idx = min(idx, sl.first + c * VE + j);
-    }
+        if (v[j] == top) idx = min(idx, at + j);
+    });
     idx = __reduce_min_sync(0xffffffffu, idx);
     if (lane == 0) cluster.map_shared_rank(S.warp_tie, 0)[my_warp] = idx;
-    cluster.sync();
+    everyone();
     if (lead && warp == 0) {
       idx = INT_MAX;
       for (int i = lane; i < warps; i += 32) idx = min(idx, S.warp_tie[i]);
@@ -485,37 +541,45 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
     return;
   }
   Weigher weigh;
-  weigh.set(top, S.ch, S.cl, table);
-  float l_min = -FLT_MAX;  // the smallest logit that min-p keeps
-  if (S.min_on) {
-    if (tid == 0) {  // exact tests around its estimate
-      const double d = S.d_min;
-      float lm = fminf(top, fmaxf(-FLT_MAX, static_cast<float>(top + d)));
-      for (int i = 0; i < 4 && lm > -FLT_MAX; ++i) {
-        const float below = key_value(order_key(lm) - 1);
-        if (!(static_cast<double>(below) - top >= d)) break;
-        lm = below;
-      }
-      for (int i = 0; i < 4 && lm < top; ++i) {
-        if (static_cast<double>(lm) - top >= d) break;
-        lm = key_value(order_key(lm) + 1);
-      }
-      S.l_min = lm;
-    }
-    __syncthreads();
-    l_min = S.l_min;
+  {
+    // log2(e) / t to 2^-46: quotient, and the remainder's quotient
+    constexpr float kE = 1.44269502f, kEl = 1.92596299e-8f;  // log2(e)
+    const float c = kE / t;
+    weigh.set(top, fminf(c, 1e30f), c < 1e30f ? (fmaf(-c, t, kE) + kEl) / t : 0.0f, table);
   }
-  const int k = S.k;
-  const bool p_on = S.p < 1.0f;
-  const float share = fmaxf(S.p, 0.0f);
-  const float u = fminf(fmaxf(S.u, 0.0f), 1.0f);  // NaN: 0
-  // bins of width t / 128 below the largest logit, the last one open;
+  float l_min = -FLT_MAX;  // the smallest logit that min-p keeps
+  if (min_on) {
+    // by the weights themselves: the lowest of the logits, as order keys, whose
+    // weight reaches min-p's.  Each round of a warp tests 32 of them; the first
+    // range is an estimate's, if its ends are on both sides
+    bool more;
+    const unsigned long long unit = 1ull << 44;
+    unsigned long long least = share_of(fminf(min_p, 1.0f), unit, more);
+    least = min(max(least + (more ? 1 : 0), 1ull), unit);
+    const float at = t * logf(fminf(min_p, 1.0f)), off = 1e-5f * (1.0f + fabsf(at) + fabsf(top));
+    uint32_t lo = order_key(-FLT_MAX), hi = order_key(top);  // hi's weight reaches it
+    const float a = top + at - off, b = top + at + off;
+    const bool up = weigh(fminf(lane ? b : a, top)) >= least;
+    const unsigned both = __ballot_sync(0xffffffffu, up);
+    if (a > -FLT_MAX && !(both & 1u)) lo = order_key(a);
+    if (b < top && (both & 2u)) hi = order_key(b);
+    while (lo < hi) {
+      const uint32_t step = (hi - lo + 31) / 32;
+      const uint32_t key = min(hi, lo + step * lane);
+      const unsigned reach = __ballot_sync(0xffffffffu, weigh(key_value(key)) >= least);
+      const int j = reach ? __ffs(reach) - 1 : 32;
+      hi = min(hi, lo + step * j);
+      if (j > 0) lo = lo + step * (j - 1) + 1;
+    }
+    l_min = key_value(hi);
+  }
+  // bins of width t / 256 below the largest logit, the last one open;
   // monotonous in l, which is all that they have to be
-  const float bin_scale = fminf(kBinsPerT / S.t, 1e30f);
-  auto bin_of = [&](float l) {
-    const float z = fminf((top - l) * bin_scale, static_cast<float>(kBins - 1));
-    return __float_as_int(z + 12582912.0f) - 0x4b400000;
+  const float bin_scale = fminf(kBinsPerT / t, 1e30f);
+  auto bin_at = [&](float z) {
+    return __float_as_int(fminf(z, static_cast<float>(kBins - 1)) + 12582912.0f) - 0x4b400000;
   };
+  auto bin_of = [&](float l) { return bin_at((top - l) * bin_scale); };
   // the first running sum of weights above u times their total is above this
   auto target = [&](unsigned long long total) {
     bool more;
@@ -531,140 +595,237 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
   // ---- B: bins win_lo .. win_hi go to the list, those before are kept
   bool generic = false, weigh_all = !k, weigh_above = true;
   int win_lo = INT_MAX, win_hi = INT_MAX, above_n = 0;
-  if (k || p_on) {
-    // k of the threads' largest, where there are well over k of them
-    const bool small = k && k <= kSmallK && k * 4ll * VE <= A.V;
-    if (small) {  // one count a thread, eight bins together
-      if (mine >= l_min) atomicAdd(&S.cnt[bin_of(mine) >> 3], 1u);
-    } else {
-      unsigned tail = 0;  // the last bin holds the far tail: added once
-      for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-        float v[VE];
-        sl.get(c0 + lane, v);
+  // The window for a border that lies `need` (2^-24 of the largest weight, as
+  // the counts have it) or k tokens down, among the bins around it
+  int near_c0 = -1;
+  auto choose = [&](float need) {
+    if (warp == 0) {
+      // one warp, kOne neighbouring bins a lane: the border's bin, then the
+      // window: as many bins before it as 64 tokens allow (for top-k, whose
+      // bin is exact, 256), as many after it as 128 in all allow
+      constexpr int kOne = kNear / 32;
+      int n[kOne], n_sum = 0;
+      float w[kOne], w_sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          if (v[j] >= l_min) {
-            const int b = bin_of(v[j]);
-            if (b == kBins - 1) ++tail;
-            else atomicAdd(&S.cnt[b], 1u);
-          }
+      for (int i = 0; i < kOne; ++i) {
+        n[i] = S.near_n[lane * kOne + i];
+        w[i] = S.near_w[lane * kOne + i];
+        n_sum += n[i];
+        w_sum += w[i];
+      }
+      int n_at = n_sum;
+      float w_at = w_sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, n_at, off);
+        const float z = __shfl_up_sync(0xffffffffu, w_at, off);
+        if (lane >= off) {
+          n_at += y;
+          w_at += z;
         }
       }
-      tail = __reduce_add_sync(0xffffffffu, tail);
-      if (lane == 0 && tail) atomicAdd(&S.cnt[kBins - 1], tail);
-    }
-    if (tid == 0) {
-      S.at_bin = kBins - 1;
-      S.at_count = INT_MAX;
-      S.win_lo = kBins;
-      S.win_hi = -1;
-    }
-    cluster.sync();
-    constexpr int PER = kBins / kSampThreads;
-    static_assert(PER == 8, "two 16-byte loads a thread");
-    int cn[PER] = {};
-    long long en, ew, tn, tw;
-    if (small) {  // a thread holds 8 bins' count in one
-      uint32_t x[kMaxCluster];
+      n_at += S.near_above - n_sum;  // tokens before this lane's bins
+      w_at += S.near_w_above - w_sum;
+      unsigned at_i = kNear - 1;
+      int n_i = n_at;
+      float w_i = w_at;
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r)
-        x[r] = r < C ? *cluster.map_shared_rank(S.cnt + tid, r) : 0;
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) cn[0] += x[r];
-      scan_pair(cn[0], 0, S.scan, en, ew, tn, tw);
-      if (en < k && en + cn[0] >= k) S.at_bin = tid * PER + PER - 1;
-    } else {
-      // CTA r adds up the r-th part of the bins and puts the sums in all CTAs,
-      // in place: nobody else reads or writes that part
-      const int part = kBins / C;
-      for (int i = rank * part + tid; i < (rank + 1) * part; i += kSampThreads) {
-        uint32_t x[kMaxCluster], sum = 0;
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          x[r] = r < C ? *cluster.map_shared_rank(S.cnt + i, r) : 0;
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) sum += x[r];
-        for (int r = 0; r < C; ++r) *cluster.map_shared_rank(S.cnt + i, r) = sum;
+      for (int i = 0; i < kOne; ++i) {
+        const bool hit = k ? n_i < k && n_i + n[i] >= k
+                           : w_i <= need && w_i + w[i] >= need && n[i] > 0;
+        if (hit) at_i = min(at_i, static_cast<unsigned>(lane * kOne + i));
+        n_i += n[i];
+        w_i += w[i];
       }
-      cluster.sync();
-      {
-        const uint4* from = reinterpret_cast<const uint4*>(S.cnt) + tid * 2;
-        const uint4 x = from[0], y = from[1];
-        cn[0] = x.x; cn[1] = x.y; cn[2] = x.z; cn[3] = x.w;
-        cn[4] = y.x; cn[5] = y.y; cn[6] = y.z; cn[7] = y.w;
+      const int border = static_cast<int>(__reduce_min_sync(0xffffffffu, at_i));
+      int through = 0;  // tokens down to the border's bin, itself included
+      n_i = n_at;
+#pragma unroll
+      for (int i = 0; i < kOne; ++i) {
+        n_i += n[i];
+        if (lane * kOne + i == border) through = n_i;
       }
-      long long sn = 0;
-      float sw = 0.0f, step = 0.0f;
+      through = __reduce_max_sync(0xffffffffu, through);
+      unsigned lo = border;
+      n_i = n_at;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sn += cn[i];
-      if (!k) {
-        // weights as whole numbers of 2^-24: only the window's choice goes by them
-        step = 16777216.0f * exp2f(-1.44269504f / kBinsPerT * (tid * PER));
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-          sw = fmaf(sw, 0.99221794f, static_cast<float>(cn[i]));  // exp(-1 / 128)
-        sw *= step;
+      for (int i = 0; i < kOne; ++i) {
+        if (lane * kOne + i <= border && through - n_i <= (k ? kList : kList / 4))
+          lo = min(lo, static_cast<unsigned>(lane * kOne + i));
+        n_i += n[i];
       }
-      scan_pair(sn, static_cast<long long>(sw), S.scan, en, ew, tn, tw);
-      const float need = static_cast<float>(tw) * share;
-      long long n_at = en;
-      float w_at = static_cast<float>(ew);
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      int above = INT_MAX;
+      n_i = n_at;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float wi = static_cast<float>(cn[i]) * step;
-        const bool here = k ? n_at < k && n_at + cn[i] >= k
-                            : w_at <= need && w_at + wi >= need && cn[i] > 0;
-        if (here) atomicMin(&S.at_bin, tid * PER + i);
-        n_at += cn[i];
-        w_at += wi;
-        step *= 0.99221794f;
+      for (int i = 0; i < kOne; ++i) {
+        if (lane * kOne + i == static_cast<int>(lo)) above = n_i;
+        n_i += n[i];
+      }
+      above = __reduce_min_sync(0xffffffffu, above);
+      w_i = w_at;
+#pragma unroll
+      for (int i = 0; i < kOne; ++i) {
+        if (lane * kOne + i == static_cast<int>(lo)) S.win_w = w_i;
+        w_i += w[i];
+      }
+      int hi = border;
+      n_i = n_at;
+#pragma unroll
+      for (int i = 0; i < kOne; ++i) {
+        n_i += n[i];
+        if (!k && n_i - above <= kList / 2) hi = max(hi, lane * kOne + i);
+      }
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) {
+        S.at_count = through - above;
+        S.above_n = above;
+        S.win_lo = above == 0 ? 0 : min(kBins - 1, near_c0 * kPer + static_cast<int>(lo));
+        S.win_hi = min(kBins - 1, near_c0 * kPer + hi);
       }
     }
     __syncthreads();
-    const int at_bin = S.at_bin;
+    win_lo = S.win_lo;
+    win_hi = S.win_hi;
+    above_n = S.above_n;
+  };
+  if (k || p_on) {
+    // groups, where there are well over k of them
+    const bool small = k && k <= kSmallK && k * 4 <= min(C * kSampThreads * kGroups, A.V / VE);
     if (small) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        if (group[i] >= l_min) atomicAdd(&S.cnt[bin_of(group[i]) / kCoarse], 1u);
+    } else {
+      unsigned tail = 0;  // the last bin holds the far tail: added once
+      float more[2] = {0.0f, 0.0f};  // the likeliest tokens' weights are not just their bin's
+      sl.template sweep<4>([&](const float (&v)[VE], int, int) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float z = (top - v[j]) * bin_scale;  // NaN: in no bin
+          const int b = bin_at(z);
+          const bool ok = v[j] >= l_min, last = b == kBins - 1;
+          tail += ok && last;
+          red_add(&S.cnt[count_at(b)], 1u, ok && !last);
+          if (!k && __any_sync(0xffffffffu, b < 2 * kBand)) {
+            constexpr float kLog = -1.44269504f / kBinsPerT;
+            const float e = ok ? ex2_approx(z * kLog) - ex2_approx(static_cast<float>(b) * kLog) : 0.0f;
+            more[0] += b < kBand ? e : 0.0f;
+            more[1] += b >= kBand && b < 2 * kBand ? e : 0.0f;
+          }
+        }
+      });
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        more[0] += __shfl_xor_sync(0xffffffffu, more[0], off);
+        more[1] += __shfl_xor_sync(0xffffffffu, more[1], off);
+      }
+      if (lane < 2) S.band[lane][warp] = more[lane];
+      tail = __reduce_add_sync(0xffffffffu, tail);
+      if (lane == 0 && tail) atomicAdd(&S.cnt[count_at(kBins - 1)], tail);
+      // coarse bins: this thread's kPer together
+      __syncthreads();
+      uint32_t n = 0;
+      float w = 0.0f, scale = k ? 0.0f : exp2f(-1.44269504f / kBinsPerT * (tid * kPer));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t c = S.cnt[tid + i * (kSampThreads + 1)];
+        n += c;
+        w = fmaf(static_cast<float>(c), scale, w);
+        scale *= kBinStep;
+      }
+      // a band's correction counts from its end on
+      if (!k && (tid + 1 == kBand / kPer || tid + 1 == 2 * kBand / kPer))
+        for (int i = 0; i < kSampWarps; ++i) w += S.band[tid * kPer / kBand][i];
+      S.coarse_n[tid] = n;
+      S.coarse_w[tid] = w;
+    }
+    everyone();
+    long long en, ew, tn, tw;
+    if (small) {  // every CTA adds the counts up for itself
+      constexpr int kTwo = kBins / kCoarse / kSampThreads;
+      static_assert(kTwo == 2, "two coarse bins a thread");
+      int cn[2] = {0, 0};
+      uint2 x[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        x[r] = r < C ? reinterpret_cast<const uint2*>(cluster.map_shared_rank(S.cnt, r))[tid]
+                     : make_uint2(0, 0);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        cn[0] += x[r].x;
+        cn[1] += x[r].y;
+      }
+      scan_pair(cn[0] + cn[1], 0, S.scan, en, ew, tn, tw);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (en < k && en + cn[i] >= k) S.at_bin = (2 * tid + i) * kCoarse + kCoarse - 1;
+        en += cn[i];
+      }
+      __syncthreads();
       win_lo = 0;
-      win_hi = at_bin;
+      win_hi = min(S.at_bin, kBins - 1);
       weigh_above = false;
     } else {
-      // the window: from as many bins before the border's as 256 tokens (for
-      // top-k, whose bin is exact, 512) allow, to as many as 512 allow
-      if (at_bin / PER == tid) {
-        long long incl = en;
+      // every CTA adds the coarse bins up for itself, in the same order
+      uint32_t cn[kMaxCluster];
+      float cw[kMaxCluster], sw = 0.0f;
+      int sn = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (i <= at_bin % PER) incl += cn[i];
-        S.at_count = cut_to_int(incl);
+      for (int r = 0; r < kMaxCluster; ++r) {
+        cn[r] = r < C ? *cluster.map_shared_rank(S.coarse_n + tid, r) : 0;
+        cw[r] = r < C && !k ? *cluster.map_shared_rank(S.coarse_w + tid, r) : 0.0f;
+      }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        sn += cn[r];
+        sw += cw[r];
+      }
+      // weights as whole numbers of 2^-24 of the largest one: only the
+      // window's choice goes by them
+      constexpr float kUnit = 16777216.0f;
+      const long long wi = static_cast<long long>(sw * kUnit);
+      scan_pair(sn, wi, S.scan, en, ew, tn, tw);
+      const float need = static_cast<float>(tw) * share;  // before the border
+      const bool here = k ? en < k && en + sn >= k
+                          : static_cast<float>(ew) <= need &&
+                                static_cast<float>(ew + wi) >= need && sn > 0;
+      if (here) atomicMin(&S.at_bin, tid);
+      __syncthreads();
+      const bool found = S.at_bin < kSampThreads;  // else top-k keeps everything
+      const int c0 = found ? max(0, S.at_bin - 1) : 0;
+      if (tid == c0) {
+        S.near_above = static_cast<int>(en);
+        S.near_w_above = static_cast<float>(ew);
+      }
+      // the bins around it, from all CTAs
+      for (int i = tid; i < kNear; i += kSampThreads) {
+        const int b = c0 * kPer + i;
+        int n = 0;
+        float w = 0.0f;
+        if (b < kBins) {
+          uint32_t x[kMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            x[r] = r < C ? *cluster.map_shared_rank(S.cnt + count_at(b), r) : 0;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) n += x[r];
+          if (!k)
+            w = static_cast<float>(n) * kUnit * exp2f(-1.44269504f / kBinsPerT * b);
+        }
+        S.near_n[i] = n;
+        S.near_w[i] = w;
       }
       __syncthreads();
-      const long long through = S.at_count;
-      const int most = k ? kList : kList / 2;
-      long long n_at = en;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (tid * PER + i <= at_bin && through - n_at <= most) atomicMin(&S.win_lo, tid * PER + i);
-        n_at += cn[i];
+      near_c0 = c0;
+      if (found) choose(need);
+      if (found) {
+        generic = S.at_count > kList;
+      } else {
+        win_lo = 0;
+        win_hi = kBins - 1;
+        generic = !k || tn > kList;
       }
-      __syncthreads();
-      win_lo = min(S.win_lo, at_bin);
-      if (win_lo / PER == tid) {
-        long long ex = en;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (i < win_lo % PER) ex += cn[i];
-        S.above_n = cut_to_int(ex);
-      }
-      __syncthreads();
-      above_n = S.above_n;
-      n_at = en;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        n_at += cn[i];
-        if (tid * PER + i >= win_lo && n_at - above_n <= kList) atomicMax(&S.win_hi, tid * PER + i);
-      }
-      __syncthreads();
-      win_hi = k ? at_bin : S.win_hi;
-      generic = win_hi < at_bin || through - above_n > kList;
       weigh_above = above_n > 0;
     }
   }
@@ -672,18 +833,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
   const bool list_on = k || p_on;
   unsigned long long w_mine = 0;  // this warp's kept weight, where no list is needed
   if (!list_on) {
-    for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-      float v[VE];
-      sl.get(c0 + lane, v);
+    sl.template sweep<kFew>([&](const float (&v)[VE], int, int) {
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        const bool ok = v[j] >= l_min;
-        const unsigned long long w = weigh(ok ? v[j] : top);
-        w_mine += ok ? w : 0;
+        const unsigned long long w = weigh(v[j]);
+        if (!min_on || v[j] >= l_min) w_mine += w;
       }
-    }
+    });
     w_mine = warp_sum(w_mine);
-  } else if (!generic) {
+  }
+  for (int tries = 0; list_on && !generic; ++tries) {
     // ---- C
     unsigned long long above = 0, everything = 0;
     auto enlist = [&](float v, int idx) {
@@ -694,41 +853,38 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
       }
     };
     if (weigh_all) {
-      for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-        float v[VE];
-        sl.get(c0 + lane, v);
+      sl.template sweep<kFew>([&](const float (&v)[VE], int at, int) {
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const bool ok = v[j] >= l_min;
-          const unsigned long long w = weigh(ok ? v[j] : top);
+          const unsigned long long w = weigh(v[j]);
+          const bool ok = v[j] >= l_min;  // else (min-p, -inf, NaN) out of every bin
           const int b = ok ? bin_of(v[j]) : INT_MAX;
-          everything += ok ? w : 0;
-          above += b < win_lo ? w : 0;
-          if (b >= win_lo && b <= win_hi) enlist(v[j], sl.first + (c0 + lane) * VE + j);
+          if (!min_on || ok) everything += w;
+          if (b < win_lo) above += w;
+          if (static_cast<unsigned>(b - win_lo) <= static_cast<unsigned>(win_hi - win_lo))
+            enlist(v[j], at + j);
         }
-      }
+      });
     } else {
       // nothing below this logit can lie in the window's bins: a chunk without
       // one that reaches it needs no closer look
       const float reach =
           fmaxf(l_min, top - (static_cast<float>(win_hi) + 2.0f) / bin_scale);
-      for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-        float v[VE];
-        sl.get(c0 + lane, v);
+      sl.template sweep<4>([&](const float (&v)[VE], int at, int) {
         float most = v[0];
 #pragma unroll
         for (int j = 1; j < VE; ++j) most = fmaxf(most, v[j]);
-        if (!__any_sync(0xffffffffu, most >= reach)) continue;
+        if (!__any_sync(0xffffffffu, most >= reach)) return;
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const int b = v[j] >= l_min ? bin_of(v[j]) : INT_MAX;
-          if (b >= win_lo && b <= win_hi) enlist(v[j], sl.first + (c0 + lane) * VE + j);
+          if (b >= win_lo && b <= win_hi) enlist(v[j], at + j);
           if (weigh_above && __any_sync(0xffffffffu, b < win_lo)) {
             const unsigned long long w = weigh_call(weigh, b < win_lo ? v[j] : top);
             above += b < win_lo ? w : 0;
           }
         }
-      }
+      });
     }
     if (weigh_all || weigh_above) {
       above = warp_sum(above);
@@ -745,7 +901,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
     if (tid < S.list_n && S.list_at + tid < kList)
       cluster.map_shared_rank(S.all, 0)[S.list_at + tid] =
           (static_cast<unsigned long long>(~S.list_key[tid]) << 32) | S.list_pos[tid];
-    cluster.sync();
+    everyone();
     int size = 32;  // of the group that works on the list
     const int n_list = S.all_n;  // (of the first CTA)
     while (size < min(n_list, kList)) size *= 2;
@@ -779,6 +935,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
       const unsigned long long to = target(total);
       if (missed || above_n == 0) {
         if (tid == 0) S.result.state = missed ? 2 : 0;
+        if (missed && tid == 0 && !k && n_list <= kList && tries < 2 && near_c0 >= 0) {
+          // the window lay beside the border: its place by the exact sum
+          S.result.state = 3;
+          const unsigned long long border = border_of(everything);
+          const float miss = border >= above ? static_cast<float>(border - above)
+                                             : -static_cast<float>(above - border);
+          S.result.need = S.win_w + miss * 9.5367432e-7f;  // 2^-44 to 2^-24
+        }
         if (!missed) {  // the draw is among the list, in order of the index
           S.list_w[tid] = w;
           x = keep ? (static_cast<unsigned long long>(pos) << 32) | static_cast<uint32_t>(tid)
@@ -831,72 +995,70 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
       group_sync(size);
       if (tid > 0 && tid < C) cluster.map_shared_rank(&S, tid)->result = S.result;
     }
-    cluster.sync();
-    if (S.result.state == 0) return;
-    generic = S.result.state == 2;
+    everyone();
+    const int state = S.result.state;
+    if (state == 0) return;
+    if (state == 1) break;
+    generic = state == 2;
+    if (state == 3) {
+      const float need = S.result.need;
+      if (tid == 0) S.list_n = S.all_n = 0;
+      choose(need);
+      generic = S.at_count > kList;
+      weigh_above = above_n > 0;
+      everyone();
+    }
   }
 
-  struct {
-    uint32_t key;
-    int idx;
-  } cut = {0, INT_MAX};
+  Cut cut = {0, INT_MAX};
   if (generic) {
-    // ---- D.  Histograms of counts or weights over order keys hi - 2^sh i
-    auto clear = [&]() {
-      cluster.sync();  // nobody reads the last one any more
-      for (int i = tid; i < kBins; i += kSampThreads) S.cnt[i] = 0;
-      __syncthreads();
-    };
-    // the bin where the count or the weight passes `need`; in all CTAs
+    // ---- D.  `narrow`: the order key where the count or the weight of the
+    // keys from it up, lo at least, reaches `need`; the same in all CTAs.
+    // Histograms over keys hi - 2^sh i, on ever fewer keys
     auto narrow = [&](bool mass, long long need, uint32_t lo, long long& passed) {
       uint32_t hi = order_key(top);
       passed = 0;  // count or weight of the keys above hi
       for (;;) {
         const int sh = max(0, 32 - __clz(hi - lo) - 11);  // 2^11 bins
-        clear();
-        for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-          float v[VE];
-          sl.get(c0 + lane, v);
+        everyone();  // nobody reads the last histogram any more
+        for (int i = tid; i < kKeyBins; i += kSampThreads) S.lo[i] = S.hi[i] = 0;
+        __syncthreads();
+        sl.template sweep<1>([&](const float (&v)[VE], int, int) {
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             const uint32_t key = order_key(v[j]);
             const bool ok = v[j] >= l_min && key >= lo && key <= hi;
-            if (!__any_sync(0xffffffffu, ok)) continue;
-            const int b = static_cast<int>((hi - key) >> sh);
-            if (!mass) {
-              if (ok) atomicAdd(&S.lo[b], 1u);
-            } else {
-              const unsigned long long w = weigh_call(weigh, ok ? v[j] : top);
+            if (__any_sync(0xffffffffu, ok)) {
+              const int b = static_cast<int>((hi - key) >> sh);
+              unsigned long long w = 1;
+              if (mass) w = weigh_call(weigh, ok ? v[j] : top);
               if (ok && w) {
                 const uint32_t add = static_cast<uint32_t>(w);
                 const uint32_t old = atomicAdd(&S.lo[b], add);
-                atomicAdd(&S.hi[b], static_cast<uint32_t>(w >> 32) + (old + add < old ? 1u : 0u));
+                const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + add < old ? 1u : 0u);
+                if (up) atomicAdd(&S.hi[b], up);
               }
             }
           }
-        }
-        if (tid == 0) S.at_bin = kKeyBins - 1;
-        cluster.sync();
-        constexpr int PER = kKeyBins / kSampThreads;
-        long long cw[PER] = {}, sum = 0;
+        });
+        everyone();
+        constexpr int kMine = kKeyBins / kSampThreads;
+        long long cw[kMine] = {}, sum = 0;
         for (int r = 0; r < C; ++r) {
-          const SampShared* o = cluster.map_shared_rank(&S, r);
-          const uint4 l = *reinterpret_cast<const uint4*>(&o->lo[tid * PER]);
-          const uint4 h = *reinterpret_cast<const uint4*>(&o->hi[tid * PER]);
-          cw[0] += (static_cast<long long>(h.x) << 32) + l.x;
-          cw[1] += (static_cast<long long>(h.y) << 32) + l.y;
-          cw[2] += (static_cast<long long>(h.z) << 32) + l.z;
-          cw[3] += (static_cast<long long>(h.w) << 32) + l.w;
+          const uint32_t* l = cluster.map_shared_rank(S.lo, r) + tid * kMine;
+          const uint32_t* h = cluster.map_shared_rank(S.hi, r) + tid * kMine;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) cw[i] += (static_cast<long long>(h[i]) << 32) + l[i];
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += cw[i];
+        for (int i = 0; i < kMine; ++i) sum += cw[i];
         long long ex, unused, tot, tot_b;
         scan_pair(sum, 0, S.scan, ex, unused, tot, tot_b);
         long long at = passed + ex;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = 0; i < kMine; ++i) {
           if (at < need && at + cw[i] >= need) {
-            S.at_bin = tid * PER + i;
+            S.at_bin = tid * kMine + i;
             S.at_mass = static_cast<unsigned long long>(at);
           }
           at += cw[i];
@@ -912,52 +1074,43 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
     // a sum over all tokens of the row, the same in all CTAs
     auto row_sum = [&](unsigned long long x) {
       x = warp_sum(x);
-      cluster.sync();
+      everyone();
       if (lane < C) cluster.map_shared_rank(S.warp_all, lane)[my_warp] = x;
-      cluster.sync();
+      everyone();
       x = 0;
       for (int i = lane; i < warps; i += 32) x += S.warp_all[i];
       return warp_sum(x);
     };
-    auto mass_above = [&](uint32_t key) {
+    const uint32_t key_min = order_key(l_min);
+    long long ties = LLONG_MAX, passed;  // kept of the tokens equal to the cut
+    if (k) {
+      unsigned long long live = 0;
+      sl.template sweep<4>([&](const float (&v)[VE], int, int) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) live += v[j] >= l_min;
+      });
+      if (row_sum(live) > static_cast<unsigned long long>(k)) {
+        cut.key = narrow(false, k, key_min, passed);
+        ties = k - passed;
+      }
+    }
+    if (p_on) {
       unsigned long long x = 0;
-      for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-        float v[VE];
-        sl.get(c0 + lane, v);
+      sl.template sweep<1>([&](const float (&v)[VE], int, int) {
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const bool ok = v[j] >= l_min && order_key(v[j]) > key;
+          const bool ok = v[j] >= l_min && order_key(v[j]) > cut.key;
           const unsigned long long w = weigh_call(weigh, ok ? v[j] : top);
           x += ok ? w : 0;
         }
-      }
-      return row_sum(x);
-    };
-    auto count_of = [&]() {
-      unsigned long long x = 0;
-      for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-        float v[VE];
-        sl.get(c0 + lane, v);
-#pragma unroll
-        for (int j = 0; j < VE; ++j) x += v[j] >= l_min;
-      }
-      return row_sum(x);
-    };
-    const uint32_t key_min = order_key(l_min);
-    uint32_t cut_key = 0;
-    long long ties = LLONG_MAX, passed;  // kept of the tokens equal to the cut
-    if (k && count_of() > static_cast<unsigned long long>(k)) {
-      cut_key = narrow(false, k, key_min, passed);
-      ties = k - passed;
-    }
-    if (p_on) {
-      const unsigned long long over_cut = mass_above(cut_key);
-      const unsigned long long w_cut = weigh_call(weigh, cut_key ? key_value(cut_key) : top);
-      const unsigned long long at_cut = cut_key ? w_cut * static_cast<unsigned long long>(ties) : 0;
+      });
+      const unsigned long long over_cut = row_sum(x);
+      const unsigned long long w_cut = weigh_call(weigh, cut.key ? key_value(cut.key) : top);
+      const unsigned long long at_cut = cut.key ? w_cut * static_cast<unsigned long long>(ties) : 0;
       const unsigned long long border = max(1ull, border_of(over_cut + at_cut));
       if (border <= over_cut) {
-        cut_key = narrow(true, static_cast<long long>(border), max(key_min, cut_key + 1), passed);
-        const unsigned long long w = weigh_call(weigh, key_value(cut_key));
+        cut.key = narrow(true, static_cast<long long>(border), max(key_min, cut.key + 1), passed);
+        const unsigned long long w = weigh_call(weigh, key_value(cut.key));
         ties = static_cast<long long>((border - passed + w - 1) / w);
       } else {  // among top-k's ties
         ties = min(ties, static_cast<long long>((border - over_cut + w_cut - 1) / w_cut));
@@ -965,99 +1118,117 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
     }
     // the index of the last kept tie
     int here = 0;
-    for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-      float v[VE];
-      sl.get(c0 + lane, v);
+    sl.template sweep<4>([&](const float (&v)[VE], int, int) {
 #pragma unroll
-      for (int j = 0; j < VE; ++j) here += v[j] >= l_min && order_key(v[j]) == cut_key;
-    }
+      for (int j = 0; j < VE; ++j) here += v[j] >= l_min && order_key(v[j]) == cut.key;
+    });
     here = __reduce_add_sync(0xffffffffu, here);
     if (lane < C) cluster.map_shared_rank(S.warp_tie, lane)[my_warp] = here;
-    if (tid == 0) S.cut_pos = INT_MAX;
-    cluster.sync();
-    long long before = 0;
-    for (int i = lane; i < my_warp; i += 32) before += S.warp_tie[i];
-    before = static_cast<long long>(warp_sum(static_cast<unsigned long long>(before)));
-    if (before < ties && before + here >= ties) {
-      int left = static_cast<int>(ties - before);  // the left-th tie of this warp
-      for (int c0 = sl.begin; c0 < sl.end && left > 0; c0 += 32) {
-        float v[VE];
-        sl.get(c0 + lane, v);
+    if (tid == 0) S.cut_idx = INT_MAX;
+    everyone();
+    unsigned long long ties_before = 0;
+    for (int i = lane; i < my_warp; i += 32) ties_before += static_cast<unsigned>(S.warp_tie[i]);
+    long long left = ties - static_cast<long long>(warp_sum(ties_before));
+    if (left > 0 && here >= left) {  // the left-th tie of this warp
+      sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
         int hit = 0;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) hit += v[j] >= l_min && order_key(v[j]) == cut_key;
+        for (int j = 0; j < VE; ++j) hit += v[j] >= l_min && order_key(v[j]) == cut.key;
         int incl = hit;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, incl, off);
           if (lane >= off) incl += y;
         }
-        if (incl >= left && incl - hit < left) {
-          int at = incl - hit;
+        int n = incl - hit;
 #pragma unroll
-          for (int j = 0; j < VE; ++j) {
-            if (v[j] >= l_min && order_key(v[j]) == cut_key && ++at == left) {
-              const uint32_t idx = static_cast<uint32_t>(sl.first + (c0 + lane) * VE + j);
-              for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&S.cut_pos, r) = idx;
-            }
-          }
-        }
+        for (int j = 0; j < VE; ++j)
+          if (v[j] >= l_min && order_key(v[j]) == cut.key && ++n == left)
+            for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&S.cut_idx, r) = at + j;
         left -= __shfl_sync(0xffffffffu, incl, 31);
-      }
+      });
     }
-    cluster.sync();
-    const int idx_cut = static_cast<int>(S.cut_pos);
-    // the warps' sums of what is kept; everyone finds the draw's warp
-    for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-      float v[VE];
-      sl.get(c0 + lane, v);
+    everyone();
+    cut.idx = S.cut_idx;
+    // this warp's weight of what is kept
+    sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        const uint32_t key = order_key(v[j]);
-        const bool ok = v[j] >= l_min && (key > cut_key || (key == cut_key &&
-                                          sl.first + (c0 + lane) * VE + j <= idx_cut));
-        if (!__any_sync(0xffffffffu, ok)) continue;
+        const bool ok = v[j] >= l_min && cut.keeps(order_key(v[j]), at + j);
         const unsigned long long w = weigh_call(weigh, ok ? v[j] : top);
         w_mine += ok ? w : 0;
       }
-    }
+    });
     w_mine = warp_sum(w_mine);
-    cut.key = cut_key;
-    cut.idx = idx_cut;
   }
+  unsigned long long before, total, to;
+  int who = -1;
   if (generic || !list_on) {
-    // every CTA finds the warp that the draw falls on
+    // every warp finds the one that the draw falls on
     if (lane < C) cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = w_mine;
-    cluster.sync();
-    unsigned long long sum = 0, total = 0;
-    for (int i = lane; i < warps; i += 32) {
-      const unsigned long long w = S.warp_mass[i];
-      total += w;
-      if (i < my_warp) sum += w;
-    }
-    sum = warp_sum(sum);
+    everyone();
+    total = 0;
+    for (int i = lane; i < warps; i += 32) total += S.warp_mass[i];
     total = warp_sum(total);
-    const unsigned long long to = target(total);
-    if (!(sum <= to && to < sum + w_mine)) return;
-    if (lane == 0) S.result = {1, my_warp, cut.key, cut.idx, sum, total, to};
-    __syncwarp();
+    to = target(total);
+    unsigned long long sum = 0;
+    before = 0;
+    for (int i0 = 0; i0 < warps; i0 += 32) {
+      const unsigned long long m = i0 + lane < warps ? S.warp_mass[i0 + lane] : 0;
+      unsigned long long incl = m;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      const unsigned hit =
+          __ballot_sync(0xffffffffu, sum + incl - m <= to && to < sum + incl);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        who = i0 + at;
+        before = __shfl_sync(0xffffffffu, sum + incl - m, at);
+      }
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  } else {
+    const Result R = S.result;
+    who = R.who;
+    cut.key = R.cut_key;
+    cut.idx = R.idx_cut;
+    before = R.before;
+    total = R.total;
+    to = R.to;
   }
-
-  // ---- the warp that the draw falls on walks through its tokens
-  const Result R = S.result;
-  if (R.who != my_warp) return;
-  unsigned long long before = R.before;
-  for (int c0 = sl.begin; c0 < sl.end; c0 += 32) {
-    float v[VE];
-    sl.get(c0 + lane, v);
+  if (who / kSampWarps != rank) return;
+  // ---- that warp's tokens once more: every warp of its CTA adds up an eighth
+  // of them, and the one whose eighth the draw falls in walks through it
+  {
+    const int from = min(chunks, who % kSampWarps * per_warp), end = min(chunks, from + per_warp);
+    const int part = (end - from + 32 * kSampWarps - 1) / (32 * kSampWarps) * 32;
+    sl.begin = min(end, from + warp * part);
+    sl.end = min(end, sl.begin + part);
+  }
+  auto kept_weight = [&](float v, int idx) {
+    const bool ok = v >= l_min && cut.keeps(order_key(v), idx);
+    const unsigned long long w = weigh(v);
+    return ok ? w : 0ull;
+  };
+  unsigned long long in_part = 0;
+  sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) in_part += kept_weight(v[j], at + j);
+  });
+  in_part = warp_sum(in_part);
+  if (lane == 0) S.part_mass[warp] = in_part;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before += S.part_mass[w];
+  if (!(before <= to && to < before + in_part)) return;
+  sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
+    if (before > to) return;  // drawn
     unsigned long long w[VE], here = 0;
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
-      const uint32_t key = order_key(v[j]);
-      const bool ok = v[j] >= l_min && (key > R.cut_key || (key == R.cut_key &&
-                                        sl.first + (c0 + lane) * VE + j <= R.idx_cut));
-      w[j] = weigh(ok ? v[j] : top);
-      if (!ok) w[j] = 0;
+      w[j] = kept_weight(v[j], at + j);
       here += w[j];
     }
     unsigned long long incl = here;
@@ -1069,25 +1240,47 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampArgs 
     unsigned long long sum = before + incl - here;
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
-      if (sum <= R.to && R.to < sum + w[j]) {
-        A.ids[row] = sl.first + (c0 + lane) * VE + j;
-        if (A.probs) A.probs[row] = static_cast<float>(w[j]) / static_cast<float>(R.total);
+      if (sum <= to && to < sum + w[j]) {
+        A.ids[row] = at + j;
+        if (A.probs) A.probs[row] = static_cast<float>(w[j]) / static_cast<float>(total);
       }
       sum += w[j];
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
-    if (before > R.to) break;
-  }
+  });
 }
 
-template <typename LT>
-static cudaError_t launch_sample(const SampArgs& a, int B, int cluster, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(a.slice) * sizeof(LT) + 31) / 16 * 16;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(sample_kernel<LT>), kMaxSlice, done);
-  if (e != cudaSuccess) return e;
-  return launch_cluster(sample_kernel<LT>, dim3(static_cast<unsigned>(B) * cluster),
-                        dim3(kSampThreads), cluster, smem, st, a);
+// The largest cluster for a row on the current device: 16 CTAs where one fits
+// (more than the portable 8: asked once per device and type), 0 on an error
+static int max_cluster(int logits_dtype) {
+  static std::atomic<int> known[2][64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& mine = known[logits_dtype][dev];
+  int n = mine.load(std::memory_order_relaxed);
+  if (n) return n;
+  const void* kern = logits_dtype == MOE_LOGITS_F32
+                         ? reinterpret_cast<const void*>(sample_kernel<float>)
+                         : reinterpret_cast<const void*>(sample_kernel<__nv_bfloat16>);
+  n = 8;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+      cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCluster);
+    cfg.blockDim = dim3(kSampThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) == cudaSuccess && fit > 0)
+      n = kMaxCluster;
+  }
+  cudaGetLastError();  // a refusal above leaves 8
+  mine.store(n, std::memory_order_relaxed);
+  return n;
 }
 
 }  // namespace moe
@@ -1105,19 +1298,26 @@ int moe_sample(const void* logits, int logits_dtype, int B, int V, long long row
   if (!logits || !u || !ids) return MOE_ERR_INVALID_ARG;
   const int es = logits_dtype == MOE_LOGITS_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) & (es - 1)) return MOE_ERR_INVALID_ARG;
-  // CTAs per row: enough that a slice is at most 64 KB (two CTAs per SM), and
-  // more while the GPU is not full and a slice keeps 4 KB
+  // CTAs per row: so many that the rows in flight, four CTAs on each of 152
+  // SMs, take no more than about 96 MB of the L2, and more while the GPU is not
+  // full and a CTA has 2048 tokens at least
+  const long long slots = 152 * kSampCtas, bytes = static_cast<long long>(V) * es;
+  const int most = max_cluster(logits_dtype);
+  if (most < 1) return MOE_ERR_CUDA;
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<long long>(V) * es > 65536ll * cluster) cluster *= 2;
-  while (cluster < kMaxCluster && static_cast<long long>(B) * cluster < 152 &&
-         static_cast<long long>(V) * es > 8192ll * cluster)
+  while (cluster < 8 && (B < slots / cluster ? B : slots / cluster) * bytes > 96ll << 20)
     cluster *= 2;
-  SampArgs a = {logits, row_stride, u, temperature, top_k, top_p, min_p, ids, probs, V,
-                (((V + cluster - 1) / cluster) + 7) / 8 * 8};
+  while (cluster < most && static_cast<long long>(B) * cluster * 2 <= slots &&
+         V >= 4096ll * cluster)
+    cluster *= 2;
+  const SampArgs a = {logits, row_stride, u, temperature, top_k, top_p, min_p, ids, probs, V,
+                      (((V + cluster - 1) / cluster) + 7) / 8 * 8};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits_dtype == MOE_LOGITS_F32
-                            ? launch_sample<float>(a, B, cluster, st)
-                            : launch_sample<__nv_bfloat16>(a, B, cluster, st);
+  const dim3 grid(static_cast<unsigned>(B) * cluster);
+  const cudaError_t e =
+      logits_dtype == MOE_LOGITS_F32
+          ? launch_cluster(sample_kernel<float>, grid, dim3(kSampThreads), cluster, 0, st, a)
+          : launch_cluster(sample_kernel<__nv_bfloat16>, grid, dim3(kSampThreads), cluster, 0, st, a);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
