@@ -25,10 +25,10 @@
 //      token exactly; the draw is among the list when nothing lies above it,
 //      else it goes by the warps' sums, and the warp whose tokens it falls on
 //      walks through them once more.
-//   D  where the window does not hold the border (a bin with more than 256
-//      tokens, a border the counts misjudged, top-p among the many that a large
-//      top-k left): the border is narrowed to one logit value by histograms
-//      over order keys (at most three), and ties are counted in index order.
+//   D  where the border's bin alone has more than 256 tokens (equal ones, with
+//      bf16), or there is no such bin (top-p among the many that a large top-k
+//      left): the border is narrowed to one logit value by histograms over
+//      order keys (at most three), and ties are counted in index order.
 // Rows without top-k and top-p only need their sums.  Bound by the row's bytes
 // where top-k is small; where the whole vocabulary has to be weighed, by the
 // weights' instructions (about 50 a token, once).
@@ -248,6 +248,7 @@ struct SampShared {
   // first
   float warp_top[kMaxCluster * kSampWarps];
   int warp_tie[kMaxCluster * kSampWarps];
+  uint2 warp_key[kMaxCluster * kSampWarps];
   unsigned long long warp_mass[kMaxCluster * kSampWarps];
   unsigned long long warp_all[kMaxCluster * kSampWarps];
   unsigned long long part_mass[kSampWarps];
@@ -258,6 +259,7 @@ struct SampShared {
   int near_above;
   float near_w_above, win_w;
   unsigned long long at_mass;
+  unsigned long long key_sum[kSampThreads];
 };
 
 __device__ __forceinline__ int cut_to_int(long long v) {
@@ -593,11 +595,12 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
   };
 
   // ---- B: bins win_lo .. win_hi go to the list, those before are kept
-  bool generic = false, weigh_all = !k, weigh_above = true;
+  bool generic = false, dense = false;  // dense: the window is one bin, too full for the list
+  bool weigh_all = !k, weigh_above = true;
   int win_lo = INT_MAX, win_hi = INT_MAX, above_n = 0;
   // The window for a border that lies `need` (2^-24 of the largest weight, as
   // the counts have it) or k tokens down, among the bins around it
-  int near_c0 = -1;
+  int near_c0 = -1, near_at = 0;  // first coarse bin of those, the border's among them
   auto choose = [&](float need) {
     if (warp == 0) {
       // one warp, kOne neighbouring bins a lane: the border's bin, then the
@@ -626,13 +629,12 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       }
       n_at += S.near_above - n_sum;  // tokens before this lane's bins
       w_at += S.near_w_above - w_sum;
-      unsigned at_i = kNear - 1;
+      unsigned at_i = (near_at + 1) * kPer - 1;  // where rounding hides the border
       int n_i = n_at;
       float w_i = w_at;
 #pragma unroll
       for (int i = 0; i < kOne; ++i) {
-        const bool hit = k ? n_i < k && n_i + n[i] >= k
-                           : w_i <= need && w_i + w[i] >= need && n[i] > 0;
+        const bool hit = n[i] > 0 && (k ? n_i + n[i] >= k : w_i + w[i] >= need);
         if (hit) at_i = min(at_i, static_cast<unsigned>(lane * kOne + i));
         n_i += n[i];
         w_i += w[i];
@@ -677,7 +679,13 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         if (!k && n_i - above <= kList / 2) hi = max(hi, lane * kOne + i);
       }
       hi = __reduce_max_sync(0xffffffffu, hi);
+      __syncwarp();
       if (lane == 0) {
+        // few enough: all tokens from the largest logit on
+        if (through <= (k ? kList : kList / 2)) {
+          above = 0;
+          S.win_w = 0.0f;
+        }
         S.at_count = through - above;
         S.above_n = above;
         S.win_lo = above == 0 ? 0 : min(kBins - 1, near_c0 * kPer + static_cast<int>(lo));
@@ -787,9 +795,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       const long long wi = static_cast<long long>(sw * kUnit);
       scan_pair(sn, wi, S.scan, en, ew, tn, tw);
       const float need = static_cast<float>(tw) * share;  // before the border
-      const bool here = k ? en < k && en + sn >= k
-                          : static_cast<float>(ew) <= need &&
-                                static_cast<float>(ew + wi) >= need && sn > 0;
+      const bool here = sn > 0 && (k ? en + sn >= k : static_cast<float>(ew + wi) >= need);
       if (here) atomicMin(&S.at_bin, tid);
       __syncthreads();
       const bool found = S.at_bin < kSampThreads;  // else top-k keeps everything
@@ -818,9 +824,11 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       }
       __syncthreads();
       near_c0 = c0;
+      near_at = S.at_bin - c0;
       if (found) choose(need);
       if (found) {
-        generic = S.at_count > kList;
+        dense = S.at_count > kList;
+        generic = dense && k && p_on;
       } else {
         win_lo = 0;
         win_hi = kBins - 1;
@@ -842,10 +850,17 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     });
     w_mine = warp_sum(w_mine);
   }
+  uint32_t bin_lo = 0xffffffffu, bin_hi = 0;  // a dense bin's order keys
+  unsigned long long above = 0, everything = 0;
   for (int tries = 0; list_on && !generic; ++tries) {
     // ---- C
-    unsigned long long above = 0, everything = 0;
+    above = everything = 0;
     auto enlist = [&](float v, int idx) {
+      if (dense) {
+        bin_lo = min(bin_lo, order_key(v));
+        bin_hi = max(bin_hi, order_key(v));
+        return;
+      }
       const int at = atomicAdd(&S.list_n, 1);
       if (at < kList) {
         S.list_key[at] = order_key(v);
@@ -890,6 +905,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       above = warp_sum(above);
       everything = warp_sum(everything);
     }
+    if (dense) break;
     if (lane == 0) {
       cluster.map_shared_rank(S.warp_mass, 0)[my_warp] = above;
       cluster.map_shared_rank(S.warp_all, 0)[my_warp] = everything;
@@ -1004,20 +1020,19 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       const float need = S.result.need;
       if (tid == 0) S.list_n = S.all_n = 0;
       choose(need);
-      generic = S.at_count > kList;
+      dense = S.at_count > kList;
       weigh_above = above_n > 0;
       everyone();
     }
   }
 
   Cut cut = {0, INT_MAX};
-  if (generic) {
-    // ---- D.  `narrow`: the order key where the count or the weight of the
-    // keys from it up, lo at least, reaches `need`; the same in all CTAs.
-    // Histograms over keys hi - 2^sh i, on ever fewer keys
-    auto narrow = [&](bool mass, long long need, uint32_t lo, long long& passed) {
-      uint32_t hi = order_key(top);
-      passed = 0;  // count or weight of the keys above hi
+  if (generic || dense) {
+    // ---- D.  `narrow`: the order key, lo .. hi, where the count or the weight
+    // of the keys from it up reaches `need`, or 0; the same in all CTAs.
+    // Histograms over keys hi - 2^sh i, on ever fewer keys.  passed: what the
+    // keys above hi come to, then those above the result
+    auto narrow = [&](bool mass, long long need, uint32_t lo, uint32_t hi, long long& passed) {
       for (;;) {
         const int sh = max(0, 32 - __clz(hi - lo) - 11);  // 2^11 bins
         everyone();  // nobody reads the last histogram any more
@@ -1041,27 +1056,56 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
             }
           }
         });
-        everyone();
+        __syncthreads();
+        // as in B: coarse bins of all CTAs first, then the fine ones of one
         constexpr int kMine = kKeyBins / kSampThreads;
-        long long cw[kMine] = {}, sum = 0;
-        for (int r = 0; r < C; ++r) {
-          const uint32_t* l = cluster.map_shared_rank(S.lo, r) + tid * kMine;
-          const uint32_t* h = cluster.map_shared_rank(S.hi, r) + tid * kMine;
+        unsigned long long sum = 0;
 #pragma unroll
-          for (int i = 0; i < kMine; ++i) cw[i] += (static_cast<long long>(h[i]) << 32) + l[i];
+        for (int i = 0; i < kMine; ++i)
+          sum += (static_cast<unsigned long long>(S.hi[tid * kMine + i]) << 32) +
+                 S.lo[tid * kMine + i];
+        S.key_sum[tid] = sum;
+        if (tid == 0) S.at_bin = -1;
+        everyone();
+        {
+          unsigned long long x[kMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            x[r] = r < C ? *cluster.map_shared_rank(S.key_sum + tid, r) : 0;
+          sum = 0;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) sum += x[r];
         }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) sum += cw[i];
         long long ex, unused, tot, tot_b;
-        scan_pair(sum, 0, S.scan, ex, unused, tot, tot_b);
-        long long at = passed + ex;
+        scan_pair(static_cast<long long>(sum), 0, S.scan, ex, unused, tot, tot_b);
+        if (passed + ex < need && passed + ex + static_cast<long long>(sum) >= need) {
+          S.at_bin = tid;
+          S.at_mass = static_cast<unsigned long long>(passed + ex);
+        }
+        __syncthreads();
+        if (S.at_bin < 0) return 0u;
+        if (warp == 0) {
+          unsigned long long w = 0;  // lane i: fine bin i
+          if (lane < kMine) {
+            const int i = S.at_bin * kMine + lane;
+            for (int r = 0; r < C; ++r)
+              w += (static_cast<unsigned long long>(*cluster.map_shared_rank(S.hi + i, r)) << 32) +
+                   *cluster.map_shared_rank(S.lo + i, r);
+          }
+          unsigned long long incl = w;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          if (at < need && at + cw[i] >= need) {
-            S.at_bin = tid * kMine + i;
+          for (int off = 1; off < 32; off <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+          }
+          const long long at = static_cast<long long>(S.at_mass + incl - w);
+          const unsigned hit = __ballot_sync(
+              0xffffffffu, lane < kMine && at < need && at + static_cast<long long>(w) >= need);
+          __syncwarp();
+          if (hit && lane == __ffs(hit) - 1) {
+            S.at_bin = S.at_bin * kMine + lane;
             S.at_mass = static_cast<unsigned long long>(at);
           }
-          at += cw[i];
         }
         __syncthreads();
         passed = static_cast<long long>(S.at_mass);
@@ -1081,39 +1125,84 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       for (int i = lane; i < warps; i += 32) x += S.warp_all[i];
       return warp_sum(x);
     };
-    const uint32_t key_min = order_key(l_min);
-    long long ties = LLONG_MAX, passed;  // kept of the tokens equal to the cut
-    if (k) {
-      unsigned long long live = 0;
-      sl.template sweep<4>([&](const float (&v)[VE], int, int) {
-#pragma unroll
-        for (int j = 0; j < VE; ++j) live += v[j] >= l_min;
-      });
-      if (row_sum(live) > static_cast<unsigned long long>(k)) {
-        cut.key = narrow(false, k, key_min, passed);
-        ties = k - passed;
+    const uint32_t key_min = order_key(l_min), key_top = order_key(top);
+    long long ties = LLONG_MAX, passed = 0;  // kept of the tokens equal to the cut
+    unsigned long long base = 0;             // this warp's weight above key_end
+    uint32_t key_end = 0xffffffffu;
+    if (dense && !generic) {
+      // the border lies in one bin, all of whose tokens are often alike (bf16)
+      bin_lo = __reduce_min_sync(0xffffffffu, bin_lo);
+      bin_hi = __reduce_max_sync(0xffffffffu, bin_hi);
+      if (lane < C) {
+        cluster.map_shared_rank(S.warp_all, lane)[my_warp] = everything;
+        cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = above;
+        cluster.map_shared_rank(S.warp_key, lane)[my_warp] = make_uint2(bin_lo, bin_hi);
+      }
+      everyone();
+      base = above;
+      above = everything = 0;
+      for (int i = lane; i < warps; i += 32) {
+        above += S.warp_mass[i];
+        everything += S.warp_all[i];
+        bin_lo = min(bin_lo, S.warp_key[i].x);
+        bin_hi = max(bin_hi, S.warp_key[i].y);
+      }
+      above = warp_sum(above);
+      everything = warp_sum(everything);
+      bin_lo = __reduce_min_sync(0xffffffffu, bin_lo);
+      bin_hi = __reduce_max_sync(0xffffffffu, bin_hi);
+      const unsigned long long border = k ? k : border_of(everything);
+      passed = static_cast<long long>(k ? above_n : above);
+      generic = static_cast<unsigned long long>(passed) >= border;
+      if (!generic) {
+        cut.key = narrow(!k, static_cast<long long>(border), bin_lo, bin_hi, passed);
+        generic = cut.key == 0;
+      }
+      if (!generic) {
+        const unsigned long long w = k ? 1 : weigh_call(weigh, key_value(cut.key));
+        ties = static_cast<long long>((border - passed + w - 1) / w);
+        key_end = bin_hi;
       }
     }
-    if (p_on) {
-      unsigned long long x = 0;
-      sl.template sweep<1>([&](const float (&v)[VE], int, int) {
+    if (generic) {
+      base = 0;
+      passed = 0;
+      cut.key = 0;
+      if (k) {
+        unsigned long long live = 0;
+        sl.template sweep<4>([&](const float (&v)[VE], int, int) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const bool ok = v[j] >= l_min && order_key(v[j]) > cut.key;
-          const unsigned long long w = weigh_call(weigh, ok ? v[j] : top);
-          x += ok ? w : 0;
+          for (int j = 0; j < VE; ++j) live += v[j] >= l_min;
+        });
+        if (row_sum(live) > static_cast<unsigned long long>(k)) {
+          cut.key = narrow(false, k, key_min, key_top, passed);
+          ties = k - passed;
         }
-      });
-      const unsigned long long over_cut = row_sum(x);
-      const unsigned long long w_cut = weigh_call(weigh, cut.key ? key_value(cut.key) : top);
-      const unsigned long long at_cut = cut.key ? w_cut * static_cast<unsigned long long>(ties) : 0;
-      const unsigned long long border = max(1ull, border_of(over_cut + at_cut));
-      if (border <= over_cut) {
-        cut.key = narrow(true, static_cast<long long>(border), max(key_min, cut.key + 1), passed);
-        const unsigned long long w = weigh_call(weigh, key_value(cut.key));
-        ties = static_cast<long long>((border - passed + w - 1) / w);
-      } else {  // among top-k's ties
-        ties = min(ties, static_cast<long long>((border - over_cut + w_cut - 1) / w_cut));
+      }
+      if (p_on) {
+        unsigned long long x = 0;
+        sl.template sweep<1>([&](const float (&v)[VE], int, int) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const bool ok = v[j] >= l_min && order_key(v[j]) > cut.key;
+            const unsigned long long w = weigh_call(weigh, v[j]);
+            x += ok ? w : 0;
+          }
+        });
+        const unsigned long long over_cut = row_sum(x);
+        const unsigned long long w_cut = weigh_call(weigh, cut.key ? key_value(cut.key) : top);
+        const unsigned long long at_cut =
+            cut.key ? w_cut * static_cast<unsigned long long>(ties) : 0;
+        const unsigned long long border = max(1ull, border_of(over_cut + at_cut));
+        if (border <= over_cut) {
+          passed = 0;
+          cut.key = narrow(true, static_cast<long long>(border), max(key_min, cut.key + 1), key_top,
+                           passed);
+          const unsigned long long w = weigh_call(weigh, key_value(cut.key));
+          ties = static_cast<long long>((border - passed + w - 1) / w);
+        } else {  // among top-k's ties
+          ties = min(ties, static_cast<long long>((border - over_cut + w_cut - 1) / w_cut));
+        }
       }
     }
     // the index of the last kept tie
@@ -1154,16 +1243,19 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        const bool ok = v[j] >= l_min && cut.keeps(order_key(v[j]), at + j);
-        const unsigned long long w = weigh_call(weigh, ok ? v[j] : top);
-        w_mine += ok ? w : 0;
+        const uint32_t key = order_key(v[j]);
+        const bool ok = v[j] >= l_min && key <= key_end && cut.keeps(key, at + j);
+        if (__any_sync(0xffffffffu, ok)) {
+          const unsigned long long w = weigh_call(weigh, v[j]);
+          w_mine += ok ? w : 0;
+        }
       }
     });
-    w_mine = warp_sum(w_mine);
+    w_mine = warp_sum(w_mine) + base;
   }
   unsigned long long before, total, to;
   int who = -1;
-  if (generic || !list_on) {
+  if (generic || dense || !list_on) {
     // every warp finds the one that the draw falls on
     if (lane < C) cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = w_mine;
     everyone();
