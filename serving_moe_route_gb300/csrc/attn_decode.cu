@@ -7,10 +7,10 @@
 // keep loads in flight, and the products only have to keep out of the way.
 //
 //   work     A unit is (request, kv head, block of 16 query heads); its tokens
-//            form tiles of 16 per warp.  The tiles of all units, in order, are
-//            cut into equal contiguous ranges, one per CTA of a single wave,
-//            so ragged lengths and long single requests balance alike; a
-//            range may begin and end inside a unit.
+//            form tiles, a stage per warp, and it counts its tiles and one or two
+//            more for its end, which takes as long.  The counts of all units, in order, are cut into equal contiguous ranges, one per
+//            CTA of a single wave, so ragged lengths and long single requests
+//            balance alike; a range may begin and end inside a unit.
 //   loads    Each warp has a ring of ST stages of 16 keys and 16 values and
 //            fills it with 16-byte cp.async, ST-1 stages ahead, across unit
 //            borders; page ids are fetched one stage before that.  Warps
@@ -45,7 +45,6 @@
 namespace moe {
 
 constexpr int kRows = 16;  // query heads of a unit: the m of the mma instructions
-constexpr int kKeys = 16;  // keys of a warp's stage
 constexpr int kMaxLen = INT_MAX - 1024;  // a tile's end stays an int
 
 struct AttnArgs {
@@ -66,7 +65,7 @@ struct AttnArgs {
   unsigned* err;
   float scale_log2;
   int B, Hq, heads, group, blocks;  // blocks: of 16 query heads per kv head
-  int dim, page, num_pages, max_pages, window, min_tiles;
+  int dim, page, page_shift, num_pages, max_pages, window, min_tiles;
 };
 
 // ------------------------------------------------------------ instructions
@@ -169,6 +168,15 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ configuration
+#ifndef ATT_C2
+#define ATT_C2 4
+#define ATT_S2 6
+#define ATT_C4 3
+#define ATT_S4 4
+#define ATT_C8 2
+#define ATT_S8 3
+#define ATT_QREG 128
+#endif
 // Bytes of a warp's stage (16 keys and 16 values), warps and stages per CTA,
 // CTAs per SM: about 96 KB of ring per CTA and two CTAs per SM while a stage
 // is at most 8 KB (one CTA's joins overlap the other's loads), else one CTA.
@@ -176,14 +184,20 @@ template <int KV, int DP>
 struct AttnCfg {
   static constexpr int ES = kv_esize(KV);
   static constexpr int RB = DP * ES;             // bytes of a row
-  static constexpr int SB = 2 * kKeys * RB;      // bytes of a warp's stage
-  static constexpr int NW = SB <= 16384 ? 4 : 2;
-  static constexpr int CTAS = SB <= 8192 ? 2 : 1;
-  static constexpr int ST = SB <= 2048 ? 8 : SB <= 4096 ? 6 : 3;
+  static constexpr int KEYS = KV == MOE_KV_F32 ? 8 : 16;  // keys of a warp's stage
+  static constexpr int NJ = KEYS / 8;
+  static constexpr int SB = 2 * KEYS * RB;       // bytes of a warp's stage
+  static constexpr int NW = SB <= 8192 ? 4 : 6;
+  static constexpr int CTAS = SB <= 2048 ? ATT_C2 : SB <= 4096 ? ATT_C4 : SB <= 8192 ? ATT_C8 : 1;
+  static constexpr int ST = SB <= 2048 ? ATT_S2 : SB <= 4096 ? ATT_S4 : SB <= 8192 ? ATT_S8 : 2;
   static constexpr int THREADS = 32 * NW;
-  static constexpr int TILE = NW * kKeys;
+  // what a unit's end and the next one's begin cost, in tiles (of a batch of
+  // 64 with bf16, 180 MB: 56 us with 0, 45 with 1, 42 with 2 and 3; f32, whose
+  // tiles take longer: 190, 178, 179, 181 us)
+  static constexpr int END = KV == MOE_KV_F32 ? 1 : 2;
+  static constexpr int TILE = NW * KEYS;
   // Q in shared memory unless its fragments fit registers
-  static constexpr bool QREG = KV != MOE_KV_F32 && DP <= 128;
+  static constexpr bool QREG = KV != MOE_KV_F32 && DP <= ATT_QREG;
   static constexpr int QES = KV == MOE_KV_F32 ? 4 : 2;
   // row pitch of Q: conflict-free for ldmatrix (bf16), 8-byte (f16) and
   // 16-byte (f32) fragment loads
@@ -228,13 +242,12 @@ __device__ __forceinline__ int tiles_of(int2 span, int tile) {
 struct Cursor {
   int b, x, t, nt;  // request, unit in request, tile in unit, tiles of a unit
   int first, len;   // the request's attended tokens
-  long long left;   // tiles of the range from here on
+  long long left;   // places of the range from here on, units' ends included
 };
 
+// to the first tile of the next unit (left is the caller's business)
 template <int TILE>
-__device__ __forceinline__ void advance(Cursor& c, const AttnArgs& A, int units) {
-  --c.left;
-  if (++c.t < c.nt) return;
+__device__ __forceinline__ void next_unit(Cursor& c, const AttnArgs& A, int units) {
   c.t = 0;
   if (++c.x < units) return;
   c.x = 0;
@@ -245,6 +258,13 @@ __device__ __forceinline__ void advance(Cursor& c, const AttnArgs& A, int units)
   c.first = s.x;
   c.len = s.y;
   c.nt = tiles_of(s, TILE);
+}
+template <int TILE, int END>
+__device__ __forceinline__ void advance(Cursor& c, const AttnArgs& A, int units) {
+  --c.left;
+  if (++c.t < c.nt) return;
+  c.left -= END;
+  next_unit<TILE>(c, A, units);
 }
 
 template <int KV>
@@ -261,7 +281,7 @@ template <int KV, int DP>
 __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTAS)
     attn_decode_kernel(const AttnArgs A) {
   using C = AttnCfg<KV, DP>;
-  constexpr int NW = C::NW, ST = C::ST, RB = C::RB, NT = DP / 8;
+  constexpr int NW = C::NW, ST = C::ST, RB = C::RB, NT = DP / 8, NJ = C::NJ;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_sum[NW];
   __shared__ int s_b;
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   const int per = (A.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(A.B, static_cast<int>(threadIdx.x) * per), b1 = min(A.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of(span_of(A, b, cut), C::TILE);
+  for (int b = b0; b < b1; ++b) mine += tiles_of(span_of(A, b, cut), C::TILE) + C::END;
   long long incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -308,7 +328,8 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
       long long at = lo;
       int b = b0;
       for (;; ++b) {
-        const long long n = static_cast<long long>(tiles_of(span_of(A, b, cut), C::TILE)) * units;
+        const long long n =
+            static_cast<long long>(tiles_of(span_of(A, b, cut), C::TILE) + C::END) * units;
         if (begin < at + n) break;
         at += n;
       }
@@ -324,9 +345,14 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
     cc.first = s.x;
     cc.len = s.y;
     cc.nt = tiles_of(s, C::TILE);
-    cc.x = static_cast<int>(s_off / cc.nt);
-    cc.t = static_cast<int>(s_off - static_cast<long long>(cc.x) * cc.nt);
+    const int places = cc.nt + C::END;
+    cc.x = static_cast<int>(s_off / places);
+    cc.t = static_cast<int>(s_off - static_cast<long long>(cc.x) * places);
     cc.left = end - begin;
+    if (cc.t >= cc.nt) {  // the range begins with a unit's end: on to the next
+      cc.left -= places - cc.t;
+      next_unit<C::TILE>(cc, A, units);
+    }
   }
   Cursor lc = cc;
   bool bad_page = false;
@@ -337,6 +363,8 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   constexpr int RPI = CPR >= 32 ? 1 : 32 / CPR;    // rows per instruction
   constexpr int IPR = CPR > 32 ? CPR / 32 : 1;     // instructions per row
   const int chunks = A.dim * C::ES / 16;
+  const long long lane_off =
+      (RPI > 1 ? lane / CPR : 0) * A.s_token + (RPI > 1 ? lane % CPR : lane) * 16;
   struct Want {
     int row;   // row in the page of this lane's key (lanes 0 .. 15), -1: none
     int page;
@@ -344,9 +372,9 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   // page id of this lane's key at cursor c
   auto want = [&](const Cursor& c) {
     Want w = {-1, 0};
-    const int pos = c.first + c.t * C::TILE + warp * kKeys + (lane & 15);
+    const int pos = c.first + c.t * C::TILE + warp * C::KEYS + lane % C::KEYS;
     if (c.left > 0 && pos < c.len) {
-      const int p = pos / A.page;
+      const int p = A.page_shift >= 0 ? pos >> A.page_shift : pos / A.page;
       w.row = pos - p * A.page;
       w.page = __ldg(A.table + c.b * A.table_stride + p);
     }
@@ -356,25 +384,47 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
     const bool in = w.page >= 0 && w.page < A.num_pages;
     bad_page |= w.row >= 0 && !in;
     const bool live = w.row >= 0 && in;
-    const unsigned mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
+    const unsigned mask = __ballot_sync(0xffffffffu, live) & ((1u << C::KEYS) - 1);
     if (lane == 0) s_mask[warp][stage] = static_cast<unsigned short>(mask);
+    const uint32_t base = ring + stage * C::SB;
     if (mask) {
-      const long long off = live ? w.page * A.s_page + w.row * A.s_token +
-                                       (c.x / A.blocks) * A.s_head
-                                 : 0;
-      const uint32_t base = ring + stage * C::SB;
+      const long long off =
+          live ? w.page * A.s_page + w.row * A.s_token + (c.x / A.blocks) * A.s_head : 0;
+      // rows that follow one another in one page: no row needs its own address
+      const int row0 = __shfl_sync(0xffffffffu, w.row, 0);
+      const int page0 = __shfl_sync(0xffffffffu, w.page, 0);
+      const bool run = w.page == page0 && w.row == row0 + lane % C::KEYS;
+      if (mask == (1u << C::KEYS) - 1 && __all_sync(0xffffffffu, run)) {
+        const long long o = __shfl_sync(0xffffffffu, off, 0) + lane_off;
+        const char *kp = A.k + o, *vp = A.v + o;
 #pragma unroll
-      for (int i = 0; i < kKeys / RPI; ++i) {
-        const int r = i * RPI + (RPI > 1 ? lane / CPR : 0);
-        const long long o = __shfl_sync(0xffffffffu, off, r);
-        const bool row_live = (mask >> r) & 1u;
+        for (int i = 0; i < C::KEYS / RPI; ++i) {
+          const int r = i * RPI + (RPI > 1 ? lane / CPR : 0);
 #pragma unroll
-        for (int j = 0; j < IPR; ++j) {
-          const int ch = (RPI > 1 ? lane % CPR : lane) + 32 * j;
-          const bool real = row_live && ch < chunks;
-          const long long at = o + (ch < chunks ? ch * 16 : 0);
-          cp_async16(base + chunk_at<RB>(r, ch, true), A.k + at, real);
-          cp_async16(base + kKeys * RB + chunk_at<RB>(r, ch, KV != MOE_KV_F32), A.v + at, real);
+          for (int j = 0; j < IPR; ++j) {
+            const int ch = (RPI > 1 ? lane % CPR : lane) + 32 * j;
+            const bool real = ch < chunks;
+            cp_async16(base + chunk_at<RB>(r, ch, true), real ? kp + 512 * j : A.k, real);
+            cp_async16(base + C::KEYS * RB + chunk_at<RB>(r, ch, KV != MOE_KV_F32),
+                       real ? vp + 512 * j : A.v, real);
+          }
+          kp += RPI * A.s_token;
+          vp += RPI * A.s_token;
+        }
+      } else {
+#pragma unroll 2
+        for (int i = 0; i < C::KEYS / RPI; ++i) {
+          const int r = i * RPI + (RPI > 1 ? lane / CPR : 0);
+          const long long o = __shfl_sync(0xffffffffu, off, r);
+          const bool row_live = (mask >> r) & 1u;
+#pragma unroll
+          for (int j = 0; j < IPR; ++j) {
+            const int ch = (RPI > 1 ? lane % CPR : lane) + 32 * j;
+            const bool real = row_live && ch < chunks;
+            const long long at = o + (ch < chunks ? ch * 16 : 0);
+            cp_async16(base + chunk_at<RB>(r, ch, true), A.k + at, real);
+            cp_async16(base + C::KEYS * RB + chunk_at<RB>(r, ch, KV != MOE_KV_F32), A.v + at, real);
+          }
         }
       }
     }
@@ -382,19 +432,21 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   };
 
   // the first ST - 1 stages: all their page ids are asked for before any use
-  Want next;
+  Want next = want(lc);
   {
-    Want w[ST];
-    Cursor at[ST - 1];
+    Want w[ST - 1];
+    Cursor at = lc;
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
-      at[s] = lc;
-      w[s] = want(lc);
-      if (lc.left > 0) advance<C::TILE>(lc, A, units);
+      w[s] = next;
+      if (lc.left > 0) advance<C::TILE, C::END>(lc, A, units);
+      next = want(lc);
     }
-    next = want(lc);
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) load(at[s], w[s], s);
+    for (int s = 0; s < ST - 1; ++s) {
+      load(at, w[s], s);
+      if (at.left > 0) advance<C::TILE, C::END>(at, A, units);
+    }
   }
 
   // ---- per-unit state
@@ -527,19 +579,19 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         const int to = slot == 0 ? ST - 1 : slot - 1;
         const Cursor at = lc;
         const Want w = next;
-        if (lc.left > 0) advance<C::TILE>(lc, A, units);
+        if (lc.left > 0) advance<C::TILE, C::END>(lc, A, units);
         next = want(lc);
         load(at, w, to);
       }
       const unsigned mask = s_mask[warp][slot];
       if (mask) {
-        const uint32_t kb = ring + slot * C::SB, vb = kb + kKeys * RB;
-        float s[2][4];
+        const uint32_t kb = ring + slot * C::SB, vb = kb + C::KEYS * RB;
+        float s[NJ][4];
         if constexpr (KV == MOE_KV_F32) {
           // 3 products of (hi, lo) pairs; hi * hi and the small ones in sums
           // of their own, and few terms to a chain: the tensor cores cut,
           // not round, their sums
-          float hh[2][2][4] = {}, hl[2][4] = {};
+          float hh[NJ][2][4] = {}, hl[NJ][2][4] = {};
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             // lane c's columns of the two k = 8 steps: 4c, 4c+1 and 4c+2, 4c+3
@@ -555,7 +607,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
             split_tf32(qa.w, ah[1][2], al[1][2]);
             split_tf32(qb.w, ah[1][3], al[1][3]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < NJ; ++j) {
               const float4 kv = lds4(kb + chunk_at<RB>(8 * j + g, 4 * kk + c4, true));
               uint32_t h0_, h1_, h2_, h3_, l0_, l1_, l2_, l3_;
               split_tf32(kv.x, h0_, l0_);
@@ -564,16 +616,17 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
               split_tf32(kv.w, h3_, l3_);
               mma_tf32(hh[j][0], ah[0], h0_, h1_);
               mma_tf32(hh[j][1], ah[1], h2_, h3_);
-              mma_tf32(hl[j], al[0], h0_, h1_);
-              mma_tf32(hl[j], ah[0], l0_, l1_);
-              mma_tf32(hl[j], al[1], h2_, h3_);
-              mma_tf32(hl[j], ah[1], l2_, l3_);
+              mma_tf32(hl[j][0], al[0], h0_, h1_);
+              mma_tf32(hl[j][1], ah[0], l0_, l1_);
+              mma_tf32(hl[j][0], al[1], h2_, h3_);
+              mma_tf32(hl[j][1], ah[1], l2_, l3_);
             }
           }
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = hh[j][0][e] + hh[j][1][e] + hl[j][e];
+            for (int e = 0; e < 4; ++e)
+              s[j][e] = hh[j][0][e] + hh[j][1][e] + (hl[j][0][e] + hl[j][1][e]);
         } else {
           float part[2][2][4] = {};  // even and odd steps: shorter chains
 #pragma unroll
@@ -633,7 +686,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         // rows g (e = 0, 1) and g + 8 (e = 2, 3), keys 8 j + 2 c + (e & 1)
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool live = (mask >> (8 * j + 2 * c4 + (e & 1))) & 1u;
@@ -653,7 +706,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         const float z0 = m[0] == -INFINITY ? 0.0f : m[0], z1 = m[1] == -INFINITY ? 0.0f : m[1];
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s[j][e] = ex2(s[j][e] - (e < 2 ? z0 : z1));
@@ -717,9 +770,9 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         } else {
           // step j takes keys 8 j ..: lane c's two are 8 j + 2 c and + 1, the
           // very ones whose weights it holds
-          uint32_t ph[2][4], pl[2][4];
+          uint32_t ph[NJ][4], pl[NJ][4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < NJ; ++j) {
             split_tf32(s[j][0], ph[j][0], pl[j][0]);
             split_tf32(s[j][2], ph[j][1], pl[j][1]);
             split_tf32(s[j][1], ph[j][2], pl[j][2]);
@@ -729,7 +782,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
           for (int dd = 0; dd < DP / 32; ++dd) {
             float o[4][4] = {}, o2[4][4] = {};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < NJ; ++j) {
               const float4 a = lds4(vb + chunk_at<RB>(8 * j + 2 * c4, 8 * dd + g, false));
               const float4 b = lds4(vb + chunk_at<RB>(8 * j + 2 * c4 + 1, 8 * dd + g, false));
               const float va[4] = {a.x, a.y, a.z, a.w}, vb4[4] = {b.x, b.y, b.z, b.w};
@@ -826,13 +879,13 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
     if (!whole && t_first == 0 && threadIdx.x == 0) {
       // the unit begins here and goes on in the next CTAs, up to the one
       // whose range holds its last tile
-      const long long last = end - unit.left + unit.nt - 1;
+      const long long last = end - unit.left + unit.nt - 1;  // place of its last tile
       const long long who = ((last + 1) * ctas - 1) / total;
       A.info[cta] = make_int4(cc.b, cc.x, static_cast<int>(who - cta + 1), 0);
     }
     __syncthreads();  // the stages and s_m may be used again
     slot = slot + 1 == ST ? 0 : slot + 1;
-    advance<C::TILE>(cc, A, units);
+    advance<C::TILE, C::END>(cc, A, units);
   }
   cp_wait<0>();
   if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
@@ -841,13 +894,14 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
 // Joins the parts of a unit that range borders cut.  Block (c, r): row r of
 // the unit that begins in CTA c and does not end there (most blocks find
 // none).  Its parts are c's first slot, then the second slots of the next
-// CTAs; the four warps take every fourth part, so the loads of a long
-// request's 300 parts overlap.
+// CTAs; the warps take every 16th part, so that the loads of a long request's
+// hundred parts are all in flight.
+constexpr int kJoinWarps = 16;
 template <int KV, int DP>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs A) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs A) {
   constexpr int VL = DP / 32;  // columns per lane
-  __shared__ float s_o[4][DP];
-  __shared__ float s_l[4];
+  __shared__ float s_o[kJoinWarps][DP];
+  __shared__ float s_l[kJoinWarps];
   pdl_wait();
   const int cta = blockIdx.x, r = blockIdx.y;
   const int4 u = A.info[cta];
@@ -864,15 +918,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs A) {
   float o[VL] = {};
   float sum = 0.0f;
 #pragma unroll 4
-  for (int i = warp; i < u.z; i += 4) {
+  for (int i = warp; i < u.z; i += kJoinWarps) {
     const float2 ml = A.part_ml[at(i)];
-    const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
     const float* x = A.part_o + at(i) * DP + lane * VL;
-    sum += f * ml.y;
     float v[VL];
 #pragma unroll
     for (int j = 0; j < VL; j += 2)
       *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(x + j);
+    const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
+    sum += f * ml.y;
 #pragma unroll
     for (int j = 0; j < VL; ++j) o[j] += f * v[j];
   }
@@ -880,19 +934,23 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs A) {
   for (int j = 0; j < VL; ++j) s_o[warp][lane * VL + j] = o[j];
   if (lane == 0) s_l[warp] = sum;
   __syncthreads();
-  sum = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
-  const float inv = sum == 0.0f ? 0.0f : mul / sum;
-  for (int d = threadIdx.x * 4; d < A.dim; d += 512) {
-    float v[4];
+  const int warps = min(kJoinWarps, u.z);
+  for (int d = threadIdx.x * 4; d < A.dim; d += 128 * kJoinWarps) {
+    sum = 0.0f;
+    float v[4] = {};
+    for (int w = 0; w < warps; ++w) {
+      sum += s_l[w];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = (s_o[0][d + j] + s_o[1][d + j] + s_o[2][d + j] + s_o[3][d + j]) * inv;
-    store4<KV>(A.out, u.x * A.o_b + (h0 + r) * A.o_h + d, make_float4(v[0], v[1], v[2], v[3]));
+      for (int j = 0; j < 4; ++j) v[j] += s_o[w][d + j];
+    }
+    const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
+    const float inv = sum == 0.0f ? 0.0f : mul / sum;
+    store4<KV>(A.out, u.x * A.o_b + (h0 + r) * A.o_h + d,
+               make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+    if (d == 0 && A.lse)
+      A.lse[static_cast<long long>(u.x) * A.Hq + h0 + r] =
+          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
-  if (threadIdx.x == 0 && A.lse)
-    A.lse[static_cast<long long>(u.x) * A.Hq + h0 + r] =
-        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------ host
@@ -920,7 +978,7 @@ static cudaError_t launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
   e = launch_chained(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, st, a);
   if (e != cudaSuccess) return e;
   return launch_chained(attn_join_kernel<KV, DP>, dim3(ctas, a.group < kRows ? a.group : kRows),
-                        dim3(128), 0, st, a);
+                        dim3(32 * kJoinWarps), 0, st, a);
 }
 
 template <int KV>
@@ -1010,6 +1068,9 @@ int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stri
   a.blocks = (a.group + kRows - 1) / kRows;
   a.dim = cache->head_dim;
   a.page = cache->page_size;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page == 1 << i) a.page_shift = i;
   a.num_pages = cache->num_pages;
   a.max_pages = max_pages;
   a.window = window;
