@@ -97,10 +97,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ float4 lds4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr)
                : "memory");
   return v;
@@ -117,13 +117,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -131,32 +124,32 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t tf32_rna(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
+// x = hi + lo with 11 bits each, both rounded (the instruction cuts lo's last
+// bits): products of two such pairs without lo * lo are off by 3 x 2^-22 of
+// |x y| at most
+__device__ __forceinline__ uint32_t tf32_hi(float x) {
+  return (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
 }
-// x = hi + lo with 11 bits each: products of two such pairs without lo * lo
-// are off by 2^-22 of |x y| at most
+__device__ __forceinline__ uint32_t tf32_lo(float x, uint32_t hi) {
+  return __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+}
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = tf32_rna(x);
-  const float h = __uint_as_float(hi);
-  lo = h == x ? 0u : tf32_rna(x - h);  // an infinite x has no rest
+  hi = tf32_hi(x);
+  lo = tf32_lo(x, hi);
 }
-// two e4m3 codes (the low and the high byte of 16 bits) as f16: exact
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(r)
-      : "r"(codes));
-  return r;
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-      : "=r"(r)
+// four e4m3 codes as two pairs of f16: exact
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(codes));
-  return r;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -168,41 +161,33 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ configuration
-#ifndef ATT_C2
-#define ATT_C2 4
-#define ATT_S2 6
-#define ATT_C4 3
-#define ATT_S4 4
-#define ATT_C8 2
-#define ATT_S8 3
-#define ATT_QREG 128
-#endif
-// Bytes of a warp's stage (16 keys and 16 values), warps and stages per CTA,
-// CTAs per SM: about 96 KB of ring per CTA and two CTAs per SM while a stage
-// is at most 8 KB (one CTA's joins overlap the other's loads), else one CTA.
+// Keys of a warp's stage (one k step of bf16 and f32 products, two of e4m3's,
+// in f16), its bytes (keys and values), warps and stages per CTA, CTAs per SM:
+// about 200 KB of an SM's shared memory hold stages.
 template <int KV, int DP>
 struct AttnCfg {
   static constexpr int ES = kv_esize(KV);
   static constexpr int RB = DP * ES;             // bytes of a row
-  static constexpr int KEYS = KV == MOE_KV_F32 ? 8 : 16;  // keys of a warp's stage
+  static constexpr int KEYS = KV == MOE_KV_F32 ? 8 : KV == MOE_KV_BF16 || DP == 256 ? 16 : 32;
   static constexpr int NJ = KEYS / 8;
-  static constexpr int SB = 2 * KEYS * RB;       // bytes of a warp's stage
-  static constexpr int NW = SB <= 8192 ? 4 : 6;
-  static constexpr int CTAS = SB <= 2048 ? ATT_C2 : SB <= 4096 ? ATT_C4 : SB <= 8192 ? ATT_C8 : 1;
-  static constexpr int ST = SB <= 2048 ? ATT_S2 : SB <= 4096 ? ATT_S4 : SB <= 8192 ? ATT_S8 : 2;
+  static constexpr int SB = 2 * KEYS * RB;
+  static constexpr int NW = SB == 16384 ? (KV == MOE_KV_F32 ? 5 : 6)
+                            : KV == MOE_KV_F32 && DP == 128 ? 8 : 4;
+  static constexpr int CTAS = SB == 16384 || NW == 8 ? 1 : SB == 8192 ? 2 : 3;
+  static constexpr int ST = SB == 16384 ? 2 : SB == 8192 ? 3 : 4;
   static constexpr int THREADS = 32 * NW;
   // what a unit's end and the next one's begin cost, in tiles (of a batch of
-  // 64 with bf16, 180 MB: 56 us with 0, 45 with 1, 42 with 2 and 3; f32, whose
-  // tiles take longer: 190, 178, 179, 181 us)
-  static constexpr int END = KV == MOE_KV_F32 ? 1 : 2;
+  // 64 with bf16, 180 MB: 56 us with 0, 45 with 1, 42 with 2 and 3)
+  static constexpr int END = 2;
   static constexpr int TILE = NW * KEYS;
-  // Q in shared memory unless its fragments fit registers
-  static constexpr bool QREG = KV != MOE_KV_F32 && DP <= ATT_QREG;
-  static constexpr int QES = KV == MOE_KV_F32 ? 4 : 2;
-  // row pitch of Q: conflict-free for ldmatrix (bf16), 8-byte (f16) and
-  // 16-byte (f32) fragment loads
-  static constexpr int QP = DP * QES + (KV == MOE_KV_F32 ? 64 : KV == MOE_KV_BF16 ? 16 : 32);
-  static constexpr int QBYTES = QREG ? 0 : kRows * QP;
+  // Q in shared memory unless its fragments fit registers; for f32 as two
+  // terms, one after the other
+  static constexpr bool QREG = KV != MOE_KV_F32 && DP <= 128;
+  // row pitch of a term: conflict-free for ldmatrix (bf16) and for 8-byte
+  // (f16) and 16-byte (f32) fragment loads
+  static constexpr int QP = KV == MOE_KV_F32 ? DP * 4 + 64 : KV == MOE_KV_BF16 ? DP * 2 + 16 : DP * 2 + 32;
+  static constexpr int QTERM = kRows * QP;
+  static constexpr int QBYTES = QREG ? 0 : (KV == MOE_KV_F32 ? 2 : 1) * QTERM;
   static constexpr int RING = NW * ST * SB;
   static constexpr int SMEM = RING + QBYTES;
   // columns of O that fit a warp's stage as fp32 (joining the warps)
@@ -286,8 +271,9 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   __shared__ long long s_sum[NW];
   __shared__ int s_b;
   __shared__ long long s_off;
-  __shared__ unsigned short s_mask[NW][ST];
+  __shared__ uint32_t s_mask[NW][ST];
   __shared__ float s_m[NW][kRows], s_l[NW][kRows], s_q[kRows];
+  constexpr uint32_t kAll = 0xffffffffu >> (32 - C::KEYS);  // a mask of live keys
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c4 = lane & 3;
   const int units = A.heads * A.blocks;
@@ -384,8 +370,8 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
     const bool in = w.page >= 0 && w.page < A.num_pages;
     bad_page |= w.row >= 0 && !in;
     const bool live = w.row >= 0 && in;
-    const unsigned mask = __ballot_sync(0xffffffffu, live) & ((1u << C::KEYS) - 1);
-    if (lane == 0) s_mask[warp][stage] = static_cast<unsigned short>(mask);
+    const uint32_t mask = __ballot_sync(0xffffffffu, live) & kAll;
+    if (lane == 0) s_mask[warp][stage] = mask;
     const uint32_t base = ring + stage * C::SB;
     if (mask) {
       const long long off =
@@ -394,7 +380,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
       const int row0 = __shfl_sync(0xffffffffu, w.row, 0);
       const int page0 = __shfl_sync(0xffffffffu, w.page, 0);
       const bool run = w.page == page0 && w.row == row0 + lane % C::KEYS;
-      if (mask == (1u << C::KEYS) - 1 && __all_sync(0xffffffffu, run)) {
+      if (mask == kAll && __all_sync(0xffffffffu, run)) {
         const long long o = __shfl_sync(0xffffffffu, off, 0) + lane_off;
         const char *kp = A.k + o, *vp = A.v + o;
 #pragma unroll
@@ -454,7 +440,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   float m[2], l[2];
   uint32_t qf[C::QREG ? DP / 16 : 1][4];
   float sl = 0.0f, v_mul = 1.0f;  // logits' factor in base 2, values' factor
-  float q_mul[2] = {1.0f, 1.0f};  // E4M3: power of two taken out of a row of Q
+  float q_mul[2] = {1.0f, 1.0f};  // e4m3: power of two taken out of a row of Q
   int rows = 0, t_first = 0;
   int slot = 0;                   // stage of the products' tile
   const uint32_t qs = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + C::RING;
@@ -475,93 +461,123 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         const int r = i / (DP / 4), d = i % (DP / 4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows && d < A.dim) v = __ldg(reinterpret_cast<const float4*>(q + r * A.q_h + d));
-        *reinterpret_cast<float4*>(smem + C::RING + r * C::QP + d * 4) = v;
+        uint4 hi, lo;
+        split_tf32(v.x, hi.x, lo.x);
+        split_tf32(v.y, hi.y, lo.y);
+        split_tf32(v.z, hi.z, lo.z);
+        split_tf32(v.w, hi.w, lo.w);
+        *reinterpret_cast<uint4*>(smem + C::RING + r * C::QP + d * 4) = hi;
+        *reinterpret_cast<uint4*>(smem + C::RING + C::QTERM + r * C::QP + d * 4) = lo;
       }
       __syncthreads();
     } else {
       const __nv_bfloat16* q =
           static_cast<const __nv_bfloat16*>(A.q) + cc.b * A.q_b + h0 * A.q_h;
-      if constexpr (C::QREG) {
-        // fragment layout: rows g and g + 8; 16 columns of a step kk as
-        // {2c, 2c+1} and {2c+8, 2c+9}; E4M3 keys come as 4 neighbouring codes
-        // per lane, so there lane c's columns are 4c .. 4c+3 instead
-        float big[2] = {0.0f, 0.0f};
+      // four neighbouring columns of a row as f16.  The row is first scaled by
+      // a power of two that brings its largest value into [1, 2): bf16 has 8
+      // bits and f16 11, nothing is rounded but what lies below 2^-17 of that
+      auto as_f16 = [](uint2 v, float inv) {
+        return make_uint2(f16x2(__uint_as_float(v.x << 16) * inv,
+                                __uint_as_float(v.x & 0xffff0000u) * inv),
+                          f16x2(__uint_as_float(v.y << 16) * inv,
+                                __uint_as_float(v.y & 0xffff0000u) * inv));
+      };
+      auto largest = [](uint2 v) {
+        return fmaxf(fmaxf(fabsf(__uint_as_float(v.x << 16)),
+                           fabsf(__uint_as_float(v.x & 0xffff0000u))),
+                     fmaxf(fabsf(__uint_as_float(v.y << 16)),
+                           fabsf(__uint_as_float(v.y & 0xffff0000u))));
+      };
+      // (exponent of the scale, its inverse) for a row's largest value
+      auto scale_of = [](float big, float& mul) {
+        const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253);
+        mul = __uint_as_float(static_cast<uint32_t>(e) << 23);
+        return __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      };
+      if constexpr (KV == MOE_KV_BF16 && C::QREG) {
+        // fragments: rows g and g + 8, columns {2c, 2c+1} and {2c+8, 2c+9} of 16
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int r = g + (j & 1) * 8;
-            const int d = 16 * kk + (KV == MOE_KV_BF16 ? 2 * c4 + (j >> 1) * 8
-                                                       : 4 * c4 + (j >> 1) * 2);
-            uint32_t v = 0;
-            if (r < rows && d < A.dim)
-              v = __ldg(reinterpret_cast<const unsigned int*>(q + r * A.q_h + d));
-            qf[kk][j] = v;
-            if constexpr (KV == MOE_KV_E4M3)
-              big[j & 1] = fmaxf(big[j & 1], fmaxf(fabsf(__uint_as_float(v << 16)),
-                                                   fabsf(__uint_as_float(v & 0xffff0000u))));
+            const int r = g + (j & 1) * 8, d = 16 * kk + 2 * c4 + (j >> 1) * 8;
+            qf[kk][j] = r < rows && d < A.dim
+                               ? __ldg(reinterpret_cast<const unsigned int*>(q + r * A.q_h + d))
+                               : 0u;
           }
         }
-        if constexpr (KV == MOE_KV_E4M3) {
-          // rows of Q as f16: a row is first scaled by a power of two that
-          // brings its largest value into [1, 2).  bf16 has 8 bits, f16 11:
-          // nothing is rounded but what lies below 2^-17 of that value
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            big[j] = fmaxf(big[j], __shfl_xor_sync(0xffffffffu, big[j], 1));
-            big[j] = fmaxf(big[j], __shfl_xor_sync(0xffffffffu, big[j], 2));
-            const int e = min(max(static_cast<int>(__float_as_uint(big[j]) >> 23), 1), 253);
-            q_mul[j] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-          }
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float inv = __uint_as_float(
-                  (254u - (__float_as_uint(q_mul[j & 1]) >> 23)) << 23);
-              const uint32_t v = qf[kk][j];
-              qf[kk][j] = f16x2(__uint_as_float(v << 16) * inv,
-                                __uint_as_float(v & 0xffff0000u) * inv);
-            }
-        }
-      } else {
-        // rows of Q in shared memory: warp w brings rows w, w + NW, ...
+      } else if constexpr (KV == MOE_KV_BF16) {
         for (int r = warp; r < kRows; r += NW) {
-          uint32_t v[DP / 64];
-          float big = 0.0f;
 #pragma unroll
           for (int j = 0; j < DP / 64; ++j) {
             const int d = 2 * (lane + 32 * j);
-            v[j] = 0;
-            if (r < rows && d < A.dim)
-              v[j] = __ldg(reinterpret_cast<const unsigned int*>(q + r * A.q_h + d));
-            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(v[j] << 16)),
-                                   fabsf(__uint_as_float(v[j] & 0xffff0000u))));
+            *reinterpret_cast<uint32_t*>(smem + C::RING + r * C::QP + 2 * d) =
+                r < rows && d < A.dim
+                    ? __ldg(reinterpret_cast<const unsigned int*>(q + r * A.q_h + d))
+                    : 0u;
           }
-          if constexpr (KV == MOE_KV_E4M3) {
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-              big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-            const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253);
-            const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-#pragma unroll
-            for (int j = 0; j < DP / 64; ++j)
-              v[j] = f16x2(__uint_as_float(v[j] << 16) * inv,
-                           __uint_as_float(v[j] & 0xffff0000u) * inv);
-            if (lane == 0) s_q[r] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-          }
-#pragma unroll
-          for (int j = 0; j < DP / 64; ++j)
-            *reinterpret_cast<uint32_t*>(smem + C::RING + r * C::QP + 4 * (lane + 32 * j)) = v[j];
         }
         __syncthreads();
-        if constexpr (KV == MOE_KV_E4M3) {
-          q_mul[0] = s_q[g];
-          q_mul[1] = s_q[g + 8];
+      } else if constexpr (C::QREG) {
+        // keys come as 4 neighbouring codes per lane: lane c's columns of a
+        // step of 16 are 4c .. 4c+3
+        uint2 raw[DP / 16][2];
+        float big[2] = {0.0f, 0.0f}, inv[2];
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = g + j * 8, d = 16 * kk + 4 * c4;
+            raw[kk][j] = r < rows && d < A.dim
+                             ? __ldg(reinterpret_cast<const uint2*>(q + r * A.q_h + d))
+                             : make_uint2(0u, 0u);
+            big[j] = fmaxf(big[j], largest(raw[kk][j]));
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          big[j] = fmaxf(big[j], __shfl_xor_sync(0xffffffffu, big[j], 1));
+          big[j] = fmaxf(big[j], __shfl_xor_sync(0xffffffffu, big[j], 2));
+          inv[j] = scale_of(big[j], q_mul[j]);
+        }
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint2 x = as_f16(raw[kk][j], inv[j]);
+            qf[kk][j] = x.x;
+            qf[kk][2 + j] = x.y;
+          }
+      } else {
+        for (int r = warp; r < kRows; r += NW) {
+          uint2 v[DP / 128];
+          float big = 0.0f, mul;
+#pragma unroll
+          for (int j = 0; j < DP / 128; ++j) {
+            const int d = 4 * (lane + 32 * j);
+            v[j] = r < rows && d < A.dim ? __ldg(reinterpret_cast<const uint2*>(q + r * A.q_h + d))
+                                         : make_uint2(0u, 0u);
+            big = fmaxf(big, largest(v[j]));
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+          const float inv = scale_of(big, mul);
+          if (lane == 0) s_q[r] = mul;
+#pragma unroll
+          for (int j = 0; j < DP / 128; ++j)
+            *reinterpret_cast<uint2*>(smem + C::RING + r * C::QP + 8 * (lane + 32 * j)) =
+                as_f16(v[j], inv);
+        }
+        __syncthreads();
+        q_mul[0] = s_q[g];
+        q_mul[1] = s_q[g + 8];
       }
     }
-    const float f0 = sl * q_mul[0], f1 = sl * q_mul[1];
+    // a logit is f s in base 2; a negative scale turns the sign of s instead,
+    // so that the largest s is the largest logit
+    const bool flip = sl < 0.0f;
+    const float f[2] = {fabsf(sl) * q_mul[0], fabsf(sl) * q_mul[1]};
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.0f;
 #pragma unroll
@@ -588,140 +604,151 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         const uint32_t kb = ring + slot * C::SB, vb = kb + C::KEYS * RB;
         float s[NJ][4];
         if constexpr (KV == MOE_KV_F32) {
-          // 3 products of (hi, lo) pairs; hi * hi and the small ones in sums
-          // of their own, and few terms to a chain: the tensor cores cut,
-          // not round, their sums
-          float hh[NJ][2][4] = {}, hl[NJ][2][4] = {};
+          // 3 products of (hi, lo) pairs; few terms to a chain: the tensor
+          // cores cut, not round, their sums
+          float hh[2][4] = {}, hl[2][4] = {};
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             // lane c's columns of the two k = 8 steps: 4c, 4c+1 and 4c+2, 4c+3
-            const float4 qa = lds4(qs + g * C::QP + (4 * kk + c4) * 16);
-            const float4 qb = lds4(qs + (g + 8) * C::QP + (4 * kk + c4) * 16);
-            uint32_t ah[2][4], al[2][4];
-            split_tf32(qa.x, ah[0][0], al[0][0]);
-            split_tf32(qb.x, ah[0][1], al[0][1]);
-            split_tf32(qa.y, ah[0][2], al[0][2]);
-            split_tf32(qb.y, ah[0][3], al[0][3]);
-            split_tf32(qa.z, ah[1][0], al[1][0]);
-            split_tf32(qb.z, ah[1][1], al[1][1]);
-            split_tf32(qa.w, ah[1][2], al[1][2]);
-            split_tf32(qb.w, ah[1][3], al[1][3]);
+            const uint32_t at = qs + g * C::QP + (4 * kk + c4) * 16;
+            const uint4 ha = lds4(at), hb = lds4(at + 8 * C::QP);
+            const uint4 la = lds4(at + C::QTERM), lb = lds4(at + C::QTERM + 8 * C::QP);
+            const uint4 kv = lds4(kb + chunk_at<RB>(g, 4 * kk + c4, true));
+            const uint32_t ah[2][4] = {{ha.x, hb.x, ha.y, hb.y}, {ha.z, hb.z, ha.w, hb.w}};
+            const uint32_t al[2][4] = {{la.x, lb.x, la.y, lb.y}, {la.z, lb.z, la.w, lb.w}};
+            uint32_t kh[4], kl[4];
+            split_tf32(__uint_as_float(kv.x), kh[0], kl[0]);
+            split_tf32(__uint_as_float(kv.y), kh[1], kl[1]);
+            split_tf32(__uint_as_float(kv.z), kh[2], kl[2]);
+            split_tf32(__uint_as_float(kv.w), kh[3], kl[3]);
+            mma_tf32(hh[0], ah[0], kh[0], kh[1]);
+            mma_tf32(hh[1], ah[1], kh[2], kh[3]);
+            mma_tf32(hl[0], al[0], kh[0], kh[1]);
+            mma_tf32(hl[1], ah[0], kl[0], kl[1]);
+            mma_tf32(hl[0], al[1], kh[2], kh[3]);
+            mma_tf32(hl[1], ah[1], kl[2], kl[3]);
+          }
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const float4 kv = lds4(kb + chunk_at<RB>(8 * j + g, 4 * kk + c4, true));
-              uint32_t h0_, h1_, h2_, h3_, l0_, l1_, l2_, l3_;
-              split_tf32(kv.x, h0_, l0_);
-              split_tf32(kv.y, h1_, l1_);
-              split_tf32(kv.z, h2_, l2_);
-              split_tf32(kv.w, h3_, l3_);
-              mma_tf32(hh[j][0], ah[0], h0_, h1_);
-              mma_tf32(hh[j][1], ah[1], h2_, h3_);
-              mma_tf32(hl[j][0], al[0], h0_, h1_);
-              mma_tf32(hl[j][1], ah[0], l0_, l1_);
-              mma_tf32(hl[j][0], al[1], h2_, h3_);
-              mma_tf32(hl[j][1], ah[1], l2_, l3_);
+          for (int e = 0; e < 4; ++e) s[0][e] = hh[0][e] + hh[1][e] + (hl[0][e] + hl[1][e]);
+        } else if constexpr (KV == MOE_KV_BF16) {
+          float part[2][NJ][4] = {};  // even and odd steps: shorter chains
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            uint32_t qa[4], r[4];
+            if constexpr (C::QREG) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) qa[j] = qf[kk][j];
+            } else {
+              ldsm4(qs + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::QP + (2 * kk + (lane >> 4)) * 16,
+                    qa);
+            }
+            ldsm4(kb + chunk_at<RB>((lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1), true),
+                  r);
+            mma_bf16(part[kk & 1][0], qa, r[0], r[1]);
+            mma_bf16(part[kk & 1][1], qa, r[2], r[3]);
+          }
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = part[0][j][e] + part[1][j][e];
+        } else {
+          float part[2][NJ][4] = {};  // even and odd steps: shorter chains
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; kk += 2) {
+            uint32_t qa[2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if constexpr (C::QREG) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qa[t][j] = qf[kk + t][j];
+              } else {
+                const uint32_t at = qs + g * C::QP + (4 * (kk + t) + c4) * 8;
+                const uint2 a = lds2(at), b = lds2(at + 8 * C::QP);
+                qa[t][0] = a.x;
+                qa[t][1] = b.x;
+                qa[t][2] = a.y;
+                qa[t][3] = b.y;
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < C::KEYS / 16; ++h) {
+              // x4: chunks kk and kk + 1 (16 columns each) of 16 keys
+              uint32_t r[4], lo, hi;
+              ldsm4(kb + chunk_at<RB>(16 * h + (lane & 7) + ((lane >> 3) & 1) * 8, kk + (lane >> 4),
+                                      true),
+                    r);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                e4m3x4_f16x4(r[j], lo, hi);
+                mma_f16(part[j >> 1][2 * h + (j & 1)], qa[j >> 1], lo, hi);
+              }
             }
           }
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[j][e] = hh[j][0][e] + hh[j][1][e] + (hl[j][0][e] + hl[j][1][e]);
-        } else {
-          float part[2][2][4] = {};  // even and odd steps: shorter chains
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
-            uint32_t qa[4];
-            if constexpr (C::QREG) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) qa[j] = qf[kk][j];
-            } else if constexpr (KV == MOE_KV_BF16) {
-              ldsm4(qs + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::QP + (2 * kk + (lane >> 4)) * 16,
-                    qa);
-            } else {
-              const uint2 a = lds2(qs + g * C::QP + (4 * kk + c4) * 8);
-              const uint2 b = lds2(qs + (g + 8) * C::QP + (4 * kk + c4) * 8);
-              qa[0] = a.x;
-              qa[1] = b.x;
-              qa[2] = a.y;
-              qa[3] = b.y;
-            }
-            if constexpr (KV == MOE_KV_BF16) {
-              uint32_t r[4];
-              ldsm4(kb + chunk_at<RB>((lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1), true),
-                    r);
-              mma_bf16(part[kk & 1][0], qa, r[0], r[1]);
-              mma_bf16(part[kk & 1][1], qa, r[2], r[3]);
-            } else {
-              // one x4 load brings the 16-byte chunks kk and kk + 1 of 16 keys
-              static_assert(DP % 32 == 0, "E4M3 steps come in pairs");
-              if (kk % 2 == 0) {
-                uint32_t r[4], qn[4];
-                ldsm4(kb + chunk_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, kk + (lane >> 4), true),
-                      r);
-                mma_f16(part[0][0], qa, e4m3x2_f16x2(r[0]), e4m3x2_f16x2_hi(r[0]));
-                mma_f16(part[0][1], qa, e4m3x2_f16x2(r[1]), e4m3x2_f16x2_hi(r[1]));
-                if constexpr (C::QREG) {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) qn[j] = qf[kk + 1][j];
-                } else {
-                  const uint2 a = lds2(qs + g * C::QP + (4 * kk + 4 + c4) * 8);
-                  const uint2 b = lds2(qs + (g + 8) * C::QP + (4 * kk + 4 + c4) * 8);
-                  qn[0] = a.x;
-                  qn[1] = b.x;
-                  qn[2] = a.y;
-                  qn[3] = b.y;
-                }
-                mma_f16(part[1][0], qn, e4m3x2_f16x2(r[2]), e4m3x2_f16x2_hi(r[2]));
-                mma_f16(part[1][1], qn, e4m3x2_f16x2(r[3]), e4m3x2_f16x2_hi(r[3]));
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
             for (int e = 0; e < 4; ++e) s[j][e] = part[0][j][e] + part[1][j][e];
         }
-        // masked keys out (their rows hold zeros), then the running softmax:
-        // rows g (e = 0, 1) and g + 8 (e = 2, 3), keys 8 j + 2 c + (e & 1)
+        // the running softmax: rows g (e = 0, 1) and g + 8 (e = 2, 3), keys
+        // 8 j + 2 c + (e & 1); masked keys (their rows hold zeros) are left out
+        if (flip) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = -s[j][e];
+        }
+        if (mask != kAll) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((mask >> (8 * j + 2 * c4 + (e & 1))) & 1u)) s[j][e] = -INFINITY;
+        }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool live = (mask >> (8 * j + 2 * c4 + (e & 1))) & 1u;
-            s[j][e] = live ? s[j][e] * (e < 2 ? f0 : f1) : -INFINITY;
-            top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
-          }
-        float keep[2];
+          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[j][e]);
+        bool grow = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
           top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-          const float now = fmaxf(m[r], top[r]);
-          // a maximum of -inf (every logit is -inf so far) stands for 0
-          keep[r] = now == -INFINITY ? 1.0f : ex2(m[r] - now);
-          m[r] = now;
+          // (-inf: every key of the row is masked here, or its logit is -inf)
+          top[r] = top[r] == -INFINITY ? -INFINITY : top[r] * f[r];
+          grow = grow || top[r] > m[r] + 8.0f;
         }
-        const float z0 = m[0] == -INFINITY ? 0.0f : m[0], z1 = m[1] == -INFINITY ? 0.0f : m[1];
-        float sum[2] = {0.0f, 0.0f};
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (top[r] > m[r] + 8.0f) {
+              const float keep = ex2(m[r] - top[r]);
+              m[r] = top[r];
+              l[r] *= keep;
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                acc[i][2 * r] *= keep;
+                acc[i][2 * r + 1] *= keep;
+              }
+            }
+          }
+        }
+        const float z[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[j][e] = ex2(s[j][e] - (e < 2 ? z0 : z1));
-            sum[e >> 1] += s[j][e];
-          }
-        l[0] = l[0] * keep[0] + sum[0];
-        l[1] = l[1] * keep[1] + sum[1];
-        if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+          for (int e = 0; e < 4; ++e) s[j][e] = ex2(fmaf(s[j][e], f[e >> 1], -z[e >> 1]));
+        if (mask != kAll) {
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            acc[i][0] *= keep[0];
-            acc[i][1] *= keep[0];
-            acc[i][2] *= keep[1];
-            acc[i][3] *= keep[1];
-          }
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((mask >> (8 * j + 2 * c4 + (e & 1))) & 1u)) s[j][e] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          l[0] += s[j][0] + s[j][1];
+          l[1] += s[j][2] + s[j][3];
         }
         // ---- O += P V
         if constexpr (KV == MOE_KV_BF16) {
@@ -748,59 +775,62 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         } else if constexpr (KV == MOE_KV_E4M3) {
           // P rounded to f16: 2^-12 of each weight, as against the 2^-4 of
           // the cached values themselves
-          uint32_t p[4];
+          uint32_t pt[C::KEYS / 16][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            p[j] = f16x2(s[j >> 1][(j & 1) * 2], s[j >> 1][(j & 1) * 2 + 1]);
+          for (int h = 0; h < C::KEYS / 16; ++h)
 #pragma unroll
-          for (int dd = 0; dd < DP / 32; ++dd) {
-            // x4: keys 0..7 and 8..15 of chunks 2 dd and 2 dd + 1; a register
-            // holds codes (d, d+1) of keys 2c and 2c + 1, d = 2g: bytes 0 and
-            // 2 are column d of both keys, bytes 1 and 3 column d + 1
-            uint32_t r[4];
-            ldsm4t(vb + chunk_at<RB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * dd + (lane >> 4), true),
+            for (int j = 0; j < 4; ++j) {
+              const float* const x = s[2 * h + (j >> 1)] + (j & 1) * 2;
+              pt[h][j] = f16x2(x[0], x[1]);
+            }
+          // x4: 16 columns of keys 0..7, 8..15, 16..23 and 24..31 (of 16 keys: two
+          // times 16 columns).  A register holds codes (d, d+1), d = 2g, of keys
+          // 2c and 2c + 1 of its 8: bytes 0 and 2 are column d of both keys,
+          // bytes 1 and 3 column d + 1
+          constexpr int kHalves = C::KEYS / 16;
+#pragma unroll
+          for (int ch = 0; ch < DP / 16; ch += 3 - kHalves) {
+            uint32_t r[4], e[4], o[4];
+            ldsm4t(vb + (kHalves == 2 ? chunk_at<RB>(lane, ch, true)
+                                      : chunk_at<RB>(lane & 15, ch + (lane >> 4), true)),
                    r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = __byte_perm(r[j], 0, 0x3120);
-            mma_f16(acc[4 * dd], p, e4m3x2_f16x2(r[0]), e4m3x2_f16x2(r[1]));
-            mma_f16(acc[4 * dd + 1], p, e4m3x2_f16x2_hi(r[0]), e4m3x2_f16x2_hi(r[1]));
-            mma_f16(acc[4 * dd + 2], p, e4m3x2_f16x2(r[2]), e4m3x2_f16x2(r[3]));
-            mma_f16(acc[4 * dd + 3], p, e4m3x2_f16x2_hi(r[2]), e4m3x2_f16x2_hi(r[3]));
+            for (int j = 0; j < 4; ++j) e4m3x4_f16x4(__byte_perm(r[j], 0, 0x3120), e[j], o[j]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int at = 2 * (kHalves == 2 ? ch : ch + h);
+              mma_f16(acc[at], pt[kHalves == 2 ? h : 0], e[2 * h], e[2 * h + 1]);
+              mma_f16(acc[at + 1], pt[kHalves == 2 ? h : 0], o[2 * h], o[2 * h + 1]);
+            }
           }
         } else {
-          // step j takes keys 8 j ..: lane c's two are 8 j + 2 c and + 1, the
-          // very ones whose weights it holds
-          uint32_t ph[NJ][4], pl[NJ][4];
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            split_tf32(s[j][0], ph[j][0], pl[j][0]);
-            split_tf32(s[j][2], ph[j][1], pl[j][1]);
-            split_tf32(s[j][1], ph[j][2], pl[j][2]);
-            split_tf32(s[j][3], ph[j][3], pl[j][3]);
-          }
+          // lane c's two keys are 2c and 2c + 1, the very ones whose weights it
+          // holds
+          uint32_t ph[4], pl[4];
+          split_tf32(s[0][0], ph[0], pl[0]);
+          split_tf32(s[0][2], ph[1], pl[1]);
+          split_tf32(s[0][1], ph[2], pl[2]);
+          split_tf32(s[0][3], ph[3], pl[3]);
 #pragma unroll
           for (int dd = 0; dd < DP / 32; ++dd) {
-            float o[4][4] = {}, o2[4][4] = {};
+            float o[4][4] = {};
+            const uint4 a = lds4(vb + chunk_at<RB>(2 * c4, 8 * dd + g, false));
+            const uint4 b = lds4(vb + chunk_at<RB>(2 * c4 + 1, 8 * dd + g, false));
+            const uint32_t va[4] = {a.x, a.y, a.z, a.w}, vb4[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const float4 a = lds4(vb + chunk_at<RB>(8 * j + 2 * c4, 8 * dd + g, false));
-              const float4 b = lds4(vb + chunk_at<RB>(8 * j + 2 * c4 + 1, 8 * dd + g, false));
-              const float va[4] = {a.x, a.y, a.z, a.w}, vb4[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                uint32_t ah, al, bh, bl;
-                split_tf32(va[t], ah, al);
-                split_tf32(vb4[t], bh, bl);
-                mma_tf32(o[t], ph[j], ah, bh);
-                mma_tf32(o2[t], pl[j], ah, bh);
-                mma_tf32(o2[t], ph[j], al, bl);
-              }
+            for (int t = 0; t < 4; ++t) {
+              uint32_t ah, al, bh, bl;
+              split_tf32(__uint_as_float(va[t]), ah, al);
+              split_tf32(__uint_as_float(vb4[t]), bh, bl);
+              mma_tf32(o[t], pl, ah, bh);
+              mma_tf32(o[t], ph, al, bl);
+              mma_tf32(o[t], ph, ah, bh);
             }
             // the long sum over tiles in rounded fp32 additions
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[4 * dd + t][e] += o[t][e] + o2[t][e];
+              for (int e = 0; e < 4; ++e) acc[4 * dd + t][e] += o[t][e];
           }
         }
       }
@@ -828,10 +858,10 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
     const long long part = 2ll * cta + (t_first == 0 ? 0 : 1);
     constexpr int PASSES = DP / C::JC;
     float* const dump = reinterpret_cast<float*>(smem + (warp * ST + slot) * C::SB);
+    __syncwarp();  // every lane is done with the stage
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       if (p > 0) __syncthreads();
-      __syncwarp();  // every lane is done with the stage
 #pragma unroll
       for (int i = p * (NT / PASSES); i < (p + 1) * (NT / PASSES); ++i)
 #pragma unroll
@@ -844,7 +874,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         }
       __syncthreads();
       for (int i = threadIdx.x; i < rows * (C::JC / 4); i += C::THREADS) {
-        const int r = i / (C::JC / 4), d = i % (C::JC / 4) * 4;
+        const int r = i / (C::JC / 4), d = i % (C::JC / 4) * 4 + p * C::JC;
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w][r]);
@@ -852,27 +882,26 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-          const float f = top == -INFINITY ? 1.0f : ex2(s_m[w][r] - top);
+          const float k = top == -INFINITY ? 1.0f : ex2(s_m[w][r] - top);
           const float4 x = *reinterpret_cast<const float4*>(
-              smem + (w * ST + slot) * C::SB + (r * C::JC + d) * 4);
-          sum += f * s_l[w][r];
-          o.x += f * x.x;
-          o.y += f * x.y;
-          o.z += f * x.z;
-          o.w += f * x.w;
+              smem + (w * ST + slot) * C::SB + (r * C::JC + d - p * C::JC) * 4);
+          sum += k * s_l[w][r];
+          o.x += k * x.x;
+          o.y += k * x.y;
+          o.z += k * x.z;
+          o.w += k * x.w;
         }
-        const int dd = d + p * C::JC;
         if (whole) {
           const float inv = sum == 0.0f ? 0.0f : v_mul / sum;
-          if (dd < A.dim)
-            store4<KV>(A.out, cc.b * A.o_b + (h0 + r) * A.o_h + dd,
+          if (d < A.dim)
+            store4<KV>(A.out, cc.b * A.o_b + (h0 + r) * A.o_h + d,
                        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-          if (dd == 0 && A.lse)
+          if (d == 0 && A.lse)
             A.lse[static_cast<long long>(cc.b) * A.Hq + h0 + r] =
                 sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         } else {
-          *reinterpret_cast<float4*>(A.part_o + (part * kRows + r) * DP + dd) = o;
-          if (dd == 0) A.part_ml[part * kRows + r] = make_float2(top, sum);
+          *reinterpret_cast<float4*>(A.part_o + (part * kRows + r) * DP + d) = o;
+          if (d == 0) A.part_ml[part * kRows + r] = make_float2(top, sum);
         }
       }
     }
