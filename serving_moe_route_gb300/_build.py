@@ -1,7 +1,9 @@
 """Build step for the CUDA library: nvcc for sm_103a, in-tree.
 
 ``build()`` compiles ``csrc/*.cu`` (one translation unit each, in parallel) and
-links ``_lib/libmoe_route.so``.  The objects go to ``_build/``.
+links ``_lib/libmoe_route.so``, and with g++ the Python calls of the decode-step
+operators (``csrc/decode_ext.cpp``, against PyTorch's headers) into an extension
+module beside it.  The objects go to ``_build/``.
 """
 from __future__ import annotations
 
@@ -9,6 +11,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -19,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_route.so")
+EXT_SRC = os.path.join(CSRC, "decode_ext.cpp")
+EXT_PATH = os.path.join(LIB_DIR, "moe_decode_ext" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -40,10 +45,25 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return all(os.path.getmtime(p) <= t for p in _deps()) and \
+        os.path.getmtime(EXT_SRC) <= os.path.getmtime(EXT_PATH)
+
+
+def _torch_flags():
+    """Include, define and link flags for PyTorch's headers and libraries."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    return ["-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+            "-I", os.path.join(cuda, "include"),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"], [
+                "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+                f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -64,8 +84,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=4) as ex:
+    torch_cc, torch_ld = _torch_flags()
+
+    def compile_ext():
+        obj = os.path.join(BUILD_DIR, "decode_ext.o")
+        r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", *torch_cc, "-c", EXT_SRC, "-o", obj],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {EXT_SRC}:\n{r.stderr}")
+        return obj
+
+    with ThreadPoolExecutor(max_workers=8) as ex:
+        ext = ex.submit(compile_ext)
         results = list(ex.map(compile_one, _sources()))
+        ext_obj = ext.result()
     objs = [o for o, _ in results]
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
     os.close(fd)
@@ -76,6 +108,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.unlink(tmp)
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
+    os.close(fd)
+    cmd = ["g++", "-shared", "-o", tmp, ext_obj, "-L", LIB_DIR, "-lmoe_route",
+           "-Wl,-rpath,$ORIGIN", *torch_ld]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        os.unlink(tmp)
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, EXT_PATH)
     if verbose:
         for _, log in results:
             print(log)
