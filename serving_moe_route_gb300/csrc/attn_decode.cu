@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   __shared__ long long s_sum[NW];
   __shared__ int s_b;
   __shared__ long long s_off;
+  __shared__ int2 s_span;
   __shared__ uint32_t s_mask[NW][ST];
   __shared__ float s_m[NW][kRows], s_l[NW][kRows], s_q[kRows];
   constexpr uint32_t kAll = 0xffffffffu >> (32 - C::KEYS);  // a mask of live keys
@@ -285,7 +286,11 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   const int per = (A.B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(A.B, static_cast<int>(threadIdx.x) * per), b1 = min(A.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of(span_of(A, b, cut), C::TILE) + C::END;
+  int2 last = make_int2(0, 0);
+  for (int b = b0; b < b1; ++b) {
+    last = span_of(A, b, cut);
+    mine += tiles_of(last, C::TILE) + C::END;
+  }
   long long incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -313,13 +318,15 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
     if (begin >= lo && begin < hi) {
       long long at = lo;
       int b = b0;
-      for (;; ++b) {
-        const long long n =
-            static_cast<long long>(tiles_of(span_of(A, b, cut), C::TILE) + C::END) * units;
+      int2 s = last;  // of the only request, where it is one
+      for (; per > 1; ++b) {
+        s = span_of(A, b, cut);
+        const long long n = static_cast<long long>(tiles_of(s, C::TILE) + C::END) * units;
         if (begin < at + n) break;
         at += n;
       }
       s_b = b;
+      s_span = s;
       s_off = begin - at;
     }
   }
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   Cursor cc;
   cc.b = s_b;
   {
-    const int2 s = span_of(A, cc.b, cut);
+    const int2 s = s_span;
     cc.first = s.x;
     cc.len = s.y;
     cc.nt = tiles_of(s, C::TILE);

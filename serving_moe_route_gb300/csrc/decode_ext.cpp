@@ -255,6 +255,15 @@ PyObject* entry(Py_ssize_t n, Py_ssize_t want, F f) {
   return nullptr;
 }
 
+// n elements of a buffer, from `at` on, as a tensor of its own
+Tensor cut(const Tensor& buffer, int64_t at, int64_t n) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()),
+                                                      buffer.key_set(), buffer.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 int32_t* i32(const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
 
 // (ctx_lens, new_lens, block_table, free_pages, n_free, page_size, num_pages,
@@ -276,11 +285,12 @@ PyObject* kv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     tokens = integer(a[7], "max_tokens");
     if (tokens < 0) refuse("max_tokens must not be negative");
     if (B > INT32_MAX || cap > INT32_MAX || t.width > INT32_MAX) refuse("sizes must fit 32 bits");
-    const Tensor slots = at_.make({tokens}, at::kInt), positions = at_.make({tokens}, at::kInt),
-                 starts = at_.make({B + 1}, at::kInt), lens = at_.make({B}, at::kInt);
+    const Tensor all = at_.make({2 * tokens + 2 * B + 2}, at::kInt);
+    const Tensor slots = cut(all, 0, tokens), positions = cut(all, tokens, tokens),
+                 starts = cut(all, 2 * tokens, B + 1), lens = cut(all, 2 * tokens + B + 1, B);
     Tensor out;
     if (a[8] == Py_None) {
-      out = at_.make({1}, at::kInt);
+      out = cut(all, 2 * tokens + 2 * B + 1, 1);
     } else {
       out = tensor(a[8], "n_free_out");
       vec(out, at::kInt, 1, "n_free_out", dev);

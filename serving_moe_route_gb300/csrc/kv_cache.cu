@@ -66,7 +66,7 @@ struct StepArgs {
   int *slots, *positions, *starts, *seq_lens;
   unsigned* err;
   long long table_stride;
-  int B, max_pages, free_cap, num_pages, page, max_tokens;
+  int B, max_pages, free_cap, num_pages, page, page_shift, max_tokens;
 };
 
 __device__ __forceinline__ int cut_int(long long v) {
@@ -74,7 +74,7 @@ __device__ __forceinline__ int cut_int(long long v) {
 }
 
 // last index r with a[r] <= i (a ascending, a[0] == 0 <= i)
-__device__ __forceinline__ int last_at_most(const int* a, int n, long long i) {
+__device__ __forceinline__ int last_at_most(const int* a, int n, int i) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -84,50 +84,58 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, long long i) {
   return lo;
 }
 
-// One cluster of 1 .. 8 CTAs.  Every CTA scans the requests' new tokens and
-// new pages for itself (two exclusive sums, at most 8 steps of 1024
-// requests) and keeps them in shared memory; then the token rows and the new
-// table entries are dealt out over all threads, each of which finds its
-// request by bisection.  A new page's id is taken straight from the free
-// list by its rank, so no thread waits for another's table entry.  Bound by
-// latency (a few dependent loads): more CTAs than one only serve steps with
-// thousands of token rows.
-__global__ void __launch_bounds__(kStepThreads) kv_step_kernel(const StepArgs A) {
+// Every CTA scans the requests' new tokens and new pages for itself (two
+// exclusive sums, at most 8 steps of 1024 requests) and keeps them in shared
+// memory; then the token rows and the new table entries are dealt out over
+// all threads, each of which finds its request by bisection.  A new page's id
+// is taken straight from the free list by its rank, so no thread waits for
+// another's table entry.  Bound by latency (a few dependent loads).  If
+// n_free_out is n_free_in, the CTAs are one cluster and all read it before one
+// writes it; else there may be any number of them.
+__global__ void __launch_bounds__(kStepThreads) kv_step_kernel(const StepArgs A, bool cluster) {
   extern __shared__ int step_smem[];
-  int* const start = step_smem;         // [B] first token row
-  int* const base = step_smem + A.B;    // [B] rank of the first new page
+  int* const start = step_smem;           // [B] first token row
+  int* const base = step_smem + A.B;      // [B] rank of the first new page
+  int* const ctx = step_smem + 2 * A.B;   // [B]
   __shared__ long long sums[64];
   pdl_wait();
   const int tid = threadIdx.x, cta = blockIdx.x, nthreads = kStepThreads * gridDim.x;
   const int n_free = max(0, min(*A.n_free_in, A.free_cap));
-  const int P = A.page, W = A.max_pages;
+  const int W = A.max_pages;
+  const unsigned P = A.page;
+  // below 2^32: a context and its new tokens both fit an int
+  auto page_of = [&](unsigned pos) { return A.page_shift >= 0 ? pos >> A.page_shift : pos / P; };
+  auto pages_for = [&](unsigned n) {
+    return n ? min(page_of(n - 1) + 1u, static_cast<unsigned>(W)) : 0u;
+  };
   unsigned bad = 0;
   long long tokens = 0, pages = 0;
   for (int r0 = 0; r0 < A.B; r0 += kStepThreads) {
     const int r = r0 + tid;
-    long long c = 0, n = 0, take = 0;
+    int c = 0, n = 0, take = 0;
     if (r < A.B) {
       c = max(A.ctx[r], 0);
       n = max(A.nw[r], 0);
-      const long long need = (c + n + P - 1) / P;
-      take = min(need, static_cast<long long>(W)) - min((c + P - 1) / P, static_cast<long long>(W));
-      if (need > W && n > 0) bad |= MOE_DEVERR_NO_SPACE;
+      const unsigned all = static_cast<unsigned>(c) + static_cast<unsigned>(n);
+      take = static_cast<int>(pages_for(all) - pages_for(c));
+      if (n > 0 && page_of(all - 1) >= static_cast<unsigned>(W)) bad |= MOE_DEVERR_NO_SPACE;
     }
     long long ex_t, ex_p, tot_t, tot_p;
     scan2(n, take, sums, ex_t, ex_p, tot_t, tot_p);
     if (r < A.B) {
       start[r] = cut_int(tokens + ex_t);
       base[r] = cut_int(pages + ex_p);
+      ctx[r] = c;
       if (cta == 0) {
         A.starts[r] = start[r];
-        A.seq_lens[r] = cut_int(c + n);
+        A.seq_lens[r] = cut_int(static_cast<long long>(c) + n);
       }
     }
     tokens += tot_t;
     pages += tot_p;
   }
   __syncthreads();
-  if (gridDim.x > 1) cluster_sync();  // every CTA has read n_free_in: it may be n_free_out
+  if (cluster) cluster_sync();
   if (cta == 0 && tid == 0) {
     A.starts[A.B] = cut_int(tokens);
     *A.n_free_out = static_cast<int>(max(0ll, n_free - pages));
@@ -136,21 +144,19 @@ __global__ void __launch_bounds__(kStepThreads) kv_step_kernel(const StepArgs A)
   // the page of rank `rank` among the new ones, -1 where there is none
   auto fresh = [&](long long rank) {
     if (rank >= n_free) return -1;
-    const int id = A.free_pages[n_free - 1 - rank];
+    const int id = __ldg(A.free_pages + (n_free - 1 - rank));
     if (id >= 0 && id < A.num_pages) return id;
     bad |= MOE_DEVERR_BAD_PAGE;
     return -1;
   };
-  for (long long i = static_cast<long long>(cta) * kStepThreads + tid; i < A.max_tokens;
-       i += nthreads) {
+  for (int i = cta * kStepThreads + tid; i < A.max_tokens; i += nthreads) {
     int slot = -1, pos = 0;
     if (i < tokens) {
       const int r = last_at_most(start, A.B, i);
-      const long long c = max(A.ctx[r], 0);
-      const long long p = c + i - start[r];
-      const long long col = p / P, have = min((c + P - 1) / P, static_cast<long long>(W));
+      const unsigned c = ctx[r], p = c + static_cast<unsigned>(i - start[r]), col = page_of(p);
       pos = cut_int(p);
-      if (col < W) {
+      if (col < static_cast<unsigned>(W)) {
+        const unsigned have = pages_for(c);
         int id;
         if (col < have) {
           id = A.table[r * A.table_stride + col];
@@ -159,18 +165,18 @@ __global__ void __launch_bounds__(kStepThreads) kv_step_kernel(const StepArgs A)
             bad |= MOE_DEVERR_BAD_PAGE;
           }
         } else {
-          id = fresh(base[r] + col - have);
+          id = fresh(static_cast<long long>(base[r]) + col - have);
         }
-        if (id >= 0) slot = id * P + static_cast<int>(p - col * P);
+        if (id >= 0) slot = id * static_cast<int>(P) + static_cast<int>(p - col * P);
       }
     }
     A.slots[i] = slot;
     A.positions[i] = pos;
+    if (i > INT_MAX - nthreads) break;
   }
   for (long long i = static_cast<long long>(cta) * kStepThreads + tid; i < pages; i += nthreads) {
-    const int r = last_at_most(base, A.B, i);
-    const long long c = max(A.ctx[r], 0);
-    const long long col = min((c + P - 1) / P, static_cast<long long>(W)) + i - base[r];
+    const int r = last_at_most(base, A.B, cut_int(i));
+    const long long col = static_cast<long long>(pages_for(ctx[r])) + i - base[r];
     A.table[r * A.table_stride + col] = fresh(i);
   }
   if (bad && A.err) atomicOr(A.err, bad);
@@ -240,49 +246,60 @@ struct AppendArgs {
   bool vec;  // source rows are 16-byte aligned
 };
 
-// 16 bytes of one cached vector per thread (blockIdx.y: keys, values); bound
-// by its bytes: a source vector is read once and a cached one written once.
-template <int KV>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs A) {
+// 16 bytes of cached vectors per thread and step (blockIdx.y: keys, values), U
+// steps with all their loads before the first store; bound by its bytes: a
+// source vector is read once and a cached one written once.
+constexpr int kAppendThreads = 256;
+template <int KV, int U>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs A) {
   constexpr int ES = kv_esize(KV), QS = KV == MOE_KV_F32 ? 4 : 2;
   constexpr int VE = 16 / ES;            // elements per thread
   constexpr int LD = VE * QS / 16;       // 16-byte source loads
   pdl_wait();
   const int which = blockIdx.y;
-  const int per_head = A.dim / VE;
+  const unsigned per_head = A.dim / VE;
   const unsigned per_token = static_cast<unsigned>(A.heads) * per_head;
   const long long total = static_cast<long long>(A.N) * per_token;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const long long t = i / per_token;
-    const unsigned in = static_cast<unsigned>(i - t * per_token);
-    const unsigned h = in / per_head, c = in - h * per_head;
-    const int slot = A.slots[t];
-    if (slot < 0) {
-      if (slot != -1 && A.err && in == 0) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
-      continue;
-    }
-    const int pg = slot / A.page;
-    if (pg >= A.num_pages) {
-      if (A.err && in == 0) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
-      continue;
-    }
-    const char* s = A.src[which] + t * A.src_t[which] + h * A.src_h[which] +
-                    static_cast<size_t>(c) * VE * QS;
-    uint4 raw[LD];
-    if (A.vec) {
+  const long long i0 = static_cast<long long>(blockIdx.x) * kAppendThreads * U + threadIdx.x;
+  unsigned h[U], c[U];
+  int slot[U];
+  uint4 raw[U][LD];
 #pragma unroll
-      for (int j = 0; j < LD; ++j) raw[j] = __ldg(reinterpret_cast<const uint4*>(s) + j);
-    } else {
-      using ET = typename std::conditional<QS == 4, uint32_t, uint16_t>::type;
-      ET* e = reinterpret_cast<ET*>(raw);
+  for (int u = 0; u < U; ++u) {
+    const long long i = i0 + u * kAppendThreads;
+    slot[u] = -1;
+    if (i < total) {
+      // 32-bit division where it does
+      const long long t = total <= UINT_MAX ? static_cast<unsigned>(i) / per_token : i / per_token;
+      const unsigned in = static_cast<unsigned>(i - t * per_token);
+      h[u] = in / per_head;
+      c[u] = in - h[u] * per_head;
+      slot[u] = __ldg(A.slots + t);
+      const char* s = A.src[which] + t * A.src_t[which] + h[u] * A.src_h[which] +
+                      static_cast<size_t>(c[u]) * VE * QS;
+      if (A.vec) {
 #pragma unroll
-      for (int j = 0; j < VE; ++j) e[j] = __ldg(reinterpret_cast<const ET*>(s) + j);
+        for (int j = 0; j < LD; ++j) raw[u][j] = __ldg(reinterpret_cast<const uint4*>(s) + j);
+      } else {
+        using ET = typename std::conditional<QS == 4, uint32_t, uint16_t>::type;
+        ET* e = reinterpret_cast<ET*>(raw[u]);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) e[j] = __ldg(reinterpret_cast<const ET*>(s) + j);
+      }
+      if (slot[u] != -1 && (slot[u] < 0 || slot[u] / A.page >= A.num_pages)) {
+        slot[u] = -1;
+        if (A.err && in == 0) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
+      }
     }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (slot[u] < 0) continue;
+    const int pg = slot[u] / A.page;
     uint4 out;
     if constexpr (KV == MOE_KV_E4M3) {
-      const float sc = A.scale[which][h];
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+      const float sc = __ldg(A.scale[which] + h[u]);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(raw[u]);
       __nv_fp8x2_storage_t q[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -293,12 +310,25 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs A) {
       }
       out = *reinterpret_cast<const uint4*>(q);
     } else {
-      out = raw[0];
+      out = raw[u][0];
     }
-    char* d = A.dst[which] + pg * A.dst_page + (slot - pg * A.page) * A.dst_t + h * A.dst_h +
-              static_cast<size_t>(c) * 16;
+    char* d = A.dst[which] + pg * A.dst_page + (slot[u] - pg * A.page) * A.dst_t +
+              h[u] * A.dst_h + static_cast<size_t>(c[u]) * 16;
     *reinterpret_cast<uint4*>(d) = out;
   }
+}
+
+template <int KV>
+static cudaError_t launch_append(const AppendArgs& a, long long items, cudaStream_t st) {
+  // four steps a thread once that leaves two CTAs for each SM (16384 tokens of
+  // 8 heads of 128, bf16: APPEND_FIG)
+  constexpr int U = 4;
+  const long long one = (items + kAppendThreads - 1) / kAppendThreads;
+  if (one < 152ll * 2 * U)
+    return launch_chained(kv_append_kernel<KV, 1>, dim3(static_cast<unsigned>(one), 2),
+                          dim3(kAppendThreads), 0, st, a);
+  return launch_chained(kv_append_kernel<KV, U>, dim3(static_cast<unsigned>((one + U - 1) / U), 2),
+                        dim3(kAppendThreads), 0, st, a);
 }
 
 int kv_cache_ok(const moe_kv_cache_t* c) {
@@ -338,21 +368,31 @@ int moe_kv_step(const int32_t* ctx_lens, const int32_t* new_lens, int B, int32_t
   if (B > 0 && (!ctx_lens || !new_lens || !block_table || !seq_lens)) return MOE_ERR_INVALID_ARG;
   if (max_tokens > 0 && (!slots || !positions)) return MOE_ERR_INVALID_ARG;
   if (free_capacity > 0 && !free_pages) return MOE_ERR_INVALID_ARG;
-  StepArgs a = {ctx_lens, new_lens, block_table, free_pages, n_free_in, n_free_out, slots,
-                positions, starts, seq_lens, err, table_stride, B, max_pages, free_capacity,
-                num_pages, page_size, max_tokens};
-  // one CTA deals out about 2048 token rows; eight is the largest cluster
-  // that every GPU of this kind takes
+  int shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) shift = i;
+  const StepArgs a = {ctx_lens, new_lens, block_table, free_pages, n_free_in, n_free_out, slots,
+                      positions, starts, seq_lens, err, table_stride, B, max_pages, free_capacity,
+                      num_pages, page_size, shift, max_tokens};
+  // a token row a thread, up to the eight CTAs that every GPU of this kind
+  // takes as a cluster, or 64 where none is needed (32768 rows: 4.1 us with 32
+  // CTAs)
+  const bool in_place = n_free_in == n_free_out;
+  const long long want = (static_cast<long long>(max_tokens) + kStepThreads - 1) / kStepThreads;
   int ctas = 1;
-  while (ctas < 8 && max_tokens > 2048ll * ctas) ctas *= 2;
-  const size_t smem = static_cast<size_t>(B) * 2 * sizeof(int);
+  if (in_place)
+    while (ctas < 8 && want > ctas) ctas *= 2;
+  else
+    ctas = static_cast<int>(want < 1 ? 1 : want < 64 ? want : 64);
+  const size_t smem = static_cast<size_t>(B) * 3 * sizeof(int);
   static std::atomic<uint64_t> done{0};
   if (smem > 32 * 1024 &&
       allow_smem(reinterpret_cast<const void*>(kv_step_kernel),
-                 MOE_KV_MAX_REQUESTS * 2 * static_cast<int>(sizeof(int)), done) != cudaSuccess)
+                 MOE_KV_MAX_REQUESTS * 3 * static_cast<int>(sizeof(int)), done) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return launch_cluster(kv_step_kernel, dim3(ctas), dim3(kStepThreads), ctas, smem,
-                        static_cast<cudaStream_t>(stream), a) == cudaSuccess
+  const bool cluster = in_place && ctas > 1;
+  return launch_cluster(kv_step_kernel, dim3(ctas), dim3(kStepThreads), cluster ? ctas : 1, smem,
+                        static_cast<cudaStream_t>(stream), a, cluster) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -412,16 +452,11 @@ int moe_kv_append(const moe_kv_cache_t* cache, const void* k, long long k_stride
   a.page = cache->page_size;
   a.num_pages = cache->num_pages;
   const long long items = static_cast<long long>(N) * a.heads * (a.dim * es / 16);
-  const long long blocks = (items + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)), 2);
+  if (items / (4 * kAppendThreads) >= INT_MAX) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (cache->kv_dtype == MOE_KV_F32)
-    e = launch_chained(kv_append_kernel<MOE_KV_F32>, grid, dim3(256), 0, st, a);
-  else if (cache->kv_dtype == MOE_KV_BF16)
-    e = launch_chained(kv_append_kernel<MOE_KV_BF16>, grid, dim3(256), 0, st, a);
-  else
-    e = launch_chained(kv_append_kernel<MOE_KV_E4M3>, grid, dim3(256), 0, st, a);
+  const cudaError_t e = cache->kv_dtype == MOE_KV_F32    ? launch_append<MOE_KV_F32>(a, items, st)
+                        : cache->kv_dtype == MOE_KV_BF16 ? launch_append<MOE_KV_BF16>(a, items, st)
+                                                         : launch_append<MOE_KV_E4M3>(a, items, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
