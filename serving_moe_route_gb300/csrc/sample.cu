@@ -107,6 +107,13 @@ __device__ __forceinline__ float key_value(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
+// x >> n, 0 for an n of 64 or more (a negative n is one)
+__device__ __forceinline__ unsigned long long shift_right(unsigned long long x, int n) {
+  unsigned long long y;
+  asm("shr.u64 %0, %1, %2;" : "=l"(y) : "l"(x), "r"(n));
+  return y;
+}
+
 // What turns a logit l into its weight 2^x, x = (l - top) log2(e) / t, as a
 // whole number of 2^-44 (an even one: rounded at 2^-43).  Every lane of the
 // warp calls it, lane j holding T[j] = 2^(44 + j / 32).
@@ -130,7 +137,9 @@ struct Weigher {
     tg = rintf(p * 1024.0f) * 0.0009765625f;
     tl = (p - tg) + fmaf(top, cl, fmaf(top, ch, -p));
   }
-  // l is at most top; -inf and NaN, and all below 2^-45, get 0: their k is -1504
+  // l is at most top.  What lies below 2^-45, -inf and NaN get 0: z's bits then
+  // stand for a shift by more than 45 (the bits of floats ascend with them, a
+  // negative z or NaN gives a negative shift, which counts as 2^32 less that),
   // and the shift leaves nothing, whatever the fraction's bits
   __device__ __forceinline__ unsigned long long operator()(float l) const {
     constexpr float kRound = 12582912.0f;  // 1.5 2^23: x + kRound - kRound rounds x
@@ -138,7 +147,7 @@ struct Weigher {
     if (near) {
       const float p = l * ch;
       const float e = fmaf(l, ch, -p);  // exact
-      z = fmaf(fmaxf(p - tg, -47.0f), 32.0f, kRound);
+      z = fmaf(p - tg, 32.0f, kRound);
       rh = p - fmaf(z - kRound, 0.03125f, tg);  // the fma is exact: a multiple of 2^-10
       small = fmaf(l, cl, e - tl);
     } else {
@@ -147,11 +156,11 @@ struct Weigher {
       const float b = dh - l;
       const float dl = (l - (dh - b)) - (top + b);
       const float ph = dh * ch;
-      z = fmaf(fmaxf(ph, -47.0f), 32.0f, kRound);
+      z = fmaf(ph, 32.0f, kRound);
       rh = fmaf(z - kRound, -0.03125f, ph);
       small = fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch);
     }
-    const int k = __float_as_int(z) - 0x4b400000;
+    const int bits = __float_as_int(z);  // 0x4b400000 + k
     // 2^r - 1 in units of 2^-37: ln 2 as a pair, degrees 2 to 4 in floats
     constexpr float kC1 = 95265423360.0f, kC1l = -261.773682f;
     constexpr float kC2 = 33016479744.0f, kC3 = 7628426752.0f, kC4 = 1321905536.0f;
@@ -160,13 +169,13 @@ struct Weigher {
     const float r = rh + small;
     const float q = fmaf(fmaf(r, kC4, kC3), r, kC2);
     const int E = __float2int_rn(a) + __float2int_rn(fmaf(q, r * r, rest));
-    const uint32_t hi = __shfl_sync(0xffffffffu, t_hi, k);
-    const uint32_t lo = __shfl_sync(0xffffffffu, t_lo, k);
+    const uint32_t hi = __shfl_sync(0xffffffffu, t_hi, bits);
+    const uint32_t lo = __shfl_sync(0xffffffffu, t_lo, bits);
     const long long T = static_cast<long long>((static_cast<unsigned long long>(hi) << 32) | lo);
     const int t31 = static_cast<int>(__funnelshift_r(lo, hi, 14));
     const unsigned long long w =
         static_cast<unsigned long long>(T + ((static_cast<long long>(t31) * E) >> 23));
-    return ((w >> ((-(k >> 5)) & 63)) + 1ull) & ~1ull;
+    return (shift_right(w, (0x4b400000 >> 5) - (bits >> 5)) + 1ull) & ~1ull;
   }
 };
 
@@ -523,6 +532,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
   }
   if (!(t > 0.0f)) {  // greedy: the lowest index of the largest logit
     int idx = INT_MAX;
+    if (S.warp_top[my_warp] != top && !sl.has_inf) sl.end = sl.begin;  // not here
     sl.template sweep<4>([&](const float (&v)[VE], int at, int) {
 #pragma unroll
       for (int j = VE - 1; j >= 0; --j)
@@ -885,6 +895,8 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       // one that reaches it needs no closer look
       const float reach =
           fmaxf(l_min, top - (static_cast<float>(win_hi) + 2.0f) / bin_scale);
+      const int end = sl.end;
+      if (!weigh_above && S.warp_top[my_warp] < reach) sl.end = sl.begin;  // none of this warp's
       sl.template sweep<4>([&](const float (&v)[VE], int at, int) {
         float most = v[0];
 #pragma unroll
@@ -900,6 +912,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
           }
         }
       });
+      sl.end = end;
     }
     if (weigh_all || weigh_above) {
       above = warp_sum(above);
