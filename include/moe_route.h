@@ -549,7 +549,7 @@ size_t moe_attn_workspace(int kv_dtype, int head_dim);
  * whose w sum reaches top_p of theirs (at least one token).  The draw is the
  * first kept token, by index, at which the running sum of w exceeds u times
  * the kept sum.  A row without a token to draw gets id -1 and probability 0.
- * Sums are whole numbers of 2^-44 of the largest w, so they depend on no order
+ * Sums are whole numbers of 2^-43 of the largest w, so they depend on no order
  * of addition.  Requires 1 <= V <= 2^18, B <= 65535.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
  */

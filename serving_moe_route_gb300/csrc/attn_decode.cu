@@ -7,26 +7,41 @@
 // keep loads in flight, and the products only have to keep out of the way.
 //
 //   work     A unit is (request, kv head, block of 16 query heads); its tokens
-//            form tiles, a stage per warp, and it counts its tiles and one or two
-//            more for its end, which takes as long.  The counts of all units, in order, are cut into equal contiguous ranges, one per
-//            CTA of a single wave, so ragged lengths and long single requests
+//            form tiles, a stage per warp, and it counts its tiles and one or
+//            two more for its end, which takes as long.  The counts of all
+//            units, in order, are cut into equal contiguous ranges, one per CTA
+//            of a single wave, so ragged lengths and long single requests
 //            balance alike; a range may begin and end inside a unit.
-//   loads    Each warp has a ring of ST stages of 16 keys and 16 values and
+//   loads    Each warp has a ring of ST stages of 8 to 32 keys and values and
 //            fills it with 16-byte cp.async, ST-1 stages ahead, across unit
 //            borders; page ids are fetched one stage before that.  Warps
 //            share nothing in the loop: no CTA-wide barrier, no producer.
-//   math     S = Q K^T and O += P V on m16n8k16 / m16n8k8 tensor core
-//            instructions with the 16 query heads as rows.  One pass keeps
-//            the running maximum m and sum l of each row in fp32 (base 2) and
-//            rescales O when m grows.  tcgen05 needs 128 rows on its M side
-//            and its result in tensor memory; here one operand has 16 rows
-//            or fewer, the softmax works on its rows between the two
-//            products, and the legacy instructions take under a third of the
-//            time that the tile's bytes take.
+//            Rows that follow one another in one page (every stage of pages of
+//            16 tokens or more, but for windows) need no address of their own.
+//   math     S = Q K^T and O += P V on m16n8k16 (bf16; e4m3 as f16, which holds
+//            it exactly) and m16n8k8 (f32 as two 11-bit terms) tensor core
+//            instructions with the 16 query heads as rows.  One pass keeps a
+//            reference m and the sum l of each row in fp32 (base 2); m is a
+//            logit that was the largest when it was taken, and O is rescaled
+//            only when one lies 8 above it (weights stay below 2^8).  tcgen05
+//            needs 128 rows on its M side and its result in tensor memory; here
+//            one operand has 16 rows or fewer and the softmax works on its rows
+//            between the two products.  The m16n8 instructions suffice: without
+//            the loads' waiting a bf16 tile takes a third of the time of its
+//            bytes.  e4m3 products of e4m3 operands (m16n8k32) were tried: 245 us
+//            where f16's take 137, and sums 2^-8 off.
 //   joining  At a unit's end the CTA's warps join through shared memory.  A
 //            unit inside one range is written at once; parts of a unit cut by
 //            range borders go to the workspace in fp32 and the second kernel
 //            joins them in range order: no atomics, one fixed result.
+//
+// Bound by the cache's bytes on long lengths and by a fixed part otherwise,
+// about 4 us before the first product (lengths, page ids, first rows) and 4
+// after the last (the second kernel).  Measured on a GB300, 32 query heads on 4
+// of 128: one request of 262161 tokens, bf16: 88 us, 6.1 TB/s (90% of the copy
+// bandwidth); 256 up to 8192, e4m3: 137 us, 5.2 TB/s; 64 up to 4096, bf16:
+// 42 us, 4.3 TB/s, f32: 92 us, 3.9 TB/s, whose split operands' instructions
+// bound it; one of 700: 8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -161,9 +176,10 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ configuration
-// Keys of a warp's stage (one k step of bf16 and f32 products, two of e4m3's,
-// in f16), its bytes (keys and values), warps and stages per CTA, CTAs per SM:
-// about 200 KB of an SM's shared memory hold stages.
+// Keys of a warp's stage (one k step of bf16 and f32 products, two of e4m3's in
+// f16: 137 us against 160 with one; at head_dim 256, where that makes stages of
+// 16 KB, one: 80 us against 106), its bytes (keys and values), warps and stages
+// per CTA, CTAs per SM: about 200 KB of an SM's shared memory hold stages.
 template <int KV, int DP>
 struct AttnCfg {
   static constexpr int ES = kv_esize(KV);
@@ -176,9 +192,10 @@ struct AttnCfg {
   static constexpr int CTAS = SB == 16384 || NW == 8 ? 1 : SB == 8192 ? 2 : 3;
   static constexpr int ST = SB == 16384 ? 2 : SB == 8192 ? 3 : 4;
   static constexpr int THREADS = 32 * NW;
-  // what a unit's end and the next one's begin cost, in tiles (of a batch of
-  // 64 with bf16, 180 MB: 56 us with 0, 45 with 1, 42 with 2 and 3)
-  static constexpr int END = 2;
+  // what a unit's end and the next one's begin cost, in tiles (a batch of 64
+  // with bf16, 180 MB: 56 us with 0, 45 with 1, 42 with 2 and 3; with f32, whose
+  // tiles take longer, 92 us with 1, 95 with 2)
+  static constexpr int END = KV == MOE_KV_F32 ? 1 : 2;
   static constexpr int TILE = NW * KEYS;
   // Q in shared memory unless its fragments fit registers; for f32 as two
   // terms, one after the other

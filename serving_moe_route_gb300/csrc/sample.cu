@@ -3,10 +3,10 @@
 // and top-p, then the draw by the running sum over the vocabulary.
 //
 // A token is chosen by where a sum passes a border, so two ways to add give
-// two answers unless the sums are exact: weights are whole numbers of 2^-44
-// of the largest one (1), computed to about 2^-38 of themselves, and added as
-// 64-bit integers.  A vocabulary of 2^18 stays below 2^63, and no order of
-// additions, of CTAs or of atomics changes a sum.
+// two answers unless the sums are exact: weights are whole numbers of 2^-43
+// of the largest one, computed to about 2^-38 of themselves, and added as
+// 64-bit integers (in units of 2^-44).  A vocabulary of 2^18 stays below 2^63,
+// and no order of additions, of CTAs or of atomics changes a sum.
 //
 // One cluster of C CTAs works on a row, each on a slice that it sweeps two or
 // three times, the first from HBM and the others out of L2 (rows in flight
@@ -29,9 +29,16 @@
 //      bf16), or there is no such bin (top-p among the many that a large top-k
 //      left): the border is narrowed to one logit value by histograms over
 //      order keys (at most three), and ties are counted in index order.
-// Rows without top-k and top-p only need their sums.  Bound by the row's bytes
-// where top-k is small; where the whole vocabulary has to be weighed, by the
-// weights' instructions (about 50 a token, once).
+// Rows without top-k and top-p only need their sums.
+//
+// Bound by latency for few rows (a dozen steps, each a few dependent loads or a
+// cluster barrier); for many by the row's bytes where it is greedy or top-k is
+// small, and by the weights' instructions (about 60 a token, once) and the
+// counts' shared-memory additions where the whole vocabulary has to be weighed.
+// Measured on a GB300: one row of 131072 f32 with every restriction 13 us; 64 of
+// 50257 bf16 with mixed ones 32 us; 512 of 131072 f32 greedy 76 us (3.5 TB/s of
+// logits), top-k 119, no restriction 187, top-p 348.  With the rows' slices kept
+// in shared memory (two CTAs an SM) the last four took 101, 222, 257 and 563 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
