@@ -62,7 +62,6 @@ constexpr int kSampCtas = 4;    // per SM
 constexpr int kSampWarps = kSampThreads / 32;
 constexpr int kBins = 8192;     // of counts
 constexpr int kPer = kBins / kSampThreads;            // a thread's: a coarse bin
-constexpr int kCounts = kPer * (kSampThreads + 1);    // words that hold them
 constexpr int kBand = 512;      // bins of each of the two best bands (2 t wide)
 constexpr int kCoarse = 16;     // bins in one where groups are counted
 constexpr int kNear = 3 * kPer; // bins around the border among which the window lies
@@ -75,12 +74,10 @@ constexpr int kSmallK = 96;          // the largest top-k that starts from them
 constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 1 << 18;
 
-// Where bin b's count lies: a thread's kPer neighbouring bins a row apart, so
-// that threads read theirs, and tokens of neighbouring bins add to them,
-// without bank conflicts
-__device__ __forceinline__ int count_at(int b) {
-  return b / kPer + (b % kPer) * (kSampThreads + 1);
-}
+// Where bin b's count lies: so that threads read their kPer neighbouring bins,
+// and tokens of neighbouring bins add to them, without bank conflicts
+static_assert(kPer == 32 && (kBins & (kBins - 1)) == 0, "the swizzle below");
+__device__ __forceinline__ int count_at(int b) { return (b ^ ((b >> 5) & 31)) & (kBins - 1); }
 
 struct SampArgs {
   const void* logits;
@@ -195,12 +192,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// adds to shared memory where `on`: a predicate, not a branch
-__device__ __forceinline__ void red_add(uint32_t* p, uint32_t v, bool on) {
+// adds 1 to shared memory where a < end: a predicate, not a branch
+__device__ __forceinline__ void red_one(uint32_t addr, int a, int end) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
-      "@q red.shared.add.u32 [%0], %1;\n\t}" ::"r"(smem_u32(p)),
-      "r"(v), "r"(static_cast<uint32_t>(on))
+      "{\n\t.reg .pred q;\n\tsetp.lt.s32 q, %1, %2;\n\t"
+      "@q red.shared.add.u32 [%0], 1;\n\t}" ::"r"(addr),
+      "r"(a), "r"(end)
       : "memory");
 }
 
@@ -244,7 +241,7 @@ struct Result {
 
 struct SampShared {
   union {
-    alignas(16) uint32_t cnt[kCounts];
+    alignas(16) uint32_t cnt[kBins];
     struct {
       uint32_t lo[kKeyBins], hi[kKeyBins];  // 64-bit sums of weights
     };
@@ -494,7 +491,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     sl.has_inf = false;
   }
   if (k || p_on)
-    for (int i = tid; i < kCounts; i += kSampThreads) S.cnt[i] = 0;
+    for (int i = tid; i < kBins; i += kSampThreads) S.cnt[i] = 0;
   if (tid == 0) {
     S.list_n = S.all_n = 0;
     S.at_bin = INT_MAX;
@@ -566,31 +563,36 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     const float c = kE / t;
     weigh.set(top, fminf(c, 1e30f), c < 1e30f ? (fmaf(-c, t, kE) + kEl) / t : 0.0f, table);
   }
-  float l_min = -FLT_MAX;  // the smallest logit that min-p keeps
-  if (min_on) {
-    // by the weights themselves: the lowest of the logits, as order keys, whose
-    // weight reaches min-p's.  Each round of a warp tests 32 of them; the first
-    // range is an estimate's, if its ends are on both sides
-    bool more;
-    const unsigned long long unit = 1ull << 44;
-    unsigned long long least = share_of(fminf(min_p, 1.0f), unit, more);
-    least = min(max(least + (more ? 1 : 0), 1ull), unit);
-    const float at = t * logf(fminf(min_p, 1.0f)), off = 1e-5f * (1.0f + fabsf(at) + fabsf(top));
-    uint32_t lo = order_key(-FLT_MAX), hi = order_key(top);  // hi's weight reaches it
-    const float a = top + at - off, b = top + at + off;
-    const bool up = weigh(fminf(lane ? b : a, top)) >= least;
-    const unsigned both = __ballot_sync(0xffffffffu, up);
+  // The lowest float for which `in`, which holds for the largest logit and for
+  // every float above one for which it holds.  Each round of a warp tests 32 of
+  // them, by order key; the first range is around an estimate, if its ends are
+  // on both sides
+  auto lowest = [&](float estimate, float off, auto in) {
+    uint32_t lo = order_key(-FLT_MAX), hi = order_key(top);  // `in` holds for hi
+    const float a = estimate - off, b = estimate + off;
+    const unsigned both = __ballot_sync(0xffffffffu, in(fminf(lane ? b : a, top)));
     if (a > -FLT_MAX && !(both & 1u)) lo = order_key(a);
     if (b < top && (both & 2u)) hi = order_key(b);
     while (lo < hi) {
       const uint32_t step = (hi - lo + 31) / 32;
       const uint32_t key = min(hi, lo + step * lane);
-      const unsigned reach = __ballot_sync(0xffffffffu, weigh(key_value(key)) >= least);
+      const unsigned reach = __ballot_sync(0xffffffffu, in(key_value(key)));
       const int j = reach ? __ffs(reach) - 1 : 32;
       hi = min(hi, lo + step * j);
       if (j > 0) lo = lo + step * (j - 1) + 1;
     }
-    l_min = key_value(hi);
+    return key_value(hi);
+  };
+  float l_min = -FLT_MAX;  // the smallest logit that min-p keeps
+  if (min_on) {
+    // by the weights themselves
+    bool more;
+    const unsigned long long unit = 1ull << 44;
+    unsigned long long least = share_of(fminf(min_p, 1.0f), unit, more);
+    least = min(max(least + (more ? 1 : 0), 1ull), unit);
+    const float at = t * logf(fminf(min_p, 1.0f));
+    l_min = lowest(top + at, 1e-5f * (1.0f + fabsf(at) + fabsf(top)),
+                   [&](float l) { return weigh(l) >= least; });
   }
   // bins of width t / 256 below the largest logit, the last one open;
   // monotonous in l, which is all that they have to be
@@ -724,17 +726,26 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     } else {
       unsigned tail = 0;  // the last bin holds the far tail: added once
       float more[2] = {0.0f, 0.0f};  // the likeliest tokens' weights are not just their bin's
+      const uint32_t counts = smem_u32(S.cnt);
+      constexpr int kLast = 0x4b400000 + kBins - 1;  // bins as bits of 1.5 2^23 + b
       sl.template sweep<4>([&](const float (&v)[VE], int, int) {
+        float z[VE], best = INFINITY;
+        int bits[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const float z = (top - v[j]) * bin_scale;  // NaN: in no bin
-          const int b = bin_at(z);
-          const bool ok = v[j] >= l_min, last = b == kBins - 1;
-          tail += ok && last;
-          red_add(&S.cnt[count_at(b)], 1u, ok && !last);
-          if (!k && __any_sync(0xffffffffu, b < 2 * kBand)) {
-            constexpr float kLog = -1.44269504f / kBinsPerT;
-            const float e = ok ? ex2_approx(z * kLog) - ex2_approx(static_cast<float>(b) * kLog) : 0.0f;
+          z[j] = (top - v[j]) * bin_scale;  // NaN and -inf: in the last bin, not counted
+          bits[j] = __float_as_int(fminf(z[j], static_cast<float>(kBins - 1)) + 12582912.0f);
+          if (!(v[j] >= l_min)) bits[j] = kLast + 1;
+          tail += bits[j] == kLast;
+          red_one(counts + 4 * count_at(bits[j]), bits[j], kLast);
+          best = fminf(best, z[j]);
+        }
+        if (!k && __any_sync(0xffffffffu, best < 2.0f * kBand)) {
+          constexpr float kLog = -1.44269504f / kBinsPerT;
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const int b = bits[j] - 0x4b400000;
+            const float e = ex2_approx(z[j] * kLog) - ex2_approx(static_cast<float>(b) * kLog);
             more[0] += b < kBand ? e : 0.0f;
             more[1] += b >= kBand && b < 2 * kBand ? e : 0.0f;
           }
@@ -754,7 +765,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       float w = 0.0f, scale = k ? 0.0f : exp2f(-1.44269504f / kBinsPerT * (tid * kPer));
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const uint32_t c = S.cnt[tid + i * (kSampThreads + 1)];
+        const uint32_t c = S.cnt[count_at(tid * kPer + i)];
         n += c;
         w = fmaf(static_cast<float>(c), scale, w);
         scale *= kBinStep;
@@ -868,6 +879,16 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     w_mine = warp_sum(w_mine);
   }
   uint32_t bin_lo = 0xffffffffu, bin_hi = 0;  // a dense bin's order keys
+  // the lowest logit in the bins 0 .. b that min-p keeps; above the largest for
+  // b < 0
+  auto edge = [&](int b) {
+    if (b < 0) return static_cast<float>(INFINITY);
+    if (b >= kBins - 1) return l_min;
+    const float width = 1.0f / bin_scale;
+    return fmaxf(l_min, lowest(top - (static_cast<float>(b) + 0.5f) * width,
+                               1e-5f * (1.0f + fabsf(top) + static_cast<float>(b) * width),
+                               [&](float l) { return bin_of(l) <= b; }));
+  };
   unsigned long long above = 0, everything = 0;
   for (int tries = 0; list_on && !generic; ++tries) {
     // ---- C
@@ -884,38 +905,33 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         S.list_pos[at] = (static_cast<uint32_t>(my_warp) << 18) | static_cast<uint32_t>(idx);
       }
     };
+    const float from = edge(win_lo - 1), down_to = edge(win_hi);  // the window's ends
     if (weigh_all) {
       sl.template sweep<kFew>([&](const float (&v)[VE], int at, int) {
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
           const unsigned long long w = weigh(v[j]);
-          const bool ok = v[j] >= l_min;  // else (min-p, -inf, NaN) out of every bin
-          const int b = ok ? bin_of(v[j]) : INT_MAX;
-          if (!min_on || ok) everything += w;
-          if (b < win_lo) above += w;
-          if (static_cast<unsigned>(b - win_lo) <= static_cast<unsigned>(win_hi - win_lo))
-            enlist(v[j], at + j);
+          if (!min_on || v[j] >= l_min) everything += w;
+          if (v[j] >= from) above += w;
+          else if (v[j] >= down_to) enlist(v[j], at + j);
         }
       });
     } else {
-      // nothing below this logit can lie in the window's bins: a chunk without
-      // one that reaches it needs no closer look
-      const float reach =
-          fmaxf(l_min, top - (static_cast<float>(win_hi) + 2.0f) / bin_scale);
       const int end = sl.end;
-      if (!weigh_above && S.warp_top[my_warp] < reach) sl.end = sl.begin;  // none of this warp's
+      if (!weigh_above && S.warp_top[my_warp] < down_to) sl.end = sl.begin;  // none of this warp's
       sl.template sweep<4>([&](const float (&v)[VE], int at, int) {
         float most = v[0];
 #pragma unroll
         for (int j = 1; j < VE; ++j) most = fmaxf(most, v[j]);
-        if (!__any_sync(0xffffffffu, most >= reach)) return;
+        // a chunk without a logit that reaches the window needs no closer look
+        if (!__any_sync(0xffffffffu, most >= down_to)) return;
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const int b = v[j] >= l_min ? bin_of(v[j]) : INT_MAX;
-          if (b >= win_lo && b <= win_hi) enlist(v[j], at + j);
-          if (weigh_above && __any_sync(0xffffffffu, b < win_lo)) {
-            const unsigned long long w = weigh_call(weigh, b < win_lo ? v[j] : top);
-            above += b < win_lo ? w : 0;
+          const bool up = v[j] >= from;
+          if (v[j] >= down_to && !up) enlist(v[j], at + j);
+          if (weigh_above && __any_sync(0xffffffffu, up)) {
+            const unsigned long long w = weigh_call(weigh, v[j]);
+            above += up ? w : 0;
           }
         }
       });
