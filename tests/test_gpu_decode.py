@@ -393,3 +393,55 @@ def test_wrappers_refuse_what_does_not_fit():
         moe.kv_step(n, n, table, n, n[:1], page_size=16, num_pages=4, max_tokens=-1)
     with pytest.raises(ValueError, match="overlap"):
         moe.kv_step(n, n, table[:1].expand(2, -1), n, n[:1], page_size=16, num_pages=4, max_tokens=1)
+
+
+def test_a_whole_step_in_a_graph():
+    # tables, append, attention and sampling of one step, captured once and
+    # replayed while lengths and tables grow on the device
+    B, Hq, Hkv, D, page, V = 5, 8, 2, 64, 4, 300
+    g = torch.Generator(device=DEV).manual_seed(0)
+    pool, width = 40, 6
+    kc, vc = _empty_cache(pool, page, Hkv, D, "bf16", "token")
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    free, n_free = torch.arange(pool, dtype=torch.int32, device=DEV), _i32([pool])
+    ctx, new, err = _i32([0] * B), _i32([1, 1, 0, 1, 1]), _word()
+    qkv = torch.empty(B, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    logits = torch.empty(B, V, device=DEV)
+    u = torch.empty(B, device=DEV)
+
+    def step():
+        s = moe.kv_step(ctx, new, table, free, n_free, page_size=page, num_pages=pool,
+                        max_tokens=B, n_free_out=n_free, err=err)
+        moe.kv_append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], s.slots, kc, vc, err=err)
+        out = moe.attn_decode(qkv[:, :Hq], kc, vc, table, s.seq_lens, err=err)
+        ids, _ = moe.sample_tokens(logits, u)
+        ctx.copy_(s.seq_lens)
+        return out, ids
+
+    def inputs(i):
+        qkv.copy_(torch.randn(qkv.shape, generator=g, device=DEV))
+        logits.copy_(torch.randn(B, V, generator=g, device=DEV) * 3)
+        u.copy_(torch.rand(B, generator=g, device=DEV))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # the first calls load what a capture may not
+        inputs(0)
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, ids = step()
+    # the capture ran nothing: one step is behind, ten more follow
+    for i in range(10):
+        inputs(i + 1)
+        q = qkv[:, :Hq].clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ctx.tolist() == [i + 2, i + 2, 0, i + 2, i + 2]
+        _check(q, kc, vc, table, ctx, out, None)
+        want, _ = moe.sample_tokens(logits, u)
+        assert torch.equal(ids, want)
+    assert moe.check_word(err) == (0, 0)
+    used = table[table >= 0].tolist()
+    assert len(set(used)) == len(used) == pool - int(n_free) == 4 * 3

@@ -209,3 +209,24 @@ def test_in_a_graph():
         graph.replay()
         want, wp = moe.sample_tokens(y, v, top_p=p)
         assert torch.equal(ids, want) and torch.equal(probs, wp)
+
+
+@pytest.mark.parametrize("dt,spread", [("bf16", 1.8), ("f32", 0.4), ("f32", 1.8)])
+def test_borders_among_many_tokens(dt, spread):
+    # hundreds of tokens, equal ones with bf16, in the bin of the cut
+    B, V = 10, 262144
+    x, u = _logits(21, B, V, dt, spread=spread, likely=12)
+    rng = np.random.default_rng(2)
+    _check(x, u, least=0.7, top_p=rng.uniform(0.6, 0.99, B), temperature=rng.uniform(0.9, 3.0, B))
+    _check(x, u, least=0.7, top_k=rng.integers(5000, 200000, B))
+
+
+def test_a_few_allowed_tokens():
+    # fewer tokens than top-k left by a mask, and every one of them kept
+    x, u = _logits(22, 9, 40000, "f32")
+    keep = torch.zeros(40000, dtype=torch.bool, device=DEV)
+    keep[::4001] = True
+    x[:, ~keep] = float("-inf")
+    ids = _check(x, u, top_k=np.full(9, 500))
+    assert (ids % 4001 == 0).all()
+    _check(x, u, top_k=np.full(9, 50), top_p=np.full(9, 0.9))
