@@ -236,6 +236,7 @@ struct Result {
   uint32_t cut_key;
   int idx_cut;
   float need;
+  int below;                  // of 3: the border is below the window, not above it
   unsigned long long before, total, to;
 };
 
@@ -618,9 +619,12 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
   bool weigh_all = !k, weigh_above = true;
   int win_lo = INT_MAX, win_hi = INT_MAX, above_n = 0;
   // The window for a border that lies `need` (2^-24 of the largest weight, as
-  // the counts have it) or k tokens down, among the bins around it
+  // the counts have it) or k tokens down, among the bins around it.  Where a
+  // sweep has shown the exact border to lie below bin `after`, or above bin
+  // `until`, it is taken from there on: the bins' weights are not exact
+  int few = 0;                    // coarse bins whose tokens are half a list at most
   int near_c0 = -1, near_at = 0;  // first coarse bin of those, the border's among them
-  auto choose = [&](float need) {
+  auto choose = [&](float need, int after, int until) {
     if (warp == 0) {
       // one warp, kOne neighbouring bins a lane: the border's bin, then the
       // window: as many bins before it as 64 tokens allow (for top-k, whose
@@ -648,17 +652,25 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       }
       n_at += S.near_above - n_sum;  // tokens before this lane's bins
       w_at += S.near_w_above - w_sum;
+      after -= near_c0 * kPer;
+      until -= near_c0 * kPer;
       unsigned at_i = (near_at + 1) * kPer - 1;  // where rounding hides the border
+      if (static_cast<int>(at_i) <= after) at_i = kNear - 1;
+      int last = -1;  // bin that has tokens and lies above `until`
       int n_i = n_at;
       float w_i = w_at;
 #pragma unroll
       for (int i = 0; i < kOne; ++i) {
-        const bool hit = n[i] > 0 && (k ? n_i + n[i] >= k : w_i + w[i] >= need);
-        if (hit) at_i = min(at_i, static_cast<unsigned>(lane * kOne + i));
+        const int b = lane * kOne + i;
+        const bool hit = n[i] > 0 && b > after && (k ? n_i + n[i] >= k : w_i + w[i] >= need);
+        if (hit) at_i = min(at_i, static_cast<unsigned>(b));
+        if (n[i] > 0 && b < until) last = b;
         n_i += n[i];
         w_i += w[i];
       }
-      const int border = static_cast<int>(__reduce_min_sync(0xffffffffu, at_i));
+      int border = static_cast<int>(__reduce_min_sync(0xffffffffu, at_i));
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (border >= until && last >= 0) border = last;
       int through = 0;  // tokens down to the border's bin, itself included
       n_i = n_at;
 #pragma unroll
@@ -715,6 +727,9 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     win_lo = S.win_lo;
     win_hi = S.win_hi;
     above_n = S.above_n;
+    // a window from the largest logit on goes as far as its tokens allow, past
+    // a gap that is wider than the bins around the border
+    if (!k && above_n == 0 && S.at_count <= kList) win_hi = max(win_hi, few * kPer - 1);
   };
   if (k || p_on) {
     // groups, where there are well over k of them
@@ -825,7 +840,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       const float need = static_cast<float>(tw) * share;  // before the border
       const bool here = sn > 0 && (k ? en + sn >= k : static_cast<float>(ew + wi) >= need);
       if (here) atomicMin(&S.at_bin, tid);
-      __syncthreads();
+      few = __syncthreads_count(en + sn <= kList / 2);
       const bool found = S.at_bin < kSampThreads;  // else top-k keeps everything
       const int c0 = found ? max(0, S.at_bin - 1) : 0;
       if (tid == c0) {
@@ -853,7 +868,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       __syncthreads();
       near_c0 = c0;
       near_at = S.at_bin - c0;
-      if (found) choose(need);
+      if (found) choose(need, -1, 2 * kBins);
       if (found) {
         dense = S.at_count > kList;
         generic = dense && k && p_on;
@@ -908,12 +923,18 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     const float from = edge(win_lo - 1), down_to = edge(win_hi);  // the window's ends
     if (weigh_all) {
       sl.template sweep<kFew>([&](const float (&v)[VE], int at, int) {
+        bool in = false;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
+        for (int j = 0; j < VE; ++j) {  // without branches: the weights' steps interleave
           const unsigned long long w = weigh(v[j]);
-          if (!min_on || v[j] >= l_min) everything += w;
-          if (v[j] >= from) above += w;
-          else if (v[j] >= down_to) enlist(v[j], at + j);
+          everything += v[j] >= l_min ? w : 0;
+          above += v[j] >= from ? w : 0;
+          in |= v[j] >= down_to && !(v[j] >= from);
+        }
+        if (in) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (v[j] >= down_to && !(v[j] >= from)) enlist(v[j], at + j);
         }
       });
     } else {
@@ -991,6 +1012,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
           // the window lay beside the border: its place by the exact sum
           S.result.state = 3;
           const unsigned long long border = border_of(everything);
+          S.result.below = border > above;
           const float miss = border >= above ? static_cast<float>(border - above)
                                              : -static_cast<float>(above - border);
           S.result.need = S.win_w + miss * 9.5367432e-7f;  // 2^-44 to 2^-24
@@ -1055,7 +1077,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     if (state == 3) {
       const float need = S.result.need;
       if (tid == 0) S.list_n = S.all_n = 0;
-      choose(need);
+      choose(need, S.result.below ? win_hi : -1, S.result.below ? 2 * kBins : win_lo);
       dense = S.at_count > kList;
       weigh_above = above_n > 0;
       everyone();

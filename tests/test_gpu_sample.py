@@ -230,3 +230,23 @@ def test_a_few_allowed_tokens():
     ids = _check(x, u, top_k=np.full(9, 500))
     assert (ids % 4001 == 0).all()
     _check(x, u, top_k=np.full(9, 50), top_p=np.full(9, 0.9))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("likely,spread", [(3, 0.5), (40, 1.8), (0, 1.0)])
+def test_top_p_beside_a_sum(dt, likely, spread):
+    # top_p just below and just above the share of the first m tokens, where the
+    # next one is close by or far away
+    B, V = 64, 40000
+    x, u = _logits(23, B, V, dt, spread=spread, likely=likely)
+    l = np.sort(R.f64(x), axis=1)[:, ::-1]
+    w = np.exp(l - l[:, :1])
+    share = (np.cumsum(w, axis=1) / w.sum(axis=1, keepdims=True)).astype(np.float32)
+    rng = np.random.default_rng(3)
+    m = np.minimum(np.exp(rng.uniform(0, np.log(V / 2), B)).astype(int), V - 2)
+    m[:16] = np.arange(16)
+    top_p = share[np.arange(B), m]
+    side = np.where(rng.random(B) < 0.5, np.float32(-1), np.float32(2))
+    for _ in range(2):
+        top_p = np.nextafter(top_p, side).astype(np.float32)
+    _check(x, u, least=0.5, top_p=np.clip(top_p, 0, 1))
