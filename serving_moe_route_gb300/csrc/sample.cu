@@ -246,18 +246,22 @@ struct SampShared {
     struct {
       uint32_t lo[kKeyBins], hi[kKeyBins];  // 64-bit sums of weights
     };
-    unsigned long long list_w[kList];  // once all CTAs have read the counts
+    struct {  // once all CTAs have read the counts
+      unsigned long long list_x[kList], list_w[kList];
+    };
   };
   float band[2][kSampWarps];  // what the bands' tokens weigh more than their bins
-  uint32_t coarse_n[kSampThreads];
-  float coarse_w[kSampThreads];
+  alignas(8) float2 coarse[kSampThreads];  // count (as bits) and weight
   int near_n[kNear];  // the row's counts and weights around the border
   float near_w[kNear];
-  uint32_t list_key[kList];
-  uint32_t list_pos[kList];  // warp of the row << 18 | index: ordered by index
-  unsigned long long all[kList];  // the row's list (first CTA)
-  int list_n, list_at, all_n;
-  int next_kept[kSampWarps];
+  // tokens of the window: ~order key << 32 | warp of the row << 18 | index, in
+  // the order that they are kept in
+  unsigned long long list[kList];
+  alignas(16) unsigned long long all[kList];  // the row's (first CTA)
+  int list_n;
+  int cta_n[kMaxCluster];  // CTAs' counts (first CTA)
+  unsigned long long kept;
+  float edge[2];
   // by warp of the row, written by all CTAs into every one (tie, top) or the
   // first
   float warp_top[kMaxCluster * kSampWarps];
@@ -315,6 +319,39 @@ __device__ __forceinline__ void scan_pair(long long a, long long b, long long* s
   __syncthreads();
 }
 
+// the same for a count and a weight, the weight's sums as they round in this order
+__device__ __forceinline__ void scan_pair(int a, float b, long long* sums, int& ex_a, float& ex_b,
+                                          float& tot_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = a;
+  float y = b;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, off);
+    const float v = __shfl_up_sync(0xffffffffu, y, off);
+    if (lane >= off) {
+      x += u;
+      y += v;
+    }
+  }
+  float2* const at = reinterpret_cast<float2*>(sums);
+  if (lane == 31) at[warp] = make_float2(__int_as_float(x), y);
+  __syncthreads();
+  ex_a = x - a;
+  ex_b = y - b;
+  tot_b = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kSampWarps; ++w) {
+    const float2 v = at[w];
+    if (w < warp) {
+      ex_a += __float_as_int(v.x);
+      ex_b += v.y;
+    }
+    tot_b += v.y;
+  }
+  __syncthreads();
+}
+
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -322,31 +359,10 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 }
 
 // The first `size` threads of a CTA (a power of two, 32 or more), as a group
-// that sorts and adds up one value a thread
+// that orders and adds up one value a thread
 __device__ __forceinline__ void group_sync(int size) {
   if (size == 32) __syncwarp();
   else named_bar_sync(1, size);
-}
-
-// ascending; buf: one value a thread
-__device__ __forceinline__ unsigned long long group_sort(unsigned long long x, int size,
-                                                         unsigned long long* buf) {
-  const int tid = threadIdx.x;
-  for (int k = 2; k <= size; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      unsigned long long y;
-      if (j >= 32) {
-        buf[tid] = x;
-        group_sync(size);
-        y = buf[tid ^ j];
-        group_sync(size);
-      } else {
-        y = __shfl_xor_sync(0xffffffffu, x, j);
-      }
-      x = ((tid & j) == 0) == ((tid & k) == 0) ? min(x, y) : max(x, y);
-    }
-  }
-  return x;
 }
 
 // the sum of the values before this thread's, and of all
@@ -494,7 +510,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
   if (k || p_on)
     for (int i = tid; i < kBins; i += kSampThreads) S.cnt[i] = 0;
   if (tid == 0) {
-    S.list_n = S.all_n = 0;
+    S.list_n = 0;
     S.at_bin = INT_MAX;
   }
 
@@ -788,11 +804,11 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       // a band's correction counts from its end on
       if (!k && (tid + 1 == kBand / kPer || tid + 1 == 2 * kBand / kPer))
         for (int i = 0; i < kSampWarps; ++i) w += S.band[tid * kPer / kBand][i];
-      S.coarse_n[tid] = n;
-      S.coarse_w[tid] = w;
+      S.coarse[tid] = make_float2(__uint_as_float(n), w);
     }
     everyone();
-    long long en, ew, tn, tw;
+    int en;
+    float ew, tw;
     if (small) {  // every CTA adds the counts up for itself
       constexpr int kTwo = kBins / kCoarse / kSampThreads;
       static_assert(kTwo == 2, "two coarse bins a thread");
@@ -807,7 +823,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         cn[0] += x[r].x;
         cn[1] += x[r].y;
       }
-      scan_pair(cn[0] + cn[1], 0, S.scan, en, ew, tn, tw);
+      scan_pair(cn[0] + cn[1], 0.0f, S.scan, en, ew, tw);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (en < k && en + cn[i] >= k) S.at_bin = (2 * tid + i) * kCoarse + kCoarse - 1;
@@ -819,33 +835,30 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       weigh_above = false;
     } else {
       // every CTA adds the coarse bins up for itself, in the same order
-      uint32_t cn[kMaxCluster];
-      float cw[kMaxCluster], sw = 0.0f;
+      float2 x[kMaxCluster];
+      float sw = 0.0f;
       int sn = 0;
 #pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        cn[r] = r < C ? *cluster.map_shared_rank(S.coarse_n + tid, r) : 0;
-        cw[r] = r < C && !k ? *cluster.map_shared_rank(S.coarse_w + tid, r) : 0.0f;
-      }
+      for (int r = 0; r < kMaxCluster; ++r)
+        x[r] = r < C ? *cluster.map_shared_rank(S.coarse + tid, r) : make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        sn += cn[r];
-        sw += cw[r];
+        sn += __float_as_int(x[r].x);
+        sw += x[r].y;
       }
-      // weights as whole numbers of 2^-24 of the largest one: only the
-      // window's choice goes by them
+      // in units of 2^-24 of the largest one: only the window's choice goes by them
       constexpr float kUnit = 16777216.0f;
-      const long long wi = static_cast<long long>(sw * kUnit);
-      scan_pair(sn, wi, S.scan, en, ew, tn, tw);
-      const float need = static_cast<float>(tw) * share;  // before the border
-      const bool here = sn > 0 && (k ? en + sn >= k : static_cast<float>(ew + wi) >= need);
+      sw *= kUnit;
+      scan_pair(sn, sw, S.scan, en, ew, tw);
+      const float need = tw * share;  // before the border
+      const bool here = sn > 0 && (k ? en + sn >= k : ew + sw >= need);
       if (here) atomicMin(&S.at_bin, tid);
       few = __syncthreads_count(en + sn <= kList / 2);
       const bool found = S.at_bin < kSampThreads;  // else top-k keeps everything
       const int c0 = found ? max(0, S.at_bin - 1) : 0;
       if (tid == c0) {
-        S.near_above = static_cast<int>(en);
-        S.near_w_above = static_cast<float>(ew);
+        S.near_above = en;
+        S.near_w_above = ew;
       }
       // the bins around it, from all CTAs
       for (int i = tid; i < kNear; i += kSampThreads) {
@@ -875,7 +888,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       } else {
         win_lo = 0;
         win_hi = kBins - 1;
-        generic = !k || tn > kList;
+        generic = __syncthreads_or(en + sn > kList) != 0 || !k;
       }
       weigh_above = above_n > 0;
     }
@@ -905,7 +918,120 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
                                [&](float l) { return bin_of(l) <= b; }));
   };
   unsigned long long above = 0, everything = 0;
-  for (int tries = 0; list_on && !generic; ++tries) {
+  // The last kept token of the row's list, and the draw or the warp that it falls
+  // on: by the first CTA's first `size` threads, x a token of each
+  int tries = 0;
+  auto pick = [&](int n_list, int n, int size, unsigned long long x) {
+    above = everything = 0;
+    for (int i = lane; i < warps; i += 32) {
+      above += S.warp_mass[i];
+      everything += S.warp_all[i];
+    }
+    above = warp_sum(above);
+    everything = warp_sum(everything);
+    // in order: each token's place is the number of those before it
+    {
+      const unsigned long long w = weigh(x == ~0ull ? top : key_value(~static_cast<uint32_t>(x >> 32)));
+      int place = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; i += 2) {  // beyond n: ~0
+        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(S.all + i);
+        place += (y.x < x) + (y.y < x);
+      }
+      if (x != ~0ull) {
+        S.list_x[place] = x;
+        S.list_w[place] = w;
+      }
+    }
+    group_sync(size);
+    const bool have = tid < n;
+    x = have ? S.list_x[tid] : 0;
+    const unsigned long long w = have ? S.list_w[tid] : 0;
+    const uint32_t pos = static_cast<uint32_t>(x);
+    const int better = above_n + tid;
+    bool keep = have && (!k || better < k);
+    unsigned long long* const buf = reinterpret_cast<unsigned long long*>(S.scan);
+    unsigned long long kept_w;
+    const unsigned long long ex = group_scan(keep ? w : 0, size, buf, kept_w);
+    bool missed = n_list > kList;  // a list that ran over means D
+    unsigned long long border = ~0ull;
+    if (p_on) {
+      const unsigned long long left = above + kept_w;
+      border = border_of(k ? left : everything);
+      missed = missed || (above_n > 0 && above >= border) || left < border;
+      keep = keep && (better == 0 || above + ex < border);
+    }
+    // the last one that is kept
+    if (keep && !(tid + 1 < n && (!k || better + 1 < k) && above + ex + w < border)) {
+      S.kept = ex + w;
+      S.result.cut_key = ~static_cast<uint32_t>(x >> 32);
+      S.result.idx_cut = static_cast<int>(pos & 0x3ffffu);
+    }
+    const bool drawn = above_n == 0;  // the draw is among the list
+    if (missed) {
+      if (tid == 0) S.result.state = 2;
+      if (tid == 0 && !k && n_list <= kList && tries < 2 && near_c0 >= 0) {
+        // the window lay beside the border: its place by the exact sum
+        S.result.state = 3;
+        S.result.below = border > above;
+        const float miss = border >= above ? static_cast<float>(border - above)
+                                           : -static_cast<float>(above - border);
+        S.result.need = S.win_w + miss * 9.5367432e-7f;  // 2^-44 to 2^-24
+      }
+    } else if (drawn) {
+      if (have) {
+        S.all[tid] = pos;
+        S.list_w[tid] = keep ? w : 0;
+      }
+    } else if (keep) {
+      atomicAdd(&S.warp_mass[pos >> 18], w);
+    }
+    group_sync(size);
+    const unsigned long long total = above + S.kept;
+    const unsigned long long to = target(total);
+    if (!missed && drawn) {  // in order of the index
+      if (tid == 0) S.result.state = 0;
+      unsigned long long sum = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) sum += static_cast<uint32_t>(S.all[i]) < pos ? S.list_w[i] : 0;
+      if (keep && sum <= to && to < sum + w) {
+        A.ids[row] = static_cast<int>(pos & 0x3ffffu);
+        if (A.probs) A.probs[row] = static_cast<float>(w) / static_cast<float>(total);
+      }
+    } else if (!missed && warp == 0) {
+      // the warps' sums, with the list's kept tokens: which one the draw falls on
+      constexpr int kOne = kMaxCluster * kSampWarps / 32;
+      unsigned long long m[kOne], incl = 0;
+#pragma unroll
+      for (int i = 0; i < kOne; ++i) {
+        m[i] = lane * kOne + i < warps ? S.warp_mass[lane * kOne + i] : 0;
+        incl += m[i];
+      }
+      const unsigned long long mine = incl;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      unsigned long long sum = incl - mine;
+#pragma unroll
+      for (int i = 0; i < kOne; ++i) {
+        if (sum <= to && to < sum + m[i]) {
+          S.result.who = lane * kOne + i;
+          S.result.before = sum;
+        }
+        sum += m[i];
+      }
+      if (lane == 0) {
+        S.result.state = 1;
+        S.result.total = total;
+        S.result.to = to;
+      }
+    }
+    group_sync(size);
+    if (tid > 0 && tid < C) cluster.map_shared_rank(&S, tid)->result = S.result;
+  };
+  for (; list_on && !generic; ++tries) {
     // ---- C
     above = everything = 0;
     auto enlist = [&](float v, int idx) {
@@ -915,12 +1041,16 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         return;
       }
       const int at = atomicAdd(&S.list_n, 1);
-      if (at < kList) {
-        S.list_key[at] = order_key(v);
-        S.list_pos[at] = (static_cast<uint32_t>(my_warp) << 18) | static_cast<uint32_t>(idx);
-      }
+      if (at < kList)
+        S.list[at] = (static_cast<unsigned long long>(~order_key(v)) << 32) |
+                     (static_cast<uint32_t>(my_warp) << 18) | static_cast<uint32_t>(idx);
     };
-    const float from = edge(win_lo - 1), down_to = edge(win_hi);  // the window's ends
+    if (warp < 2) {
+      const float e = edge(warp ? win_hi : win_lo - 1);
+      if (lane == 0) S.edge[warp] = e;
+    }
+    __syncthreads();
+    const float from = S.edge[0], down_to = S.edge[1];  // the window's ends
     if (weigh_all) {
       sl.template sweep<kFew>([&](const float (&v)[VE], int at, int) {
         bool in = false;
@@ -967,107 +1097,30 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       cluster.map_shared_rank(S.warp_mass, 0)[my_warp] = above;
       cluster.map_shared_rank(S.warp_all, 0)[my_warp] = everything;
     }
-    // this CTA's list to the end of the first one's; its order does not matter
     __syncthreads();
-    if (tid == 0) S.list_at = atomicAdd(cluster.map_shared_rank(&S.all_n, 0), S.list_n);
-    __syncthreads();
-    if (tid < S.list_n && S.list_at + tid < kList)
-      cluster.map_shared_rank(S.all, 0)[S.list_at + tid] =
-          (static_cast<unsigned long long>(~S.list_key[tid]) << 32) | S.list_pos[tid];
+    if (tid == 0) cluster.map_shared_rank(S.cta_n, 0)[rank] = S.list_n;
     everyone();
-    int size = 32;  // of the group that works on the list
-    const int n_list = S.all_n;  // (of the first CTA)
-    while (size < min(n_list, kList)) size *= 2;
-    if (lead && tid < size) {
-      above = everything = 0;
-      for (int i = lane; i < warps; i += 32) {
-        above += S.warp_mass[i];
-        everything += S.warp_all[i];
+    if (lead) {
+      // thread i takes the CTAs' i-th token; which order they come in does not matter
+      int n_list = 0, from_cta = -1, from_at = 0;
+      for (int r = 0; r < C; ++r) {
+        const int n = S.cta_n[r];
+        if (tid >= n_list && tid < n_list + n) {
+          from_cta = r;
+          from_at = tid - n_list;
+        }
+        n_list += n;
       }
-      above = warp_sum(above);
-      everything = warp_sum(everything);
-      // in order: key descending, index ascending
-      const bool have = tid < n_list;
-      unsigned long long x = group_sort(have ? S.all[tid] : ~0ull, size, S.list_w);
-      const uint32_t key = ~static_cast<uint32_t>(x >> 32), pos = static_cast<uint32_t>(x);
-      unsigned long long w = weigh(have ? key_value(key) : top);
-      if (!have) w = 0;
-      const int better = above_n + tid;
-      bool keep = have && (!k || better < k);
-      unsigned long long* const buf = reinterpret_cast<unsigned long long*>(S.scan);
-      unsigned long long kept_w, ex = group_scan(keep ? w : 0, size, buf, kept_w);
-      bool missed = n_list > kList;  // a list that ran over means D
-      if (p_on) {
-        const unsigned long long left = above + kept_w;
-        const unsigned long long border = border_of(k ? left : everything);
-        missed = missed || (above_n > 0 && above >= border) || left < border;
-        keep = keep && (better == 0 || above + ex < border);
-        ex = group_scan(keep ? w : 0, size, buf, kept_w);
-      }
-      const unsigned long long total = above + kept_w;
-      const unsigned long long to = target(total);
-      if (missed || above_n == 0) {
-        if (tid == 0) S.result.state = missed ? 2 : 0;
-        if (missed && tid == 0 && !k && n_list <= kList && tries < 2 && near_c0 >= 0) {
-          // the window lay beside the border: its place by the exact sum
-          S.result.state = 3;
-          const unsigned long long border = border_of(everything);
-          S.result.below = border > above;
-          const float miss = border >= above ? static_cast<float>(border - above)
-                                             : -static_cast<float>(above - border);
-          S.result.need = S.win_w + miss * 9.5367432e-7f;  // 2^-44 to 2^-24
-        }
-        if (!missed) {  // the draw is among the list, in order of the index
-          S.list_w[tid] = w;
-          x = keep ? (static_cast<unsigned long long>(pos) << 32) | static_cast<uint32_t>(tid)
-                   : ~0ull;
-          x = group_sort(x, size, S.all);
-          group_sync(size);
-          w = x == ~0ull ? 0 : S.list_w[static_cast<uint32_t>(x)];
-          ex = group_scan(w, size, buf, kept_w);
-          if (ex <= to && to < ex + w) {
-            A.ids[row] = static_cast<int>((x >> 32) & 0x3ffffu);
-            if (A.probs) A.probs[row] = static_cast<float>(w) / static_cast<float>(total);
-          }
-        }
-      } else {
-        // the last kept token of the list, and the warps' sums with the
-        // list's kept tokens: which warp the draw falls on
-        if (tid == 0) {
-          S.result.state = 1;
-          S.result.total = total;
-          S.result.to = to;
-        }
-        const bool next = __shfl_down_sync(0xffffffffu, keep, 1);
-        if (lane == 0) S.next_kept[warp] = keep;
-        group_sync(size);
-        const bool after = lane < 31 ? next : tid + 1 < size && S.next_kept[warp + 1];
-        if (keep && !after) {
-          S.result.cut_key = key;
-          S.result.idx_cut = static_cast<int>(pos & 0x3ffffu);
-        }
-        if (keep) atomicAdd(&S.warp_mass[pos >> 18], w);
-        group_sync(size);
-        if (warp == 0) {
-          unsigned long long sum = 0;
-          for (int i0 = 0; i0 < warps; i0 += 32) {
-            const unsigned long long m = i0 + lane < warps ? S.warp_mass[i0 + lane] : 0;
-            unsigned long long incl = m;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-              const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
-              if (lane >= off) incl += y;
-            }
-            if (sum + incl - m <= to && to < sum + incl) {
-              S.result.who = i0 + lane;
-              S.result.before = sum + incl - m;
-            }
-            sum += __shfl_sync(0xffffffffu, incl, 31);
-          }
-        }
-      }
-      group_sync(size);
-      if (tid > 0 && tid < C) cluster.map_shared_rank(&S, tid)->result = S.result;
+      const bool have = from_cta >= 0 && from_at < kList;
+      unsigned long long x = ~0ull;
+      if (have) x = cluster.map_shared_rank(S.list, from_cta)[from_at];
+      S.all[tid] = x;
+      if (tid == 0) S.kept = 0;
+      __syncthreads();
+      const int n = min(n_list, kList);
+      int size = 32;  // of the group that works on the list
+      while (size < n) size *= 2;
+      if (tid < size) pick(n_list, n, size, x);
     }
     everyone();
     const int state = S.result.state;
@@ -1076,7 +1129,7 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     generic = state == 2;
     if (state == 3) {
       const float need = S.result.need;
-      if (tid == 0) S.list_n = S.all_n = 0;
+      if (tid == 0) S.list_n = 0;
       choose(need, S.result.below ? win_hi : -1, S.result.below ? 2 * kBins : win_lo);
       dense = S.at_count > kList;
       weigh_above = above_n > 0;
