@@ -4,7 +4,7 @@
 //
 // A token is chosen by where a sum passes a border, so two ways to add give
 // two answers unless the sums are exact: weights are whole numbers of 2^-43
-// of the largest one, computed to about 2^-38 of themselves, and added as
+// of the largest one, right to 2^-35 of themselves, and added as
 // 64-bit integers (in units of 2^-44).  A vocabulary of 2^18 stays below 2^63,
 // and no order of additions, of CTAs or of atomics changes a sum.
 //
@@ -118,17 +118,44 @@ __device__ __forceinline__ unsigned long long shift_right(unsigned long long x, 
   return y;
 }
 
+// Two floats in a register pair, and what one instruction does to both
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // What turns a logit l into its weight 2^x, x = (l - top) log2(e) / t, as a
 // whole number of 2^-44 (an even one: rounded at 2^-43).  Every lane of the
 // warp calls it, lane j holding T[j] = 2^(44 + j / 32).
 //   x = k / 32 + r:  2^x = 2^(k >> 5) T[k & 31] (1 + (2^r - 1)),  |r| <= 2^-6,
-// with r as the sum of an exact float and a small one, and 2^r - 1 in fixed
-// point of 2^-37: the sum is right to about 2^-38.
+// with l - top, log2(e) / t and r each as the sum of two floats, and 2^r - 1 in
+// fixed point of 2^-37: right to 2^-35 (two roundings to 2^-37, T's first 31
+// bits, three roundings of the second degree's term).
 struct Weigher {
   float top, ch, cl;    // c = log2(e) / t as a pair
-  float tg, tl;         // top c as a multiple of 2^-10 and the rest
   uint32_t t_hi, t_lo;  // T[lane], 45 bits
-  bool near;            // |top c| < 2^12: l c itself is a float pair near tg
 
   __device__ __forceinline__ void set(float top_, float ch_, float cl_, unsigned long long T) {
     top = top_;
@@ -136,43 +163,54 @@ struct Weigher {
     cl = cl_;
     t_hi = static_cast<uint32_t>(T >> 32);
     t_lo = static_cast<uint32_t>(T);
-    const float p = top * ch;
-    near = fabsf(p) < 4096.0f;
-    tg = rintf(p * 1024.0f) * 0.0009765625f;
-    tl = (p - tg) + fmaf(top, cl, fmaf(top, ch, -p));
   }
-  // l is at most top.  What lies below 2^-45, -inf and NaN get 0: z's bits then
-  // stand for a shift by more than 45 (the bits of floats ascend with them, a
-  // negative z or NaN gives a negative shift, which counts as 2^32 less that),
-  // and the shift leaves nothing, whatever the fraction's bits
+  // of two logits, by the same operations on pairs of floats (512 rows of
+  // 131072 with top-p: 303 -> 287 us).  A logit is at most top
+  __device__ __forceinline__ void both(float l0, float l1, unsigned long long& w0,
+                                       unsigned long long& w1) const {
+    F2 z;
+    const int2 E = fraction(l0, l1, z);
+    w0 = whole(halves(z).x, E.x);
+    w1 = whole(halves(z).y, E.y);
+  }
   __device__ __forceinline__ unsigned long long operator()(float l) const {
+    F2 z;
+    const int E = fraction(l, l, z).x;
+    return whole(halves(z).x, E);
+  }
+
+ private:
+  // 2^r - 1 in units of 2^-37; z: k as the low bits of a float
+  __device__ __forceinline__ int2 fraction(float l0, float l1, F2& z) const {
     constexpr float kRound = 12582912.0f;  // 1.5 2^23: x + kRound - kRound rounds x
-    float rh, small, z;  // r = rh + small, rh exact; z: k as the low bits of a float
-    if (near) {
-      const float p = l * ch;
-      const float e = fmaf(l, ch, -p);  // exact
-      z = fmaf(p - tg, 32.0f, kRound);
-      rh = p - fmaf(z - kRound, 0.03125f, tg);  // the fma is exact: a multiple of 2^-10
-      small = fmaf(l, cl, e - tl);
-    } else {
-      // large logits or a small t: from the difference, with its rounding error
-      const float dh = l - top;
-      const float b = dh - l;
-      const float dl = (l - (dh - b)) - (top + b);
-      const float ph = dh * ch;
-      z = fmaf(ph, 32.0f, kRound);
-      rh = fmaf(z - kRound, -0.03125f, ph);
-      small = fmaf(dh, ch, -ph) + fmaf(dh, cl, dl * ch);
-    }
-    const int bits = __float_as_int(z);  // 0x4b400000 + k
-    // 2^r - 1 in units of 2^-37: ln 2 as a pair, degrees 2 to 4 in floats
+    const F2 round = f2(kRound, kRound), back = f2(-kRound, -kRound), l32 = f2(32.0f, 32.0f);
+    F2 rh, small;  // r = rh + small, rh exact
+    const F2 l = f2(l0, l1), c = f2(ch, ch), t = f2(top, top), minus = f2(-1.0f, -1.0f);
+    const F2 dh = add2(l, f2(-top, -top));
+    const F2 b = fma2(l, minus, dh);  // (a product with -1 is exact)
+    const F2 dl = fma2(add2(t, b), minus, fma2(fma2(b, minus, dh), minus, l));
+    const F2 ph = mul2(dh, c);
+    z = fma2(ph, l32, round);
+    rh = fma2(add2(z, back), f2(-0.03125f, -0.03125f), ph);
+    small = add2(fma2(dh, c, mul2(dh, f2(-ch, -ch))), fma2(dh, f2(cl, cl), mul2(dl, c)));
+    // ln 2 as a pair, degrees 2 to 4 in floats
     constexpr float kC1 = 95265423360.0f, kC1l = -261.773682f;
     constexpr float kC2 = 33016479744.0f, kC3 = 7628426752.0f, kC4 = 1321905536.0f;
-    const float a = rh * kC1;
-    const float rest = fmaf(small, kC1, fmaf(rh, kC1l, fmaf(rh, kC1, -a)));
-    const float r = rh + small;
-    const float q = fmaf(fmaf(r, kC4, kC3), r, kC2);
-    const int E = __float2int_rn(a) + __float2int_rn(fmaf(q, r * r, rest));
+    const F2 C1 = f2(kC1, kC1), a = mul2(rh, C1);
+    const F2 rest = fma2(small, C1,
+                         fma2(rh, f2(kC1l, kC1l), fma2(rh, C1, mul2(rh, f2(-kC1, -kC1)))));
+    const F2 r = add2(rh, small);
+    const F2 q = fma2(fma2(r, f2(kC4, kC4), f2(kC3, kC3)), r, f2(kC2, kC2));
+    const float2 x = halves(a), y = halves(fma2(q, mul2(r, r), rest));
+    return make_int2(__float2int_rn(x.x) + __float2int_rn(y.x),
+                     __float2int_rn(x.y) + __float2int_rn(y.y));
+  }
+  // What lies below 2^-45, -inf and NaN get 0: z's bits then stand for a shift
+  // by more than 45 (the bits of floats ascend with them, a negative z or NaN
+  // gives a negative shift, which counts as 2^32 less that), and the shift
+  // leaves nothing, whatever the fraction's bits
+  __device__ __forceinline__ unsigned long long whole(float z, int E) const {
+    const int bits = __float_as_int(z);  // 0x4b400000 + k
     const uint32_t hi = __shfl_sync(0xffffffffu, t_hi, bits);
     const uint32_t lo = __shfl_sync(0xffffffffu, t_lo, bits);
     const long long T = static_cast<long long>((static_cast<unsigned long long>(hi) << 32) | lo);
@@ -899,9 +937,10 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
   if (!list_on) {
     sl.template sweep<kFew>([&](const float (&v)[VE], int, int) {
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const unsigned long long w = weigh(v[j]);
-        if (!min_on || v[j] >= l_min) w_mine += w;
+      for (int j = 0; j < VE; j += 2) {
+        unsigned long long w[2];
+        weigh.both(v[j], v[j + 1], w[0], w[1]);
+        w_mine += (v[j] >= l_min ? w[0] : 0) + (v[j + 1] >= l_min ? w[1] : 0);
       }
     });
     w_mine = warp_sum(w_mine);
@@ -1055,11 +1094,15 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       sl.template sweep<kFew>([&](const float (&v)[VE], int at, int) {
         bool in = false;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {  // without branches: the weights' steps interleave
-          const unsigned long long w = weigh(v[j]);
-          everything += v[j] >= l_min ? w : 0;
-          above += v[j] >= from ? w : 0;
-          in |= v[j] >= down_to && !(v[j] >= from);
+        for (int j = 0; j < VE; j += 2) {  // without branches: the weights' steps interleave
+          unsigned long long w[2];
+          weigh.both(v[j], v[j + 1], w[0], w[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            everything += v[j + i] >= l_min ? w[i] : 0;
+            above += v[j + i] >= from ? w[i] : 0;
+            in |= v[j + i] >= down_to && !(v[j + i] >= from);
+          }
         }
         if (in) {
 #pragma unroll

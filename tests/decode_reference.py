@@ -110,7 +110,7 @@ def attend(q, k, v, table, lens, scale, window=0, k_scale=None, v_scale=None):
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, largest=np.inf):
     """ids and probs of every row (largest: what +inf counts as), how near a
     border the draw and the top-p cut came, and how far the sums they are
-    compared with may be off: weights that are right to 2^-38 of themselves and
+    compared with may be off: weights that are right to 2^-35 of themselves and
     to 2^-45 of the largest one, on both sides of the border.  Both as a share
     of the kept sum."""
     B, V = logits.shape
@@ -147,7 +147,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, larg
         j = min(int((sums <= border).sum()), int(np.flatnonzero(w[kept])[-1]))
         near[b] = min(near[b], np.abs(sums - border).min() / sums[-1])
         ids[b], probs[b] = kept[j], w[kept[j]] / sums[-1]
-        off[b] = 2 * (2.0 ** -38 + len(order) * 2.0 ** -45 / sums[-1])
+        off[b] = 2 * (2.0 ** -35 + len(order) * 2.0 ** -45 / sums[-1])
     return ids, probs, near, off
 
 
