@@ -308,7 +308,7 @@ struct SampShared {
   unsigned long long warp_mass[kMaxCluster * kSampWarps];
   unsigned long long warp_all[kMaxCluster * kSampWarps];
   unsigned long long part_mass[kSampWarps];
-  int cut_idx;  // written by one CTA into every one
+  int cut_idx;
   Result result;
   long long scan[2 * kSampWarps];
   int at_bin, at_count, win_lo, win_hi, above_n;
@@ -945,7 +945,6 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     });
     w_mine = warp_sum(w_mine);
   }
-  uint32_t bin_lo = 0xffffffffu, bin_hi = 0;  // a dense bin's order keys
   // the lowest logit in the bins 0 .. b that min-p keeps; above the largest for
   // b < 0
   auto edge = [&](int b) {
@@ -956,7 +955,26 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
                                1e-5f * (1.0f + fabsf(top) + static_cast<float>(b) * width),
                                [&](float l) { return bin_of(l) <= b; }));
   };
+  Cut cut = {0, INT_MAX};
+  long long ties = LLONG_MAX;      // kept of the tokens equal to the cut
+  bool alike = false;              // a dense bin holds one value
   unsigned long long above = 0, everything = 0;
+  // a dense bin's first and last order key, and the sums, from the warps'
+  auto dense_sums = [&](uint32_t& bin_lo, uint32_t& bin_hi) {
+    above = everything = 0;
+    bin_lo = 0xffffffffu;
+    bin_hi = 0;
+    for (int i = lane; i < warps; i += 32) {
+      above += S.warp_mass[i];
+      everything += S.warp_all[i];
+      bin_lo = min(bin_lo, S.warp_key[i].x);
+      bin_hi = max(bin_hi, S.warp_key[i].y);
+    }
+    above = warp_sum(above);
+    everything = warp_sum(everything);
+    bin_lo = __reduce_min_sync(0xffffffffu, bin_lo);
+    bin_hi = __reduce_max_sync(0xffffffffu, bin_hi);
+  };
   // The last kept token of the row's list, and the draw or the warp that it falls
   // on: by the first CTA's first `size` threads, x a token of each
   int tries = 0;
@@ -1070,15 +1088,11 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     group_sync(size);
     if (tid > 0 && tid < C) cluster.map_shared_rank(&S, tid)->result = S.result;
   };
+  float from = 0.0f, down_to = 0.0f;  // the window's ends
   for (; list_on && !generic; ++tries) {
     // ---- C
     above = everything = 0;
     auto enlist = [&](float v, int idx) {
-      if (dense) {
-        bin_lo = min(bin_lo, order_key(v));
-        bin_hi = max(bin_hi, order_key(v));
-        return;
-      }
       const int at = atomicAdd(&S.list_n, 1);
       if (at < kList)
         S.list[at] = (static_cast<unsigned long long>(~order_key(v)) << 32) |
@@ -1089,7 +1103,8 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       if (lane == 0) S.edge[warp] = e;
     }
     __syncthreads();
-    const float from = S.edge[0], down_to = S.edge[1];  // the window's ends
+    from = S.edge[0];
+    down_to = S.edge[1];
     if (weigh_all) {
       sl.template sweep<kFew>([&](const float (&v)[VE], int at, int) {
         bool in = false;
@@ -1180,9 +1195,49 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     }
   }
 
-  Cut cut = {0, INT_MAX};
-  if (generic || dense) {
-    // ---- D.  `narrow`: the order key, lo .. hi, where the count or the weight
+  // ---- D
+  if (dense && !generic) {
+    // the border lies in one bin, all of whose tokens are often alike (bf16):
+    // then their number and the sums say everything
+    uint32_t bin_lo = 0xffffffffu, bin_hi = 0;
+    int n = 0;
+    sl.template sweep<4>([&](const float (&v)[VE], int, int) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        if (v[j] >= down_to && !(v[j] >= from)) {
+          bin_lo = min(bin_lo, order_key(v[j]));
+          bin_hi = max(bin_hi, order_key(v[j]));
+          ++n;
+        }
+    });
+    bin_lo = __reduce_min_sync(0xffffffffu, bin_lo);
+    bin_hi = __reduce_max_sync(0xffffffffu, bin_hi);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane < C) {
+      cluster.map_shared_rank(S.warp_all, lane)[my_warp] = everything;
+      cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = above;
+      cluster.map_shared_rank(S.warp_key, lane)[my_warp] = make_uint2(bin_lo, bin_hi);
+      cluster.map_shared_rank(S.warp_tie, lane)[my_warp] = n;
+    }
+    everyone();
+    w_mine = above;
+    dense_sums(bin_lo, bin_hi);
+    const long long border = k ? k : max(1ll, static_cast<long long>(border_of(everything)));
+    const long long passed = k ? above_n : static_cast<long long>(above);
+    bool missed = passed >= border;
+    if (!missed && bin_lo == bin_hi) {
+      const long long w = k ? 1 : static_cast<long long>(weigh_call(weigh, key_value(bin_lo)));
+      missed = w == 0 || border - passed > w * S.at_count;
+      if (!missed) {
+        alike = true;
+        cut.key = bin_lo;
+        ties = (border - passed + w - 1) / w;
+      }
+    }
+    generic = missed;  // the border is beside the bin
+  }
+  if ((generic || dense) && !alike) {
+    // `narrow`: the order key, lo .. hi, where the count or the weight
     // of the keys from it up reaches `need`, or 0; the same in all CTAs.
     // Histograms over keys hi - 2^sh i, on ever fewer keys.  passed: what the
     // keys above hi come to, then those above the result
@@ -1192,7 +1247,12 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         everyone();  // nobody reads the last histogram any more
         for (int i = tid; i < kKeyBins; i += kSampThreads) S.lo[i] = S.hi[i] = 0;
         __syncthreads();
-        sl.template sweep<1>([&](const float (&v)[VE], int, int) {
+        sl.template sweep<4>([&](const float (&v)[VE], int, int) {
+          bool some = false;  // most chunks have none
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            some |= v[j] >= l_min && order_key(v[j]) >= lo && order_key(v[j]) <= hi;
+          if (!__any_sync(0xffffffffu, some)) return;
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             const uint32_t key = order_key(v[j]);
@@ -1266,6 +1326,9 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         hi -= static_cast<uint32_t>(S.at_bin) << sh;
         __syncthreads();
         if (sh == 0) return hi;
+        // keys of bf16 lie 2^16 apart, so a bin has one: those of negative
+        // logits end in ones, one below where a positive hi's bins begin
+        if (ES == 2 && sh <= 16) return (hi & 0x8000ffffu) == 0 ? hi - 1 : hi;
         lo = max(lo, hi - ((1u << sh) - 1u));
       }
     };
@@ -1280,48 +1343,25 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
       return warp_sum(x);
     };
     const uint32_t key_min = order_key(l_min), key_top = order_key(top);
-    long long ties = LLONG_MAX, passed = 0;  // kept of the tokens equal to the cut
-    unsigned long long base = 0;             // this warp's weight above key_end
-    uint32_t key_end = 0xffffffffu;
-    if (dense && !generic) {
-      // the border lies in one bin, all of whose tokens are often alike (bf16)
-      bin_lo = __reduce_min_sync(0xffffffffu, bin_lo);
-      bin_hi = __reduce_max_sync(0xffffffffu, bin_hi);
-      if (lane < C) {
-        cluster.map_shared_rank(S.warp_all, lane)[my_warp] = everything;
-        cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = above;
-        cluster.map_shared_rank(S.warp_key, lane)[my_warp] = make_uint2(bin_lo, bin_hi);
-      }
-      everyone();
-      base = above;
-      above = everything = 0;
-      for (int i = lane; i < warps; i += 32) {
-        above += S.warp_mass[i];
-        everything += S.warp_all[i];
-        bin_lo = min(bin_lo, S.warp_key[i].x);
-        bin_hi = max(bin_hi, S.warp_key[i].y);
-      }
-      above = warp_sum(above);
-      everything = warp_sum(everything);
-      bin_lo = __reduce_min_sync(0xffffffffu, bin_lo);
-      bin_hi = __reduce_max_sync(0xffffffffu, bin_hi);
-      const unsigned long long border = k ? k : border_of(everything);
-      passed = static_cast<long long>(k ? above_n : above);
-      generic = static_cast<unsigned long long>(passed) >= border;
-      if (!generic) {
-        cut.key = narrow(!k, static_cast<long long>(border), bin_lo, bin_hi, passed);
-        generic = cut.key == 0;
-      }
-      if (!generic) {
-        const unsigned long long w = k ? 1 : weigh_call(weigh, key_value(cut.key));
-        ties = static_cast<long long>((border - passed + w - 1) / w);
-        key_end = bin_hi;
-      }
+    long long passed = 0;
+    uint32_t key_end = 0xffffffffu;  // w_mine has the weights of the keys above it
+    if (!generic) {
+      uint32_t bin_lo;
+      dense_sums(bin_lo, key_end);
+      const long long border = k ? k : max(1ll, static_cast<long long>(border_of(everything)));
+      passed = k ? above_n : static_cast<long long>(above);
+      cut.key = narrow(!k, border, bin_lo, key_end, passed);
+      const long long w =
+          k ? 1 : static_cast<long long>(weigh_call(weigh, key_value(cut.key ? cut.key : bin_lo)));
+      generic = cut.key == 0 || w == 0;  // the border is beside the bin
+      if (!generic) ties = (border - passed + w - 1) / w;
     }
     if (generic) {
-      base = 0;
-      passed = 0;
       cut.key = 0;
+      ties = LLONG_MAX;
+      key_end = 0xffffffffu;
+      w_mine = 0;
+      passed = 0;
       if (k) {
         unsigned long long live = 0;
         sl.template sweep<4>([&](const float (&v)[VE], int, int) {
@@ -1359,80 +1399,83 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
         }
       }
     }
-    // the index of the last kept tie
-    int here = 0;
+    int here = 0;              // this warp's tokens equal to the cut
+    unsigned long long x = 0;  // and the weights between it and key_end
     sl.template sweep<4>([&](const float (&v)[VE], int, int) {
+      bool some = false;
 #pragma unroll
-      for (int j = 0; j < VE; ++j) here += v[j] >= l_min && order_key(v[j]) == cut.key;
-    });
-    here = __reduce_add_sync(0xffffffffu, here);
-    if (lane < C) cluster.map_shared_rank(S.warp_tie, lane)[my_warp] = here;
-    if (tid == 0) S.cut_idx = INT_MAX;
-    everyone();
-    unsigned long long ties_before = 0;
-    for (int i = lane; i < my_warp; i += 32) ties_before += static_cast<unsigned>(S.warp_tie[i]);
-    long long left = ties - static_cast<long long>(warp_sum(ties_before));
-    if (left > 0 && here >= left) {  // the left-th tie of this warp
-      sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
-        int hit = 0;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) hit += v[j] >= l_min && order_key(v[j]) == cut.key;
-        int incl = hit;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += y;
-        }
-        int n = incl - hit;
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-          if (v[j] >= l_min && order_key(v[j]) == cut.key && ++n == left)
-            for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&S.cut_idx, r) = at + j;
-        left -= __shfl_sync(0xffffffffu, incl, 31);
-      });
-    }
-    everyone();
-    cut.idx = S.cut_idx;
-    // this warp's weight of what is kept
-    sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
+      for (int j = 0; j < VE; ++j)
+        some |= v[j] >= l_min && order_key(v[j]) >= cut.key && order_key(v[j]) <= key_end;
+      if (!__any_sync(0xffffffffu, some)) return;
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
         const uint32_t key = order_key(v[j]);
-        const bool ok = v[j] >= l_min && key <= key_end && cut.keeps(key, at + j);
+        const bool ok = v[j] >= l_min && key > cut.key && key <= key_end;
+        here += v[j] >= l_min && key == cut.key;
         if (__any_sync(0xffffffffu, ok)) {
           const unsigned long long w = weigh_call(weigh, v[j]);
-          w_mine += ok ? w : 0;
+          x += ok ? w : 0;
         }
       }
     });
-    w_mine = warp_sum(w_mine) + base;
+    w_mine += warp_sum(x);
+    here = __reduce_add_sync(0xffffffffu, here);
+    everyone();  // the sums before have been read
+    if (lane < C) cluster.map_shared_rank(S.warp_tie, lane)[my_warp] = here;
   }
+  const unsigned long long w_cut = cut.key ? weigh_call(weigh, key_value(cut.key)) : 0;
   unsigned long long before, total, to;
   int who = -1;
   if (generic || dense || !list_on) {
-    // every warp finds the one that the draw falls on
-    if (lane < C) cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = w_mine;
-    everyone();
+    // every warp finds the one that the draw falls on.  A warp's tokens equal to
+    // the cut count as far as there are `ties` left for them
+    if (!alike) {
+      if (lane < C) cluster.map_shared_rank(S.warp_mass, lane)[my_warp] = w_mine;
+      everyone();
+    }
+    unsigned long long tied = 0;
     total = 0;
-    for (int i = lane; i < warps; i += 32) total += S.warp_mass[i];
+    for (int i = lane; i < warps; i += 32) {
+      total += S.warp_mass[i];
+      if (cut.key) tied += static_cast<unsigned>(S.warp_tie[i]);
+    }
     total = warp_sum(total);
+    if (cut.key) total += min(warp_sum(tied), static_cast<unsigned long long>(ties)) * w_cut;
     to = target(total);
     unsigned long long sum = 0;
+    long long ties_left = ties;
     before = 0;
     for (int i0 = 0; i0 < warps; i0 += 32) {
-      const unsigned long long m = i0 + lane < warps ? S.warp_mass[i0 + lane] : 0;
+      unsigned long long m = i0 + lane < warps ? S.warp_mass[i0 + lane] : 0;
+      int n = 0, kept = 0;
+      if (cut.key) {
+        n = i0 + lane < warps ? S.warp_tie[i0 + lane] : 0;
+        int upto = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
+        }
+        kept = static_cast<int>(max(0ll, min(static_cast<long long>(n), ties_left - (upto - n))));
+        m += static_cast<unsigned long long>(kept) * w_cut;
+        ties_left -= __shfl_sync(0xffffffffu, upto, 31);
+      }
       unsigned long long incl = m;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += y;
       }
-      const unsigned hit =
-          __ballot_sync(0xffffffffu, sum + incl - m <= to && to < sum + incl);
+      const unsigned hit = __ballot_sync(0xffffffffu, sum + incl - m <= to && to < sum + incl);
       if (hit) {
         const int at = __ffs(hit) - 1;
         who = i0 + at;
         before = __shfl_sync(0xffffffffu, sum + incl - m, at);
+        if (cut.key) {
+          kept = __shfl_sync(0xffffffffu, kept, at);
+          n = __shfl_sync(0xffffffffu, n, at);
+          cut.idx = kept == n ? INT_MAX : -1 - kept;
+        }
       }
       sum += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -1446,6 +1489,29 @@ __global__ void __launch_bounds__(kSampThreads, kSampCtas) sample_kernel(const S
     to = R.to;
   }
   if (who / kSampWarps != rank) return;
+  if (cut.idx < -1) {  // of that warp's tokens equal to the cut so many are kept: up to which index
+    if (warp == who % kSampWarps) {
+      int left = -1 - cut.idx;
+      sl.template sweep<1>([&](const float (&v)[VE], int at, int) {
+        int hit = 0;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) hit += v[j] >= l_min && order_key(v[j]) == cut.key;
+        int incl = hit;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += y;
+        }
+        int n = incl - hit;
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          if (v[j] >= l_min && order_key(v[j]) == cut.key && ++n == left) S.cut_idx = at + j;
+        left -= __shfl_sync(0xffffffffu, incl, 31);
+      });
+    }
+    __syncthreads();
+    cut.idx = S.cut_idx;
+  }
   // ---- that warp's tokens once more: every warp of its CTA adds up an eighth
   // of them, and the one whose eighth the draw falls in walks through it
   {

@@ -250,3 +250,22 @@ def test_top_p_beside_a_sum(dt, likely, spread):
     for _ in range(2):
         top_p = np.nextafter(top_p, side).astype(np.float32)
     _check(x, u, least=0.5, top_p=np.clip(top_p, 0, 1))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("values", [(2.0,), (0.5, 0.498), (-0.25, -0.251), (0.0, -0.001, 0.002),
+                                    (1.0, 0.996, 0.992, 0.988)])
+def test_many_tokens_of_few_values(dt, values):
+    # the border's bin holds hundreds of tokens of one or of a few values, above
+    # and below zero, with others around them
+    B, V = 12, 30000
+    x, u = _logits(31, B, V, "f32", spread=1.0, likely=5)
+    g = torch.Generator(device=DEV).manual_seed(7)
+    pick = torch.randint(len(values) + 1, (B, V), generator=g, device=DEV)
+    for i, v in enumerate(values):
+        x[pick == i] = v
+    x = x.to(DT[dt])
+    rng = np.random.default_rng(4)
+    _check(x, u, least=0.7, top_p=rng.uniform(0.3, 0.95, B), temperature=rng.uniform(0.7, 2.0, B))
+    _check(x, u, top_k=rng.integers(200, 20000, B))
+    _check(x, u, least=0.7, top_k=rng.integers(200, 20000, B), top_p=rng.uniform(0.3, 0.95, B))
