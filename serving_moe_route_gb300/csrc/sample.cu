@@ -25,19 +25,23 @@
 //      token exactly; the draw is among the list when nothing lies above it,
 //      else it goes by the warps' sums, and the warp whose tokens it falls on
 //      walks through them once more.
-//   D  where the border's bin alone has more than 256 tokens (equal ones, with
-//      bf16), or there is no such bin (top-p among the many that a large top-k
-//      left): the border is narrowed to one logit value by histograms over
-//      order keys (at most three), and ties are counted in index order.
+//      A border that the bins' weights put into the wrong bin is looked for once
+//      more, beyond the window that the exact sums rule out.
+//   D  where the border's bin alone has more than 256 tokens: equal ones, as is
+//      usual with bf16, need their number only.  Others, or where there is no
+//      such bin (top-p among the many that a large top-k left): the border is
+//      narrowed to one logit value by histograms over order keys (at most
+//      three), and ties count in index order.
 // Rows without top-k and top-p only need their sums.
 //
 // Bound by latency for few rows (a dozen steps, each a few dependent loads or a
 // cluster barrier); for many by the row's bytes where it is greedy or top-k is
-// small, and by the weights' instructions (about 60 a token, once) and the
-// counts' shared-memory additions where the whole vocabulary has to be weighed.
-// Measured on a GB300: one row of 131072 f32 with every restriction 13 us; 64 of
-// 50257 bf16 with mixed ones 32 us; 512 of 131072 f32 greedy 76 us (3.5 TB/s of
-// logits), top-k 119, no restriction 187, top-p 348.  With the rows' slices kept
+// small, and by instructions where the whole vocabulary has to be weighed (55 a
+// token in all; 97 with the counts and the list of top-p, and the counts'
+// shared-memory additions).
+// Measured on a GB300: one row of 131072 f32 with every restriction 12 us; 64 of
+// 50257 bf16 with mixed ones 30 us; 512 of 131072 f32 greedy 76 us (3.5 TB/s of
+// logits), top-k 111, no restriction 181, top-p 296.  With the rows' slices kept
 // in shared memory (two CTAs an SM) the last four took 101, 222, 257 and 563 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
