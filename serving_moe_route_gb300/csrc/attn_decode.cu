@@ -36,11 +36,11 @@
 //            joins them in range order: no atomics, one fixed result.
 //
 // Bound by the cache's bytes on long lengths and by a fixed part otherwise,
-// about 4 us before the first product (lengths, page ids, first rows) and 4
+// about 4 us before the first product (lengths, page ids, first rows) and 3
 // after the last (the second kernel).  Measured on a GB300, 32 query heads on 4
-// of 128: one request of 262161 tokens, bf16: 88 us, 6.1 TB/s (90% of the copy
-// bandwidth); 256 up to 8192, e4m3: 137 us, 5.2 TB/s; 64 up to 4096, bf16:
-// 42 us, 4.3 TB/s, f32: 92 us, 3.9 TB/s, whose split operands' instructions
+// of 128: one request of 262161 tokens, bf16: 89 us, 6.0 TB/s (89% of the copy
+// bandwidth); 256 up to 8192, e4m3: 128 us, 5.6 TB/s; 64 up to 4096, bf16:
+// 38 us, 4.8 TB/s, f32: 90 us, 4.0 TB/s, whose split operands' instructions
 // bound it; one of 700: 8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -929,12 +929,13 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
         }
       }
     }
-    if (!whole && t_first == 0 && threadIdx.x == 0) {
-      // the unit begins here and goes on in the next CTAs, up to the one
-      // whose range holds its last tile
-      const long long last = end - unit.left + unit.nt - 1;  // place of its last tile
-      const long long who = ((last + 1) * ctas - 1) / total;
-      A.info[cta] = make_int4(cc.b, cc.x, static_cast<int>(who - cta + 1), 0);
+    if (threadIdx.x == 0 && t_last + 1 < unit.nt) {
+      // the unit goes on in the next CTAs, up to the one whose range holds its
+      // last tile: how many have a part of it, and this one's place among them
+      const long long from = end - unit.left - t_first, to = from + unit.nt - 1;
+      const int c0 = static_cast<int>(((from + 1) * ctas - 1) / total);
+      const int c1 = static_cast<int>(((to + 1) * ctas - 1) / total);
+      A.info[cta] = make_int4(cc.b, cc.x, c1 - c0 + 1, cta - c0);
     }
     __syncthreads();  // the stages and s_m may be used again
     slot = slot + 1 == ST ? 0 : slot + 1;
@@ -944,65 +945,114 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
 }
 
-// Joins the parts of a unit that range borders cut.  Block (c, r): row r of
-// the unit that begins in CTA c and does not end there (most blocks find
-// none).  Its parts are c's first slot, then the second slots of the next
-// CTAs; the warps take every 16th part, so that the loads of a long request's
-// hundred parts are all in flight.
-constexpr int kJoinWarps = 16;
+// Joins the parts of the units that range borders cut: a unit that begins in
+// CTA c and does not end there has c's first slot, then the second slots of the
+// next CTAs.  Block c joins the unit that begins in CTA c if it has few parts, a
+// row a warp.  The rows of a unit of many parts go to the blocks of all CTAs that
+// it does not end in, whose warps take every 8th part, so that the loads of a
+// long request's hundred parts are all in flight.  One block per CTA of the first
+// kernel: all fit on the GPU at once (a block for each row and CTA, most without
+// work, started in waves: 42 us instead of 38 for 64 requests up to 4096).
+constexpr int kJoinWarps = 8;
+constexpr int kFewParts = 8;
 template <int KV, int DP>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs A) {
   constexpr int VL = DP / 32;  // columns per lane
   __shared__ float s_o[kJoinWarps][DP];
   __shared__ float s_l[kJoinWarps];
   pdl_wait();
-  const int cta = blockIdx.x, r = blockIdx.y;
-  const int4 u = A.info[cta];
-  if (u.z == 0) return;
-  const int kvh = u.y / A.blocks, h0 = kvh * A.group + (u.y % A.blocks) * kRows;
-  if (h0 + r >= (kvh + 1) * A.group) return;
+  const int4 unit = A.info[blockIdx.x];
+  const int parts = unit.z, cta = blockIdx.x - unit.w;
+  const bool few = parts <= kFewParts;
+  if (parts == 0 || (few && unit.w > 0)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto at = [&](int i) { return (2ll * (cta + i) + (i == 0 ? 0 : 1)) * kRows + r; };
-  float top = -INFINITY;
-  for (int i = lane; i < u.z; i += 32) top = fmaxf(top, A.part_ml[at(i)].x);
+  const int kvh = unit.y / A.blocks, h0 = kvh * A.group + (unit.y % A.blocks) * kRows;
+  const int rows = min(kRows, (kvh + 1) * A.group - h0);
+  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
+  for (int r = few ? warp : unit.w; r < rows; r += few ? kJoinWarps : parts - 1) {
+    auto at = [&](int p) { return (2ll * (cta + p) + (p == 0 ? 0 : 1)) * kRows + r; };
+    auto load = [&](int p, float (&v)[VL]) {
+      const float* x = A.part_o + at(p) * DP + lane * VL;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  float o[VL] = {};
-  float sum = 0.0f;
+      for (int j = 0; j < VL; j += 2)
+        *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(x + j);
+    };
+    float top = -INFINITY, sum = 0.0f;
+    float o[VL] = {};
+    if (few) {
+      const float2 ml = lane < parts ? A.part_ml[at(lane)] : make_float2(-INFINITY, 0.0f);
+      top = ml.x;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
+#pragma unroll
+      for (int p0 = 0; p0 < kFewParts; p0 += 4) {
+        if (p0 >= parts) break;
+        float v[4][VL];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          if (p0 + p < parts) load(p0 + p, v[p]);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if (p0 + p >= parts) break;
+          const float g = __shfl_sync(0xffffffffu, f, p0 + p);
+          sum += g * __shfl_sync(0xffffffffu, ml.y, p0 + p);
+#pragma unroll
+          for (int j = 0; j < VL; ++j) o[j] += g * v[p][j];
+        }
+      }
+      const float inv = sum == 0.0f ? 0.0f : mul / sum;
+      const long long to = unit.x * A.o_b + (h0 + r) * A.o_h + lane * VL;
+      if constexpr (VL >= 4) {
+#pragma unroll
+        for (int j = 0; j < VL; j += 4)
+          if (lane * VL + j < A.dim)
+            store4<KV>(A.out, to + j,
+                       make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv));
+      } else {  // two lanes' columns together
+        const float a = __shfl_down_sync(0xffffffffu, o[0], 1);
+        const float b = __shfl_down_sync(0xffffffffu, o[1], 1);
+        if (lane % 2 == 0 && lane * VL < A.dim)
+          store4<KV>(A.out, to, make_float4(o[0] * inv, o[1] * inv, a * inv, b * inv));
+      }
+    } else {
+      for (int p = lane; p < parts; p += 32) top = fmaxf(top, A.part_ml[at(p)].x);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
 #pragma unroll 4
-  for (int i = warp; i < u.z; i += kJoinWarps) {
-    const float2 ml = A.part_ml[at(i)];
-    const float* x = A.part_o + at(i) * DP + lane * VL;
-    float v[VL];
+      for (int p = warp; p < parts; p += kJoinWarps) {
+        const float2 ml = A.part_ml[at(p)];
+        float v[VL];
+        load(p, v);
+        const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
+        sum += f * ml.y;
 #pragma unroll
-    for (int j = 0; j < VL; j += 2)
-      *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(x + j);
-    const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
-    sum += f * ml.y;
+        for (int j = 0; j < VL; ++j) o[j] += f * v[j];
+      }
 #pragma unroll
-    for (int j = 0; j < VL; ++j) o[j] += f * v[j];
-  }
+      for (int j = 0; j < VL; ++j) s_o[warp][lane * VL + j] = o[j];
+      if (lane == 0) s_l[warp] = sum;
+      __syncthreads();
+      const int warps = min(kJoinWarps, parts);
+      sum = 0.0f;
+      for (int w = 0; w < warps; ++w) sum += s_l[w];
+      const int d = threadIdx.x * 4;
+      if (d < A.dim) {
+        float v[4] = {};
+        for (int w = 0; w < warps; ++w)
 #pragma unroll
-  for (int j = 0; j < VL; ++j) s_o[warp][lane * VL + j] = o[j];
-  if (lane == 0) s_l[warp] = sum;
-  __syncthreads();
-  const int warps = min(kJoinWarps, u.z);
-  for (int d = threadIdx.x * 4; d < A.dim; d += 128 * kJoinWarps) {
-    sum = 0.0f;
-    float v[4] = {};
-    for (int w = 0; w < warps; ++w) {
-      sum += s_l[w];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += s_o[w][d + j];
+          for (int j = 0; j < 4; ++j) v[j] += s_o[w][d + j];
+        const float inv = sum == 0.0f ? 0.0f : mul / sum;
+        store4<KV>(A.out, unit.x * A.o_b + (h0 + r) * A.o_h + d,
+                   make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+      }
     }
-    const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
-    const float inv = sum == 0.0f ? 0.0f : mul / sum;
-    store4<KV>(A.out, u.x * A.o_b + (h0 + r) * A.o_h + d,
-               make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
-    if (d == 0 && A.lse)
-      A.lse[static_cast<long long>(u.x) * A.Hq + h0 + r] =
+    if (A.lse && (few ? lane : static_cast<int>(threadIdx.x)) == 0)
+      A.lse[static_cast<long long>(unit.x) * A.Hq + h0 + r] =
           sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    if (!few) __syncthreads();  // s_o is used again
   }
 }
 
@@ -1030,8 +1080,7 @@ static cudaError_t launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, st, a);
   if (e != cudaSuccess) return e;
-  return launch_chained(attn_join_kernel<KV, DP>, dim3(ctas, a.group < kRows ? a.group : kRows),
-                        dim3(32 * kJoinWarps), 0, st, a);
+  return launch_chained(attn_join_kernel<KV, DP>, dim3(ctas), dim3(32 * kJoinWarps), 0, st, a);
 }
 
 template <int KV>

@@ -445,3 +445,17 @@ def test_a_whole_step_in_a_graph():
     assert moe.check_word(err) == (0, 0)
     used = table[table >= 0].tolist()
     assert len(set(used)) == len(used) == pool - int(n_free) == 4 * 3
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,Hq,Hkv", [
+    ([60000, 300, 0, 9000], 32, 2),   # parts by the hundred, a few and none, in one call
+    ([30011], 20, 1),                 # two units of 16 and of 4 rows on one cached head
+    ([900] * 40, 5, 1)])              # a cut about every unit
+def test_attend_joins_few_and_many_parts(kv, D, lens, Hq, Hkv):
+    q, kc, vc, table, lens, sc = _case(5, len(lens), Hq, Hkv, D, 16, kv, lens)
+    out, lse = moe.attn_decode(q, kc, vc, table, lens, return_lse=True, **sc)
+    _check(q, kc, vc, table, lens, out, lse, **sc)
+    again = moe.attn_decode(q, kc, vc, table, lens, **sc)
+    assert torch.equal(out, again)
