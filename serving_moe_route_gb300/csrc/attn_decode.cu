@@ -35,9 +35,9 @@
 //            range borders go to the workspace in fp32 and the second kernel
 //            joins them in range order: no atomics, one fixed result.
 //
-// Bound by the cache's bytes on long lengths and by a fixed part otherwise,
-// about 4 us before the first product (lengths, page ids, first rows) and 3
-// after the last (the second kernel).  Measured on a GB300, 32 query heads on 4
+// Bound by the cache's bytes on long lengths and by a fixed part otherwise, 7
+// us: 4 before the first product (lengths, page ids, first rows) and 1 for the
+// second kernel, which is left out where no unit can be cut.  Measured on a GB300, 32 query heads on 4
 // of 128: one request of 262161 tokens, bf16: 89 us, 6.0 TB/s (89% of the copy
 // bandwidth); 256 up to 8192, e4m3: 128 us, 5.6 TB/s; 64 up to 4096, bf16:
 // 38 us, 4.8 TB/s, f32: 90 us, 4.0 TB/s, whose split operands' instructions
@@ -1080,6 +1080,10 @@ static cudaError_t launch_attn(const AttnArgs& a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, st, a);
   if (e != cudaSuccess) return e;
+  // units of one tile are never cut: nothing to join
+  long long longest = static_cast<long long>(a.max_pages) * a.page;
+  if (a.window > 0 && a.window < longest) longest = a.window;
+  if (longest <= C::TILE) return cudaSuccess;
   return launch_chained(attn_join_kernel<KV, DP>, dim3(ctas), dim3(32 * kJoinWarps), 0, st, a);
 }
 
