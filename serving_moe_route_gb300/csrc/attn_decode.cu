@@ -36,12 +36,12 @@
 //            joins them in range order: no atomics, one fixed result.
 //
 // Bound by the cache's bytes on long lengths and by a fixed part otherwise, 7
-// us: 4 before the first product (lengths, page ids, first rows) and 1 for the
-// second kernel, which is left out where no unit can be cut.  Measured on a GB300, 32 query heads on 4
-// of 128: one request of 262161 tokens, bf16: 89 us, 6.0 TB/s (89% of the copy
-// bandwidth); 256 up to 8192, e4m3: 128 us, 5.6 TB/s; 64 up to 4096, bf16:
-// 38 us, 4.8 TB/s, f32: 90 us, 4.0 TB/s, whose split operands' instructions
-// bound it; one of 700: 8 us.
+// us: 4 before the first product (lengths, page ids, first rows) and 1 to 2 for
+// the second kernel, which is left out where no unit can be cut.  Measured on a
+// GB300, 32 query heads on 4 of 128: one request of 262161 tokens, bf16: 87 us,
+// 6.2 TB/s (91% of the copy bandwidth); 256 up to 8192, e4m3: 128 us, 5.6 TB/s;
+// 64 up to 4096, bf16: 37 us, 4.9 TB/s, f32: 89 us, 4.1 TB/s, whose split
+// operands' instructions bound it; one of 700: 7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -952,14 +952,16 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
 // it does not end in, whose warps take every 8th part, so that the loads of a
 // long request's hundred parts are all in flight.  One block per CTA of the first
 // kernel: all fit on the GPU at once (a block for each row and CTA, most without
-// work, started in waves: 42 us instead of 38 for 64 requests up to 4096).
+// work, started in waves: 42 us instead of 38 for 64 requests up to 4096).  A
+// part is loaded along with its maximum, a warp's rescaled to its own reference
+// (all maxima first: one load more in the chain, 0.7 us of a short call's 7.9).
 constexpr int kJoinWarps = 8;
 constexpr int kFewParts = 8;
 template <int KV, int DP>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs A) {
   constexpr int VL = DP / 32;  // columns per lane
   __shared__ float s_o[kJoinWarps][DP];
-  __shared__ float s_l[kJoinWarps];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   pdl_wait();
   const int4 unit = A.info[blockIdx.x];
   const int parts = unit.z, cta = blockIdx.x - unit.w;
@@ -981,11 +983,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
     float o[VL] = {};
     if (few) {
       const float2 ml = lane < parts ? A.part_ml[at(lane)] : make_float2(-INFINITY, 0.0f);
-      top = ml.x;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
+      float f = 0.0f;
 #pragma unroll
       for (int p0 = 0; p0 < kFewParts; p0 += 4) {
         if (p0 >= parts) break;
@@ -993,6 +991,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
 #pragma unroll
         for (int p = 0; p < 4; ++p)
           if (p0 + p < parts) load(p0 + p, v[p]);
+        if (p0 == 0) {  // with the first parts on their way
+          top = ml.x;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
+        }
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           if (p0 + p >= parts) break;
@@ -1017,33 +1022,60 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
           store4<KV>(A.out, to, make_float4(o[0] * inv, o[1] * inv, a * inv, b * inv));
       }
     } else {
-      for (int p = lane; p < parts; p += 32) top = fmaxf(top, A.part_ml[at(p)].x);
+      // a warp's parts by its own reference, then the warps by theirs
+      constexpr int kOnce = VL > 4 ? 2 : 4;
+      for (int p0 = warp; p0 < parts; p0 += kOnce * kJoinWarps) {
+        float2 ml[kOnce];
+        float v[kOnce][VL], t = top;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-#pragma unroll 4
-      for (int p = warp; p < parts; p += kJoinWarps) {
-        const float2 ml = A.part_ml[at(p)];
-        float v[VL];
-        load(p, v);
-        const float f = top == -INFINITY ? 1.0f : ex2(ml.x - top);
-        sum += f * ml.y;
+        for (int i = 0; i < kOnce; ++i) {
+          const int p = p0 + i * kJoinWarps;
+          ml[i] = make_float2(-INFINITY, 0.0f);
+          if (p < parts) {
+            ml[i] = A.part_ml[at(p)];
+            load(p, v[i]);
+          }
+        }
 #pragma unroll
-        for (int j = 0; j < VL; ++j) o[j] += f * v[j];
+        for (int i = 0; i < kOnce; ++i) t = fmaxf(t, ml[i].x);
+        const float g = t == -INFINITY ? 1.0f : ex2(top - t);
+        top = t;
+        sum *= g;
+#pragma unroll
+        for (int j = 0; j < VL; ++j) o[j] *= g;
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) {
+          if (p0 + i * kJoinWarps >= parts) break;
+          const float f = t == -INFINITY ? 1.0f : ex2(ml[i].x - t);
+          sum += f * ml[i].y;
+#pragma unroll
+          for (int j = 0; j < VL; ++j) o[j] += f * v[i][j];
+        }
       }
 #pragma unroll
       for (int j = 0; j < VL; ++j) s_o[warp][lane * VL + j] = o[j];
-      if (lane == 0) s_l[warp] = sum;
+      if (lane == 0) {
+        s_m[warp] = top;
+        s_l[warp] = sum;
+      }
       __syncthreads();
-      const int warps = min(kJoinWarps, parts);
+      float f[kJoinWarps];
+      top = -INFINITY;
       sum = 0.0f;
-      for (int w = 0; w < warps; ++w) sum += s_l[w];
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = top == -INFINITY ? 1.0f : ex2(s_m[w] - top);
+        sum += f[w] * s_l[w];
+      }
       const int d = threadIdx.x * 4;
       if (d < A.dim) {
         float v[4] = {};
-        for (int w = 0; w < warps; ++w)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] += s_o[w][d + j];
+        for (int w = 0; w < kJoinWarps; ++w)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] += f[w] * s_o[w][d + j];
         const float inv = sum == 0.0f ? 0.0f : mul / sum;
         store4<KV>(A.out, unit.x * A.o_b + (h0 + r) * A.o_h + d,
                    make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
