@@ -512,8 +512,11 @@ int moe_kv_append(const moe_kv_cache_t* cache, const void* k, long long k_stride
  *                the call
  * Tokens whose page id lies outside the cache are left out and set
  * MOE_DEVERR_BAD_PAGE.  What the cache holds beyond a request's tokens (in
- * the rest of its last page) is never used, whatever its bits; an infinite or
- * NaN key or value that is attended makes its rows of out infinite or NaN.
+ * the rest of its last page) is never used, whatever its bits.  An attended NaN
+ * makes what it reaches NaN, whatever its bits (a key the rows of its head, a
+ * value its column of them); an infinite logit counts as in the formula (-inf
+ * has weight 0, +inf gives NaN); an infinite value makes its column infinite
+ * or, in a BF16 cache, NaN.
  * q and out must be 16-byte aligned with strides of a multiple of 16 bytes.
  * The result is the same from call to call: no atomics join the parts.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (head_dim, strides,

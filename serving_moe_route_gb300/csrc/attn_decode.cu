@@ -139,18 +139,17 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo with 11 bits each, both rounded (the instruction cuts lo's last
-// bits): products of two such pairs without lo * lo are off by 3 x 2^-22 of
-// |x y| at most
-__device__ __forceinline__ uint32_t tf32_hi(float x) {
-  return (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-}
-__device__ __forceinline__ uint32_t tf32_lo(float x, uint32_t hi) {
-  return __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
-}
+// x = hi + lo: hi is x rounded to 11 bits, lo has the 12 bits (and a sign) that
+// are left, of which the instruction cuts the last where there are so many:
+// 2^-23 of x.  Products of two such pairs without lo * lo are off by 2^-21 of
+// |x y| at most (and by 2^-136 of each factor: subnormal terms' last places).
+// hi stays finite: a NaN is one in lo, and an infinity is lo's, so that a
+// logit, or a value by its weight, is the infinity that it is without a split.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = tf32_hi(x);
-  lo = tf32_lo(x, hi);
+  float y;  // with x's sign: no larger than what rounds to the largest number
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(__uint_as_float(0x7f7fefffu)));
+  hi = (__float_as_uint(y) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
