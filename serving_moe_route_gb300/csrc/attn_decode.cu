@@ -23,7 +23,8 @@
 //            instructions with the 16 query heads as rows.  One pass keeps a
 //            reference m and the sum l of each row in fp32 (base 2); m is a
 //            logit that was the largest when it was taken, and O is rescaled
-//            only when one lies 8 above it (weights stay below 2^8).  tcgen05
+//            only when one lies 8 above it, so that weights stay below 2^8
+//            (e4m3's, which are f16: below 2^15, LIFT and LAG below).  tcgen05
 //            needs 128 rows on its M side and its result in tensor memory; here
 //            one operand has 16 rows or fewer and the softmax works on its rows
 //            between the two products.  The m16n8 instructions suffice: without
@@ -191,6 +192,14 @@ struct AttnCfg {
   static constexpr int CTAS = SB == 16384 || NW == 8 ? 1 : SB == 8192 ? 2 : 3;
   static constexpr int ST = SB == 16384 ? 2 : SB == 8192 ? 3 : 4;
   static constexpr int THREADS = 32 * NW;
+  // Weights are 2^(x - m): a logit x (base 2) more than LAG above the one that m
+  // was taken from moves m, and that one itself has the weight 2^LIFT.  f16
+  // weights (e4m3) need both: up to 2^15, they keep 11 bits down to 2^-27 of that
+  // weight, and below it are off by 2^-38 of it at most, 2^-20 for 2^18 tokens;
+  // without the lift they would end at 2^-25, which a token that takes nearly
+  // all of the softmax leaves to a long context's others.
+  static constexpr float LIFT = KV == MOE_KV_E4M3 ? 13.0f : 0.0f;
+  static constexpr float LAG = KV == MOE_KV_E4M3 ? 2.0f : 8.0f;
   // what a unit's end and the next one's begin cost, in tiles (a batch of 64
   // with bf16, 180 MB: 56 us with 0, 45 with 1, 42 with 2 and 3; with f32, whose
   // tiles take longer, 92 us with 1, 95 with 2)
@@ -266,6 +275,13 @@ __device__ __forceinline__ void advance(Cursor& c, const AttnArgs& A, int units)
   if (++c.t < c.nt) return;
   c.left -= END;
   next_unit<TILE>(c, A, units);
+}
+
+// ln(sum 2^top), where weights are lifted by 2^lift: top without it and sum
+// without it are both near what their rounding should be relative to
+__device__ __forceinline__ float log_sum(float top, float sum, float lift) {
+  if (sum == 0.0f) return -INFINITY;
+  return ((top + lift) + log2f(sum * exp2f(-lift))) * 0.6931471805599453f;
 }
 
 template <int KV>
@@ -739,14 +755,15 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
           top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
           // (-inf: every key of the row is masked here, or its logit is -inf)
           top[r] = top[r] == -INFINITY ? -INFINITY : top[r] * f[r];
-          grow = grow || top[r] > m[r] + 8.0f;
+          grow = grow || top[r] > m[r] + (C::LIFT + C::LAG);
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            if (top[r] > m[r] + 8.0f) {
-              const float keep = ex2(m[r] - top[r]);
-              m[r] = top[r];
+            if (top[r] > m[r] + (C::LIFT + C::LAG)) {
+              const float to = top[r] - C::LIFT;
+              const float keep = ex2(m[r] - to);
+              m[r] = to;
               l[r] *= keep;
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
@@ -796,8 +813,9 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
             mma_bf16(acc[2 * dd + 1], pl, r[2], r[3]);
           }
         } else if constexpr (KV == MOE_KV_E4M3) {
-          // P rounded to f16: 2^-12 of each weight, as against the 2^-4 of
-          // the cached values themselves
+          // P rounded to f16: 2^-11 of each weight, as against the 2^-4 of the
+          // cached values themselves (as pairs of f16, like bf16's: 147 us for
+          // 256 requests up to 8192 where these take 129)
           uint32_t pt[C::KEYS / 16][4];
 #pragma unroll
           for (int h = 0; h < C::KEYS / 16; ++h)
@@ -920,8 +938,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
             store4<KV>(A.out, cc.b * A.o_b + (h0 + r) * A.o_h + d,
                        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
           if (d == 0 && A.lse)
-            A.lse[static_cast<long long>(cc.b) * A.Hq + h0 + r] =
-                sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+            A.lse[static_cast<long long>(cc.b) * A.Hq + h0 + r] = log_sum(top, sum, C::LIFT);
         } else {
           *reinterpret_cast<float4*>(A.part_o + (part * kRows + r) * DP + d) = o;
           if (d == 0) A.part_ml[part * kRows + r] = make_float2(top, sum);
@@ -1082,7 +1099,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
     }
     if (A.lse && (few ? lane : static_cast<int>(threadIdx.x)) == 0)
       A.lse[static_cast<long long>(unit.x) * A.Hq + h0 + r] =
-          sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+          log_sum(top, sum, AttnCfg<KV, DP>::LIFT);
     if (!few) __syncthreads();  // s_o is used again
   }
 }

@@ -129,3 +129,37 @@ def test_values_near_the_largest(bits):
     for t in range(30):
         k[_at(table, page, 1, t)] *= 1e-38
     check(x, k, vc)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nats", [8.0, 12.0, 17.5])
+def test_many_weights_far_below_the_largest(kv, D, nats):
+    # one token that takes nearly all of the softmax and has no value, as a
+    # context's first one often does: the answer is what the others leave.  An
+    # f16 weight's last place, half of it, is 2^-38 of the largest weight.
+    # Enough requests that a CTA has whole ones, so that a warp sees them all
+    B, Hq, n, page = 450, 2, 1200, 16
+    q, kc, vc, table, lens, sc = _case(4, 1, Hq, 1, D, page, kv, [n])
+    table, lens = table.expand(B, -1).contiguous(), lens.expand(B).contiguous()
+    q = torch.zeros(B, Hq, D, dtype=q.dtype, device=DEV)
+    q[:, :, 0] = 1.0
+    one = {k: torch.ones_like(v) for k, v in sc.items()}
+    kc.copy_(torch.zeros_like(kc, dtype=torch.float32).to(kc.dtype))
+    g = torch.Generator(device=DEV).manual_seed(0)
+    kc[:, :, 0, 0] = (torch.rand(kc.shape[:2], generator=g, device=DEV) - 0.5).to(kc.dtype)
+    kc[_at(table, page, 0, 3)][0, 0] = torch.tensor(16.0, device=DEV).to(kc.dtype)
+    vc.copy_((torch.rand(vc.shape, generator=g, device=DEV) + 0.5).to(vc.dtype))
+    vc[_at(table, page, 0, 3)] = torch.zeros((), device=DEV).to(vc.dtype)
+    out, lse = moe.attn_decode(q, kc, vc, table, lens, scale=nats / 16, return_lse=True, **one)
+    host = [R.f64(x) for x in (q[:1], kc, vc)]
+    want, want_lse, pv, dot, count = R.attend(*host, table[:1].cpu().numpy(), [n], nats / 16)
+    f32 = kv == "f32"
+    ds = dot * (D * 2.0 ** -23 + (3 * 2.0 ** -22 if f32 else 0.0))
+    w = {"f32": 2.0 ** -22, "bf16": 2.0 ** -16, "e4m3": 2.0 ** -11}[kv]
+    share = 2 * ds + count * 2.0 ** -24 + w + 2.0 ** -20
+    tol = (2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(want) + share[..., None] * pv
+    tol += n * 2.0 ** -38 * 1.5 if kv == "e4m3" else 0.0
+    got = R.f64(out)
+    assert (np.abs(got - want) <= tol).all(), f"{(np.abs(got - want) / tol).max():.3g} of the tolerance"
+    assert (np.abs(R.f64(lse) - want_lse) <= ds + n * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * nats).all()
