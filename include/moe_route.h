@@ -515,7 +515,7 @@ int moe_kv_append(const moe_kv_cache_t* cache, const void* k, long long k_stride
  * the rest of its last page) is never used, whatever its bits.  An attended NaN
  * makes what it reaches NaN, whatever its bits (a key the rows of its head, a
  * value its column of them); an infinite logit counts as in the formula (-inf
- * has weight 0, +inf gives NaN); an infinite value makes its column infinite
+ * has weight 0, alone or +inf gives NaN); an infinite value makes its column infinite
  * or, in a BF16 cache, NaN.
  * q and out must be 16-byte aligned with strides of a multiple of 16 bytes.
  * The result is the same from call to call: no atomics join the parts.

@@ -48,6 +48,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -773,11 +774,13 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
             }
           }
         }
-        const float z[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+        // from here on the row has tokens, if only of logits -inf: m says so
+        m[0] = fmaxf(m[0], -FLT_MAX);
+        m[1] = fmaxf(m[1], -FLT_MAX);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] = ex2(fmaf(s[j][e], f[e >> 1], -z[e >> 1]));
+          for (int e = 0; e < 4; ++e) s[j][e] = ex2(fmaf(s[j][e], f[e >> 1], -m[e >> 1]));
         if (mask != kAll) {
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
@@ -933,7 +936,8 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
           o.w += k * x.w;
         }
         if (whole) {
-          const float inv = sum == 0.0f ? 0.0f : v_mul / sum;
+          // -inf: no tokens.  A sum of 0 over some (logits of -inf) leaves NaN
+          const float inv = top == -INFINITY ? 0.0f : v_mul / sum;
           if (d < A.dim)
             store4<KV>(A.out, cc.b * A.o_b + (h0 + r) * A.o_h + d,
                        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
@@ -1023,7 +1027,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
           for (int j = 0; j < VL; ++j) o[j] += g * v[p][j];
         }
       }
-      const float inv = sum == 0.0f ? 0.0f : mul / sum;
+      const float inv = top == -INFINITY ? 0.0f : mul / sum;
       const long long to = unit.x * A.o_b + (h0 + r) * A.o_h + lane * VL;
       if constexpr (VL >= 4) {
 #pragma unroll
@@ -1092,7 +1096,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
         for (int w = 0; w < kJoinWarps; ++w)
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] += f[w] * s_o[w][d + j];
-        const float inv = sum == 0.0f ? 0.0f : mul / sum;
+        const float inv = top == -INFINITY ? 0.0f : mul / sum;
         store4<KV>(A.out, unit.x * A.o_b + (h0 + r) * A.o_h + d,
                    make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
       }

@@ -163,3 +163,26 @@ def test_many_weights_far_below_the_largest(kv, D, nats):
     got = R.f64(out)
     assert (np.abs(got - want) <= tol).all(), f"{(np.abs(got - want) / tol).max():.3g} of the tolerance"
     assert (np.abs(R.f64(lse) - want_lse) <= ds + n * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * nats).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_logits_that_are_all_minus_infinity(kv, D):
+    # a softmax over -inf alone has no value, unlike one over nothing; where one
+    # warp's or one CTA's tokens are -inf and others are not, they only weigh nothing
+    page = 16
+    q, kc, vc, table, lens, _ = _case(5, 5, 2, 1, D, page, kv, [1, 300, 0, 6000, 6000])
+    q[:, :, 2] = 0.5
+    for b, live in ((0, 0), (1, 0), (3, 0), (4, 9)):
+        for t in range(live, int(lens[b])):
+            kc[_at(table, page, b, t)][0, 2] = -float("inf")
+    out, lse = moe.attn_decode(q, kc, vc, table, lens, return_lse=True)
+    assert out[[0, 1, 3]].isnan().all()
+    assert (out[2] == 0).all()
+    assert (lse[:4] == -float("inf")).all()
+    short = lens.clone()
+    short[4] = 9
+    few, few_lse = moe.attn_decode(q, kc, vc, table, short, return_lse=True)
+    assert out[4].isfinite().all()
+    torch.testing.assert_close(out[4], few[4], rtol=2.0 ** -7, atol=1e-5)
+    torch.testing.assert_close(lse[4], few_lse[4], rtol=2.0 ** -20, atol=2.0 ** -19)
