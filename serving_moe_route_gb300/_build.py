@@ -3,7 +3,8 @@
 ``build()`` compiles ``csrc/*.cu`` (one translation unit each, in parallel) and
 links ``_lib/libmoe_route.so``, and with g++ the Python calls of the decode-step
 operators (``csrc/decode_ext.cpp``, against PyTorch's headers) into an extension
-module beside it.  The objects go to ``_build/``.
+module beside it, with a note of the PyTorch that it was built against.  The
+objects go to ``_build/``.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_route.so")
 EXT_SRC = os.path.join(CSRC, "decode_ext.cpp")
 EXT_PATH = os.path.join(LIB_DIR, "moe_decode_ext" + sysconfig.get_config_var("EXT_SUFFIX"))
+EXT_STAMP = EXT_PATH + ".torch"  # the PyTorch that it was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -45,11 +47,35 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
+    """Whether the library is newer than its sources."""
+    if not os.path.exists(LIB_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _deps()) and \
-        os.path.getmtime(EXT_SRC) <= os.path.getmtime(EXT_PATH)
+    return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _torch_abi() -> str:
+    """What an extension module has to have been built against: this PyTorch."""
+    import torch
+
+    return f"torch {torch.__version__} cxx11 {int(torch._C._GLIBCXX_USE_CXX11_ABI)}\n"
+
+
+def ext_abi_matches() -> bool:
+    """Whether the extension module was built against the PyTorch that runs."""
+    try:
+        with open(EXT_STAMP) as f:
+            return f.read() == _torch_abi()
+    except OSError:
+        return False
+
+
+def ext_up_to_date() -> bool:
+    """Whether the extension module is newer than its sources and fits this PyTorch."""
+    if not os.path.exists(EXT_PATH) or not ext_abi_matches():
+        return False
+    t = os.path.getmtime(EXT_PATH)
+    return all(os.path.getmtime(p) <= t for p in (EXT_SRC, os.path.join(INCLUDE, "moe_route.h")))
 
 
 def _torch_flags():
@@ -66,12 +92,33 @@ def _torch_flags():
                 f"-Wl,-rpath,{lib}"]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
-    if not force and up_to_date():
-        return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    os.makedirs(LIB_DIR, exist_ok=True)
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stderr}")
+    return r.stderr
+
+
+def _link(cmd, path):
+    """Run a link command (its output path left out) and put the result in place at once."""
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
+    os.close(fd)
+    try:
+        _run([*cmd, "-o", tmp], "link failed")
+    except BaseException:
+        os.unlink(tmp)
+        raise
+    os.replace(tmp, path)
+
+
+def _compile_ext() -> str:
+    obj = os.path.join(BUILD_DIR, "decode_ext.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", *_torch_flags()[0], "-c", EXT_SRC, "-o", obj],
+         f"g++ failed for {EXT_SRC}")
+    return obj
+
+
+def _build_lib(verbose) -> None:
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -79,45 +126,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
-        return obj, r.stderr
-
-    torch_cc, torch_ld = _torch_flags()
-
-    def compile_ext():
-        obj = os.path.join(BUILD_DIR, "decode_ext.o")
-        r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", *torch_cc, "-c", EXT_SRC, "-o", obj],
-                           capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for {EXT_SRC}:\n{r.stderr}")
-        return obj
+        return obj, _run(cmd, f"nvcc failed for {src}")
 
     with ThreadPoolExecutor(max_workers=8) as ex:
-        ext = ex.submit(compile_ext)
         results = list(ex.map(compile_one, _sources()))
-        ext_obj = ext.result()
-    objs = [o for o, _ in results]
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
-    os.close(fd)
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
-           "-Xlinker", "-rpath=/usr/local/cuda/lib64"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        os.unlink(tmp)
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=LIB_DIR)
-    os.close(fd)
-    cmd = ["g++", "-shared", "-o", tmp, ext_obj, "-L", LIB_DIR, "-lmoe_route",
-           "-Wl,-rpath,$ORIGIN", *torch_ld]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        os.unlink(tmp)
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, EXT_PATH)
+    _link([nvcc, *ARCH, "-shared", "-cudart", "shared", *(o for o, _ in results),
+           "-Xlinker", "-rpath=/usr/local/cuda/lib64"], LIB_PATH)
     if verbose:
         for _, log in results:
             print(log)
+
+
+def build(force: bool = False, verbose: bool = False, extension: bool = True) -> str:
+    """Compile what is older than its sources; return the library's path.
+
+    The library comes first and needs nvcc only.  ``extension``: also the module
+    of the decode-step calls, which needs g++ and PyTorch's C++ headers; without
+    it everything but those calls runs."""
+    lib = force or not up_to_date()
+    ext = extension and (force or not ext_up_to_date())
+    if not lib and not ext:
+        return LIB_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    os.makedirs(LIB_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as pool:
+        ext_obj = pool.submit(_compile_ext) if ext else None
+        if lib:
+            _build_lib(verbose)
+        if ext:
+            obj = ext_obj.result()  # an error in it leaves the library built
+            if os.path.exists(EXT_STAMP):
+                os.unlink(EXT_STAMP)
+            _link(["g++", "-shared", obj, "-L", LIB_DIR, "-lmoe_route", "-Wl,-rpath,$ORIGIN",
+                   *_torch_flags()[1]], EXT_PATH)
+            with open(EXT_STAMP, "w") as f:
+                f.write(_torch_abi())
     return LIB_PATH

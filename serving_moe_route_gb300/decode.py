@@ -58,10 +58,12 @@ def _ext():
     """The extension module that makes the calls; raise if it has not been built."""
     global _ext_module
     if _ext_module is None:
+        build = "build it with serving_moe_route_gb300._build.build() (or __graft_entry__.build())"
         if not os.path.exists(_build.EXT_PATH):
-            raise RuntimeError(
-                f"extension {_build.EXT_PATH} is missing: build it with "
-                "serving_moe_route_gb300._build.build() (or __graft_entry__.build())")
+            raise RuntimeError(f"extension {_build.EXT_PATH} is missing: {build}")
+        if not _build.ext_abi_matches():
+            raise RuntimeError(f"extension {_build.EXT_PATH} was built against another PyTorch: "
+                               f"{build}")
         B.lib()
         spec = importlib.util.spec_from_file_location("moe_decode_ext", _build.EXT_PATH)
         module = importlib.util.module_from_spec(spec)
