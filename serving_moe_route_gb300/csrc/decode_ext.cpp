@@ -264,6 +264,12 @@ Tensor cut(const Tensor& buffer, int64_t at, int64_t n) {
   return t;
 }
 
+// Tells autograd that a tensor of the caller's has been written, as an in-place
+// operation does: a graph that saved it refuses to run backward through it
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 int32_t* i32(const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
 
 // (ctx_lens, new_lens, block_table, free_pages, n_free, page_size, num_pages,
@@ -302,6 +308,8 @@ PyObject* kv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       i32(slots), i32(positions), i32(starts), i32(lens), error_word(a[9], dev),
                       at_.stream),
           "moe_kv_step");
+    written(table);
+    if (a[8] != Py_None) written(out);
     PyObject* r = PyTuple_New(5);
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(slots));
     PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(positions));
@@ -330,6 +338,9 @@ PyObject* kv_release(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          static_cast<int>(integer(a[4], "num_pages")), error_word(a[5], at_.dev),
                          at_.stream),
           "moe_kv_release");
+    written(table);
+    written(free);
+    written(left);
     Py_RETURN_NONE;
   });
 }
@@ -354,6 +365,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         stride_of(v, 0), stride_of(v, 1), static_cast<int>(N),
                         static_cast<int32_t*>(ps), error_word(a[7], at_.dev), at_.stream),
           "moe_kv_append");
+    written(kc);
+    written(vc);
     Py_RETURN_NONE;
   });
 }
@@ -411,6 +424,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           stride_of(out, 1), with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
                           ws, bytes, error_word(a[12], dev), at_.stream),
           "moe_attn_decode");
+    if (a[9] != Py_None) written(out);
     if (!with_lse) return THPVariable_Wrap(out);
     PyObject* r = PyTuple_New(2);
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(out));

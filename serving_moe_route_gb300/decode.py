@@ -25,6 +25,10 @@ function enqueues on ``stream`` (the current one by default) and returns at
 once, so the step can be captured into a CUDA graph.  Outputs and workspaces
 are allocated for that stream; a tensor of one stream used on another is the
 caller's to order, as everywhere in PyTorch.
+
+Like the layer, none of these has a backward pass: outputs are cut off from the
+graph of the inputs.  What is written in place counts as modified, so autograd
+refuses a graph that needs its old values.
 """
 from __future__ import annotations
 
