@@ -1166,7 +1166,9 @@ using namespace moe;
 extern "C" {
 
 size_t moe_attn_workspace(int kv_dtype, int head_dim) {
-  if (kv_dtype < MOE_KV_F32 || kv_dtype > MOE_KV_E4M3 || head_dim < 1 || head_dim > 256) return 0;
+  if (kv_dtype < MOE_KV_F32 || kv_dtype > MOE_KV_E4M3 || head_dim < 1 || head_dim > 256 ||
+      head_dim % kv_dim_step(kv_dtype))
+    return 0;
   const int dp = attn_dp(head_dim);
   const size_t n = static_cast<size_t>(attn_sm_count()) * ctas_per_sm(kv_dtype, dp);
   return up256(n * sizeof(int4)) + up256(2 * n * kRows * sizeof(float2)) +

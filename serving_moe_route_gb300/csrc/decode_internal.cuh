@@ -16,6 +16,9 @@ __host__ __device__ constexpr int kv_esize(int kv_dtype) {
   return kv_dtype == MOE_KV_F32 ? 4 : kv_dtype == MOE_KV_BF16 ? 2 : 1;
 }
 
+// what head_dim is a multiple of
+constexpr int kv_dim_step(int kv_dtype) { return kv_dtype == MOE_KV_E4M3 ? 16 : 8; }
+
 // MOE_OK if the cache descriptor meets the header's requirements
 int kv_cache_ok(const moe_kv_cache_t* c);
 

@@ -342,7 +342,7 @@ int kv_cache_ok(const moe_kv_cache_t* c) {
   if (c->head_dim < 1 || c->stride_page < 0 || c->stride_token < 0 || c->stride_head < 0)
     return MOE_ERR_INVALID_ARG;
   const int es = kv_esize(c->kv_dtype);
-  if (c->head_dim > 256 || c->head_dim % (q8 ? 16 : 8)) return MOE_ERR_UNSUPPORTED;
+  if (c->head_dim > 256 || c->head_dim % kv_dim_step(c->kv_dtype)) return MOE_ERR_UNSUPPORTED;
   if ((c->stride_page * es) % 16 || (c->stride_token * es) % 16 || (c->stride_head * es) % 16 ||
       (reinterpret_cast<uintptr_t>(c->k) & 15) || (reinterpret_cast<uintptr_t>(c->v) & 15))
     return MOE_ERR_UNSUPPORTED;
