@@ -52,7 +52,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "../../include/moe_route.h"
 #include "decode_internal.cuh"
@@ -1109,18 +1108,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
 }
 
 // ------------------------------------------------------------ host
-static int attn_sm_count() {
-  static std::mutex mu;
-  static int count[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  if (count[dev] == 0 &&
-      cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return count[dev];
-}
-
 static int attn_dp(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 template <int KV, int DP>
@@ -1170,7 +1157,7 @@ size_t moe_attn_workspace(int kv_dtype, int head_dim) {
       head_dim % kv_dim_step(kv_dtype))
     return 0;
   const int dp = attn_dp(head_dim);
-  const size_t n = static_cast<size_t>(attn_sm_count()) * ctas_per_sm(kv_dtype, dp);
+  const size_t n = static_cast<size_t>(sm_count()) * ctas_per_sm(kv_dtype, dp);
   return up256(n * sizeof(int4)) + up256(2 * n * kRows * sizeof(float2)) +
          2 * n * kRows * dp * sizeof(float);
 }
@@ -1198,7 +1185,7 @@ int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stri
   if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_attn_workspace(cache->kv_dtype, cache->head_dim);
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
-  const int sms = attn_sm_count();
+  const int sms = sm_count();
   if (sms < 1) return MOE_ERR_CUDA;
   const int es = kv_esize(cache->kv_dtype), dp = attn_dp(cache->head_dim);
   AttnArgs a = {};

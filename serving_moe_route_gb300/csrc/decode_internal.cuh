@@ -22,6 +22,17 @@ constexpr int kv_dim_step(int kv_dtype) { return kv_dtype == MOE_KV_E4M3 ? 16 : 
 // MOE_OK if the cache descriptor meets the header's requirements
 int kv_cache_ok(const moe_kv_cache_t* c);
 
+// SMs of the current device, asked once per device; 0 on an error
+inline int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // Allow `kern` up to `bytes` of dynamic shared memory on the current device,
 // asking the runtime once per device (a microsecond a call otherwise).
 // `done`: the caller's static, a bit per device, for one kernel and its

@@ -324,7 +324,7 @@ static cudaError_t launch_append(const AppendArgs& a, long long items, cudaStrea
   // 8 heads of 128, bf16: APPEND_FIG)
   constexpr int U = 4;
   const long long one = (items + kAppendThreads - 1) / kAppendThreads;
-  if (one < 152ll * 2 * U)
+  if (one < 2ll * U * sm_count())
     return launch_chained(kv_append_kernel<KV, 1>, dim3(static_cast<unsigned>(one), 2),
                           dim3(kAppendThreads), 0, st, a);
   return launch_chained(kv_append_kernel<KV, U>, dim3(static_cast<unsigned>((one + U - 1) / U), 2),

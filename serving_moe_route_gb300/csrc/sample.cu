@@ -1614,12 +1614,13 @@ int moe_sample(const void* logits, int logits_dtype, int B, int V, long long row
   if (!logits || !u || !ids) return MOE_ERR_INVALID_ARG;
   const int es = logits_dtype == MOE_LOGITS_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) & (es - 1)) return MOE_ERR_INVALID_ARG;
-  // CTAs per row: so many that the rows in flight, four CTAs on each of 152
-  // SMs, take no more than about 96 MB of the L2, and more while the GPU is not
-  // full and a CTA has 2048 tokens at least
-  const long long slots = 152 * kSampCtas, bytes = static_cast<long long>(V) * es;
+  // CTAs per row: so many that the rows in flight, four CTAs on each SM, take
+  // no more than about 96 MB of the L2, and more while the GPU is not full and a
+  // CTA has 2048 tokens at least
+  const long long slots = static_cast<long long>(sm_count()) * kSampCtas;
+  const long long bytes = static_cast<long long>(V) * es;
   const int most = max_cluster(logits_dtype);
-  if (most < 1) return MOE_ERR_CUDA;
+  if (most < 1 || slots < 1) return MOE_ERR_CUDA;
   int cluster = 1;
   while (cluster < 8 && (B < slots / cluster ? B : slots / cluster) * bytes > 96ll << 20)
     cluster *= 2;
