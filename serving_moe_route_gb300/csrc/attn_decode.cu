@@ -81,7 +81,7 @@ struct AttnArgs {
   unsigned* err;
   float scale_log2;
   int B, Hq, heads, group, blocks;  // blocks: of 16 query heads per kv head
-  int dim, page, page_shift, num_pages, max_pages, window, min_tiles;
+  int dim, page, page_shift, num_pages, max_pages, window;
 };
 
 // ------------------------------------------------------------ instructions
@@ -339,8 +339,7 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
   }
   total *= units;
   if (cut && A.err && blockIdx.x == 0) atomicOr(A.err, MOE_DEVERR_NO_SPACE);
-  const long long wide = (total + A.min_tiles - 1) / A.min_tiles;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), wide));
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) A.info[cta] = make_int4(0, 0, 0, 0);
   if (cta >= ctas) return;
@@ -1221,7 +1220,6 @@ int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stri
   a.num_pages = cache->num_pages;
   a.max_pages = max_pages;
   a.window = window;
-  a.min_tiles = 1;
   const int full = sms * ctas_per_sm(cache->kv_dtype, dp);
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.info = reinterpret_cast<int4*>(w);
