@@ -481,6 +481,8 @@ int moe_kv_release(const int32_t* done, int B, int32_t* block_table, int max_pag
  *   slots  device int32 [N]: the slot of each token; -1 skips the token, a
  *          slot outside the cache skips it with MOE_DEVERR_BAD_PAGE.  Slots
  *          that are not skipped must differ
+ * k and v of the cache must differ, and the stride of every axis of more than one
+ * element be head_dim at least: vectors that overlap are refused.
  * F32 and BF16 caches get the vectors bit for bit; E4M3 caches get x / scale
  * rounded to nearest even and saturated at +-448 (NaN stays NaN).
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED (head_dim, strides or
@@ -504,7 +506,8 @@ int moe_kv_append(const moe_kv_cache_t* cache, const void* k, long long k_stride
  *   seq_lens     device int32 [B]; a request with len <= 0 gets out 0 and
  *                lse -inf; len is cut to max_pages * page_size with
  *                MOE_DEVERR_NO_SPACE
- *   out          device [B, Hq, head_dim], strides in elements
+ *   out          device [B, Hq, head_dim], strides in elements, head_dim at
+ *                least where there is more than one
  *   lse          NULL, or device f32 [B, Hq]: the natural logarithm of the
  *                softmax's sum (with scale; -inf when no token was attended)
  *   ws           device workspace of moe_attn_workspace(...) bytes, 256-byte

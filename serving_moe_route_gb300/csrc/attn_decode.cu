@@ -1175,6 +1175,8 @@ int moe_attn_decode(const moe_kv_cache_t* cache, const void* q, long long q_stri
     return MOE_ERR_INVALID_ARG;
   if (B == 0) return MOE_OK;
   if (!q || !block_table || !seq_lens || !out || !ws) return MOE_ERR_INVALID_ARG;
+  if (!apart(B, o_stride_b, cache->head_dim) || !apart(Hq, o_stride_h, cache->head_dim))
+    return MOE_ERR_INVALID_ARG;
   const int qs = cache->kv_dtype == MOE_KV_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
        static_cast<uintptr_t>(q_stride_b * qs) | static_cast<uintptr_t>(q_stride_h * qs) |

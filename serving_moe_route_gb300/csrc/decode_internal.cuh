@@ -16,6 +16,9 @@ __host__ __device__ constexpr int kv_esize(int kv_dtype) {
   return kv_dtype == MOE_KV_F32 ? 4 : kv_dtype == MOE_KV_BF16 ? 2 : 1;
 }
 
+// whether n vectors of dim elements, a stride apart, leave room for each other
+constexpr bool apart(int n, long long stride, int dim) { return n < 2 || stride >= dim; }
+
 // what head_dim is a multiple of
 constexpr int kv_dim_step(int kv_dtype) { return kv_dtype == MOE_KV_E4M3 ? 16 : 8; }
 

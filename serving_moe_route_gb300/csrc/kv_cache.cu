@@ -430,6 +430,11 @@ int moe_kv_append(const moe_kv_cache_t* cache, const void* k, long long k_stride
     return MOE_ERR_INVALID_ARG;
   if (N == 0) return MOE_OK;
   if (!k || !v || !slots) return MOE_ERR_INVALID_ARG;
+  // what is written must not overlap: two writers of one place race
+  if (cache->k == cache->v || !apart(cache->num_pages, cache->stride_page, cache->head_dim) ||
+      !apart(cache->page_size, cache->stride_token, cache->head_dim) ||
+      !apart(cache->kv_heads, cache->stride_head, cache->head_dim))
+    return MOE_ERR_INVALID_ARG;
   const int es = kv_esize(cache->kv_dtype), qs = cache->kv_dtype == MOE_KV_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & (qs - 1))
     return MOE_ERR_INVALID_ARG;

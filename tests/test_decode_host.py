@@ -177,3 +177,16 @@ def test_wrappers_refuse_cpu_tensors():
         moe.sample_tokens(torch.zeros(2, 8), torch.zeros(2))
     with pytest.raises(ValueError, match="CUDA"):
         moe.check_word(i[:1])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(stride_page=0), dict(stride_token=0), dict(stride_head=0), dict(stride_head=64),
+    dict(stride_token=120), dict(v=FAKE)])
+def test_append_refuses_a_cache_that_overlaps(kw):
+    # heads, rows or pages that are one memory, or keys and values that are
+    assert append(cache(**{"v": FAKE + (1 << 30), **kw})) == BAD
+
+
+@pytest.mark.parametrize("kw", [dict(ob=0), dict(oh=0), dict(oh=120), dict(ob=64)])
+def test_attend_refuses_an_output_that_overlaps(kw):
+    assert attend(cache(), **kw) == BAD
