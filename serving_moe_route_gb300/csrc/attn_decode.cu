@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(AttnCfg<KV, DP>::THREADS, AttnCfg<KV, DP>::CTA
 
   // ---- this CTA's range of tiles
   bool cut = false;
-  const int per = (A.B + C::THREADS - 1) / C::THREADS;
-  const int b0 = min(A.B, static_cast<int>(threadIdx.x) * per), b1 = min(A.B, b0 + per);
+  const int per = (A.B - 1) / C::THREADS + 1;
+  const int b0 = static_cast<int>(min(static_cast<unsigned>(A.B), threadIdx.x * per));
+  const int b1 = b0 + min(per, A.B - b0);  // (no sum passes an int)
   long long mine = 0;
   int2 last = make_int2(0, 0);
   for (int b = b0; b < b1; ++b) {
