@@ -174,7 +174,10 @@ __global__ void __launch_bounds__(kStepThreads) kv_step_kernel(const StepArgs A,
     A.positions[i] = pos;
     if (i > INT_MAX - nthreads) break;
   }
-  for (long long i = static_cast<long long>(cta) * kStepThreads + tid; i < pages; i += nthreads) {
+  // ranks from 2^31 - 1 on are no ints: there is no page for them, and no entry
+  // of theirs is touched
+  const long long ranks = min(pages, static_cast<long long>(INT_MAX));
+  for (long long i = static_cast<long long>(cta) * kStepThreads + tid; i < ranks; i += nthreads) {
     const int r = last_at_most(base, A.B, cut_int(i));
     const long long col = static_cast<long long>(pages_for(ctx[r])) + i - base[r];
     A.table[r * A.table_stride + col] = fresh(i);

@@ -175,3 +175,18 @@ def test_an_infinite_temperature_makes_tokens_alike(dt):
                                                                       top_p=np.full(20, 0.9999)))):
         u = ((torch.rand(20, generator=g, device=DEV) * kept).floor() + 0.5) / kept
         _sample_like_the_definition(x, u, least=0.5, temperature=t, **kw)
+
+
+def test_step_with_more_new_pages_than_an_int_counts():
+    # lengths that ask for more pages than 2^31: what lies past the table stays
+    rows, width, beyond = 8192, 270000, 8
+    room = torch.full((rows + beyond, width), -5, dtype=torch.int32, device=DEV)
+    room[:rows] = -1
+    ctx, new, err = _i32([0] * rows), _i32([width] * rows), _word()
+    step = moe.kv_step(ctx, new, room[:rows], _i32(range(10)), _i32([10]), page_size=1, num_pages=10,
+                       max_tokens=16, err=err)
+    assert moe.check_word(err) == (B.MOE_ERR_DEVICE, R.NO_SPACE)
+    assert (room[rows:] == -5).all()
+    assert room[0, :10].tolist() == step.slots[:10].tolist() == list(range(9, -1, -1))
+    assert step.slots[10:].tolist() == [-1] * 6 and int(step.n_free) == 0
+    assert int((room[:rows] != -1).sum()) == 10
