@@ -74,13 +74,19 @@ class Decoder:
 def generate(model, prompts, new_tokens, *, batch=4, max_pages=8, seed=0, **sampling):
     """Serve `prompts` (lists of token ids) on `batch` rows; returns the drawn
     tokens of each.  `sampling`: numbers for temperature, top_k, top_p, min_p."""
+    for i, p in enumerate(prompts):
+        if not p:
+            raise ValueError(f"prompt {i} is empty")
+    if new_tokens < 1 or not prompts:
+        return [[] for _ in prompts], model.num_pages
     i32 = dict(dtype=torch.int32, device="cuda")
     table = torch.full((batch, max_pages), -1, **i32)
     free = torch.arange(model.num_pages, **i32)
     n_free = torch.full((1,), model.num_pages, **i32)
     ctx, err = torch.zeros(batch, **i32), torch.zeros(1, **i32)
     rand = torch.Generator(device="cuda").manual_seed(seed)
-    per_row = {name: torch.full((batch,), v, **(i32 if name == "top_k" else dict(device="cuda")))
+    f32 = dict(dtype=torch.float32, device="cuda")
+    per_row = {name: torch.full((batch,), v, **(i32 if name == "top_k" else f32))
                for name, v in sampling.items()}
 
     waiting = list(range(len(prompts)))

@@ -83,3 +83,10 @@ def test_every_step_is_what_its_definitions_say(loop, kv, monkeypatch):
         given.extend(got.tolist())
     assert checked > 0.9 * len(given)
     assert all(t in given for a in answers for t in a)
+
+
+def test_settings_may_be_whole_numbers(loop):
+    model = loop.Decoder(num_pages=12)
+    a, _ = loop.generate(model, [[1, 2], [4]], 3, batch=2, temperature=0, top_p=1, min_p=0, top_k=5)
+    b, _ = loop.generate(model, [[1, 2], [4]], 3, batch=2, temperature=0.0)
+    assert a == b and [len(x) for x in a] == [3, 3]
