@@ -29,8 +29,8 @@
 //            one operand has 16 rows or fewer and the softmax works on its rows
 //            between the two products.  The m16n8 instructions suffice: without
 //            the loads' waiting a bf16 tile takes a third of the time of its
-//            bytes.  e4m3 products of e4m3 operands (m16n8k32) were tried: 245 us
-//            where f16's take 137, and sums 2^-8 off.
+//            bytes.  e4m3 products of e4m3 operands (m16n8k32) were tried: 1.8
+//            times as long as f16's, and sums 2^-8 off.
 //   joining  At a unit's end the CTA's warps join through shared memory.  A
 //            unit inside one range is written at once; parts of a unit cut by
 //            range borders go to the workspace in fp32 and the second kernel
@@ -40,9 +40,14 @@
 // us: 4 before the first product (lengths, page ids, first rows) and 1 to 2 for
 // the second kernel, which is left out where no unit can be cut.  Measured on a
 // GB300, 32 query heads on 4 of 128: one request of 262161 tokens, bf16: 87 us,
-// 6.2 TB/s (91% of the copy bandwidth); 256 up to 8192, e4m3: 128 us, 5.6 TB/s;
-// 64 up to 4096, bf16: 37 us, 4.9 TB/s, f32: 89 us, 4.1 TB/s, whose split
+// 6.1 TB/s (91% of the copy bandwidth); 256 up to 8192, e4m3: 128 us, 5.7 TB/s;
+// 64 up to 4096, bf16: 36 us, 4.8 TB/s, f32: 88 us, 3.9 TB/s, whose split
 // operands' instructions bound it; one of 700: 7 us.
+//
+// Where fewer bits than fp32 are held: weights are a pair of bf16 (2^-16) or of
+// tf32 terms, or f16 (e4m3 caches, 2^-11); f32 operands are pairs of tf32 terms;
+// and O of bf16 and e4m3 caches is summed in the instructions' accumulator, fp32
+// but cut: 2^-23 of it an instruction, 2^-10 at most for a warp's 2^16 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -177,8 +182,8 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 
 // ------------------------------------------------------------ configuration
 // Keys of a warp's stage (one k step of bf16 and f32 products, two of e4m3's in
-// f16: 137 us against 160 with one; at head_dim 256, where that makes stages of
-// 16 KB, one: 80 us against 106), its bytes (keys and values), warps and stages
+// f16: one takes 17% longer; at head_dim 256, where two make stages of 16 KB,
+// one: two take 32% longer), its bytes (keys and values), warps and stages
 // per CTA, CTAs per SM: about 200 KB of an SM's shared memory hold stages.
 template <int KV, int DP>
 struct AttnCfg {

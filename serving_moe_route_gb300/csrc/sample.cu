@@ -35,14 +35,19 @@
 // Rows without top-k and top-p only need their sums.
 //
 // Bound by latency for few rows (a dozen steps, each a few dependent loads or a
-// cluster barrier); for many by the row's bytes where it is greedy or top-k is
-// small, and by instructions where the whole vocabulary has to be weighed (55 a
-// token in all; 97 with the counts and the list of top-p, and the counts'
-// shared-memory additions).
+// cluster barrier), and for many that are greedy or have a small top-k: a CTA's
+// loads, waited for in batches, and its barriers follow one another, and the
+// other three CTAs of its SM do not fill the gaps (stalled warps per instruction
+// issued: 12 by loads and 8 at barriers, greedy; 6 and 8, top-k).  By
+// instructions where the whole vocabulary has to be weighed: 55 a token in all;
+// 97 with the counts and the list of top-p, and the counts' shared-memory
+// additions.  At 64 registers, which four CTAs an SM leave, the compiler spills:
+// 420 bytes stored and 324 loaded a thread (f32), 520 and 432 (bf16).
 // Measured on a GB300: one row of 131072 f32 with every restriction 12 us; 64 of
-// 50257 bf16 with mixed ones 30 us; 512 of 131072 f32 greedy 76 us (3.5 TB/s of
-// logits), top-k 111, no restriction 181, top-p 296.  With the rows' slices kept
-// in shared memory (two CTAs an SM) the last four took 101, 222, 257 and 563 us.
+// 50257 bf16 with mixed ones 28 us; 512 of 131072 f32 greedy 60 us (4.4 TB/s of
+// logits, 66% of the copy bandwidth), top-k 107, no restriction 170, top-p 281.
+// With the rows' slices kept in shared memory (two CTAs an SM) greedy rows took
+// 1.3 times as long, the others 1.4 to 2.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -154,7 +159,8 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 // whole number of 2^-44 (an even one: rounded at 2^-43).  Every lane of the
 // warp calls it, lane j holding T[j] = 2^(44 + j / 32).
 //   x = k / 32 + r:  2^x = 2^(k >> 5) T[k & 31] (1 + (2^r - 1)),  |r| <= 2^-6,
-// with l - top, log2(e) / t and r each as the sum of two floats, and 2^r - 1 in
+// the table by rounding the powers themselves and 2^r - 1 by the first four terms
+// of its Taylor series, with l - top, log2(e) / t and r each as the sum of two floats, and 2^r - 1 in
 // fixed point of 2^-37: right to 2^-35 (two roundings to 2^-37, T's first 31
 // bits, three roundings of the second degree's term).
 struct Weigher {
