@@ -90,13 +90,19 @@ def strip_c_comments(text):
     return " ".join("".join(out).split())
 
 
+# Sources that the layer's kernels are not built from: the decode step's
+DECODE_SOURCES = ("attn_decode.cu", "decode_internal.cuh", "kv_cache.cu", "sample.cu")
+
+
 def kernel_source_fingerprint():
-    """sha256 over the CUDA sources (csrc/*.cu, *.cuh) with comments removed."""
+    """sha256 over the layer's CUDA sources (csrc/*.cu, *.cuh) with comments removed."""
     import glob
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "serving_moe_route_gb300", "csrc")
     for fn in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
+        if os.path.basename(fn) in DECODE_SOURCES:
+            continue
         with open(fn, encoding="utf-8") as f:
             h.update(strip_c_comments(f.read()).encode())
     return h.hexdigest()

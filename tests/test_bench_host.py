@@ -102,3 +102,16 @@ def test_gemm_roofline_attributes_the_launch_that_ran():
     st = {"gemm1": [0.176], "gemm2": [0.117]}
     name, r = bench.gemm_roofline(wl8, st, acc, pk, family=None, plan=_Plan(gemm_tm=1))
     assert name == "gemm1" and r["kernel"].startswith("moe_gemm_tm_kernel")
+
+
+def test_sources_outside_the_layer_leave_its_fingerprint(tmp_path, monkeypatch):
+    # the committed traffic figures hold for the layer's kernels as they stand,
+    # whatever stands beside them
+    import json
+    with open(os.path.join(ROOT, "profiles", "ncu_traffic.json")) as f:
+        assert json.load(f)["source_sha256"] == bench.kernel_source_fingerprint()
+    csrc = os.path.join(ROOT, "serving_moe_route_gb300", "csrc")
+    for fn in os.listdir(csrc):
+        if fn.endswith((".cu", ".cuh")) and fn not in bench.DECODE_SOURCES:
+            with open(os.path.join(csrc, fn)) as f:  # nothing of the layer's is left out
+                assert not any(f'"{name}"' in f.read() for name in bench.DECODE_SOURCES)
