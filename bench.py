@@ -8,14 +8,15 @@ A step is one call of the whole layer (routing, permutation, grouped gate+up
 GEMM with SiLU, grouped down GEMM with the weighted combine, output cast)
 over one batch whose inputs are already resident in HBM.  Between timed
 steps a 256 MiB buffer is written to flush L2, outside the per-step CUDA
-events.  Rank 0 prints one JSON line.
+events.  Rank 0 prints one JSON line of less than 3000 characters, which
+readers of a log's last few lines see whole.
 
 After the headline's timed region, rank 0 also measures the batch sweep of
 the metric: every workload (decode, sparse E=400 with and without the old
 estimate and the EP8 slice, the FP8 batch sweep T=1..4096, skewed prefill)
 timed as µs per call over 24 CUDA-graph replays after 5 warm-ups, each with
 its roofline fractions, plus the routing micro-benchmark (--no-sweep skips
-both).
+both).  They go to standard error as another JSON line, before the first one.
 
 Under torchrun every rank runs an independent replica of the layer on its
 own GPU (tokens are independent; there is no exchange step), so the work
@@ -734,12 +735,13 @@ def run_ours(args):
                          "fp8_source": "torch._scaled_mm e4m3 8192^3, best of 10 (this run)"
                          if pk["fp8_tflops"] else "unavailable: 2 x bf16 used",
                          "source": pk["source"]}
-        line["routing_microbench"] = routing_bench(dev)
+        more = {"routing_microbench": routing_bench(dev)}
         t0 = time.perf_counter()
         only = tuple(n for n in args.sweep_only.split(",") if n)
-        line["sweep"] = sweep(dev, args.sweep_samples, pk, only)
-        line["sweep_wall_s"] = round(time.perf_counter() - t0, 1)
-        line["estimate_ablation"] = estimate_ablation(line["sweep"])
+        more["sweep"] = sweep(dev, args.sweep_samples, pk, only)
+        more["sweep_wall_s"] = round(time.perf_counter() - t0, 1)
+        more["estimate_ablation"] = estimate_ablation(more["sweep"])
+        print(json.dumps(more), file=sys.stderr, flush=True)
     if rank == 0:
         print(json.dumps(line), flush=True)
     if world > 1:

@@ -115,3 +115,20 @@ def test_sources_outside_the_layer_leave_its_fingerprint(tmp_path, monkeypatch):
         if fn.endswith((".cu", ".cuh")) and fn not in bench.DECODE_SOURCES:
             with open(os.path.join(csrc, fn)) as f:  # nothing of the layer's is left out
                 assert not any(f'"{name}"' in f.read() for name in bench.DECODE_SOURCES)
+
+
+def test_the_line_leaves_the_sweep_to_another():
+    # its readers see the end of a log: 20 KB of sweep hid the line
+    import ast
+    tree = ast.parse(open(bench.__file__).read())
+    run = next(n for n in tree.body if isinstance(n, ast.FunctionDef) and n.name == "run_ours")
+    keys = set()
+    for n in ast.walk(run):
+        if isinstance(n, ast.Assign) and isinstance(n.targets[0], ast.Name) and \
+                n.targets[0].id == "line":
+            keys |= {k.value for k in n.value.keys}
+        if isinstance(n, ast.Assign) and isinstance(n.targets[0], ast.Subscript) and \
+                getattr(n.targets[0].value, "id", "") == "line":
+            keys.add(n.targets[0].slice.value)
+    assert {"metric", "value", "config", "e2e", "clocks", "gpu_launches"} <= keys
+    assert not keys & {"sweep", "routing_microbench", "estimate_ablation"}
