@@ -563,6 +563,236 @@ int moe_sample(const void* logits, int logits_dtype, int B, int V, long long row
                const float* u, const float* temperature, const int32_t* top_k,
                const float* top_p, const float* min_p, int32_t* ids, float* probs, void* stream);
 
+/*
+ * Drafted tokens.  A request may bring several tokens to a step: a tree of
+ * drafts whose node 0 follows the request's context and whose other nodes each
+ * follow their parent.  moe_kv_step maps them to slots like any new tokens
+ * (new_lens: nodes), moe_tree_masks says what each attends, moe_attn_tree
+ * attends, and when a token has been drawn at every node moe_tree_accept walks
+ * from node 0 along the drafts that were drawn; moe_kv_compact moves the
+ * accepted nodes' keys and values together and moe_kv_trim gives back the pages
+ * behind them.  Rows are nodes, packed by request: request r has rows
+ * starts[r] .. starts[r+1]-1 (as moe_kv_step writes them), at most MOE_TREE_MAX;
+ * rows of no request (those that pad a batch) are left as they are, or, where it
+ * is said, written.  starts that do not rise inside [0, N] give rows to no
+ * request, or to two: nothing outside the arrays is touched.
+ *
+ * moe_tree_masks
+ *   parents    device int32 [N]: a node's parent, by its number in the request;
+ *              lower than its own, -1 for a root.  Anything else counts as -1
+ *              and sets MOE_DEVERR_BAD_ID
+ *   starts     device int32 [B+1]; seq_lens device int32 [B] as for
+ *              moe_attn_tree
+ *   max_new    nodes of a request at most; those past it get a mask of 0 and
+ *              set MOE_DEVERR_NO_SPACE
+ *   masks      device int64 [N, ceil(max_new/64)] out: bit j of a row (bit j%64
+ *              of word j/64) is set if the node attends node j of its request:
+ *              itself and its ancestors.  0 in rows of no request
+ *   positions  device int32 [N] out: context tokens + depth of each node, what
+ *              rotary embeddings go by.  0 in rows of no request
+ * Requires 1 <= max_new <= MOE_TREE_MAX.  Errors: MOE_ERR_INVALID_ARG,
+ * MOE_ERR_CUDA.
+ */
+#define MOE_TREE_MAX 256
+int moe_tree_masks(const int32_t* parents, int N, const int32_t* starts, const int32_t* seq_lens,
+                   int B, int max_new, int64_t* masks, int32_t* positions, uint32_t* err,
+                   void* stream);
+
+/*
+ * moe_tree_accept -- walk each request's tree from node 0: the next node is the
+ * lowest child of the current one whose token is the one drawn there.
+ *   tokens     device int32 [N]: the drafted token of each node (of node 0: any)
+ *   draws      device int32 [N]: the token drawn from the logits at each node;
+ *              a negative one (no token) ends the walk
+ *   parents    as for moe_tree_masks
+ *   ctx_lens   device int32 [B]: context tokens, the drafted ones not included
+ *   path       device int32 [B, max_path] out: the nodes of the walk, node 0
+ *              first, then -1
+ *   accepted   device int32 [B] out: how many; 0 for a request without nodes
+ *   next_ids   device int32 [B] out: the token drawn at the last of them (the
+ *              next step's node 0); -1 for a request without nodes
+ *   seq_lens   device int32 [B] out: ctx + accepted
+ * A walk ends after max_path nodes.  Nodes past MOE_TREE_MAX are not looked at
+ * and set MOE_DEVERR_NO_SPACE.  Requires 1 <= max_path <= MOE_TREE_MAX.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
+ */
+int moe_tree_accept(const int32_t* tokens, const int32_t* draws, const int32_t* parents, int N,
+                    const int32_t* starts, const int32_t* ctx_lens, int B, int max_path,
+                    int32_t* path, int32_t* accepted, int32_t* next_ids, int32_t* seq_lens,
+                    uint32_t* err, void* stream);
+
+/*
+ * moe_attn_tree -- moe_attn_decode for several new tokens per request.  Request
+ * r has n = starts[r+1] - starts[r] rows and len = seq_lens[r] tokens in the
+ * cache, its new ones last: ctx = max(0, len - n).  Row i attends
+ *   the tokens t < ctx (window > 0: with t >= ctx - max(0, window - c), c the
+ *     number of new tokens that it attends), and
+ *   of the new tokens ctx + j, j < min(n, len - ctx), those whose bit j is set
+ *     in its mask (masks NULL: those with j <= i, a chain).
+ * Arguments as for moe_attn_decode, but for
+ *   q, out     device [N, Hq, head_dim], packed by request; rows of no request
+ *              are not read, and left as they are
+ *   lse        NULL, or device f32 [N, Hq]
+ *   masks      NULL, or device int64 [N, ceil(max_new/64)] as moe_tree_masks
+ *              writes them; any bits are allowed
+ *   starts     device int32 [B+1]
+ *   max_new    rows of a request at most: those past it are left out, with
+ *              MOE_DEVERR_NO_SPACE
+ *   ws         moe_attn_tree_workspace(...) bytes, 256-byte aligned
+ * A row that attends nothing gets out 0 and lse -inf.  What a row does not
+ * attend has no part in its result, whatever its bits.  NaN and infinities that
+ * it attends, bad pages, lengths past max_pages and the order of sums are as for
+ * moe_attn_decode, but that in an E4M3 cache too an infinite logit may leave NaN.
+ * Requires 1 <= max_new <= MOE_TREE_MAX, N * Hq < 2^31.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ * MOE_ERR_CUDA.
+ */
+int moe_attn_tree(const moe_kv_cache_t* cache, const void* q, long long q_stride_n,
+                  long long q_stride_h, int N, int Hq, const int32_t* block_table, int max_pages,
+                  long long table_stride, const int32_t* starts, const int32_t* seq_lens, int B,
+                  const int64_t* masks, int max_new, float scale, int window, void* out,
+                  long long o_stride_n, long long o_stride_h, float* lse, void* ws,
+                  size_t ws_bytes, uint32_t* err, void* stream);
+
+/* moe_attn_tree_workspace -- bytes of workspace that moe_attn_tree needs for
+ * this cache type and head_dim on the current device, whatever the other sizes;
+ * 0 for values outside the requirements. */
+size_t moe_attn_tree_workspace(int kv_dtype, int head_dim);
+
+/*
+ * moe_kv_compact -- after a walk: token ctx + path[j] of a request moves to
+ * ctx + j, for j < accepted, as if all were read before any is written.
+ *   path       device int32 [B, max_path], rising within a row (so that no token
+ *              moves forward); where it does not rise it ends, with
+ *              MOE_DEVERR_BAD_ID
+ *   accepted   device int32 [B] (above max_path counts as max_path)
+ *   ctx_lens   device int32 [B]
+ *   block_table  as for moe_attn_decode, B <= MOE_KV_MAX_REQUESTS; pages outside
+ *              the cache skip the token with MOE_DEVERR_BAD_PAGE, places past
+ *              max_pages with MOE_DEVERR_NO_SPACE
+ * Vectors move bit for bit; the cache's scales may be NULL.  The pages that are written
+ * must belong to one request only.  The cache must not overlap itself (see
+ * moe_kv_append).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+int moe_kv_compact(const moe_kv_cache_t* cache, const int32_t* path, int max_path,
+                   const int32_t* accepted, const int32_t* ctx_lens, int B,
+                   const int32_t* block_table, int max_pages, long long table_stride,
+                   uint32_t* err, void* stream);
+
+/*
+ * Shared pages.  page_refs (device int32 [num_pages]) holds for each page how
+ * many rows hold it beyond the first: 0 for a page of one row, or of none, so
+ * moe_kv_step needs no word of it.  It starts as zeros.  A shared page must not
+ * be written: moe_kv_fork gives every fork a page of its own for the tokens to
+ * come.
+ *
+ * moe_kv_fork -- let rows of the block table go on from other rows: row
+ * dst_rows[i] gets the full pages of row src_rows[i] (page_refs + 1 each) and,
+ * if its last page is a part, a page from the end of free_pages in that one's
+ * place, forks in order.
+ *   src_rows, dst_rows  device int32 [F], F <= MOE_KV_MAX_REQUESTS; a row may be
+ *                  forked many times.  A destination must hold no pages (they
+ *                  would be lost), stand in the list once (of several only the
+ *                  first counts) and not be a source
+ *   ctx_lens       device int32 [B]: read for sources, written for destinations
+ *   n_free         device int32 [1], read and written
+ *   src_pages, dst_pages, tokens  device int32 [F] out: the partial pages and
+ *                  their tokens, for moe_kv_copy_pages on each layer's cache;
+ *                  -1, -1, 0 for a fork that needs no copy
+ * A fork is refused if a row lies outside the table (MOE_DEVERR_BAD_ID), if it
+ * breaks the rules above (MOE_DEVERR_DUP_ID), if there is no free page or its
+ * length does not fit max_pages (MOE_DEVERR_NO_SPACE), or if its partial page
+ * lies outside the pool (MOE_DEVERR_BAD_PAGE): its row and its length stay as
+ * they were and its pair is -1, -1, 0.  A shared page outside the pool becomes -1
+ * in the destination, with MOE_DEVERR_BAD_PAGE.
+ * Errors: MOE_ERR_INVALID_ARG (also F * max_pages >= 2^31), MOE_ERR_CUDA.
+ */
+int moe_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int F, int32_t* ctx_lens, int B,
+                int32_t* block_table, int max_pages, long long table_stride, int32_t* page_refs,
+                const int32_t* free_pages, int free_capacity, int32_t* n_free, int num_pages,
+                int page_size, int32_t* src_pages, int32_t* dst_pages, int32_t* tokens,
+                uint32_t* err, void* stream);
+
+/*
+ * moe_kv_copy_pages -- copy keys and values of page src_pages[i] to page
+ * dst_pages[i], i < n (device int32 [n]; a pair with a -1 is skipped, one with a
+ * page outside the cache too, with MOE_DEVERR_BAD_PAGE): the first tokens[i] of
+ * the page (device int32 [n]), or all of it where tokens is NULL.  A page that is
+ * written must stand in the call once, and must not be read by another pair.
+ * Vectors move bit for bit; the cache's scales may be NULL.  The cache must not overlap itself (see moe_kv_append).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+int moe_kv_copy_pages(const moe_kv_cache_t* cache, const int32_t* src_pages,
+                      const int32_t* dst_pages, const int32_t* tokens, int n, uint32_t* err,
+                      void* stream);
+
+/*
+ * moe_kv_trim -- give back the pages of request r past its first keep_lens[r]
+ * tokens: of the entries of its row from ceil(keep/page_size) to
+ * ceil(seq_lens[r]/page_size) each becomes -1, and the page it held goes to the
+ * end of free_pages, rows in order and columns in order; keep 0 gives back all
+ * of the request's pages, keep >= seq_lens none.
+ *   keep_lens, seq_lens  device int32 [B] (negative ones count as 0)
+ *   page_refs   NULL where no page is shared; else a shared page loses a holder
+ *               instead, and is freed, at the first of the entries that give it
+ *               back, when the call takes its last one
+ *   n_free      device int32 [1], read and written
+ * An entry outside the pool becomes -1; one other than -1 sets
+ * MOE_DEVERR_BAD_PAGE.  Pages that do not fit free_capacity are dropped with
+ * MOE_DEVERR_NO_SPACE.
+ * Errors: MOE_ERR_INVALID_ARG (also B * max_pages >= 2^31 - 1024), MOE_ERR_CUDA.
+ */
+int moe_kv_trim(const int32_t* keep_lens, const int32_t* seq_lens, int B, int32_t* block_table,
+                int max_pages, long long table_stride, int32_t* free_pages, int free_capacity,
+                int32_t* n_free, int32_t* page_refs, int num_pages, int page_size, uint32_t* err,
+                void* stream);
+
+/*
+ * moe_adjust_logits -- what a request asks of its logits before a token is
+ * drawn.  For row i of request r (rows[i], or i), token v with logit x:
+ *   1. if v occurs in r's history: x = x > 0 ? x / repetition : x * repetition
+ *   2. x -= frequency * c, and x -= presence if c > 0, where c is how often v
+ *      occurs in the history from prompt_lens[r] on
+ *   3. x += the bias listed for v (of several for one token the last counts)
+ *   4. x = -inf if v is not allowed in row i
+ * computed in f32 and rounded once.  NULL leaves a part out.
+ *   rows           device int32 [N]: the request of each row; outside
+ *                  [0, requests) it is of none (only step 4 is done), with
+ *                  MOE_DEVERR_BAD_ID
+ *   history        device int32 [requests, max_history], rows history_stride
+ *                  apart; tokens outside the vocabulary count for nothing
+ *   history_lens   device int32 [requests]; prompt_lens NULL: 0
+ *   repetition, presence, frequency  device f32 [requests] (1, 0 and 0)
+ *   bias_ids, bias device int32 and f32 [requests, n_bias]; ids outside the
+ *                  vocabulary (-1 pads a list) count for nothing; n_bias <= 65535
+ *   allowed        device int32 [N, >= ceil(V/32)], rows allowed_stride apart:
+ *                  token v is allowed if bit v%32 of word v/32 is set
+ */
+typedef struct moe_adjust {
+  int32_t requests, max_history, n_bias, reserved0;
+  int64_t history_stride, allowed_stride;
+  const int32_t* rows;
+  const int32_t* history;
+  const int32_t* history_lens;
+  const int32_t* prompt_lens;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_ids;
+  const float* bias;
+  const int32_t* allowed;
+} moe_adjust_t;
+
+/*   logits  device [N, V] (MOE_LOGITS_*), rows row_stride elements apart
+ *   out     the same type, rows out_stride >= V apart: the logits themselves,
+ *           or memory that they do not overlap
+ * Requires 1 <= V <= 2^18, N <= 65535.  Errors: MOE_ERR_INVALID_ARG,
+ * MOE_ERR_CUDA. */
+int moe_adjust_logits(const moe_adjust_t* settings, const void* logits, int logits_dtype, int N,
+                      int V, long long row_stride, void* out, long long out_stride, uint32_t* err,
+                      void* stream);
+
 /* moe_check_word -- moe_check for a caller's error word: synchronise
  * `stream`, read *err, clear it, and return MOE_OK or MOE_ERR_DEVICE. */
 int moe_check_word(uint32_t* err, uint32_t* bits, void* stream);

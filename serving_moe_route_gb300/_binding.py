@@ -37,6 +37,9 @@ EXPORTED = ("moe_plan", "moe_plan_ep", "moe_forward", "moe_forward_timed", "moe_
             "moe_ep_dispatch", "moe_ep_pack", "moe_ep_combine",
             "moe_kv_step", "moe_kv_release", "moe_kv_append", "moe_attn_decode",
             "moe_attn_workspace", "moe_sample", "moe_check_word",
+            "moe_tree_masks", "moe_tree_accept", "moe_attn_tree", "moe_attn_tree_workspace",
+            "moe_kv_compact", "moe_kv_copy_pages", "moe_kv_fork", "moe_kv_trim",
+            "moe_adjust_logits",
             "moe_strerror", "moe_abi_version")
 
 
@@ -65,6 +68,15 @@ class MoeKvCache(ctypes.Structure):
                                      "reserved0")]
     _fields_ += [(n, c_i64) for n in ("stride_page", "stride_token", "stride_head")]
     _fields_ += [(n, c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+
+
+class MoeAdjust(ctypes.Structure):
+    """Mirror of ``moe_adjust_t``."""
+    _fields_ = [(n, c_i32) for n in ("requests", "max_history", "n_bias", "reserved0")]
+    _fields_ += [(n, c_i64) for n in ("history_stride", "allowed_stride")]
+    _fields_ += [(n, c_void_p) for n in (
+        "rows", "history", "history_lens", "prompt_lens", "repetition", "presence", "frequency",
+        "bias_ids", "bias", "allowed")]
 
 
 class MoeError(RuntimeError):
@@ -144,6 +156,25 @@ def lib() -> ctypes.CDLL:
     L.moe_attn_workspace.restype = sz
     L.moe_sample.argtypes = [P, i, i, i, ll, P, P, P, P, P, P, P, P]
     L.moe_sample.restype = i
+    L.moe_tree_masks.argtypes = [P, i, P, P, i, i, P, P, P, P]
+    L.moe_tree_masks.restype = i
+    L.moe_tree_accept.argtypes = [P, P, P, i, P, P, i, i, P, P, P, P, P, P]
+    L.moe_tree_accept.restype = i
+    L.moe_attn_tree.argtypes = [cache, P, ll, ll, i, i, P, i, ll, P, P, i, P, i, f, i, P, ll, ll, P,
+                                P, sz, P, P]
+    L.moe_attn_tree.restype = i
+    L.moe_attn_tree_workspace.argtypes = [i, i]
+    L.moe_attn_tree_workspace.restype = sz
+    L.moe_kv_compact.argtypes = [cache, P, i, P, P, i, P, i, ll, P, P]
+    L.moe_kv_compact.restype = i
+    L.moe_kv_copy_pages.argtypes = [cache, P, P, P, i, P, P]
+    L.moe_kv_copy_pages.restype = i
+    L.moe_kv_fork.argtypes = [P, P, i, P, i, P, i, ll, P, P, i, P, i, i, P, P, P, P, P]
+    L.moe_kv_fork.restype = i
+    L.moe_kv_trim.argtypes = [P, P, i, P, i, ll, P, i, P, P, i, i, P, P]
+    L.moe_kv_trim.restype = i
+    L.moe_adjust_logits.argtypes = [ctypes.POINTER(MoeAdjust), P, i, i, i, ll, P, ll, P, P]
+    L.moe_adjust_logits.restype = i
     L.moe_check_word.argtypes = [P, ctypes.POINTER(c_u32), P]
     L.moe_check_word.restype = i
     if L.moe_abi_version() != 4:
@@ -286,6 +317,61 @@ def moe_sample(logits, logits_dtype, B, V, row_stride, u, temperature, top_k, to
                probs, stream):
     return lib().moe_sample(logits, logits_dtype, B, V, row_stride, u, temperature, top_k, top_p,
                             min_p, ids, probs, stream)
+
+
+def moe_tree_masks(parents, N, starts, seq_lens, B, max_new, masks, positions, err, stream):
+    return lib().moe_tree_masks(parents, N, starts, seq_lens, B, max_new, masks, positions, err,
+                                stream)
+
+
+def moe_tree_accept(tokens, draws, parents, N, starts, ctx_lens, B, max_path, path, accepted,
+                    next_ids, seq_lens, err, stream):
+    return lib().moe_tree_accept(tokens, draws, parents, N, starts, ctx_lens, B, max_path, path,
+                                 accepted, next_ids, seq_lens, err, stream)
+
+
+def moe_attn_tree_workspace(kv_dtype, head_dim):
+    return lib().moe_attn_tree_workspace(kv_dtype, head_dim)
+
+
+def moe_attn_tree(cache, q, q_stride_n, q_stride_h, N, Hq, block_table, max_pages, table_stride,
+                  starts, seq_lens, B, masks, max_new, scale, window, out, o_stride_n, o_stride_h,
+                  lse, ws, ws_bytes, err, stream):
+    return lib().moe_attn_tree(ctypes.byref(cache), q, q_stride_n, q_stride_h, N, Hq, block_table,
+                               max_pages, table_stride, starts, seq_lens, B, masks, max_new, scale,
+                               window, out, o_stride_n, o_stride_h, lse, ws, ws_bytes, err, stream)
+
+
+def moe_kv_compact(cache, path, max_path, accepted, ctx_lens, B, block_table, max_pages,
+                   table_stride, err, stream):
+    return lib().moe_kv_compact(ctypes.byref(cache), path, max_path, accepted, ctx_lens, B,
+                                block_table, max_pages, table_stride, err, stream)
+
+
+def moe_kv_copy_pages(cache, src_pages, dst_pages, tokens, n, err, stream):
+    return lib().moe_kv_copy_pages(ctypes.byref(cache), src_pages, dst_pages, tokens, n, err,
+                                   stream)
+
+
+def moe_kv_fork(src_rows, dst_rows, F, ctx_lens, B, block_table, max_pages, table_stride,
+                page_refs, free_pages, free_capacity, n_free, num_pages, page_size, src_pages,
+                dst_pages, tokens, err, stream):
+    return lib().moe_kv_fork(src_rows, dst_rows, F, ctx_lens, B, block_table, max_pages,
+                             table_stride, page_refs, free_pages, free_capacity, n_free, num_pages,
+                             page_size, src_pages, dst_pages, tokens, err, stream)
+
+
+def moe_kv_trim(keep_lens, seq_lens, B, block_table, max_pages, table_stride, free_pages,
+                free_capacity, n_free, page_refs, num_pages, page_size, err, stream):
+    return lib().moe_kv_trim(keep_lens, seq_lens, B, block_table, max_pages, table_stride,
+                             free_pages, free_capacity, n_free, page_refs, num_pages, page_size,
+                             err, stream)
+
+
+def moe_adjust_logits(settings, logits, logits_dtype, N, V, row_stride, out, out_stride, err,
+                      stream):
+    return lib().moe_adjust_logits(ctypes.byref(settings), logits, logits_dtype, N, V, row_stride,
+                                   out, out_stride, err, stream)
 
 
 def moe_check_word(err, stream):

@@ -1,0 +1,289 @@
+// adjust.cu -- penalties for repeated tokens, biases and allowed tokens applied
+// to logits before a token is drawn (moe_adjust_logits).
+//
+// One pass over the logits: each is read once and written once.  What a token's
+// logit needs to know of the request's history is a word in shared memory, bit
+// 31: it occurs, below: how often in the answer.  A row's words are spread over
+// the CTAs of a cluster, each of which holds a slice of the vocabulary; they deal
+// the history out among themselves, so that it is read once a row, and add to
+// the words of whichever CTA holds the token.  Counts are whole numbers: the
+// order of additions does not show.
+//
+// Bound by the logits' bytes for large batches (512 rows of 131072, f32: 202 us,
+// 2.7 TB/s), by the cluster's two barriers and the chain from lengths to tokens
+// to counts for few rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_route.h"
+#include "decode_internal.cuh"
+#include "moe_internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kAdjustThreads = 512;
+constexpr int kAdjustCtas = 8;  // of a cluster: every GPU of this kind takes 8
+
+struct AdjustArgs {
+  const char* x;
+  char* out;
+  long long x_row, out_row;  // elements
+  const int* rows;           // NULL: row i is request i
+  const int* history;
+  long long history_stride;
+  const int *history_lens, *prompt_lens;
+  const float *repetition, *presence, *frequency;
+  const int* bias_ids;
+  const float* bias;
+  const unsigned* allowed;
+  long long allowed_stride;  // words
+  unsigned* err;
+  int N, V, R, max_history, n_bias;
+  int slice;  // tokens of a CTA, a multiple of 32
+};
+
+template <typename T>
+__device__ __forceinline__ float as_f32(T v);
+template <>
+__device__ __forceinline__ float as_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// PAST: a history with penalties; BIAS: a list of biases
+template <typename T, bool PAST, bool BIAS>
+__global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs A) {
+  extern __shared__ uint4 adjust_smem[];
+  constexpr int VE = 16 / sizeof(T);
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int row = blockIdx.y, lo = blockIdx.x * A.slice;
+  const int n = max(0, min(A.slice, A.V - lo));
+  const T* const x = reinterpret_cast<const T*>(A.x) + row * A.x_row + lo;
+  T* const out = reinterpret_cast<T*>(A.out) + row * A.out_row + lo;
+  // the slice's tokens before the first 16-byte boundary of the logits; the words
+  // are shifted so that a vector of logits has a vector of words
+  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % VE);
+  uint32_t* const words = reinterpret_cast<uint32_t*>(adjust_smem) + skew;
+  uint16_t* const listed = reinterpret_cast<uint16_t*>(
+                               reinterpret_cast<uint32_t*>(adjust_smem) + (PAST ? A.slice + VE : 0)) +
+                           skew;
+  int req = A.rows ? A.rows[row] : row;
+  if (req < 0 || req >= A.R) {
+    if (A.err && blockIdx.x == 0 && tid == 0) atomicOr(A.err, MOE_DEVERR_BAD_ID);
+    req = -1;
+  }
+  float rep = 1.0f, freq = 0.0f, pres = 0.0f;
+  if constexpr (PAST || BIAS) {
+    const int w16 = ((PAST ? A.slice + VE : 0) * 4 + (BIAS ? A.slice + VE : 0) * 2 + 15) / 16;
+    for (int i = tid; i < w16; i += kAdjustThreads) adjust_smem[i] = make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (PAST) {
+    cluster_sync();
+    if (req >= 0) {
+      if (A.repetition) rep = A.repetition[req];
+      if (A.presence) pres = A.presence[req];
+      if (A.frequency) freq = A.frequency[req];
+      const int len = max(0, min(A.history_lens[req], A.max_history));
+      const int prompt = A.prompt_lens ? A.prompt_lens[req] : 0;
+      const int* const h = A.history + req * A.history_stride;
+      const uint32_t mine = smem_u32(words);  // in all CTAs: slices are multiples of a vector
+      for (long long i = static_cast<long long>(blockIdx.x) * kAdjustThreads + tid; i < len;
+           i += static_cast<long long>(gridDim.x) * kAdjustThreads) {
+        const int t = __ldg(h + i);
+        if (t < 0 || t >= A.V) continue;
+        const unsigned to = static_cast<unsigned>(t) / A.slice;
+        const uint32_t at = mapa_shared(mine + (t - to * A.slice) * 4, to);
+        if (i < prompt)
+          asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(at),
+                       "r"(0x80000000u)
+                       : "memory");
+        else
+          asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(1u)
+                       : "memory");
+      }
+    }
+  }
+  const float* bias = nullptr;
+  if constexpr (BIAS) {
+    if constexpr (!PAST) __syncthreads();
+    if (req >= 0) {
+      bias = A.bias + static_cast<long long>(req) * A.n_bias;
+      const int* const ids = A.bias_ids + static_cast<long long>(req) * A.n_bias;
+      for (int j = tid; j < A.n_bias; j += kAdjustThreads) {
+        const int t = __ldg(ids + j) - lo;
+        if (t < 0 || t >= n) continue;
+        // the last of equal ids counts: the largest place in the list, by
+        // comparing words that hold two tokens' places
+        uint16_t* const at = listed + t;
+        uint32_t* const word = reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(at) & ~3ull);
+        const int shift = (reinterpret_cast<uintptr_t>(at) & 2) * 8;
+        uint32_t seen = *reinterpret_cast<volatile uint32_t*>(word);
+        while (static_cast<int>(seen >> shift & 0xffffu) < j + 1) {
+          const uint32_t want = (seen & ~(0xffffu << shift)) | static_cast<uint32_t>(j + 1) << shift;
+          const uint32_t got = atomicCAS(word, seen, want);
+          if (got == seen) break;
+          seen = got;
+        }
+      }
+    }
+  }
+  if constexpr (PAST) cluster_sync();
+  else if constexpr (BIAS) __syncthreads();
+
+  const unsigned* const allowed = A.allowed ? A.allowed + row * A.allowed_stride : nullptr;
+  auto adjust = [&](float v, uint32_t word, unsigned place, bool ok) {
+    if constexpr (PAST) {
+      if (word) {
+        v = v > 0.0f ? v / rep : v * rep;
+        const uint32_t c = word & 0x7fffffffu;
+        v -= freq * static_cast<float>(c);
+        if (c) v -= pres;
+      }
+    }
+    if constexpr (BIAS)
+      if (place) v += __ldg(bias + place - 1);
+    return ok ? v : -INFINITY;
+  };
+  auto one = [&](int t) {
+    const float v = as_f32<T>(x[t]);
+    const bool ok = !allowed || (__ldg(allowed + (lo + t) / 32) >> ((lo + t) & 31) & 1u);
+    out[t] = from_f32<T>(adjust(v, PAST ? words[t] : 0u, BIAS ? listed[t] : 0u, ok));
+  };
+  const int head = min(n, (VE - skew) % VE), vecs = (n - head) / VE, tail = head + vecs * VE;
+  const bool same = reinterpret_cast<uintptr_t>(out) / sizeof(T) % VE == static_cast<unsigned>(skew);
+  if (tid < head) one(tid);
+  if (tail + tid < n) one(tail + tid);
+  for (int i = tid; i < vecs; i += kAdjustThreads) {
+    const int t = head + i * VE;
+    uint4 raw = *reinterpret_cast<const uint4*>(x + t);
+    T* const v = reinterpret_cast<T*>(&raw);
+    uint32_t w[VE];
+    uint16_t p[VE];
+    if constexpr (PAST) {
+#pragma unroll
+      for (int j = 0; j < VE; j += 4)
+        *reinterpret_cast<uint4*>(w + j) = *reinterpret_cast<const uint4*>(words + t + j);
+    }
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int j = 0; j < VE; j += 4)
+        *reinterpret_cast<uint2*>(p + j) = *reinterpret_cast<const uint2*>(listed + t + j);
+    }
+    unsigned bits = ~0u;
+    if (allowed) {  // VE tokens may lie in two words
+      const int k = (lo + t) / 32, s = (lo + t) & 31;
+      bits = __ldg(allowed + k) >> s;
+      if (s > 32 - VE) bits |= __ldg(allowed + k + 1) << (32 - s);
+    }
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+      v[j] = from_f32<T>(adjust(as_f32<T>(v[j]), PAST ? w[j] : 0u, BIAS ? p[j] : 0u, bits >> j & 1u));
+    if (same) {
+      *reinterpret_cast<uint4*>(out + t) = raw;
+    } else {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) out[t + j] = v[j];
+    }
+  }
+}
+
+template <typename T, bool PAST, bool BIAS>
+static cudaError_t launch_adjust(AdjustArgs a, cudaStream_t st) {
+  auto* kern = adjust_kernel<T, PAST, BIAS>;
+  const int ve = 16 / sizeof(T);
+  int ctas = kAdjustCtas;
+  a.slice = ((a.V + ctas - 1) / ctas + 31) / 32 * 32;
+  if (!PAST) {  // no cluster: slices of any number
+    a.slice = a.slice < 8192 ? a.slice : 8192;
+    ctas = (a.V + a.slice - 1) / a.slice;
+  }
+  const int smem = (PAST ? a.slice + ve : 0) * 4 + (BIAS ? a.slice + ve : 0) * 2 + 16;
+  static std::atomic<uint64_t> done{0};
+  if (PAST) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern),
+                                     ((1 << 18) / kAdjustCtas + ve) * (BIAS ? 6 : 4) + 16, done);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_cluster(kern, dim3(ctas, a.N), dim3(kAdjustThreads), PAST ? ctas : 1, smem, st, a);
+}
+
+template <typename T>
+static cudaError_t launch_type(const AdjustArgs& a, cudaStream_t st) {
+  const bool past = a.history && a.max_history > 0;
+  if (past) return a.n_bias > 0 ? launch_adjust<T, true, true>(a, st) : launch_adjust<T, true, false>(a, st);
+  return a.n_bias > 0 ? launch_adjust<T, false, true>(a, st) : launch_adjust<T, false, false>(a, st);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_adjust_logits(const moe_adjust_t* s, const void* logits, int logits_dtype, int N,
+                                 int V, long long row_stride, void* out, long long out_stride,
+                                 uint32_t* err, void* stream) {
+  if (!s || N < 0 || N > 65535 || V < 1 || V > (1 << 18) || row_stride < 0 ||
+      (logits_dtype != MOE_LOGITS_F32 && logits_dtype != MOE_LOGITS_BF16) || s->requests < 0 ||
+      s->max_history < 0 || s->n_bias < 0 || s->n_bias > 65535 || s->history_stride < 0 ||
+      s->allowed_stride < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (!s->rows && s->requests < N) return MOE_ERR_INVALID_ARG;
+  if (N == 0) return MOE_OK;
+  const int es = logits_dtype == MOE_LOGITS_F32 ? 4 : 2;
+  if (!logits || !out || !apart(N, out_stride, V)) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out)) & (es - 1))
+    return MOE_ERR_INVALID_ARG;
+  if (s->history && s->max_history > 0 && !s->history_lens) return MOE_ERR_INVALID_ARG;
+  if (s->n_bias > 0 && (!s->bias_ids || !s->bias)) return MOE_ERR_INVALID_ARG;
+  // the logits themselves may be the output; anything else must not overlap them
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t x1 = x0 + (static_cast<uintptr_t>(N - 1) * row_stride + V) * es;
+  const uintptr_t o1 = o0 + (static_cast<uintptr_t>(N - 1) * out_stride + V) * es;
+  const bool itself = x0 == o0 && (N == 1 || row_stride == out_stride);
+  if (!itself && x0 < o1 && o0 < x1) return MOE_ERR_INVALID_ARG;
+  AdjustArgs a = {};
+  a.x = static_cast<const char*>(logits);
+  a.out = static_cast<char*>(out);
+  a.x_row = row_stride;
+  a.out_row = out_stride;
+  a.rows = s->rows;
+  a.history = s->history;
+  a.history_stride = s->history_stride;
+  a.history_lens = s->history_lens;
+  a.prompt_lens = s->prompt_lens;
+  a.repetition = s->repetition;
+  a.presence = s->presence;
+  a.frequency = s->frequency;
+  a.bias_ids = s->bias_ids;
+  a.bias = s->bias;
+  a.allowed = reinterpret_cast<const unsigned*>(s->allowed);
+  a.allowed_stride = s->allowed_stride;
+  a.err = err;
+  a.N = N;
+  a.V = V;
+  a.R = s->requests;
+  a.max_history = s->max_history;
+  a.n_bias = s->n_bias;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = logits_dtype == MOE_LOGITS_F32 ? launch_type<float>(a, st)
+                                                       : launch_type<__nv_bfloat16>(a, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

@@ -1,0 +1,392 @@
+// attn_tree.cu -- attention of several drafted tokens per request over the paged
+// cache (moe_attn_tree, include/moe_route.h): the host's side, and the kernel in
+// fp32 arithmetic.
+#include <cuda_fp8.h>
+
+#include "attn_tree.cuh"
+
+namespace moe {
+
+constexpr int kSimtRows = 32;
+constexpr int kSimtThreads = 256;
+constexpr int kSimtEnd = 1;
+template <int DP>
+struct SimtCfg {
+  static constexpr int TILE = DP == 256 ? 32 : 64;
+  static constexpr int KP = DP + 4, PP = TILE + 4;  // pitches without bank conflicts
+  static constexpr int SMEM = 4 * (kSimtRows * KP + TILE * KP + TILE * DP + kSimtRows * PP);
+  static constexpr int CTAS = 2;  // per SM
+};
+
+__device__ __forceinline__ void tree_cp16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+
+// 16 bytes of a cached vector as f32
+template <int KV>
+__device__ __forceinline__ void widen(uint4 raw, float* out) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (KV == MOE_KV_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[2 * i] = __uint_as_float(w[i] << 16);
+      out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __nv_fp8_e4m3 e;
+        e.__x = static_cast<__nv_fp8_storage_t>(w[i] >> (8 * j));
+        out[4 * i + j] = static_cast<float>(e);
+      }
+  }
+}
+
+// S = Q K^T, the running softmax and O += P V on tiles in shared memory, 2 rows
+// by TILE / 16 tokens and by DP / 16 columns a thread, all in fp32: nothing is
+// split or rounded.  A value that a row does not attend is skipped, not
+// multiplied by 0.
+template <int KV, int DP>
+__global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
+    tree_simt_kernel(const TreeArgs A) {
+  using C = SimtCfg<DP>;
+  constexpr int TILE = C::TILE, KP = C::KP, PP = C::PP, NK = TILE / 16, NC = DP / 64;
+  constexpr int ES = kv_esize(KV), VE = 16 / ES;
+  extern __shared__ __align__(16) float simt_smem[];
+  float* const qs = simt_smem;
+  float* const ks = qs + kSimtRows * KP;
+  float* const vs = ks + TILE * KP;
+  float* const ps = vs + TILE * DP;
+  __shared__ TreeStart start;
+  __shared__ long long sums[kSimtThreads / 32];
+  __shared__ long long s_off[2][TILE];  // a token's place in the cache, -1: none
+  pdl_wait();
+  pdl_trigger();
+  tree_begin<kSimtRows, TILE, kSimtEnd>(A, &start, sums);
+  auto walk = tree_walk<kSimtRows, TILE, kSimtEnd>(A, start);
+  auto at = walk;
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  bool bad_page = false;
+
+  while (walk.next(A, at)) {
+    const TreeSpan& s = at.s;
+    const int blocks = at.units / A.heads;
+    const int kvh = at.x / blocks, r0 = at.x % blocks * kSimtRows;
+    const int rows = min(kSimtRows, s.use * A.group - r0);
+    float f = A.scale_log2, v_mul = 1.0f;
+    if constexpr (KV == MOE_KV_E4M3) {
+      f *= A.k_scale[kvh];
+      v_mul = A.v_scale[kvh];
+    }
+    auto offsets = [&](int t, int buf) {
+      if (tid >= TILE) return;
+      const int pos = s.first + t * TILE + tid;
+      long long off = -1;
+      if (t < at.t1 && pos < s.len) {
+        const int p = A.page_shift >= 0 ? pos >> A.page_shift : pos / A.page;
+        const int id = __ldg(A.table + at.b * A.table_stride + p);
+        if (id >= 0 && id < A.num_pages)
+          off = id * A.s_page + (pos - p * A.page) * A.s_token + kvh * A.s_head;
+        else
+          bad_page = true;
+      }
+      s_off[buf][tid] = off;
+    };
+    auto load = [&](const char* base, float* to, int pitch, int buf) {
+      constexpr int CPR = DP / VE;
+      for (int i = tid; i < TILE * CPR; i += kSimtThreads) {
+        const int r = i / CPR, c = i % CPR;
+        const long long off = s_off[buf][r];
+        const bool real = off >= 0 && c * VE < A.dim;
+        float* const d = to + r * pitch + c * VE;
+        if constexpr (KV == MOE_KV_F32) {
+          tree_cp16(smem_u32(d), real ? base + off + c * 16 : base, real);
+        } else {
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          if (real) raw = *reinterpret_cast<const uint4*>(base + off + c * 16);
+          widen<KV>(raw, d);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    offsets(at.t0, 0);
+    for (int i = tid; i < kSimtRows * (DP / 4); i += kSimtThreads) {
+      const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows && d < A.dim) {
+        const int R = r0 + r, node = R / A.group, h = kvh * A.group + R - node * A.group;
+        const long long from = (s.row0 + node) * A.q_n + h * A.q_h + d;
+        if constexpr (KV == MOE_KV_F32) {
+          v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + from);
+        } else {
+          const uint2 raw =
+              *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(A.q) + from);
+          v = make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u));
+        }
+      }
+      *reinterpret_cast<float4*>(qs + r * KP + d) = v;
+    }
+    int node[2], low[2];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, acc[2][4 * NC] = {};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      node[e] = (r0 + min(2 * ty + e, rows - 1)) / A.group;
+      low[e] = tree_low(A, s, node[e]);
+    }
+    __syncthreads();
+    load(A.k, ks, KP, 0);
+    load(A.v, vs, DP, 0);
+    for (int t = at.t0; t < at.t1; ++t) {
+      const int buf = (t - at.t0) & 1, pos0 = s.first + t * TILE;
+      offsets(t + 1, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();
+      float x[2][NK] = {};
+#pragma unroll 4
+      for (int d = 0; d < DP; d += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(qs + (2 * ty) * KP + d);
+        const float4 b = *reinterpret_cast<const float4*>(qs + (2 * ty + 1) * KP + d);
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const float4 k = *reinterpret_cast<const float4*>(ks + (tx + 16 * j) * KP + d);
+          x[0][j] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, x[0][j]))));
+          x[1][j] = fmaf(b.x, k.x, fmaf(b.y, k.y, fmaf(b.z, k.z, fmaf(b.w, k.w, x[1][j]))));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        unsigned live = 0;
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const int c = tx + 16 * j;
+          const uint32_t bits = tree_attends(A, s, node[e], low[e], pos0 + (c & ~31));
+          const bool on = (bits >> (c & 31) & 1u) && s_off[buf][c] >= 0;
+          live |= static_cast<unsigned>(on) << j;
+          x[e][j] *= f;
+          if (on) top = fmaxf(top, x[e][j]);
+        }
+        if (live) top = fmaxf(top, -FLT_MAX);  // the row has tokens, if only of logits -inf
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float to = fmaxf(m[e], top);
+        const float keep = to == -INFINITY ? 1.0f : tree_ex2(m[e] - to);
+        m[e] = to;
+        l[e] *= keep;
+#pragma unroll
+        for (int c = 0; c < 4 * NC; ++c) acc[e][c] *= keep;
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const float p = live >> j & 1u ? tree_ex2(x[e][j] - to) : -1.0f;
+          ps[(2 * ty + e) * PP + tx + 16 * j] = p;  // -1: not attended
+          if (live >> j & 1u) l[e] += p;
+        }
+      }
+      __syncthreads();
+      load(A.k, ks, KP, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();
+#pragma unroll 2
+      for (int c = 0; c < TILE; c += 4) {
+        const float4 a4 = *reinterpret_cast<const float4*>(ps + (2 * ty) * PP + c);
+        const float4 b4 = *reinterpret_cast<const float4*>(ps + (2 * ty + 1) * PP + c);
+        const float pa[4] = {a4.x, a4.y, a4.z, a4.w}, pb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(vs + (c + u) * DP + 4 * tx + 64 * j);
+            if (!(pa[u] < 0.0f)) {
+              acc[0][4 * j] = fmaf(pa[u], v.x, acc[0][4 * j]);
+              acc[0][4 * j + 1] = fmaf(pa[u], v.y, acc[0][4 * j + 1]);
+              acc[0][4 * j + 2] = fmaf(pa[u], v.z, acc[0][4 * j + 2]);
+              acc[0][4 * j + 3] = fmaf(pa[u], v.w, acc[0][4 * j + 3]);
+            }
+            if (!(pb[u] < 0.0f)) {
+              acc[1][4 * j] = fmaf(pb[u], v.x, acc[1][4 * j]);
+              acc[1][4 * j + 1] = fmaf(pb[u], v.y, acc[1][4 * j + 1]);
+              acc[1][4 * j + 2] = fmaf(pb[u], v.z, acc[1][4 * j + 2]);
+              acc[1][4 * j + 3] = fmaf(pb[u], v.w, acc[1][4 * j + 3]);
+            }
+          }
+        }
+      }
+      __syncthreads();
+      load(A.v, vs, DP, buf ^ 1);
+    }
+    const bool whole = at.t0 == 0 && at.t1 == at.nt;
+    const long long part = 2ll * blockIdx.x + (at.t0 == 0 ? 0 : 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+      const int r = 2 * ty + e;
+      if (r >= rows) continue;
+      if (whole) {
+        const float inv = m[e] == -INFINITY ? 0.0f : v_mul / l[e];
+        const int R = r0 + r, h = kvh * A.group + R - node[e] * A.group;
+        const long long row = s.row0 + node[e];
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          if (4 * tx + 64 * j < A.dim)
+            tree_store4<KV>(A.out, row * A.o_n + h * A.o_h + 4 * tx + 64 * j, acc[e][4 * j] * inv,
+                            acc[e][4 * j + 1] * inv, acc[e][4 * j + 2] * inv,
+                            acc[e][4 * j + 3] * inv);
+        if (A.lse && tx == 0) A.lse[row * A.Hq + h] = tree_lse(m[e], l[e]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          *reinterpret_cast<float4*>(A.part_o + (part * kSimtRows + r) * DP + 4 * tx + 64 * j) =
+              make_float4(acc[e][4 * j], acc[e][4 * j + 1], acc[e][4 * j + 2], acc[e][4 * j + 3]);
+        if (tx == 0) A.part_ml[part * kSimtRows + r] = make_float2(m[e], l[e]);
+      }
+    }
+    if (tid == 0 && at.t1 < at.nt) tree_record(A, start, at);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // all of the tiles may be used again
+  }
+  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
+}
+
+// ------------------------------------------------------------ host
+struct TreeShape {
+  int rows, tile, ctas_per_sm;
+};
+static TreeShape tree_shape(int, int dp) {
+  return {kSimtRows, dp == 256 ? SimtCfg<256>::TILE : SimtCfg<64>::TILE, SimtCfg<64>::CTAS};
+}
+static int tree_dp(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+template <int KV, int DP>
+static cudaError_t launch_simt(const TreeArgs& a, int ctas, cudaStream_t st) {
+  auto* kern = tree_simt_kernel<KV, DP>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), SimtCfg<DP>::SMEM, done);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(kern, dim3(ctas), dim3(kSimtThreads), SimtCfg<DP>::SMEM, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_chained(tree_join_kernel<KV, DP, kSimtRows>, dim3(ctas), dim3(32 * kTreeJoinWarps),
+                        0, st, a);
+}
+template <int KV>
+static cudaError_t launch_kv(int dp, const TreeArgs& a, int ctas, cudaStream_t st) {
+  return dp == 64    ? launch_simt<KV, 64>(a, ctas, st)
+         : dp == 128 ? launch_simt<KV, 128>(a, ctas, st)
+                     : launch_simt<KV, 256>(a, ctas, st);
+}
+
+static size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_attn_tree_workspace(int kv_dtype, int head_dim) {
+  if (kv_dtype < MOE_KV_F32 || kv_dtype > MOE_KV_E4M3 || head_dim < 1 || head_dim > 256 ||
+      head_dim % kv_dim_step(kv_dtype))
+    return 0;
+  const int dp = tree_dp(head_dim);
+  const TreeShape s = tree_shape(kv_dtype, dp);
+  const size_t n = static_cast<size_t>(sm_count()) * s.ctas_per_sm;
+  return up256(n * sizeof(int4)) + up256(2 * n * s.rows * sizeof(float2)) +
+         2 * n * s.rows * dp * sizeof(float);
+}
+
+int moe_attn_tree(const moe_kv_cache_t* cache, const void* q, long long q_stride_n,
+                  long long q_stride_h, int N, int Hq, const int32_t* block_table, int max_pages,
+                  long long table_stride, const int32_t* starts, const int32_t* seq_lens, int B,
+                  const int64_t* masks, int max_new, float scale, int window, void* out,
+                  long long o_stride_n, long long o_stride_h, float* lse, void* ws,
+                  size_t ws_bytes, uint32_t* err, void* stream) {
+  const int rc = kv_cache_ok(cache);
+  if (rc != MOE_OK) return rc;
+  if (N < 0 || B < 0 || Hq < 1 || Hq % cache->kv_heads || Hq > (1 << 20) ||
+      static_cast<long long>(N) * Hq > INT_MAX || max_new < 1 || max_new > MOE_TREE_MAX ||
+      max_pages < 1 || table_stride < max_pages || window < 0 ||
+      static_cast<long long>(max_pages) * cache->page_size > INT_MAX - 1024 || q_stride_n < 0 ||
+      q_stride_h < 0 || o_stride_n < 0 || o_stride_h < 0 || !std::isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return MOE_OK;
+  if (!q || !block_table || !starts || !seq_lens || !out || !ws) return MOE_ERR_INVALID_ARG;
+  if (!apart(N, o_stride_n, cache->head_dim) || !apart(Hq, o_stride_h, cache->head_dim))
+    return MOE_ERR_INVALID_ARG;
+  const int qs = cache->kv_dtype == MOE_KV_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+       static_cast<uintptr_t>(q_stride_n * qs) | static_cast<uintptr_t>(q_stride_h * qs) |
+       static_cast<uintptr_t>(o_stride_n * qs) | static_cast<uintptr_t>(o_stride_h * qs)) &
+      15)
+    return MOE_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_attn_tree_workspace(cache->kv_dtype, cache->head_dim)) return MOE_ERR_WORKSPACE;
+  const int sms = sm_count();
+  if (sms < 1) return MOE_ERR_CUDA;
+  const int es = kv_esize(cache->kv_dtype), dp = tree_dp(cache->head_dim);
+  const TreeShape shape = tree_shape(cache->kv_dtype, dp);
+  TreeArgs a = {};
+  a.k = static_cast<const char*>(cache->k);
+  a.v = static_cast<const char*>(cache->v);
+  a.s_page = cache->stride_page * es;
+  a.s_token = cache->stride_token * es;
+  a.s_head = cache->stride_head * es;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.q = q;
+  a.q_n = q_stride_n;
+  a.q_h = q_stride_h;
+  a.out = out;
+  a.o_n = o_stride_n;
+  a.o_h = o_stride_h;
+  a.lse = lse;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.starts = starts;
+  a.lens = seq_lens;
+  a.masks = reinterpret_cast<const unsigned long long*>(masks);
+  a.err = err;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.N = N;
+  a.B = B;
+  a.Hq = Hq;
+  a.heads = cache->kv_heads;
+  a.group = Hq / cache->kv_heads;
+  a.words = (max_new + 63) / 64;
+  a.max_new = max_new;
+  a.dim = cache->head_dim;
+  a.page = cache->page_size;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page == 1 << i) a.page_shift = i;
+  a.num_pages = cache->num_pages;
+  a.max_pages = max_pages;
+  a.window = window;
+  const int full = sms * shape.ctas_per_sm;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.info = reinterpret_cast<int4*>(w);
+  w += up256(full * sizeof(int4));
+  a.part_ml = reinterpret_cast<float2*>(w);
+  w += up256(2ull * full * shape.rows * sizeof(float2));
+  a.part_o = reinterpret_cast<float*>(w);
+  // no more CTAs than tiles that these sizes can hold: units by the rows there
+  // are (a block for each request that has any, and one for every full block)
+  const long long blocks = static_cast<long long>(N) * a.group / shape.rows + (B < N ? B : N);
+  const long long tiles = (static_cast<long long>(max_pages) * a.page + shape.tile - 1) / shape.tile;
+  const long long units = blocks * a.heads;
+  const int ctas = units >= full || tiles >= full || units * tiles >= full
+                       ? full
+                       : static_cast<int>(units * tiles);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = cache->kv_dtype == MOE_KV_F32    ? launch_kv<MOE_KV_F32>(dp, a, ctas, st)
+                        : cache->kv_dtype == MOE_KV_BF16 ? launch_kv<MOE_KV_BF16>(dp, a, ctas, st)
+                                                         : launch_kv<MOE_KV_E4M3>(dp, a, ctas, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

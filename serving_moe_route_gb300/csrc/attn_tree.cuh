@@ -1,0 +1,345 @@
+// attn_tree.cuh -- what the kernels of moe_attn_tree share: the arguments, the
+// deal of the work to CTAs, and which tokens a row attends.
+//
+// A unit is (request, kv head, block of ROWS rows), a row being (node, query head
+// of that kv head), nodes in order.  Its tokens form tiles of TILE; it counts its
+// tiles and END more for its end.  The counts of all units, in order, are cut into
+// equal contiguous ranges, one per CTA of a single wave, so that ragged lengths
+// and one long request balance alike.  A range may begin and end inside a unit;
+// the unit's parts go to the workspace and a second kernel joins them in order.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_route.h"
+#include "decode_internal.cuh"
+#include "moe_internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+struct TreeArgs {
+  const char *k, *v;
+  long long s_page, s_token, s_head;  // bytes
+  const float *k_scale, *v_scale;
+  const void* q;
+  long long q_n, q_h;  // elements
+  void* out;
+  long long o_n, o_h;  // elements
+  float* lse;
+  const int* table;
+  long long table_stride;
+  const int *starts, *lens;
+  const unsigned long long* masks;
+  float* part_o;    // [2 * ctas][ROWS][DP]
+  float2* part_ml;  // [2 * ctas][ROWS]
+  int4* info;       // [ctas] {unit's request, unit in request, parts, place among them}
+  unsigned* err;
+  float scale_log2;
+  int N, B, Hq, heads, group, words, max_new;
+  int dim, page, page_shift, num_pages, max_pages, window;
+};
+
+// A request's rows and tokens
+struct TreeSpan {
+  int row0, n, use;  // first row, rows, rows that are worked on
+  int ctx, first, len;  // context tokens, first token that any row attends, end
+};
+
+__device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int r, bool& cut) {
+  TreeSpan s;
+  s.row0 = max(0, min(A.starts[r], A.N));
+  s.n = max(s.row0, min(A.starts[r + 1], A.N)) - s.row0;
+  s.use = min(s.n, A.max_new);
+  const int all = max(A.lens[r], 0);
+  const long long room = static_cast<long long>(A.max_pages) * A.page;
+  s.len = static_cast<int>(min(static_cast<long long>(all), room));
+  s.ctx = max(0, all - s.n);
+  s.first = A.window > 0 ? min(max(0, s.ctx - A.window), s.len) : 0;
+  if (s.n > 0 && (s.use < s.n || s.len < all)) cut = true;
+  return s;
+}
+template <int ROWS>
+__device__ __forceinline__ int tree_units(const TreeArgs& A, const TreeSpan& s) {
+  return (s.use * A.group + ROWS - 1) / ROWS * A.heads;
+}
+template <int TILE>
+__device__ __forceinline__ int tree_tiles(const TreeSpan& s) {
+  return max(1, (s.len - s.first + TILE - 1) / TILE);
+}
+
+// A CTA's range, walked part by part: tiles [t0, t1) of the nt of unit x of
+// request b.  Every role of a CTA keeps one.
+template <int ROWS, int TILE, int END>
+struct TreeWalk {
+  TreeSpan s;
+  int b, x, t, nt, units;
+  long long left, end;  // places from here on; the range's end, counted over all units
+  int t0, t1;
+
+  __device__ __forceinline__ void enter(const TreeArgs& A, int request) {
+    bool cut = false;
+    for (b = request; b < A.B; ++b) {
+      s = tree_span(A, b, cut);
+      units = tree_units<ROWS>(A, s);
+      if (units > 0) break;
+    }
+    nt = tree_tiles<TILE>(s);
+    x = 0;
+    t = 0;
+  }
+  // the next part; false at the range's end.  `at` is its unit (s, b, x, nt)
+  __device__ __forceinline__ bool next(const TreeArgs& A, TreeWalk& at) {
+    if (left <= 0) return false;
+    at = *this;
+    at.t0 = t;
+    at.t1 = static_cast<int>(min(static_cast<long long>(nt), t + left));
+    left -= at.t1 - t;
+    if (at.t1 < nt) {
+      left = 0;
+      return true;
+    }
+    left -= END;
+    t = 0;
+    if (left > 0 && ++x >= units) enter(A, b + 1);
+    return true;
+  }
+};
+
+// Where this CTA's range begins.  Every thread of the CTA (a multiple of 32, at
+// most 1024) calls it; the result is in shared memory.  total: of all units.
+struct TreeStart {
+  long long left, end, total;
+  int b, x, t, ctas;
+};
+template <int ROWS, int TILE, int END>
+__device__ __forceinline__ void tree_begin(const TreeArgs& A, TreeStart* out, long long* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int threads = blockDim.x, nw = threads >> 5;
+  bool cut = false;
+  auto places = [&](const TreeSpan& s) {
+    return static_cast<long long>(tree_units<ROWS>(A, s)) * (tree_tiles<TILE>(s) + END);
+  };
+  const int per = (A.B - 1) / threads + 1;
+  const int b0 = static_cast<int>(min(static_cast<long long>(A.B),
+                                      static_cast<long long>(threadIdx.x) * per));
+  const int b1 = b0 + min(per, A.B - b0);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += places(tree_span(A, b, cut));
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  if (cut && A.err && blockIdx.x == 0) atomicOr(A.err, MOE_DEVERR_NO_SPACE);
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    A.info[cta] = make_int4(0, 0, 0, 0);
+    if (cta >= ctas) {
+      out->left = 0;
+      out->ctas = ctas;
+      out->total = total;
+    }
+  }
+  if (cta < ctas) {
+    const long long begin = cta * total / ctas, end = (cta + 1) * total / ctas;
+    const long long lo = before + incl - mine, hi = before + incl;
+    if (begin >= lo && begin < hi) {
+      long long at = lo;
+      int b = b0;
+      TreeSpan s;
+      for (;; ++b) {
+        s = tree_span(A, b, cut);
+        const long long n = places(s);
+        if (begin < at + n) break;
+        at += n;
+      }
+      const int one = tree_tiles<TILE>(s) + END;
+      out->b = b;
+      out->x = static_cast<int>((begin - at) / one);
+      out->t = static_cast<int>(begin - at - static_cast<long long>(out->x) * one);
+      out->left = end - begin;
+      out->end = end;
+      out->total = total;
+      out->ctas = ctas;
+    }
+  }
+  __syncthreads();
+}
+template <int ROWS, int TILE, int END>
+__device__ __forceinline__ TreeWalk<ROWS, TILE, END> tree_walk(const TreeArgs& A,
+                                                               const TreeStart& w) {
+  TreeWalk<ROWS, TILE, END> k;
+  k.left = w.left;
+  k.end = w.end;
+  if (k.left <= 0) return k;
+  k.enter(A, w.b);
+  k.x = w.x;
+  k.t = w.t;
+  if (k.t >= k.nt) {  // the range begins with a unit's end: on to the next
+    k.left -= k.nt + END - k.t;
+    k.t = 0;
+    if (k.left > 0 && ++k.x >= k.units) k.enter(A, k.b + 1);
+  }
+  return k;
+}
+
+// The record of a unit that goes on behind this CTA's range (one thread)
+template <int ROWS, int TILE, int END>
+__device__ __forceinline__ void tree_record(const TreeArgs& A, const TreeStart& w,
+                                            const TreeWalk<ROWS, TILE, END>& at) {
+  // at: as `next` left it, its `left` counted from t0 on
+  const long long from = at.end - at.left - at.t0, to = from + at.nt - 1;
+  const int c0 = static_cast<int>(((from + 1) * w.ctas - 1) / w.total);
+  const int c1 = static_cast<int>(((to + 1) * w.ctas - 1) / w.total);
+  A.info[blockIdx.x] =
+      make_int4(at.b, at.x, c1 - c0 + 1, static_cast<int>(blockIdx.x) - c0);
+}
+
+// ------------------------------------------------------------ what a row attends
+// 32 bits of node i's mask from new token j on (j may be negative)
+__device__ __forceinline__ uint32_t tree_bits(const TreeArgs& A, const TreeSpan& s, int i, int j) {
+  const int lim = min(s.n, s.len - s.ctx);  // new tokens there are
+  if (j >= lim || j <= -32) return 0;
+  uint32_t bits;
+  if (A.masks) {
+    const unsigned long long* m = A.masks + static_cast<long long>(s.row0 + i) * A.words;
+    if (j < 0) {
+      bits = static_cast<uint32_t>(m[0]) << -j;
+    } else {
+      const int w = j >> 6, sh = j & 63;
+      unsigned long long v = w < A.words ? m[w] >> sh : 0;
+      if (sh > 32 && w + 1 < A.words) v |= m[w + 1] << (64 - sh);
+      bits = static_cast<uint32_t>(v);
+    }
+  } else {
+    const int n = i + 1 - j;  // tokens j .. i
+    bits = n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1;
+    if (j < 0) bits &= ~0u << -j;
+  }
+  if (lim - j < 32) bits &= (1u << (lim - j)) - 1;
+  return bits;
+}
+// first context token that node i attends
+__device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, int i) {
+  if (A.window <= 0) return 0;
+  int c = 0;
+  for (int j = 0; j < 64 * A.words; j += 32) c += __popc(tree_bits(A, s, i, j));
+  return max(0, s.ctx - max(0, A.window - c));
+}
+// which of the 32 tokens from t on node i attends (by its mask and window alone)
+__device__ __forceinline__ uint32_t tree_attends(const TreeArgs& A, const TreeSpan& s, int i,
+                                                 int low, int t) {
+  uint32_t bits = 0;
+  const int end = min(s.ctx, s.len);
+  if (t < end && t + 32 > low) {
+    bits = ~0u;
+    if (end - t < 32) bits &= (1u << (end - t)) - 1;
+    if (low > t) bits &= ~0u << (low - t);
+  }
+  return bits | tree_bits(A, s, i, t - s.ctx);
+}
+
+__device__ __forceinline__ float tree_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float tree_lse(float top, float sum) {
+  return top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+__device__ __forceinline__ uint32_t tree_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <int KV>
+__device__ __forceinline__ void tree_store4(void* out, long long at, float a, float b, float c,
+                                            float d) {
+  if constexpr (KV == MOE_KV_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(a, b, c, d);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + at) =
+        make_uint2(tree_bf16x2(a, b), tree_bf16x2(c, d));
+}
+
+// Joins the parts of the units that range borders cut.  A unit that begins in CTA
+// c and does not end there has c's first slot, then the second slots of the next
+// CTAs; the blocks of all those but the last deal its rows out, a row a warp.
+constexpr int kTreeJoinWarps = 16;
+template <int KV, int DP, int ROWS>
+__global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const TreeArgs A) {
+  constexpr int VL = DP / 32;  // columns per lane
+  pdl_wait();
+  const int4 unit = A.info[blockIdx.x];
+  const int parts = unit.z, cta = blockIdx.x - unit.w;
+  if (parts == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool cut = false;
+  const TreeSpan s = tree_span(A, unit.x, cut);
+  const int blocks = (s.use * A.group + ROWS - 1) / ROWS;
+  const int kvh = unit.y / blocks, r0 = unit.y % blocks * ROWS;
+  const int rows = min(ROWS, s.use * A.group - r0);
+  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
+  for (int r = unit.w * kTreeJoinWarps + warp; r < rows; r += (parts - 1) * kTreeJoinWarps) {
+    auto at = [&](int p) { return (2ll * (cta + p) + (p == 0 ? 0 : 1)) * ROWS + r; };
+    float top = -INFINITY;
+    for (int p = lane; p < parts; p += 32) top = fmaxf(top, A.part_ml[at(p)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float sum = 0.0f, o[VL] = {};
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (p0 + lane < parts) ml = A.part_ml[at(p0 + lane)];
+      const float f = top == -INFINITY ? 1.0f : tree_ex2(ml.x - top);
+      const float fl = f * ml.y;
+      const int n = min(32, parts - p0);
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const float g = __shfl_sync(0xffffffffu, f, p);
+        sum += __shfl_sync(0xffffffffu, fl, p);
+        const float* x = A.part_o + at(p0 + p) * DP + lane * VL;
+        float v[VL];
+#pragma unroll
+        for (int j = 0; j < VL; j += 2)
+          *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(x + j);
+#pragma unroll
+        for (int j = 0; j < VL; ++j) o[j] += g * v[j];
+      }
+    }
+    const float inv = top == -INFINITY ? 0.0f : mul / sum;
+    const int R = r0 + r, node = R / A.group, h = kvh * A.group + R - node * A.group;
+    const long long row = s.row0 + node;
+#pragma unroll
+    for (int j = 0; j < VL; ++j) o[j] *= inv;
+    const long long to = row * A.o_n + h * A.o_h;
+    if constexpr (VL >= 4) {
+#pragma unroll
+      for (int j = 0; j < VL; j += 4)
+        if (lane * VL + j < A.dim)
+          tree_store4<KV>(A.out, to + lane * VL + j, o[j], o[j + 1], o[j + 2], o[j + 3]);
+    } else {  // two lanes' columns together
+      const float a = __shfl_down_sync(0xffffffffu, o[0], 1);
+      const float b = __shfl_down_sync(0xffffffffu, o[1], 1);
+      if (lane % 2 == 0 && lane * VL < A.dim)
+        tree_store4<KV>(A.out, to + lane * VL, o[0], o[1], a, b);
+    }
+    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse(top, sum);
+  }
+}
+
+}  // namespace moe

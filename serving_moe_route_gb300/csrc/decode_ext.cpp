@@ -153,8 +153,8 @@ void rows3(const Tensor& t, at::ScalarType type, int64_t n, int64_t heads, int64
   contiguous_last(t, name);
 }
 
-moe_kv_cache_t kv_cache(const Tensor& k, const Tensor& v, PyObject* k_scale, PyObject* v_scale,
-                        int dev) {
+// A cache whose vectors are only moved: scales do not matter
+moe_kv_cache_t kv_cache(const Tensor& k, const Tensor& v, int dev) {
   on_device(k, "k_cache", dev);
   on_device(v, "v_cache", dev);
   moe_kv_cache_t c = {};
@@ -184,6 +184,12 @@ moe_kv_cache_t kv_cache(const Tensor& k, const Tensor& v, PyObject* k_scale, PyO
   c.stride_head = stride_of(k, 2);
   c.k = k.data_ptr();
   c.v = v.data_ptr();
+  return c;
+}
+
+moe_kv_cache_t kv_cache(const Tensor& k, const Tensor& v, PyObject* k_scale, PyObject* v_scale,
+                        int dev) {
+  moe_kv_cache_t c = kv_cache(k, v, dev);
   const bool q8 = c.kv_dtype == MOE_KV_E4M3;
   if (q8 && (k_scale == Py_None || v_scale == Py_None))
     refuse("a float8_e4m3fn cache needs k_scale and v_scale");
@@ -464,6 +470,388 @@ PyObject* sample_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A contiguous matrix of n rows; returns its width
+int64_t matrix(const Tensor& t, at::ScalarType type, int64_t n, const char* name, int dev) {
+  on_device(t, name, dev);
+  of_type(t, type, name);
+  if (t.dim() != 2 || t.size(0) != n || t.size(1) > INT32_MAX) {
+    std::ostringstream o;
+    o << name << " must have shape (" << n << ", n), got " << shape_text(t.sizes());
+    refuse(o.str());
+  }
+  if (!t.is_contiguous()) refuse(std::string(name) + " must be contiguous");
+  return t.size(1);
+}
+
+// starts of B requests: B
+int64_t requests_of(const Tensor& starts, int dev) {
+  const int64_t n = length(starts, "starts");
+  if (n < 1 || n - 1 > INT32_MAX) refuse("starts must hold one number more than there are requests");
+  vec(starts, at::kInt, n, "starts", dev);
+  return n - 1;
+}
+
+void fits(int64_t n, const char* name) {
+  if (n > INT32_MAX) refuse(std::string(name) + " must fit 32 bits");
+}
+
+long long nodes_of(PyObject* o, const char* name) {
+  const long long n = integer(o, name);
+  if (n < 1 || n > MOE_TREE_MAX)
+    refuse(std::string(name) + " must be from 1 to " + std::to_string(MOE_TREE_MAX));
+  return n;
+}
+
+// (parents, starts, seq_lens, max_new, err, stream)
+PyObject* tree_masks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 6, [&]() -> PyObject* {
+    const Tensor &parents = tensor(a[0], "parents"), &starts = tensor(a[1], "starts"),
+                 &lens = tensor(a[2], "seq_lens");
+    const Place at_(parents, "parents", a[5]);
+    const int dev = at_.dev;
+    const int64_t N = length(parents, "parents"), B = requests_of(starts, dev);
+    fits(N, "parents");
+    vec(parents, at::kInt, N, "parents", dev);
+    vec(lens, at::kInt, B, "seq_lens", dev);
+    const long long max_new = nodes_of(a[3], "max_new");
+    if (B == 0 && N > 0) refuse("rows of no requests: starts holds one number");
+    const Tensor masks = at_.make({N, (max_new + 63) / 64}, at::kLong), pos = at_.make({N}, at::kInt);
+    check(moe_tree_masks(i32(parents), static_cast<int>(N), i32(starts), i32(lens),
+                         static_cast<int>(B), static_cast<int>(max_new),
+                         static_cast<int64_t*>(masks.data_ptr()), i32(pos), error_word(a[4], dev),
+                         at_.stream),
+          "moe_tree_masks");
+    PyObject* r = PyTuple_New(2);
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(masks));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(pos));
+    return r;
+  });
+}
+
+// (tokens, draws, parents, starts, ctx_lens, max_path, err, stream)
+PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 8, [&]() -> PyObject* {
+    const Tensor &tokens = tensor(a[0], "tokens"), &draws = tensor(a[1], "draws"),
+                 &parents = tensor(a[2], "parents"), &starts = tensor(a[3], "starts"),
+                 &ctx = tensor(a[4], "ctx_lens");
+    const Place at_(tokens, "tokens", a[7]);
+    const int dev = at_.dev;
+    const int64_t N = length(tokens, "tokens"), B = requests_of(starts, dev);
+    fits(N, "tokens");
+    vec(tokens, at::kInt, N, "tokens", dev);
+    vec(draws, at::kInt, N, "draws", dev);
+    vec(parents, at::kInt, N, "parents", dev);
+    vec(ctx, at::kInt, B, "ctx_lens", dev);
+    const long long max_path = nodes_of(a[5], "max_path");
+    const Tensor all = at_.make({B * (max_path + 3)}, at::kInt);
+    const Tensor path = cut(all, 0, B * max_path), accepted = cut(all, B * max_path, B),
+                 next = cut(all, B * (max_path + 1), B), lens = cut(all, B * (max_path + 2), B);
+    path.unsafeGetTensorImpl()->set_sizes_contiguous({B, max_path});
+    check(moe_tree_accept(i32(tokens), i32(draws), i32(parents), static_cast<int>(N), i32(starts),
+                          i32(ctx), static_cast<int>(B), static_cast<int>(max_path), i32(path),
+                          i32(accepted), i32(next), i32(lens), error_word(a[6], dev), at_.stream),
+          "moe_tree_accept");
+    PyObject* r = PyTuple_New(4);
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(path));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(accepted));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(next));
+    PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(lens));
+    return r;
+  });
+}
+
+// (q, k_cache, v_cache, block_table, starts, seq_lens, masks, max_new, scale,
+//  window, k_scale, v_scale, out, return_lse, workspace, err, stream)
+PyObject* attn_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 17, [&]() -> PyObject* {
+    const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"),
+                 &vc = tensor(a[2], "v_cache"), &table = tensor(a[3], "block_table"),
+                 &starts = tensor(a[4], "starts"), &lens = tensor(a[5], "seq_lens");
+    const Place at_(kc, "k_cache", a[16]);
+    const int dev = at_.dev;
+    const moe_kv_cache_t c = kv_cache(kc, vc, a[10], a[11], dev);
+    if (q.dim() != 3) refuse("q must be [N, Hq, head_dim]");
+    const int64_t N = q.size(0), hq = q.size(1), dim = c.head_dim, B = requests_of(starts, dev);
+    rows3(q, vector_type(c), N, hq, dim, "q", dev);
+    if (hq < 1 || c.kv_heads < 1 || hq % c.kv_heads) {
+      std::ostringstream o;
+      o << "Hq=" << hq << " is not a multiple of kv_heads=" << c.kv_heads;
+      refuse(o.str());
+    }
+    const Table t = block_table(table, B, dev);
+    vec(lens, at::kInt, B, "seq_lens", dev);
+    if (hq > (1 << 20) || N > INT32_MAX / hq || t.width > INT32_MAX) refuse("sizes must fit 32 bits");
+    const long long max_new = nodes_of(a[7], "max_new");
+    const int64_t* masks = nullptr;
+    if (a[6] != Py_None) {
+      const Tensor& m = tensor(a[6], "masks");
+      if (matrix(m, at::kLong, N, "masks", dev) != (max_new + 63) / 64)
+        refuse("masks must have a word for every 64 of max_new");
+      masks = static_cast<const int64_t*>(m.data_ptr());
+    }
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(dim)) : number(a[8]);
+    const long long window = integer(a[9], "window");
+    Tensor out;
+    if (a[12] == Py_None) {
+      out = at_.make({N, hq, dim}, vector_type(c));
+    } else {
+      out = tensor(a[12], "out");
+      rows3(out, vector_type(c), N, hq, dim, "out", dev);
+    }
+    const int with_lse = PyObject_IsTrue(a[13]);
+    if (with_lse < 0) throw Raised{};
+    Tensor lse;
+    if (with_lse) lse = at_.make({N, hq}, at::kFloat);
+    const size_t need = moe_attn_tree_workspace(c.kv_dtype, c.head_dim);
+    c10::DataPtr own;  // returned to the stream's pool when the call has been enqueued
+    void* ws;
+    size_t bytes = need;
+    if (a[14] == Py_None) {
+      own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+      ws = own.get();
+    } else {
+      const Tensor& w = tensor(a[14], "workspace");
+      bytes = static_cast<size_t>(length(w, "workspace"));
+      ws = vec(w, at::kByte, w.size(0), "workspace", dev);
+    }
+    check(moe_attn_tree(&c, q.data_ptr(), stride_of(q, 0), stride_of(q, 1), static_cast<int>(N),
+                        static_cast<int>(hq), t.p, static_cast<int>(t.width), t.stride, i32(starts),
+                        i32(lens), static_cast<int>(B), masks, static_cast<int>(max_new),
+                        static_cast<float>(scale), static_cast<int>(window), out.data_ptr(),
+                        stride_of(out, 0), stride_of(out, 1),
+                        with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws, bytes,
+                        error_word(a[15], dev), at_.stream),
+          "moe_attn_tree");
+    if (a[12] != Py_None) written(out);
+    if (!with_lse) return THPVariable_Wrap(out);
+    PyObject* r = PyTuple_New(2);
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(out));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(lse));
+    return r;
+  });
+}
+
+// (path, accepted, ctx_lens, block_table, k_cache, v_cache, err, stream)
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 8, [&]() -> PyObject* {
+    const Tensor &path = tensor(a[0], "path"), &accepted = tensor(a[1], "accepted"),
+                 &ctx = tensor(a[2], "ctx_lens"), &table = tensor(a[3], "block_table"),
+                 &kc = tensor(a[4], "k_cache"), &vc = tensor(a[5], "v_cache");
+    const Place at_(kc, "k_cache", a[7]);
+    const int dev = at_.dev;
+    const moe_kv_cache_t c = kv_cache(kc, vc, dev);
+    const int64_t B = length(accepted, "accepted");
+    fits(B, "accepted");
+    vec(accepted, at::kInt, B, "accepted", dev);
+    vec(ctx, at::kInt, B, "ctx_lens", dev);
+    const int64_t P = matrix(path, at::kInt, B, "path", dev);
+    const Table t = block_table(table, B, dev);
+    fits(t.width, "block_table");
+    check(moe_kv_compact(&c, i32(path), static_cast<int>(P), i32(accepted), i32(ctx),
+                         static_cast<int>(B), t.p, static_cast<int>(t.width), t.stride,
+                         error_word(a[6], dev), at_.stream),
+          "moe_kv_compact");
+    written(kc);
+    written(vc);
+    Py_RETURN_NONE;
+  });
+}
+
+// (src_pages, dst_pages, k_cache, v_cache, tokens, err, stream)
+PyObject* kv_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 7, [&]() -> PyObject* {
+    const Tensor &src = tensor(a[0], "src_pages"), &dst = tensor(a[1], "dst_pages"),
+                 &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache");
+    const Place at_(kc, "k_cache", a[6]);
+    const int dev = at_.dev;
+    const moe_kv_cache_t c = kv_cache(kc, vc, dev);
+    const int64_t F = length(src, "src_pages");
+    fits(F, "src_pages");
+    vec(src, at::kInt, F, "src_pages", dev);
+    vec(dst, at::kInt, F, "dst_pages", dev);
+    check(moe_kv_copy_pages(&c, i32(src), i32(dst),
+                            static_cast<int32_t*>(optional_vec(a[4], at::kInt, F, "tokens", dev)),
+                            static_cast<int>(F), error_word(a[5], dev), at_.stream),
+          "moe_kv_copy_pages");
+    written(kc);
+    written(vc);
+    Py_RETURN_NONE;
+  });
+}
+
+// (src_rows, dst_rows, ctx_lens, block_table, page_refs, free_pages, n_free,
+//  page_size, num_pages, err, stream)
+PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 11, [&]() -> PyObject* {
+    const Tensor &src = tensor(a[0], "src_rows"), &dst = tensor(a[1], "dst_rows"),
+                 &ctx = tensor(a[2], "ctx_lens"), &table = tensor(a[3], "block_table"),
+                 &refs = tensor(a[4], "page_refs"), &free = tensor(a[5], "free_pages"),
+                 &left = tensor(a[6], "n_free");
+    const Place at_(ctx, "ctx_lens", a[10]);
+    const int dev = at_.dev;
+    const int64_t F = length(src, "src_rows"), B = length(ctx, "ctx_lens"),
+                  cap = length(free, "free_pages");
+    vec(src, at::kInt, F, "src_rows", dev);
+    vec(dst, at::kInt, F, "dst_rows", dev);
+    vec(ctx, at::kInt, B, "ctx_lens", dev);
+    vec(free, at::kInt, cap, "free_pages", dev);
+    vec(left, at::kInt, 1, "n_free", dev);
+    const long long page = integer(a[7], "page_size"), pages = integer(a[8], "num_pages");
+    vec(refs, at::kInt, pages, "page_refs", dev);
+    const Table t = block_table(table, B, dev);
+    if (F > INT32_MAX || B > INT32_MAX || cap > INT32_MAX || t.width > INT32_MAX)
+      refuse("sizes must fit 32 bits");
+    const Tensor all = at_.make({3 * F}, at::kInt);
+    const Tensor from = cut(all, 0, F), to = cut(all, F, F), tokens = cut(all, 2 * F, F);
+    check(moe_kv_fork(i32(src), i32(dst), static_cast<int>(F), i32(ctx), static_cast<int>(B), t.p,
+                      static_cast<int>(t.width), t.stride, i32(refs), i32(free),
+                      static_cast<int>(cap), i32(left), static_cast<int>(pages),
+                      static_cast<int>(page), i32(from), i32(to), i32(tokens),
+                      error_word(a[9], dev), at_.stream),
+          "moe_kv_fork");
+    written(ctx);
+    written(table);
+    written(refs);
+    written(left);
+    PyObject* r = PyTuple_New(3);
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(from));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(to));
+    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(tokens));
+    return r;
+  });
+}
+
+// (keep_lens, seq_lens, block_table, free_pages, n_free, page_size, num_pages,
+//  page_refs, err, stream)
+PyObject* kv_trim(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 10, [&]() -> PyObject* {
+    const Tensor &keep = tensor(a[0], "keep_lens"), &lens = tensor(a[1], "seq_lens"),
+                 &table = tensor(a[2], "block_table"), &free = tensor(a[3], "free_pages"),
+                 &left = tensor(a[4], "n_free");
+    const Place at_(keep, "keep_lens", a[9]);
+    const int dev = at_.dev;
+    const int64_t B = length(keep, "keep_lens"), cap = length(free, "free_pages");
+    vec(keep, at::kInt, B, "keep_lens", dev);
+    vec(lens, at::kInt, B, "seq_lens", dev);
+    vec(free, at::kInt, cap, "free_pages", dev);
+    vec(left, at::kInt, 1, "n_free", dev);
+    const long long page = integer(a[5], "page_size"), pages = integer(a[6], "num_pages");
+    void* const refs = optional_vec(a[7], at::kInt, pages, "page_refs", dev);
+    const Table t = block_table(table, B, dev);
+    if (B > INT32_MAX || cap > INT32_MAX || t.width > INT32_MAX) refuse("sizes must fit 32 bits");
+    check(moe_kv_trim(i32(keep), i32(lens), static_cast<int>(B), t.p, static_cast<int>(t.width),
+                      t.stride, i32(free), static_cast<int>(cap), i32(left),
+                      static_cast<int32_t*>(refs), static_cast<int>(pages), static_cast<int>(page),
+                      error_word(a[8], dev), at_.stream),
+          "moe_kv_trim");
+    written(table);
+    written(free);
+    written(left);
+    if (refs) written(tensor(a[7], "page_refs"));
+    Py_RETURN_NONE;
+  });
+}
+
+// [n, V] with contiguous rows
+void logits_of(const Tensor& x, const char* name) {
+  if (x.scalar_type() != at::kFloat && x.scalar_type() != at::kBFloat16)
+    refuse(std::string(name) + " must be float32 or bfloat16");
+  if (x.dim() != 2 || x.size(1) < 1 || (x.size(1) > 1 && x.stride(1) != 1))
+    refuse(std::string(name) + " must be [N, V] with contiguous rows");
+}
+
+// (logits, rows, history, history_lens, prompt_lens, repetition, presence,
+//  frequency, bias_ids, bias, allowed, out, err, stream)
+PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry(n, 14, [&]() -> PyObject* {
+    const Tensor& x = tensor(a[0], "logits");
+    const Place at_(x, "logits", a[13]);
+    const int dev = at_.dev;
+    logits_of(x, "logits");
+    const int64_t N = x.size(0), V = x.size(1);
+    if (N > INT32_MAX || V > INT32_MAX) refuse("sizes must fit 32 bits");
+    moe_adjust_t s = {};
+    s.rows = static_cast<const int32_t*>(optional_vec(a[1], at::kInt, N, "rows", dev));
+    // requests: as many as the first tensor that speaks of them has
+    int64_t R = -1;
+    for (int i = 2; i < 10 && R < 0; ++i)
+      if (a[i] != Py_None) {
+        const Tensor& t = tensor(a[i], "a request's setting");
+        if (t.dim() < 1) refuse("settings must have a row per request");
+        R = t.size(0);
+      }
+    if (R < 0) R = s.rows ? INT32_MAX : N;
+    if (!s.rows && R != N) refuse("settings must have a row for each of logits, or rows must be given");
+    fits(R, "requests");
+    s.requests = static_cast<int32_t>(R);
+    if (a[2] != Py_None) {
+      const Tensor& h = tensor(a[2], "history");
+      on_device(h, "history", dev);
+      of_type(h, at::kInt, "history");
+      if (h.dim() != 2 || h.size(0) != R || h.size(1) > INT32_MAX ||
+          (h.size(1) > 1 && h.stride(1) != 1) || (R > 1 && h.stride(0) < 0))
+        refuse("history must be [requests, length] with contiguous rows");
+      if (a[3] == Py_None) refuse("history needs history_lens");
+      s.history = i32(h);
+      s.max_history = static_cast<int32_t>(h.size(1));
+      s.history_stride = R > 1 ? h.stride(0) : h.size(1);
+    } else {
+      for (int i = 3; i < 8; ++i)
+        if (a[i] != Py_None)
+          refuse("history_lens, prompt_lens and penalties are only used with a history");
+    }
+    s.history_lens = static_cast<const int32_t*>(optional_vec(a[3], at::kInt, R, "history_lens", dev));
+    s.prompt_lens = static_cast<const int32_t*>(optional_vec(a[4], at::kInt, R, "prompt_lens", dev));
+    s.repetition = static_cast<const float*>(optional_vec(a[5], at::kFloat, R, "repetition", dev));
+    s.presence = static_cast<const float*>(optional_vec(a[6], at::kFloat, R, "presence", dev));
+    s.frequency = static_cast<const float*>(optional_vec(a[7], at::kFloat, R, "frequency", dev));
+    if ((a[8] == Py_None) != (a[9] == Py_None)) refuse("bias_ids and bias come together");
+    if (a[8] != Py_None) {
+      const Tensor &ids = tensor(a[8], "bias_ids"), &bias = tensor(a[9], "bias");
+      const int64_t m = matrix(ids, at::kInt, R, "bias_ids", dev);
+      if (matrix(bias, at::kFloat, R, "bias", dev) != m)
+        refuse("bias must have the shape of bias_ids");
+      s.n_bias = static_cast<int32_t>(m);
+      s.bias_ids = i32(ids);
+      s.bias = static_cast<const float*>(bias.data_ptr());
+    }
+    if (a[10] != Py_None) {
+      const Tensor& w = tensor(a[10], "allowed");
+      on_device(w, "allowed", dev);
+      of_type(w, at::kInt, "allowed");
+      if (w.dim() != 2 || w.size(0) != N || w.size(1) < (V + 31) / 32 ||
+          (w.size(1) > 1 && w.stride(1) != 1)) {
+        std::ostringstream o;
+        o << "allowed must have shape (" << N << ", >= " << (V + 31) / 32
+          << ") and contiguous rows, got " << shape_text(w.sizes());
+        refuse(o.str());
+      }
+      s.allowed = i32(w);
+      s.allowed_stride = N > 1 ? w.stride(0) : w.size(1);
+    }
+    Tensor out;
+    if (a[11] == Py_None) {
+      out = at_.make({N, V}, x.scalar_type());
+    } else {
+      out = tensor(a[11], "out");
+      on_device(out, "out", dev);
+      logits_of(out, "out");
+      if (out.scalar_type() != x.scalar_type() || out.sizes() != x.sizes())
+        refuse("out must have logits' type and shape");
+    }
+    check(moe_adjust_logits(&s, x.data_ptr(),
+                            x.scalar_type() == at::kFloat ? MOE_LOGITS_F32 : MOE_LOGITS_BF16,
+                            static_cast<int>(N), static_cast<int>(V), N > 1 ? x.stride(0) : V,
+                            out.data_ptr(), N > 1 ? out.stride(0) : V, error_word(a[12], dev),
+                            at_.stream),
+          "moe_adjust_logits");
+    if (a[11] == Py_None) return THPVariable_Wrap(out);
+    written(out);
+    Py_INCREF(a[11]);
+    return a[11];
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyCFunction fast() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F));
@@ -475,6 +863,14 @@ PyMethodDef kMethods[] = {
     {"kv_append", fast<kv_append>(), METH_FASTCALL, nullptr},
     {"attn_decode", fast<attn_decode>(), METH_FASTCALL, nullptr},
     {"sample_tokens", fast<sample_tokens>(), METH_FASTCALL, nullptr},
+    {"tree_masks", fast<tree_masks>(), METH_FASTCALL, nullptr},
+    {"tree_accept", fast<tree_accept>(), METH_FASTCALL, nullptr},
+    {"attn_tree", fast<attn_tree>(), METH_FASTCALL, nullptr},
+    {"kv_compact", fast<kv_compact>(), METH_FASTCALL, nullptr},
+    {"kv_copy_pages", fast<kv_copy_pages>(), METH_FASTCALL, nullptr},
+    {"kv_fork", fast<kv_fork>(), METH_FASTCALL, nullptr},
+    {"kv_trim", fast<kv_trim>(), METH_FASTCALL, nullptr},
+    {"adjust_logits", fast<adjust_logits>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "moe_decode_ext", nullptr, -1, kMethods,

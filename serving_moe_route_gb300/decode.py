@@ -19,6 +19,29 @@ One step of a server with its state on the GPU::
     ids, probs = sample_tokens(logits, u, temperature=t, top_p=p)
     kv_release(done, block_table, free_pages, n_free, num_pages=P, err=err)
 
+A step may check several drafted tokens per request (speculation): a tree whose
+node 0 follows the context, packed by request like any new tokens::
+
+    step = kv_step(ctx_lens, nodes, block_table, free_pages, n_free, page_size=16,
+                   num_pages=P, max_tokens=N, n_free_out=n_free, err=err)
+    tree = tree_masks(parents, step.starts, step.seq_lens, max_new=M, err=err)
+    for each layer:                                  # rotary embeddings: tree.positions
+        kv_append(k, v, step.slots, k_cache, v_cache, err=err)
+        out = attn_tree(q, k_cache, v_cache, block_table, step.starts, step.seq_lens,
+                        tree.masks, max_new=M, err=err)
+        ...
+    logits = adjust_logits(logits, rows=request_of_row, history=..., allowed=..., err=err)
+    draws, _ = sample_tokens(logits, u, temperature=t)
+    walk = tree_accept(tokens, draws, parents, step.starts, ctx_lens, max_path=M, err=err)
+    for each layer:
+        kv_compact(walk.path, walk.accepted, ctx_lens, block_table, k_cache, v_cache, err=err)
+    kv_trim(walk.seq_lens, step.seq_lens, block_table, free_pages, n_free, page_size=16,
+            num_pages=P, err=err)
+
+Requests may share pages: ``kv_fork`` lets rows go on from another one's pages,
+``kv_copy_pages`` copies the partial ones, and ``kv_trim`` with the same
+``page_refs`` gives a page back when its last holder does.
+
 ``err`` is an int32 tensor of one zero that collects error bits
 (``MOE_DEVERR_*``) on the device; ``check_word`` reads and clears it.  Every
 function enqueues on ``stream`` (the current one by default) and returns at
@@ -53,6 +76,27 @@ class KVStep(NamedTuple):
     starts: torch.Tensor     # [B + 1] request r's tokens are starts[r] .. starts[r + 1] - 1
     seq_lens: torch.Tensor   # [B] tokens of each request, the new ones included
     n_free: torch.Tensor     # [1] free pages left
+
+
+class TreeMasks(NamedTuple):
+    """What ``tree_masks`` returns."""
+    masks: torch.Tensor      # int64 [N, ceil(max_new / 64)] nodes that each row attends
+    positions: torch.Tensor  # int32 [N] context tokens + depth
+
+
+class TreeAccept(NamedTuple):
+    """What ``tree_accept`` returns (int32 tensors)."""
+    path: torch.Tensor      # [B, max_path] accepted nodes, -1 behind them
+    accepted: torch.Tensor  # [B] how many
+    next_ids: torch.Tensor  # [B] the token drawn at the last one
+    seq_lens: torch.Tensor  # [B] context tokens, the accepted ones included
+
+
+class KVFork(NamedTuple):
+    """What ``kv_fork`` returns (int32 [F]): the partial pages to copy."""
+    src_pages: torch.Tensor
+    dst_pages: torch.Tensor
+    tokens: torch.Tensor
 
 
 _ext_module = None
@@ -137,6 +181,102 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     greedy.  Returns (ids int32 [B], probs float32 [B]): the drawn tokens and
     their shares of what was kept; -1 and 0 for a row without a token."""
     return _ext().sample_tokens(logits, u, temperature, top_k, top_p, min_p, _handle(stream))
+
+
+def tree_masks(parents, starts, seq_lens, *, max_new, err=None, stream=None) -> TreeMasks:
+    """Masks and positions of trees of drafted tokens.  ``parents`` (int32 [N],
+    packed by request) holds each node's parent by its number in the request,
+    lower than its own, -1 for the root; ``starts`` and ``seq_lens`` are those of
+    ``kv_step``; ``max_new`` (up to 256) bounds a request's nodes.  A node attends
+    itself and its ancestors.  Rows of no request get zeros."""
+    return TreeMasks(*_ext().tree_masks(parents, starts, seq_lens, max_new, err, _handle(stream)))
+
+
+def attn_tree(q, k_cache, v_cache, block_table, starts, seq_lens, masks=None, *, max_new,
+              scale=None, window=0, k_scale=None, v_scale=None, out=None, return_lse=False,
+              workspace=None, err=None, stream=None):
+    """Attention of several new tokens per request: q ``[N, Hq, head_dim]`` packed
+    by request.  A row attends its request's context and the new tokens whose bits
+    are set in its mask (``tree_masks``), by default those up to itself.  With a
+    ``window``, a row that attends c new tokens attends the last ``window - c`` of
+    the context.  Otherwise as ``attn_decode``: returns out, or (out, lse) with lse
+    ``[N, Hq]``; a row that attends nothing gets zeros and -inf, rows of no request
+    are left as they are.  ``workspace`` is a uint8 tensor of
+    ``attn_tree_workspace(...)`` bytes (by default one is allocated)."""
+    return _ext().attn_tree(q, k_cache, v_cache, block_table, starts, seq_lens, masks, max_new,
+                            scale, window, k_scale, v_scale, out, return_lse, workspace, err,
+                            _handle(stream))
+
+
+def attn_tree_workspace(kv_dtype: torch.dtype, head_dim: int) -> int:
+    """Bytes of workspace that ``attn_tree`` needs on the current device."""
+    if kv_dtype not in _KV_DTYPE:
+        raise ValueError(f"no cache of {kv_dtype}")
+    return B.moe_attn_tree_workspace(_KV_DTYPE[kv_dtype], head_dim)
+
+
+def tree_accept(tokens, draws, parents, starts, ctx_lens, *, max_path, err=None,
+                stream=None) -> TreeAccept:
+    """Walk each tree from node 0 along the tokens drawn: the next node is the
+    lowest child of the current one whose drafted token (``tokens``, int32 [N]) is
+    the one drawn there (``draws``, int32 [N]); at most ``max_path`` nodes."""
+    return TreeAccept(*_ext().tree_accept(tokens, draws, parents, starts, ctx_lens, max_path, err,
+                                          _handle(stream)))
+
+
+def kv_compact(path, accepted, ctx_lens, block_table, k_cache, v_cache, *, err=None, stream=None):
+    """Move the keys and values of the accepted nodes (``path`` int32 [B, P],
+    rising, ``accepted`` int32 [B]) together: token ``ctx + path[j]`` of a request
+    goes to ``ctx + j``, in place."""
+    _ext().kv_compact(path, accepted, ctx_lens, block_table, k_cache, v_cache, err,
+                      _handle(stream))
+
+
+def kv_fork(src_rows, dst_rows, ctx_lens, block_table, page_refs, free_pages, n_free, *, page_size,
+            num_pages, err=None, stream=None) -> KVFork:
+    """Let rows ``dst_rows`` of the block table (int32 [F], without pages) go on
+    from rows ``src_rows``: full pages are shared (``page_refs``, int32
+    [num_pages], counts a page's holders beyond the first), a partial last page is
+    replaced by one from the end of ``free_pages[:n_free]``.  ``ctx_lens``,
+    ``block_table``, ``page_refs`` and ``n_free`` are updated in place.  Returns
+    the partial pages, for ``kv_copy_pages`` on each layer's cache."""
+    return KVFork(*_ext().kv_fork(src_rows, dst_rows, ctx_lens, block_table, page_refs, free_pages,
+                                  n_free, page_size, num_pages, err, _handle(stream)))
+
+
+def kv_copy_pages(src_pages, dst_pages, k_cache, v_cache, *, tokens=None, err=None, stream=None):
+    """Copy the first ``tokens[i]`` tokens (all by default) of page
+    ``src_pages[i]`` to page ``dst_pages[i]`` (int32 [n]; -1 skips a pair).  A page
+    that is written must stand in the call once."""
+    _ext().kv_copy_pages(src_pages, dst_pages, k_cache, v_cache, tokens, err, _handle(stream))
+
+
+def kv_trim(keep_lens, seq_lens, block_table, free_pages, n_free, *, page_size, num_pages,
+            page_refs=None, err=None, stream=None):
+    """Give back the pages of each request past its first ``keep_lens[r]`` of
+    ``seq_lens[r]`` tokens: their entries of ``block_table`` become -1 and they go
+    to the end of ``free_pages[:n_free]``, ``n_free`` grows (all in place).  With
+    ``page_refs`` a shared page loses a holder, and is freed with its last one."""
+    _ext().kv_trim(keep_lens, seq_lens, block_table, free_pages, n_free, page_size, num_pages,
+                   page_refs, err, _handle(stream))
+
+
+def adjust_logits(logits, *, rows=None, history=None, history_lens=None, prompt_lens=None,
+                  repetition=None, presence=None, frequency=None, bias_ids=None, bias=None,
+                  allowed=None, out=None, err=None, stream=None):
+    """Logits [N, V] (float32 or bfloat16) with penalties, biases and a grammar's
+    mask applied, before ``sample_tokens``.  Row i belongs to request ``rows[i]``
+    (int32 [N]; by default i).  In this order: the logits of tokens in
+    ``history[r, :history_lens[r]]`` (int32) are divided by ``repetition[r]`` if
+    positive, multiplied otherwise; ``frequency[r]`` times a token's count in the
+    history from ``prompt_lens[r]`` on, and ``presence[r]`` if there is any, are
+    subtracted; ``bias[r, j]`` is added to token ``bias_ids[r, j]`` (-1 pads; of
+    several for one token the last counts); tokens whose bit in ``allowed`` (int32
+    [N, ceil(V / 32)], one row per row of logits) is not set become -inf.
+    ``out`` may be ``logits`` itself; by default the result is a new tensor."""
+    return _ext().adjust_logits(logits, rows, history, history_lens, prompt_lens, repetition,
+                                presence, frequency, bias_ids, bias, allowed, out, err,
+                                _handle(stream))
 
 
 def check_word(err, stream=None):
