@@ -93,7 +93,8 @@ def strip_c_comments(text):
 
 # Sources that the layer's kernels are not built from: the decode step's
 DECODE_SOURCES = ("adjust.cu", "attn_decode.cu", "attn_tree.cu", "attn_tree.cuh",
-                  "decode_internal.cuh", "kv_cache.cu", "kv_pages.cu", "sample.cu", "tree.cu")
+                  "attn_tree_tc.cu", "attn_tree_tc.cuh", "decode_internal.cuh", "kv_cache.cu",
+                  "kv_pages.cu", "sample.cu", "tree.cu")
 
 
 def kernel_source_fingerprint():

@@ -1,9 +1,8 @@
 // attn_tree.cu -- attention of several drafted tokens per request over the paged
-// cache (moe_attn_tree, include/moe_route.h): the host's side, and the kernel in
-// fp32 arithmetic.
-#include <cuda_fp8.h>
-
+// cache (moe_attn_tree, include/moe_route.h): the host's side, and the kernel for
+// f32 caches; bf16 and e4m3 caches go to attn_tree_tc.cu.
 #include "attn_tree.cuh"
+#include "attn_tree_tc.cuh"
 
 namespace moe {
 
@@ -24,38 +23,15 @@ __device__ __forceinline__ void tree_cp16(uint32_t dst, const void* src, bool re
                : "memory");
 }
 
-// 16 bytes of a cached vector as f32
-template <int KV>
-__device__ __forceinline__ void widen(uint4 raw, float* out) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  if constexpr (KV == MOE_KV_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      out[2 * i] = __uint_as_float(w[i] << 16);
-      out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        __nv_fp8_e4m3 e;
-        e.__x = static_cast<__nv_fp8_storage_t>(w[i] >> (8 * j));
-        out[4 * i + j] = static_cast<float>(e);
-      }
-  }
-}
-
 // S = Q K^T, the running softmax and O += P V on tiles in shared memory, 2 rows
 // by TILE / 16 tokens and by DP / 16 columns a thread, all in fp32: nothing is
 // split or rounded.  A value that a row does not attend is skipped, not
 // multiplied by 0.
-template <int KV, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
     tree_simt_kernel(const TreeArgs A) {
   using C = SimtCfg<DP>;
   constexpr int TILE = C::TILE, KP = C::KP, PP = C::PP, NK = TILE / 16, NC = DP / 64;
-  constexpr int ES = kv_esize(KV), VE = 16 / ES;
   extern __shared__ __align__(16) float simt_smem[];
   float* const qs = simt_smem;
   float* const ks = qs + kSimtRows * KP;
@@ -77,11 +53,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
     const int blocks = at.units / A.heads;
     const int kvh = at.x / blocks, r0 = at.x % blocks * kSimtRows;
     const int rows = min(kSimtRows, s.use * A.group - r0);
-    float f = A.scale_log2, v_mul = 1.0f;
-    if constexpr (KV == MOE_KV_E4M3) {
-      f *= A.k_scale[kvh];
-      v_mul = A.v_scale[kvh];
-    }
+    const float f = A.scale_log2;
     auto offsets = [&](int t, int buf) {
       if (tid >= TILE) return;
       const int pos = s.first + t * TILE + tid;
@@ -97,19 +69,12 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
       s_off[buf][tid] = off;
     };
     auto load = [&](const char* base, float* to, int pitch, int buf) {
-      constexpr int CPR = DP / VE;
+      constexpr int CPR = DP / 4;
       for (int i = tid; i < TILE * CPR; i += kSimtThreads) {
         const int r = i / CPR, c = i % CPR;
         const long long off = s_off[buf][r];
-        const bool real = off >= 0 && c * VE < A.dim;
-        float* const d = to + r * pitch + c * VE;
-        if constexpr (KV == MOE_KV_F32) {
-          tree_cp16(smem_u32(d), real ? base + off + c * 16 : base, real);
-        } else {
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          if (real) raw = *reinterpret_cast<const uint4*>(base + off + c * 16);
-          widen<KV>(raw, d);
-        }
+        const bool real = off >= 0 && c * 4 < A.dim;
+        tree_cp16(smem_u32(to + r * pitch + c * 4), real ? base + off + c * 16 : base, real);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -119,15 +84,8 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows && d < A.dim) {
         const int R = r0 + r, node = R / A.group, h = kvh * A.group + R - node * A.group;
-        const long long from = (s.row0 + node) * A.q_n + h * A.q_h + d;
-        if constexpr (KV == MOE_KV_F32) {
-          v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + from);
-        } else {
-          const uint2 raw =
-              *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(A.q) + from);
-          v = make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u));
-        }
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) +
+                                             (s.row0 + node) * A.q_n + h * A.q_h + d);
       }
       *reinterpret_cast<float4*>(qs + r * KP + d) = v;
     }
@@ -229,16 +187,16 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
       const int r = 2 * ty + e;
       if (r >= rows) continue;
       if (whole) {
-        const float inv = m[e] == -INFINITY ? 0.0f : v_mul / l[e];
+        const float inv = m[e] == -INFINITY ? 0.0f : 1.0f / l[e];
         const int R = r0 + r, h = kvh * A.group + R - node[e] * A.group;
         const long long row = s.row0 + node[e];
 #pragma unroll
         for (int j = 0; j < NC; ++j)
           if (4 * tx + 64 * j < A.dim)
-            tree_store4<KV>(A.out, row * A.o_n + h * A.o_h + 4 * tx + 64 * j, acc[e][4 * j] * inv,
+            tree_store4<MOE_KV_F32>(A.out, row * A.o_n + h * A.o_h + 4 * tx + 64 * j, acc[e][4 * j] * inv,
                             acc[e][4 * j + 1] * inv, acc[e][4 * j + 2] * inv,
                             acc[e][4 * j + 3] * inv);
-        if (A.lse && tx == 0) A.lse[row * A.Hq + h] = tree_lse(m[e], l[e]);
+        if (A.lse && tx == 0) A.lse[row * A.Hq + h] = tree_lse<MOE_KV_F32>(m[e], l[e]);
       } else {
 #pragma unroll
         for (int j = 0; j < NC; ++j)
@@ -258,27 +216,26 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
 struct TreeShape {
   int rows, tile, ctas_per_sm;
 };
-static TreeShape tree_shape(int, int dp) {
-  return {kSimtRows, dp == 256 ? SimtCfg<256>::TILE : SimtCfg<64>::TILE, SimtCfg<64>::CTAS};
+template <int DP>
+static TreeShape shape_of(int kv) {
+  if (kv == MOE_KV_F32) return {kSimtRows, SimtCfg<DP>::TILE, SimtCfg<DP>::CTAS};
+  return {TcCfg<DP>::ROWS, TcCfg<DP>::TILE, 1};
+}
+static TreeShape tree_shape(int kv, int dp) {
+  return dp == 64 ? shape_of<64>(kv) : dp == 128 ? shape_of<128>(kv) : shape_of<256>(kv);
 }
 static int tree_dp(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-template <int KV, int DP>
+template <int DP>
 static cudaError_t launch_simt(const TreeArgs& a, int ctas, cudaStream_t st) {
-  auto* kern = tree_simt_kernel<KV, DP>;
+  auto* kern = tree_simt_kernel<DP>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), SimtCfg<DP>::SMEM, done);
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(ctas), dim3(kSimtThreads), SimtCfg<DP>::SMEM, st, a);
   if (e != cudaSuccess) return e;
-  return launch_chained(tree_join_kernel<KV, DP, kSimtRows>, dim3(ctas), dim3(32 * kTreeJoinWarps),
-                        0, st, a);
-}
-template <int KV>
-static cudaError_t launch_kv(int dp, const TreeArgs& a, int ctas, cudaStream_t st) {
-  return dp == 64    ? launch_simt<KV, 64>(a, ctas, st)
-         : dp == 128 ? launch_simt<KV, 128>(a, ctas, st)
-                     : launch_simt<KV, 256>(a, ctas, st);
+  return launch_chained(tree_join_kernel<MOE_KV_F32, DP, kSimtRows>, dim3(ctas),
+                        dim3(32 * kTreeJoinWarps), 0, st, a);
 }
 
 static size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -383,9 +340,10 @@ int moe_attn_tree(const moe_kv_cache_t* cache, const void* q, long long q_stride
                        ? full
                        : static_cast<int>(units * tiles);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->kv_dtype == MOE_KV_F32    ? launch_kv<MOE_KV_F32>(dp, a, ctas, st)
-                        : cache->kv_dtype == MOE_KV_BF16 ? launch_kv<MOE_KV_BF16>(dp, a, ctas, st)
-                                                         : launch_kv<MOE_KV_E4M3>(dp, a, ctas, st);
+  const cudaError_t e = cache->kv_dtype != MOE_KV_F32 ? launch_tree_tc(cache->kv_dtype, dp, a, ctas, st)
+                        : dp == 64                    ? launch_simt<64>(a, ctas, st)
+                        : dp == 128                   ? launch_simt<128>(a, ctas, st)
+                                                      : launch_simt<256>(a, ctas, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -259,8 +259,15 @@ __device__ __forceinline__ float tree_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// weights of e4m3 caches, which are f16, are lifted by 2^kTreeLift
+constexpr float kTreeLift = 13.0f;
+// ln(sum 2^top): top without the lift and sum without it are both near what their
+// rounding should be relative to
+template <int KV>
 __device__ __forceinline__ float tree_lse(float top, float sum) {
-  return top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  constexpr float lift = KV == MOE_KV_E4M3 ? kTreeLift : 0.0f;
+  if (top == -INFINITY) return -INFINITY;
+  return ((top + lift) + log2f(sum * exp2f(-lift))) * 0.6931471805599453f;
 }
 __device__ __forceinline__ uint32_t tree_bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const Tr
       if (lane % 2 == 0 && lane * VL < A.dim)
         tree_store4<KV>(A.out, to + lane * VL, o[0], o[1], a, b);
     }
-    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse(top, sum);
+    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse<KV>(top, sum);
   }
 }
 
