@@ -234,7 +234,7 @@ static cudaError_t launch_simt(const TreeArgs& a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(ctas), dim3(kSimtThreads), SimtCfg<DP>::SMEM, st, a);
   if (e != cudaSuccess) return e;
-  return launch_chained(tree_join_kernel<MOE_KV_F32, DP, kSimtRows>, dim3(ctas),
+  return launch_chained(tree_join_kernel<MOE_KV_F32, DP, kSimtRows>, dim3(ctas, kTreeJoinBlocks),
                         dim3(32 * kTreeJoinWarps), 0, st, a);
 }
 

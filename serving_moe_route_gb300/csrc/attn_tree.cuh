@@ -43,12 +43,13 @@ struct TreeArgs {
   float scale_log2;
   int N, B, Hq, heads, group, words, max_new;
   int dim, page, page_shift, num_pages, max_pages, window;
+  int box;  // tokens that TMA brings at a time; 0: it cannot
 };
 
 // A request's rows and tokens
 struct TreeSpan {
   int row0, n, use;  // first row, rows, rows that are worked on
-  int ctx, first, len;  // context tokens, first token that any row attends, end
+  int ctx, first, len;  // context tokens, where tiles begin, end
 };
 
 __device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int r, bool& cut) {
@@ -60,7 +61,8 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int r, bool& cu
   const long long room = static_cast<long long>(A.max_pages) * A.page;
   s.len = static_cast<int>(min(static_cast<long long>(all), room));
   s.ctx = max(0, all - s.n);
-  s.first = A.window > 0 ? min(max(0, s.ctx - A.window), s.len) : 0;
+  // (tiles begin at multiples of their size, as TMA's boxes must)
+  s.first = A.window > 0 ? min(max(0, s.ctx - A.window), s.len) & ~127 : 0;
   if (s.n > 0 && (s.use < s.n || s.len < all)) cut = true;
   return s;
 }
@@ -283,13 +285,99 @@ __device__ __forceinline__ void tree_store4(void* out, long long at, float a, fl
         make_uint2(tree_bf16x2(a, b), tree_bf16x2(c, d));
 }
 
+// R rows of a unit, joined by a warp from its parts in CTAs cta, cta + 1, ...: the
+// loads of all of them, and of some parts at a time, are under way together.
+template <int KV, int DP, int ROWS, int R>
+__device__ __forceinline__ void tree_join_rows(const TreeArgs& A, const TreeSpan& s, int cta,
+                                               int parts, int kvh, int r0, int r, int rows,
+                                               int lane) {
+  constexpr int VL = DP / 32;  // columns per lane
+  constexpr int AHEAD = R == 1 ? 8 : 2;
+  auto at = [&](int p, int u) {
+    return (2ll * (cta + p) + (p == 0 ? 0 : 1)) * ROWS + min(r + u, rows - 1);
+  };
+  float top[R], sum[R], o[R][VL];
+#pragma unroll
+  for (int u = 0; u < R; ++u) {
+    top[u] = -INFINITY;
+    for (int p = lane; p < parts; p += 32) top[u] = fmaxf(top[u], A.part_ml[at(p, u)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], off));
+    sum[u] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VL; ++j) o[u][j] = 0.0f;
+  }
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    float f[R], fl[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      const float2 ml =
+          p0 + lane < parts ? A.part_ml[at(p0 + lane, u)] : make_float2(-INFINITY, 0.0f);
+      f[u] = top[u] == -INFINITY ? 1.0f : tree_ex2(ml.x - top[u]);
+      fl[u] = f[u] * ml.y;
+    }
+    const int n = min(32, parts - p0);
+    for (int p = 0; p < n; p += AHEAD) {
+      float v[AHEAD][R][VL];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          const float* const x = A.part_o + at(p0 + min(p + i, n - 1), u) * DP + lane * VL;
+          if constexpr (VL >= 4) {
+#pragma unroll
+            for (int j = 0; j < VL; j += 4)
+              *reinterpret_cast<float4*>(v[i][u] + j) = *reinterpret_cast<const float4*>(x + j);
+          } else {
+            *reinterpret_cast<float2*>(v[i][u]) = *reinterpret_cast<const float2*>(x);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (p + i >= n) break;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          const float g = __shfl_sync(0xffffffffu, f[u], p + i);
+          sum[u] += __shfl_sync(0xffffffffu, fl[u], p + i);
+#pragma unroll
+          for (int j = 0; j < VL; ++j) o[u][j] += g * v[i][u][j];
+        }
+      }
+    }
+  }
+  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
+#pragma unroll
+  for (int u = 0; u < R; ++u) {
+    if (r + u >= rows) break;
+    const float inv = top[u] == -INFINITY ? 0.0f : mul / sum[u];
+    const int place = r0 + r + u, node = place / A.group, h = kvh * A.group + place - node * A.group;
+    const long long row = s.row0 + node, to = row * A.o_n + h * A.o_h;
+#pragma unroll
+    for (int j = 0; j < VL; ++j) o[u][j] *= inv;
+    if constexpr (VL >= 4) {
+#pragma unroll
+      for (int j = 0; j < VL; j += 4)
+        if (lane * VL + j < A.dim)
+          tree_store4<KV>(A.out, to + lane * VL + j, o[u][j], o[u][j + 1], o[u][j + 2], o[u][j + 3]);
+    } else {  // two lanes' columns together
+      const float a = __shfl_down_sync(0xffffffffu, o[u][0], 1);
+      const float b = __shfl_down_sync(0xffffffffu, o[u][1], 1);
+      if (lane % 2 == 0 && lane * VL < A.dim)
+        tree_store4<KV>(A.out, to + lane * VL, o[u][0], o[u][1], a, b);
+    }
+    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse<KV>(top[u], sum[u]);
+  }
+}
+
 // Joins the parts of the units that range borders cut.  A unit that begins in CTA
 // c and does not end there has c's first slot, then the second slots of the next
-// CTAs; the blocks of all those but the last deal its rows out, a row a warp.
-constexpr int kTreeJoinWarps = 16;
+// CTAs.  The kTreeJoinBlocks blocks of each CTA that it does not end in deal its
+// rows out: four a warp where there are few parts, else one.  (One block for each
+// of those CTAs, a row a warp: 40 us more for 64 requests of 16 nodes.)
+constexpr int kTreeJoinWarps = 8, kTreeJoinBlocks = 8, kTreeFewParts = 8;
 template <int KV, int DP, int ROWS>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const TreeArgs A) {
-  constexpr int VL = DP / 32;  // columns per lane
   pdl_wait();
   const int4 unit = A.info[blockIdx.x];
   const int parts = unit.z, cta = blockIdx.x - unit.w;
@@ -300,52 +388,15 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const Tr
   const int blocks = (s.use * A.group + ROWS - 1) / ROWS;
   const int kvh = unit.y / blocks, r0 = unit.y % blocks * ROWS;
   const int rows = min(ROWS, s.use * A.group - r0);
-  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
-  for (int r = unit.w * kTreeJoinWarps + warp; r < rows; r += (parts - 1) * kTreeJoinWarps) {
-    auto at = [&](int p) { return (2ll * (cta + p) + (p == 0 ? 0 : 1)) * ROWS + r; };
-    float top = -INFINITY;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, A.part_ml[at(p)].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float sum = 0.0f, o[VL] = {};
-    for (int p0 = 0; p0 < parts; p0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (p0 + lane < parts) ml = A.part_ml[at(p0 + lane)];
-      const float f = top == -INFINITY ? 1.0f : tree_ex2(ml.x - top);
-      const float fl = f * ml.y;
-      const int n = min(32, parts - p0);
-#pragma unroll 4
-      for (int p = 0; p < n; ++p) {
-        const float g = __shfl_sync(0xffffffffu, f, p);
-        sum += __shfl_sync(0xffffffffu, fl, p);
-        const float* x = A.part_o + at(p0 + p) * DP + lane * VL;
-        float v[VL];
-#pragma unroll
-        for (int j = 0; j < VL; j += 2)
-          *reinterpret_cast<float2*>(v + j) = *reinterpret_cast<const float2*>(x + j);
-#pragma unroll
-        for (int j = 0; j < VL; ++j) o[j] += g * v[j];
-      }
-    }
-    const float inv = top == -INFINITY ? 0.0f : mul / sum;
-    const int R = r0 + r, node = R / A.group, h = kvh * A.group + R - node * A.group;
-    const long long row = s.row0 + node;
-#pragma unroll
-    for (int j = 0; j < VL; ++j) o[j] *= inv;
-    const long long to = row * A.o_n + h * A.o_h;
-    if constexpr (VL >= 4) {
-#pragma unroll
-      for (int j = 0; j < VL; j += 4)
-        if (lane * VL + j < A.dim)
-          tree_store4<KV>(A.out, to + lane * VL + j, o[j], o[j + 1], o[j + 2], o[j + 3]);
-    } else {  // two lanes' columns together
-      const float a = __shfl_down_sync(0xffffffffu, o[0], 1);
-      const float b = __shfl_down_sync(0xffffffffu, o[1], 1);
-      if (lane % 2 == 0 && lane * VL < A.dim)
-        tree_store4<KV>(A.out, to + lane * VL, o[0], o[1], a, b);
-    }
-    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse<KV>(top, sum);
+  const int first = (unit.w * kTreeJoinBlocks + blockIdx.y) * kTreeJoinWarps + warp;
+  const int warps = (parts - 1) * kTreeJoinBlocks * kTreeJoinWarps;
+  if (parts <= kTreeFewParts) {
+    constexpr int R = DP == 256 ? 2 : 4;
+    for (int r = R * first; r < rows; r += R * warps)
+      tree_join_rows<KV, DP, ROWS, R>(A, s, cta, parts, kvh, r0, r, rows, lane);
+  } else {
+    for (int r = first; r < rows; r += warps)
+      tree_join_rows<KV, DP, ROWS, 1>(A, s, cta, parts, kvh, r0, r, rows, lane);
   }
 }
 

@@ -13,11 +13,11 @@
 // head_dim above 128 leaves tensor memory for one O: one lane, two S tiles of
 // half the size.
 //
-//   loads    four warps fill a ring of key and value tiles with 16-byte
-//            cp.async, LOOK tiles ahead, across unit borders; any page size and
-//            strides.  e4m3 codes land in the half of their tile that the same
-//            warp will write, and are widened to f16, which holds them exactly,
-//            on the way to the full barrier.
+//   loads    one warp fills a ring of key and value tiles by TMA, as far ahead as
+//            it reaches, across unit borders (pages that 8 does not divide: two
+//            warps, by cp.async).  Four others make ready what has landed: e4m3
+//            codes lie in the half of their tile that the same warp will write,
+//            and are widened to f16, which holds them exactly.
 //   softmax  one pass with a reference m and the sum l of a row in fp32 (base 2);
 //            O is rescaled only when a logit lies LAG above the one that m was
 //            taken from.  P is rounded to bf16 (f16 for e4m3 caches) into the
@@ -39,24 +39,27 @@
 namespace moe {
 
 constexpr uint64_t kTreeWaitNs = 2000000000ull;
-constexpr int kLoadWarps = 4, kMmaWarp = 8 + kLoadWarps;
+constexpr int kLoadWarps = 2, kReadyWarps = 4, kMmaWarp = 8 + kLoadWarps + kReadyWarps;
 static_assert(kTcThreads == 32 * (kMmaWarp + 1), "two softmax warpgroups, loads, products");
 
 template <int KV, int DP>
 struct TcShape {
   using C = TcCfg<DP>;
   static constexpr int RING = 163840 / (C::TILE * DP * 2);
-  static constexpr int LOOK = RING - 2;            // tiles on their way
   static constexpr int BUF = C::TILE * DP * 2;     // bytes of a tile
   static constexpr int PANEL = C::TILE * 128;      // of 64 columns of it
   static constexpr int QBLOCK = 128 * DP * 2;
   static constexpr int NB = C::LANES == 1 ? 2 : 1; // S tiles of a lane
   static constexpr int ES = kv_esize(KV);
   static constexpr int CPR = DP * ES / 16;         // 16-byte chunks of a cached row
-  static constexpr int TPW = C::TILE / kLoadWarps; // tokens of a tile that a warp loads
-  static constexpr int RPI = 32 / CPR;             // of them at a time
   static constexpr float LIFT = KV == MOE_KV_E4M3 ? kTreeLift : 0.0f;
   static constexpr float LAG = KV == MOE_KV_E4M3 ? 2.0f : 8.0f;
+  // where e4m3 codes land: the last panels, or with one panel the second half of
+  // each 32 rows' part of it
+  static constexpr int PANELS = DP / 64;
+  static constexpr int RAW = KV == MOE_KV_E4M3 ? (DP == 64 ? 0 : PANELS / 2) : 0;  // first panel
+  static constexpr int LAND = KV == MOE_KV_E4M3 ? (DP == 64 ? 1 : PANELS / 2) : PANELS;
+  static constexpr int LAND_ROW = KV == MOE_KV_E4M3 && DP == 64 ? 64 : 128;  // bytes of a row
   static constexpr uint32_t FMT = KV == MOE_KV_E4M3 ? 0 : 1;  // f16, bf16
 };
 constexpr int kSlots = 8;  // tiles whose live and non-finite tokens are kept
@@ -68,7 +71,7 @@ struct TcTurns {
 };
 // What lies behind the tiles in shared memory
 struct TcShared {
-  uint64_t full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2], join[2], drain;
+  uint64_t landed[10], full[10], empty[10], s_full[2], p_full[2], o_full[2], q_full[2], join[2], drain;
   TreeStart start;
   long long sums[kTcThreads / 32];
   uint8_t live[kSlots][16], wild[kSlots][16];  // bits by token
@@ -160,6 +163,22 @@ __device__ __forceinline__ uint32_t tc_chunk(int r, int c, int panel) {
   return (c >> 3) * panel + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// byte where chunk c of cached row r lands
+template <int KV, int DP>
+__device__ __forceinline__ uint32_t tc_land(int r, int c) {
+  using S = TcShape<KV, DP>;
+  if constexpr (S::LAND_ROW == 64) return (r >> 5) * 4096 + 2048 + (r & 31) * 64 + c * 16;
+  return tc_chunk(r, c + 8 * S::RAW, S::PANEL);
+}
+__device__ __forceinline__ void tc_tma4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
 template <int DP>
 using TcWalk = TreeWalk<TcCfg<DP>::ROWS, TcCfg<DP>::TILE, TcCfg<DP>::END>;
 
@@ -171,30 +190,260 @@ __device__ __forceinline__ bool tc_masked(const TreeArgs& A, const TreeSpan& s, 
   return pos < low || pos + TILE > min(s.ctx, s.len);
 }
 
+// Tiles lie in the ring in the order in which they are first used.  Where one lane
+// has all of a unit's rows, the next tile's keys come before a tile's values:
+// K0 K1 V0 K2 V1 ...  Else both lanes use each tile: K0 V0 K1 V1 ...
+template <int DP>
+__device__ __forceinline__ bool tc_pair(const TreeArgs& A, const TcWalk<DP>& at) {
+  const int blocks = at.units / A.heads;
+  return TcCfg<DP>::LANES == 2 && at.s.use * A.group - at.x % blocks * TcCfg<DP>::ROWS > 128;
+}
 // ------------------------------------------------------------ loads
+// By TMA, one warp: a box is A.box tokens of a page and 64 columns, a lane has a
+// box (or two panels of it) of each tile.  The page ids of a tile are asked for a
+// tile ahead.
+template <int KV, int DP>
+__device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap* k_map,
+                                            const CUtensorMap* v_map, TcShared& sh, uint32_t ring,
+                                            int lane) {
+  using S = TcShape<KV, DP>;
+  constexpr int TILE = S::C::TILE, CH = TILE / 32;
+  auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
+  auto at = walk;
+  bool bad_page = false, ok = true, more = walk.next(A, at);
+  uint32_t n = 0;  // tiles asked for
+  int slot = 0;
+  const int boxes = TILE / A.box;
+  const int bytes = A.box * S::LAND * S::LAND_ROW;
+  struct Place {
+    int page, row;  // of this lane's box
+    bool live;
+  };
+  auto want = [&](const TcWalk<DP>& p, int t) {
+    Place w = {0, 0, false};
+    const int pos = p.s.first + t * TILE + lane * A.box;
+    if (lane < boxes && pos < p.s.len) {
+      const int col = A.page_shift >= 0 ? pos >> A.page_shift : pos / A.page;
+      w.row = pos - col * A.page;
+      w.page = __ldg(A.table + p.b * A.table_stride + col);
+      w.live = true;
+    }
+    return w;
+  };
+  auto ask = [&](bool kv, const Place& p, int kvh) {
+    const int buf = static_cast<int>(n % S::RING);
+    if (n >= S::RING && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.empty[buf]),
+                                                           (n / S::RING - 1) & 1, kTreeWaitNs,
+                                                           &sh.abort))) {
+      atomicExch(&sh.abort, 1);
+      return false;
+    }
+    const uint32_t base = ring + buf * S::BUF, bar = smem_u32(&sh.landed[buf]);
+    const int count = __popc(__ballot_sync(0xffffffffu, p.live));
+    if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
+    __syncwarp();
+    if (p.live) {
+      const int r = lane * A.box;
+#pragma unroll
+      for (int j = 0; j < S::LAND; ++j)
+        tc_tma4(base + (S::LAND_ROW == 64 ? tc_land<KV, DP>(r, 0)
+                                          : (j + S::RAW) * S::PANEL + r * 128),
+                kv ? v_map : k_map, bar, j * (S::LAND_ROW / S::ES), p.row, kvh, p.page);
+    }
+    ++n;
+    return true;
+  };
+  Place next = {0, 0, false};
+  if (more) next = want(at, at.t0);
+  while (more && ok) {
+    const int kvh = at.x / (at.units / A.heads);
+    const bool late = !tc_pair<DP>(A, at);
+    auto after = at;
+    bool goes_on = true;
+    Place now = {0, 0, false}, before = now;
+    for (int t = at.t0; ok && t < at.t1 + late; ++t) {
+      before = now;
+      if (t < at.t1) {
+        now = next;
+        if (now.live && (now.page < 0 || now.page >= A.num_pages)) {
+          bad_page = true;
+          now.live = false;
+        }
+        // which tokens there are, 32 a word
+        const uint32_t there = __ballot_sync(0xffffffffu, now.live);
+        if (lane < CH) {
+          uint32_t w = 0;
+          const int from = 32 * lane;
+          for (int b = from / A.box; b * A.box < from + 32; ++b)
+            if (there >> b & 1u)
+              w |= A.box >= 32 ? ~0u : ((1u << A.box) - 1) << (b * A.box - from);
+          const int left = at.s.len - (at.s.first + t * TILE + from);
+          if (left < 32) w = left <= 0 ? 0 : w & ((1u << left) - 1);
+          *reinterpret_cast<uint32_t*>(&sh.live[slot][4 * lane]) = w;
+        }
+        slot = (slot + 1) % kSlots;
+        __syncwarp();
+        if (t + 1 < at.t1) {
+          next = want(at, t + 1);
+        } else {
+          goes_on = walk.next(A, after);
+          if (goes_on) next = want(after, after.t0);
+        }
+        ok = ask(false, now, kvh);
+      }
+      if (ok && !(late && t == at.t0)) ok = ask(true, late ? before : now, kvh);
+    }
+    at = after;
+    more = goes_on;
+  }
+  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
+}
+
+// By cp.async, two warps, for pages that no box of eight tokens or more divides.
+// A warp has few copies under way at a time: 1.6 us for a tile of 32 KB.
 template <int KV, int DP>
 __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, uint32_t ring,
                                              int warp, int lane) {
   using S = TcShape<KV, DP>;
-  constexpr int TILE = S::C::TILE, TPW = S::TPW, CPR = S::CPR, RPI = S::RPI;
+  constexpr int TILE = S::C::TILE, TPW = TILE / kLoadWarps, NW = TPW / 32 ? TPW / 32 : 1;
+  constexpr int CPR = S::CPR, RPI = 32 / CPR;  // rows at a time
   auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
   auto at = walk;
-  bool bad_page = false, more = walk.next(A, at);
-  long long n = 0;  // tiles asked for
-  uint32_t masked = 0;  // bit i: tile n - 1 - i is one of values that masks apply to
+  bool bad_page = false, ok = true, more = walk.next(A, at);
+  uint32_t n = 0;  // tiles asked for
+  int slot = 0;
   const int row0 = lane / CPR, chunk = lane % CPR;  // of this lane, of the first rows
   const bool real_chunk = chunk * 16 < A.dim * S::ES;
 
-  // the last step of tile i: what cp.async has brought is made ready and told
-  auto ready = [&](long long i, bool tame) {
-    const int buf = static_cast<int>(i % S::RING);
+  // this lane's tokens (one of every 32 that the warp loads): their pages, asked for a
+  // tile ahead
+  struct Want {
+    int row[NW], page[NW];  // row in the page, -1: none
+  };
+  auto want = [&](const TcWalk<DP>& p, int t) {
+    Want w;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int in = 32 * i + lane, pos = p.s.first + t * TILE + warp * TPW + in;
+      w.row[i] = -1;
+      w.page[i] = 0;
+      if (in < TPW && pos < p.s.len) {
+        const int col = A.page_shift >= 0 ? pos >> A.page_shift : pos / A.page;
+        w.row[i] = pos - col * A.page;
+        w.page[i] = __ldg(A.table + p.b * A.table_stride + col);
+      }
+    }
+    return w;
+  };
+  struct Place {
+    long long off[NW];  // of this lane's tokens in the cache
+    uint32_t mask[NW];  // which of the warp's tokens are there
+  };
+  // ask for a tile of keys or values
+  auto ask = [&](bool kv, const Place& p) {
+    const int buf = static_cast<int>(n % S::RING);
+    if (n >= S::RING && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.empty[buf]),
+                                                           (n / S::RING - 1) & 1, kTreeWaitNs,
+                                                           &sh.abort))) {
+      atomicExch(&sh.abort, 1);
+      return false;
+    }
     const uint32_t base = ring + buf * S::BUF;
+    const char* const from = (kv ? A.v : A.k) + chunk * 16;
+#pragma unroll
+    for (int j = 0; j < TPW / RPI; ++j) {
+      const int r = j * RPI + row0;
+      const long long o = __shfl_sync(0xffffffffu, p.off[j * RPI / 32], r & 31);
+      const bool real = (p.mask[j * RPI / 32] >> (r & 31) & 1u) && real_chunk;
+      tc_cp16(base + tc_land<KV, DP>(warp * TPW + r, chunk), real ? from + o : A.k, real);
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                     smem_u32(&sh.landed[buf]))
+                 : "memory");
+    if (lane == 0) mbar_arrive(smem_u32(&sh.landed[buf]));  // for what was told of the tile
+    ++n;
+    return true;
+  };
+  Want next = {};
+  if (more) next = want(at, at.t0);
+  while (more && ok) {
+    const int kvh = at.x / (at.units / A.heads);
+    const bool late = !tc_pair<DP>(A, at);
+    auto after = at;
+    bool goes_on = true;
+    Place now = {}, before = {};
+    for (int t = at.t0; ok && t < at.t1 + late; ++t) {
+      before = now;
+      if (t < at.t1) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          const bool in = next.page[i] >= 0 && next.page[i] < A.num_pages;
+          const bool live = next.row[i] >= 0 && in;
+          bad_page |= next.row[i] >= 0 && !in;
+          now.off[i] = live ? next.page[i] * A.s_page + next.row[i] * A.s_token + kvh * A.s_head : 0;
+          now.mask[i] = __ballot_sync(0xffffffffu, live);
+          if (lane < (TPW < 32 ? TPW / 8 : 4))
+            sh.live[slot][warp * (TPW / 8) + 4 * i + lane] =
+                static_cast<uint8_t>(now.mask[i] >> (8 * lane));
+        }
+        slot = (slot + 1) % kSlots;
+        __syncwarp();
+        if (t + 1 < at.t1) {
+          next = want(at, t + 1);
+        } else {
+          goes_on = walk.next(A, after);
+          if (goes_on) next = want(after, after.t0);
+        }
+        ok = ask(false, now);
+      }
+      if (ok && !(late && t == at.t0)) ok = ask(true, late ? before : now);
+    }
+    at = after;
+    more = goes_on;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
+}
+
+// What has landed is made ready for the products: e4m3 codes are widened, values
+// that are not finite tamed where masks apply, and the tile passes from the
+// proxy that it was written through to the one that the products read through.
+// (A thread with copies under way would wait for them at that fence: the warps
+// that load do not take it.)
+template <int KV, int DP>
+__device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, uint32_t ring,
+                                              int warp, int lane) {
+  using S = TcShape<KV, DP>;
+  constexpr int TILE = S::C::TILE, TPW = TILE / kReadyWarps;
+  constexpr int CPR = S::CPR, RPI = 32 / CPR;
+  auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
+  auto at = walk;
+  uint32_t n = 0;
+  int slot = 0;
+  const int row0 = lane / CPR, chunk = lane % CPR;
+  auto ready = [&](bool kv, int t) {
+    const int buf = static_cast<int>(n % S::RING);
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.landed[buf]), n / S::RING & 1, kTreeWaitNs,
+                                           &sh.abort))) {
+      atomicExch(&sh.abort, 1);
+      return false;
+    }
+    const uint32_t base = ring + buf * S::BUF;
+    const bool tame = kv && tc_masked<TILE>(A, at.s, at.s.first + t * TILE);
     uint32_t wild_rows = 0;
+    // tokens that are not there: whatever lies in their rows must not count as values
+    uint32_t there = 0;
+    if (kv) {
+      const volatile uint8_t* const live = sh.live[slot] + warp * (TPW / 8);
+#pragma unroll
+      for (int i = 0; i < TPW / 8; ++i) there |= static_cast<uint32_t>(live[i]) << (8 * i);
+    }
+    const bool gaps = kv && there != (TPW == 32 ? ~0u : (1u << TPW % 32) - 1);
     if constexpr (KV == MOE_KV_E4M3) {
       uint4 raw[TPW / RPI];
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j)
-        raw[j] = tc_lds4(base + tc_chunk(warp * TPW + j * RPI + row0, CPR + chunk, S::PANEL));
+        raw[j] = tc_lds4(base + tc_land<KV, DP>(warp * TPW + j * RPI + row0, chunk));
       __syncwarp();  // the codes lie where the warp's rows are written
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j) {
@@ -204,6 +453,7 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
         tc_widen(raw[j].y, lo.z, lo.w);
         tc_widen(raw[j].z, hi.x, hi.y);
         tc_widen(raw[j].w, hi.z, hi.w);
+        if (gaps && !(there >> (j * RPI + row0) & 1u)) lo = hi = make_uint4(0, 0, 0, 0);
         if (tame) {
           bool wild = false;
           uint32_t* const w[2] = {&lo.x, &hi.x};
@@ -216,10 +466,15 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
         tc_sts4(base + tc_chunk(r, 2 * chunk, S::PANEL), lo);
         tc_sts4(base + tc_chunk(r, 2 * chunk + 1, S::PANEL), hi);
       }
-    } else if (tame) {
+    } else if (tame || gaps) {
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j) {
         const uint32_t to = base + tc_chunk(warp * TPW + j * RPI + row0, chunk, S::PANEL);
+        if (!(there >> (j * RPI + row0) & 1u)) {
+          tc_sts4(to, make_uint4(0, 0, 0, 0));
+          continue;
+        }
+        if (!tame) continue;
         uint4 v = tc_lds4(to);
         bool wild = false;
         v.x = tc_tame<0x7f80u>(v.x, wild);
@@ -235,84 +490,22 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
     if (tame) {
       wild_rows = __reduce_or_sync(0xffffffffu, wild_rows);
       if (lane < TPW / 8)
-        sh.wild[(i / 2) % kSlots][warp * (TPW / 8) + lane] =
-            static_cast<uint8_t>(wild_rows >> (8 * lane));
+        sh.wild[slot][warp * (TPW / 8) + lane] = static_cast<uint8_t>(wild_rows >> (8 * lane));
     }
+    if (kv) slot = (slot + 1) % kSlots;
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.full[buf]));
+    ++n;
+    return true;
   };
-
-  // this lane's token (the first TPW lanes have one): its page, asked for a tile ahead
-  struct Want {
-    int row, page;  // row in the page, -1: none
-  };
-  auto want = [&](const TcWalk<DP>& p, int t) {
-    Want w = {-1, 0};
-    const int pos = p.s.first + t * TILE + warp * TPW + lane;
-    if (lane < TPW && pos < p.s.len) {
-      const int col = A.page_shift >= 0 ? pos >> A.page_shift : pos / A.page;
-      w.row = pos - col * A.page;
-      w.page = __ldg(A.table + p.b * A.table_stride + col);
+  while (walk.next(A, at)) {
+    const bool late = !tc_pair<DP>(A, at);
+    for (int t = at.t0; t < at.t1 + late; ++t) {
+      if (t < at.t1 && !ready(false, t)) return;
+      if (!(late && t == at.t0) && !ready(true, late ? t - 1 : t)) return;
     }
-    return w;
-  };
-  Want next = {-1, 0};
-  if (more) next = want(at, at.t0);
-  while (more) {
-    const int kvh = at.x / (at.units / A.heads);
-    auto after = at;
-    bool goes_on = true;
-    for (int t = at.t0; t < at.t1; ++t) {
-      const bool in = next.page >= 0 && next.page < A.num_pages;
-      const bool live = next.row >= 0 && in;
-      bad_page |= next.row >= 0 && !in;
-      const long long off =
-          live ? next.page * A.s_page + next.row * A.s_token + kvh * A.s_head : 0;
-      const uint32_t mask = __ballot_sync(0xffffffffu, live);
-      if (t + 1 < at.t1) {
-        next = want(at, t + 1);
-      } else {
-        goes_on = walk.next(A, after);
-        if (goes_on) next = want(after, after.t0);
-      }
-      if (lane < TPW / 8)
-        sh.live[(n / 2) % kSlots][warp * (TPW / 8) + lane] = static_cast<uint8_t>(mask >> (8 * lane));
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        const int buf = static_cast<int>(n % S::RING);
-        if (n >= S::RING &&
-            !mbar_wait(smem_u32(&sh.empty[buf]), static_cast<uint32_t>(n / S::RING - 1) & 1,
-                       kTreeWaitNs, &sh.abort)) {
-          atomicExch(&sh.abort, 1);
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-          return;
-        }
-        const uint32_t base = ring + buf * S::BUF;
-        const char* const from = (kv ? A.v : A.k) + chunk * 16;
-#pragma unroll
-        for (int j = 0; j < TPW / RPI; ++j) {
-          const int r = j * RPI + row0;
-          const long long o = __shfl_sync(0xffffffffu, off, r);
-          const bool real = (mask >> r & 1u) && real_chunk;
-          tc_cp16(base + tc_chunk(warp * TPW + r, KV == MOE_KV_E4M3 ? CPR + chunk : chunk, S::PANEL),
-                  real ? from + o : A.k, real);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        ++n;
-        masked = masked << 1 | (kv && tc_masked<TILE>(A, at.s, at.s.first + t * TILE));
-        if (n > S::LOOK) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(S::LOOK) : "memory");
-          ready(n - 1 - S::LOOK, masked >> S::LOOK & 1u);
-        }
-      }
-    }
-    at = after;
-    more = goes_on;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  for (long long i = n > S::LOOK ? n - S::LOOK : 0; i < n; ++i) ready(i, masked >> (n - 1 - i) & 1u);
-  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
 }
 
 // ------------------------------------------------------------ products (one thread)
@@ -336,21 +529,21 @@ __device__ __forceinline__ void tc_mma_role(const TreeArgs& A, TcShared& sh, uin
   };
   while (walk.next(A, at)) {
     const int n = at.t1 - at.t0;
-    const int blocks = at.units / A.heads;
-    const int rows = min(S::C::ROWS, at.s.use * A.group - at.x % blocks * S::C::ROWS);
-    const bool pair = LANES == 2 && rows > 128;
+    const bool pair = tc_pair<DP>(A, at);
     for (int l = 0; l <= static_cast<int>(pair); ++l)
       if (!wait(&sh.q_full[l], q_n[l]++)) goto out;
     {
-      // the tile that lane l's i-th is, in the part
+      // the tile that lane l's i-th is, in the part, and the tiles' places in the ring
       auto tile = [&](int l, int i) { return LANES == 1 || pair ? i : 2 * i + l; };
+      auto keys = [&](int t) { return base + (pair ? 2ll * t : t == 0 ? 0 : 2ll * t - 1); };
+      auto vals = [&](int t) { return base + (pair || t == n - 1 ? 2ll * t + 1 : 2ll * t + 2); };
       auto issue_s = [&](int l, int i) {
         const int t = tile(l, i);
-        const long long k = base + 2ll * t, q = seq[l] + i;
+        const long long k = keys(t), q = seq[l] + i;
         const int buf = static_cast<int>(k % S::RING), b = NB == 2 ? static_cast<int>(q & 1) : l;
         if (!wait(&sh.full[buf], k / S::RING)) return;
         // the S tile holds the weights of the lane's tile NB before: used up
-        if (q >= NB && !wait(&sh.o_full[l], q - NB)) return;
+        if (q >= NB && !wait(&sh.o_full[b], NB == 2 ? q / 2 - 1 : q - 1)) return;
         tc_fence_after();
         const uint32_t qa = qs + (pair ? l : 0) * S::QBLOCK, ka = ring + buf * S::BUF;
 #pragma unroll
@@ -362,7 +555,7 @@ __device__ __forceinline__ void tc_mma_role(const TreeArgs& A, TcShared& sh, uin
       };
       auto issue_o = [&](int l, int i) {
         const int t = tile(l, i);
-        const long long v = base + 2ll * t + 1, q = seq[l] + i;
+        const long long v = vals(t), q = seq[l] + i;
         const int buf = static_cast<int>(v % S::RING), b = NB == 2 ? static_cast<int>(q & 1) : l;
         if (!wait(&sh.p_full[b], NB == 2 ? q / 2 : q)) return;
         if (!wait(&sh.full[buf], v / S::RING)) return;
@@ -372,7 +565,7 @@ __device__ __forceinline__ void tc_mma_role(const TreeArgs& A, TcShared& sh, uin
         for (int ks = 0; ks < TILE / 16; ++ks)
           tc_mma_ts(tmem + 256 + l * DP, tmem + b * TILE + 8 * ks,
                     tc_desc_tokens(va + ks * 2048, S::PANEL), kO, i > 0 || ks > 0);
-        mma_commit(smem_u32(&sh.o_full[l]));
+        mma_commit(smem_u32(&sh.o_full[b]));
         if (!pair || l == 1) mma_commit(smem_u32(&sh.empty[buf]));
       };
       const int n0 = LANES == 1 || pair ? n : (n + 1) / 2, n1 = LANES == 1 ? 0 : pair ? n : n / 2;
@@ -418,12 +611,18 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
     ok = mbar_wait(smem_u32(bar), static_cast<uint32_t>(phase) & 1, kTreeWaitNs, &sh.abort);
     return __all_sync(0xffffffffu, ok);
   };
+  // the product with the weights of the lane's tile q.  (A barrier tells a phase
+  // from the one before it only, and with two S tiles two products may be under
+  // way: a barrier for each)
+  auto wait_o = [&](long long q) -> bool {
+    return NB == 2 ? wait(&sh.o_full[q & 1], q / 2) : wait(&sh.o_full[l], q);
+  };
   while (walk.next(A, at)) {
     const TreeSpan& s = at.s;
     const int blocks = at.units / A.heads;
     const int kvh = at.x / blocks, r0 = at.x % blocks * S::C::ROWS;
     const int rows = min(S::C::ROWS, s.use * A.group - r0);
-    const bool pair = LANES == 2 && rows > 128, alternate = LANES == 2 && !pair;
+    const bool pair = tc_pair<DP>(A, at), alternate = LANES == 2 && !pair;
     const int R = r0 + (pair ? 128 * l : 0) + r;
     const bool mine = R < r0 + rows;
     const int Rc = min(R, r0 + rows - 1), node = Rc / A.group, h = kvh * A.group + Rc - node * A.group;
@@ -547,7 +746,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
         sum *= keep;
       }
       if (i > 0 && __any_sync(0xffffffffu, grow)) {
-        if (!wait(&sh.o_full[l], q - 1)) goto out;
+        if (!wait_o(q - 1)) goto out;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < DP; c += 32) {
@@ -590,7 +789,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       if (!all && tc_masked<TILE>(A, s, pos)) {
         // values that are not finite: what they leave in the rows that attend them
         // (told before the values' barrier, which this product has waited for)
-        if (!wait(&sh.o_full[l], q)) goto out;
+        if (!wait_o(q)) goto out;
         tc_fence_after();
         uint32_t wild = 0;
 #pragma unroll
@@ -639,7 +838,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
     seq += mine_n;
     tiles += n;
     if (mine_n > 0) {
-      if (!wait(&sh.o_full[l], seq - 1)) goto out;
+      if (!wait_o(seq - 1)) goto out;
       tc_fence_after();
     }
     // ---- the part's end: the lanes that took turns join, each half of the columns
@@ -721,7 +920,9 @@ out:
 }
 
 template <int KV, int DP>
-__global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const TreeArgs A) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_tc_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map) {
   using S = TcShape<KV, DP>;
   extern __shared__ uint8_t tc_smem[];
   const uint32_t base = (smem_u32(tc_smem) + 1023) & ~1023u;
@@ -737,7 +938,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const TreeArgs A
   }
   if (tid == 0) {
     for (int i = 0; i < S::RING; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), kLoadWarps);
+      mbar_init(smem_u32(&sh.landed[i]), A.box ? 1 : 33 * kLoadWarps);
+      mbar_init(smem_u32(&sh.full[i]), kReadyWarps);
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -758,7 +960,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const TreeArgs A
   if (warp < 8) {
     tc_softmax_role<KV, DP>(A, sh, turns, qs, warp, lane);
   } else if (warp < 8 + kLoadWarps) {
-    tc_load_role<KV, DP>(A, sh, ring, warp - 8, lane);
+    if (A.box == 0) tc_load_role<KV, DP>(A, sh, ring, warp - 8, lane);
+    else if (warp == 8) tc_tma_role<KV, DP>(A, &k_map, &v_map, sh, ring, lane);
+  } else if (warp < kMmaWarp) {
+    tc_ready_role<KV, DP>(A, sh, ring, warp - 8 - kLoadWarps, lane);
   } else if (lane == 0) {
     tc_mma_role<KV, DP>(A, sh, qs, ring);
   }
@@ -769,8 +974,54 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_tc_kernel(const TreeArgs A
   if (warp == kMmaWarp) tmem_dealloc(sh.tmem, 512);
 }
 
+// ------------------------------------------------------------ host
+typedef CUresult (*TreeEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static TreeEncodeFn tree_encode_fn() {
+  static const TreeEncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                                     cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<TreeEncodeFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// The maps of keys and values for boxes of 64 columns by `box` tokens of a page;
+// false where there are none of these pages and strides
 template <int KV, int DP>
-static cudaError_t launch_tc(const TreeArgs& a, int ctas, cudaStream_t st) {
+static bool tree_maps(const TreeArgs& a, int box, CUtensorMap* maps) {
+  using S = TcShape<KV, DP>;
+  const TreeEncodeFn fn = tree_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.page),
+                              static_cast<cuuint64_t>(a.heads),
+                              static_cast<cuuint64_t>(a.num_pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(a.dim) * S::ES;  // where an axis has one element
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.s_token),
+                                 a.heads > 1 ? static_cast<cuuint64_t>(a.s_head) : row,
+                                 a.num_pages > 1 ? static_cast<cuuint64_t>(a.s_page) : row};
+  const cuuint32_t shape[4] = {S::LAND_ROW / S::ES, static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] < row || strides[i] >= 1ull << 40) return false;
+  for (int i = 0; i < 2; ++i)
+    if (fn(maps + i, KV == MOE_KV_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+           4, const_cast<char*>(i ? a.v : a.k), dims, strides, shape, ones,
+           CU_TENSOR_MAP_INTERLEAVE_NONE,
+           S::LAND_ROW == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
+template <int KV, int DP>
+static cudaError_t launch_tc(TreeArgs a, int ctas, cudaStream_t st) {
   using S = TcShape<KV, DP>;
   constexpr int SMEM = 1024 + S::C::LANES * S::QBLOCK + S::RING * S::BUF + kTcShared;
   static_assert(SMEM <= 227 * 1024, "shared memory of an SM");
@@ -778,10 +1029,17 @@ static cudaError_t launch_tc(const TreeArgs& a, int ctas, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), SMEM, done);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kern, dim3(ctas), dim3(kTcThreads), SMEM, st, a);
+  // a box: the largest power of two that divides a page, up to what lands in one
+  // piece; tiles begin at multiples of it
+  constexpr int kMost = S::LAND_ROW == 64 ? 32 : S::C::TILE;
+  int box = a.page & -a.page;
+  box = box < kMost ? box : kMost;
+  CUtensorMap maps[2] = {};
+  a.box = box >= 8 && tree_maps<KV, DP>(a, box, maps) ? box : 0;
+  e = launch_chained(kern, dim3(ctas), dim3(kTcThreads), SMEM, st, a, maps[0], maps[1]);
   if (e != cudaSuccess) return e;
-  return launch_chained(tree_join_kernel<KV, DP, S::C::ROWS>, dim3(ctas), dim3(32 * kTreeJoinWarps),
-                        0, st, a);
+  return launch_chained(tree_join_kernel<KV, DP, S::C::ROWS>, dim3(ctas, kTreeJoinBlocks),
+                        dim3(32 * kTreeJoinWarps), 0, st, a);
 }
 
 cudaError_t launch_tree_tc(int kv, int dp, const TreeArgs& a, int ctas, cudaStream_t st) {

@@ -5,7 +5,7 @@
 
 namespace moe {
 
-constexpr int kTcThreads = 416;  // 16 warps' registers: 128 a thread
+constexpr int kTcThreads = 480;  // 16 warps' registers: 128 a thread
 constexpr int kTcShared = 1024;  // bytes beside the tiles
 
 template <int DP>
