@@ -90,11 +90,13 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
       *reinterpret_cast<float4*>(qs + r * KP + d) = v;
     }
     int node[2], low[2];
+    TreeMask mask[2];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, acc[2][4 * NC] = {};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       node[e] = (r0 + min(2 * ty + e, rows - 1)) / A.group;
-      low[e] = tree_low(A, s, node[e]);
+      mask[e] = tree_mask(A, s, node[e]);
+      low[e] = tree_low(A, s, mask[e]);
     }
     __syncthreads();
     load(A.k, ks, KP, 0);
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
           const int c = tx + 16 * j;
-          const uint32_t bits = tree_attends(A, s, node[e], low[e], pos0 + (c & ~31));
+          const uint32_t bits = tree_attends(s, mask[e], low[e], pos0 + (c & ~31));
           const bool on = (bits >> (c & 31) & 1u) && s_off[buf][c] >= 0;
           live |= static_cast<unsigned>(on) << j;
           x[e][j] *= f;

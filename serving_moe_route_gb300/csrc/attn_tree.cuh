@@ -213,47 +213,65 @@ __device__ __forceinline__ void tree_record(const TreeArgs& A, const TreeStart& 
 }
 
 // ------------------------------------------------------------ what a row attends
-// 32 bits of node i's mask from new token j on (j may be negative)
-__device__ __forceinline__ uint32_t tree_bits(const TreeArgs& A, const TreeSpan& s, int i, int j) {
-  const int lim = min(s.n, s.len - s.ctx);  // new tokens there are
+// A node's mask, in registers
+struct TreeMask {
+  unsigned long long m[MOE_TREE_MAX / 64];
+};
+__device__ __forceinline__ TreeMask tree_mask(const TreeArgs& A, const TreeSpan& s, int i) {
+  TreeMask t;
+#pragma unroll
+  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
+    if (A.masks) {
+      t.m[w] = w < A.words
+                   ? __ldg(A.masks + static_cast<long long>(s.row0 + i) * A.words + w)
+                   : 0;
+    } else {  // nodes up to i
+      const int n = i + 1 - 64 * w;
+      t.m[w] = n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+    }
+  }
+  return t;
+}
+// 32 bits of it from new token j on (j may be negative), of the tokens there are
+__device__ __forceinline__ uint32_t tree_bits(const TreeSpan& s, const TreeMask& t, int j) {
+  const int lim = min(s.n, s.len - s.ctx);
   if (j >= lim || j <= -32) return 0;
   uint32_t bits;
-  if (A.masks) {
-    const unsigned long long* m = A.masks + static_cast<long long>(s.row0 + i) * A.words;
-    if (j < 0) {
-      bits = static_cast<uint32_t>(m[0]) << -j;
-    } else {
-      const int w = j >> 6, sh = j & 63;
-      unsigned long long v = w < A.words ? m[w] >> sh : 0;
-      if (sh > 32 && w + 1 < A.words) v |= m[w + 1] << (64 - sh);
-      bits = static_cast<uint32_t>(v);
-    }
+  if (j < 0) {
+    bits = static_cast<uint32_t>(t.m[0]) << -j;
   } else {
-    const int n = i + 1 - j;  // tokens j .. i
-    bits = n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1;
-    if (j < 0) bits &= ~0u << -j;
+    const int w = j >> 6, sh = j & 63;
+    unsigned long long lo = 0, hi = 0;
+#pragma unroll
+    for (int k = 0; k < MOE_TREE_MAX / 64; ++k) {
+      if (w == k) lo = t.m[k];
+      if (w + 1 == k) hi = t.m[k];
+    }
+    bits = static_cast<uint32_t>(lo >> sh);
+    if (sh > 32) bits |= static_cast<uint32_t>(hi << (64 - sh));
   }
   if (lim - j < 32) bits &= (1u << (lim - j)) - 1;
   return bits;
 }
-// first context token that node i attends
-__device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, int i) {
+// first context token that its node attends
+__device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, const TreeMask& t) {
   if (A.window <= 0) return 0;
   int c = 0;
-  for (int j = 0; j < 64 * A.words; j += 32) c += __popc(tree_bits(A, s, i, j));
+#pragma unroll
+  for (int j = 0; j < MOE_TREE_MAX; j += 32) c += __popc(tree_bits(s, t, j));
   return max(0, s.ctx - max(0, A.window - c));
 }
-// which of the 32 tokens from t on node i attends (by its mask and window alone)
-__device__ __forceinline__ uint32_t tree_attends(const TreeArgs& A, const TreeSpan& s, int i,
-                                                 int low, int t) {
+// which of the 32 tokens from pos on its node attends (by its mask and window alone)
+__device__ __forceinline__ uint32_t tree_attends(const TreeSpan& s, const TreeMask& t, int low,
+                                                 int pos) {
   uint32_t bits = 0;
   const int end = min(s.ctx, s.len);
-  if (t < end && t + 32 > low) {
+  if (pos < end && pos + 32 > low) {
     bits = ~0u;
-    if (end - t < 32) bits &= (1u << (end - t)) - 1;
-    if (low > t) bits &= ~0u << (low - t);
+    if (end - pos < 32) bits &= (1u << (end - pos)) - 1;
+    if (low > pos) bits &= ~0u << (low - pos);
   }
-  return bits | tree_bits(A, s, i, t - s.ctx);
+  return bits | tree_bits(s, t, pos - s.ctx);
 }
 
 __device__ __forceinline__ float tree_ex2(float x) {

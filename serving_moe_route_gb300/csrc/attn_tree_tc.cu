@@ -62,6 +62,8 @@ struct TcShape {
   static constexpr int LAND_ROW = KV == MOE_KV_E4M3 && DP == 64 ? 64 : 128;  // bytes of a row
   static constexpr uint32_t FMT = KV == MOE_KV_E4M3 ? 0 : 1;  // f16, bf16
 };
+// a logit's factor is not 0, so that -inf stays -inf
+constexpr float kTcLeast = 1e-37f;
 constexpr int kSlots = 8;  // tiles whose live and non-finite tokens are kept
 
 // The second block of Q's memory where a unit has one block only: what the
@@ -439,14 +441,29 @@ __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, u
       for (int i = 0; i < TPW / 8; ++i) there |= static_cast<uint32_t>(live[i]) << (8 * i);
     }
     const bool gaps = kv && there != (TPW == 32 ? ~0u : (1u << TPW % 32) - 1);
+    const bool care = tame || gaps;
     if constexpr (KV == MOE_KV_E4M3) {
       uint4 raw[TPW / RPI];
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j)
         raw[j] = tc_lds4(base + tc_land<KV, DP>(warp * TPW + j * RPI + row0, chunk));
       __syncwarp();  // the codes lie where the warp's rows are written
+      if (!care) {
+#pragma unroll
+        for (int j = 0; j < TPW / RPI; ++j) {
+          const int r = warp * TPW + j * RPI + row0;
+          uint4 lo, hi;
+          tc_widen(raw[j].x, lo.x, lo.y);
+          tc_widen(raw[j].y, lo.z, lo.w);
+          tc_widen(raw[j].z, hi.x, hi.y);
+          tc_widen(raw[j].w, hi.z, hi.w);
+          tc_sts4(base + tc_chunk(r, 2 * chunk, S::PANEL), lo);
+          tc_sts4(base + tc_chunk(r, 2 * chunk + 1, S::PANEL), hi);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j) {
+        if (!care) break;
         const int r = warp * TPW + j * RPI + row0;
         uint4 lo, hi;
         tc_widen(raw[j].x, lo.x, lo.y);
@@ -466,7 +483,7 @@ __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, u
         tc_sts4(base + tc_chunk(r, 2 * chunk, S::PANEL), lo);
         tc_sts4(base + tc_chunk(r, 2 * chunk + 1, S::PANEL), hi);
       }
-    } else if (tame || gaps) {
+    } else if (care) {
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j) {
         const uint32_t to = base + tc_chunk(warp * TPW + j * RPI + row0, chunk, S::PANEL);
@@ -493,7 +510,8 @@ __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, u
         sh.wild[slot][warp * (TPW / 8) + lane] = static_cast<uint8_t>(wild_rows >> (8 * lane));
     }
     if (kv) slot = (slot + 1) % kSlots;
-    fence_proxy_async_shared();
+    // (what TMA has written needs none)
+    if (KV == MOE_KV_E4M3 || A.box == 0 || care) fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.full[buf]));
     ++n;
@@ -627,6 +645,9 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
     const bool mine = R < r0 + rows;
     const int Rc = min(R, r0 + rows - 1), node = Rc / A.group, h = kvh * A.group + Rc - node * A.group;
     const long long row = s.row0 + node;
+    // a warp whose rows are all beyond the block's only keeps step
+    const bool idle = (pair ? 128 * l : 0) + (warp & 3) * 32 >= rows;
+    const TreeMask mask = tree_mask(A, s, node);
     float sl = A.scale_log2, v_mul = 1.0f, f = 0.0f;  // f: of logits, in base 2
     if constexpr (KV == MOE_KV_E4M3) {
       sl *= A.k_scale[kvh];
@@ -686,11 +707,11 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       }
       fence_proxy_async_shared();
       mbar_arrive(smem_u32(&sh.q_full[l]));
-      f = fabsf(sl) * mul;
+      f = fmaxf(fabsf(sl) * mul, kTcLeast);
     }
     const int n = at.t1 - at.t0;
     const int mine_n = alternate ? (n + 1 - l) / 2 : n;
-    const int low = tree_low(A, s, node);
+    const int low = tree_low(A, s, mask);
     float m = -INFINITY, sum = 0.0f;
     for (int i = 0; i < mine_n; ++i) {
       const int t = alternate ? 2 * i + l : i;
@@ -699,42 +720,56 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       const int b = NB == 2 ? static_cast<int>(q & 1) : l;
       const uint32_t t_s = tmem + b * TILE;
       if (!wait(&sh.s_full[b], NB == 2 ? q / 2 : q)) goto out;
+      if (idle) {
+        mbar_arrive(smem_u32(&sh.p_full[b]));
+        continue;
+      }
       tc_fence_after();
       if (i == 0 && alternate && l == 1) {
-        f = fabsf(sl);
-        if constexpr (KV == MOE_KV_E4M3) f *= turns.q_mul[r];
+        f = fmaxf(fabsf(sl) * (KV == MOE_KV_E4M3 ? turns.q_mul[r] : 1.0f), kTcLeast);
       }
       const int slot = static_cast<int>((tiles + t) % kSlots);
-      uint32_t word[CH];
-      bool all = !tc_masked<TILE>(A, s, pos);
+      // (loops over the columns are rolled up: a longer program, most of it run once
+      // a tile, was fetched for 6 us at the first tile that masks apply to)
+      auto attended = [&](int c) {
+        return *reinterpret_cast<const volatile uint32_t*>(&sh.live[slot][4 * c]) &
+               tree_attends(s, mask, low, pos + 32 * c);
+      };
+      const bool masked = tc_masked<TILE>(A, s, pos);
+      bool all = !masked, any = true;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        word[c] = *reinterpret_cast<const volatile uint32_t*>(&sh.live[slot][4 * c]);
-        all = all && word[c] == ~0u;
-      }
-      bool any = true;
-      if (!all) {  // (the same for all rows)
-        any = false;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          word[c] &= tree_attends(A, s, node, low, pos + 32 * c);
-          any = any || word[c];
-        }
-      }
+      for (int c = 0; c < CH; ++c)
+        all = all && *reinterpret_cast<const volatile uint32_t*>(&sh.live[slot][4 * c]) == ~0u;
       float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float v[32];
-        tmem_ld32(t_s + 32 * c, v);
-        tmem_wait_ld(v);
-        if (!all) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = word[c] >> j & 1u ? v[j] : -INFINITY;
-        }
+      auto largest = [&](const float (&v)[32]) {
         float x[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int j = 4; j < 32; ++j) x[j & 3] = fmaxf(x[j & 3], v[j]);
         top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+      };
+      if (all) {  // (the same for all rows)
+#pragma unroll 1
+        for (int c = 0; c < CH; ++c) {
+          float v[32];
+          tmem_ld32(t_s + 32 * c, v);
+          tmem_wait_ld(v);
+          largest(v);
+        }
+      } else {  // logits that do not count become -inf
+        any = false;
+#pragma unroll 1
+        for (int c = 0; c < CH; ++c) {
+          float v[32];
+          tmem_ld32(t_s + 32 * c, v);
+          const uint32_t word = attended(c);
+          any = any || word;
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = word >> j & 1u ? v[j] : -INFINITY;
+          largest(v);
+          tc_st32(t_s + 32 * c, v);
+        }
+        tc_wait_st();
       }
       top = top == -INFINITY ? top : top * f;
       const bool grow = top > m + (S::LIFT + S::LAG);
@@ -762,17 +797,13 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       if (any) m = fmaxf(m, -FLT_MAX);
       const float ref = m == -INFINITY ? 0.0f : m;
       float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < CH; ++c) {
         float v[32];
         tmem_ld32(t_s + 32 * c, v);
         tmem_wait_ld(v);
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = tree_ex2(fmaf(v[j], f, -ref));
-        if (!all) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = word[c] >> j & 1u ? v[j] : 0.0f;
-        }
         uint32_t p[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -786,7 +817,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&sh.p_full[b]));
-      if (!all && tc_masked<TILE>(A, s, pos)) {
+      if (masked) {
         // values that are not finite: what they leave in the rows that attend them
         // (told before the values' barrier, which this product has waited for)
         if (!wait_o(q)) goto out;
@@ -804,7 +835,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
 #pragma unroll 1
             for (int c = 0; c < CH; ++c) {
               uint32_t left =
-                  *reinterpret_cast<const volatile uint32_t*>(&sh.wild[slot][4 * c]) & word[c];
+                  *reinterpret_cast<const volatile uint32_t*>(&sh.wild[slot][4 * c]) & attended(c);
               while (left) {
                 const int tok = pos + 32 * c + __ffs(left) - 1;
                 left &= left - 1;
@@ -865,7 +896,8 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       const uint32_t o_base = tmem + 256 + (pair ? l * DP : 0);
       constexpr int W = 32;
 #pragma unroll 1
-      for (int d = alternate ? l * (DP / 2) : 0; d < (alternate ? (l + 1) * (DP / 2) : DP); d += W) {
+      for (int d = alternate ? l * (DP / 2) : 0;
+           !idle && d < (alternate ? (l + 1) * (DP / 2) : DP); d += W) {
         float o[W];
         tmem_ld32(o_base + d, o);
         tmem_wait_ld(o);
