@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
   float* const vs = ks + TILE * KP;
   float* const ps = vs + TILE * DP;
   __shared__ TreeStart start;
-  __shared__ long long sums[kSimtThreads / 32];
+  __shared__ long long sums[33];
   __shared__ long long s_off[2][TILE];  // a token's place in the cache, -1: none
   pdl_wait();
   pdl_trigger();
@@ -50,8 +50,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
 
   while (walk.next(A, at)) {
     const TreeSpan& s = at.s;
-    const int blocks = at.units / A.heads;
-    const int kvh = at.x / blocks, r0 = at.x % blocks * kSimtRows;
+    const int kvh = at.head(), r0 = at.block() * kSimtRows;
     const int rows = min(kSimtRows, s.use * A.group - r0);
     const float f = A.scale_log2;
     auto offsets = [&](int t, int buf) {
@@ -221,7 +220,7 @@ struct TreeShape {
 template <int DP>
 static TreeShape shape_of(int kv) {
   if (kv == MOE_KV_F32) return {kSimtRows, SimtCfg<DP>::TILE, SimtCfg<DP>::CTAS};
-  return {TcCfg<DP>::ROWS, TcCfg<DP>::TILE, 1};
+  return {TcCfg<DP>::ROWS, TcCfg<DP>::TILE, TcCfg<DP>::CTAS};
 }
 static TreeShape tree_shape(int kv, int dp) {
   return dp == 64 ? shape_of<64>(kv) : dp == 128 ? shape_of<128>(kv) : shape_of<256>(kv);
@@ -333,14 +332,15 @@ int moe_attn_tree(const moe_kv_cache_t* cache, const void* q, long long q_stride
   a.part_ml = reinterpret_cast<float2*>(w);
   w += up256(2ull * full * shape.rows * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(w);
-  // no more CTAs than tiles that these sizes can hold: units by the rows there
-  // are (a block for each request that has any, and one for every full block)
-  const long long blocks = static_cast<long long>(N) * a.group / shape.rows + (B < N ? B : N);
+  // no more CTAs than (block, tile) pairs that these sizes can hold, whole groups
+  const long long most = (static_cast<long long>(N < max_new ? N : max_new) * a.group +
+                          shape.rows - 1) / shape.rows;
+  const int size = static_cast<int>(most < kTreeGroup ? most : kTreeGroup);
   const long long tiles = (static_cast<long long>(max_pages) * a.page + shape.tile - 1) / shape.tile;
-  const long long units = blocks * a.heads;
-  const int ctas = units >= full || tiles >= full || units * tiles >= full
+  const long long units = (B < N ? B : N) * ((most + size - 1) / size) * a.heads;
+  const int ctas = units >= full || tiles >= full || units * tiles * size >= full
                        ? full
-                       : static_cast<int>(units * tiles);
+                       : static_cast<int>(units * tiles) * size;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->kv_dtype != MOE_KV_F32 ? launch_tree_tc(cache->kv_dtype, dp, a, ctas, st)
                         : dp == 64                    ? launch_simt<64>(a, ctas, st)

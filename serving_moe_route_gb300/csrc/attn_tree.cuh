@@ -3,10 +3,13 @@
 //
 // A unit is (request, kv head, block of ROWS rows), a row being (node, query head
 // of that kv head), nodes in order.  Its tokens form tiles of TILE; it counts its
-// tiles and END more for its end.  The counts of all units, in order, are cut into
-// equal contiguous ranges, one per CTA of a single wave, so that ragged lengths
-// and one long request balance alike.  A range may begin and end inside a unit;
-// the unit's parts go to the workspace and a second kernel joins them in order.
+// tiles and END more for its end.  CTAs work in groups of as many as the largest
+// request has blocks (8 at most), one block each, on the same tokens at the same
+// time, so that all but one find them in L2.  The counts of all (request, kv head),
+// in order, are cut into equal contiguous ranges, one per group of a single wave,
+// so that ragged lengths and one long request balance alike.  A range may begin
+// and end inside a unit; the unit's parts go to the workspace and a second kernel
+// joins them in order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -38,7 +41,7 @@ struct TreeArgs {
   const unsigned long long* masks;
   float* part_o;    // [2 * ctas][ROWS][DP]
   float2* part_ml;  // [2 * ctas][ROWS]
-  int4* info;       // [ctas] {unit's request, unit in request, parts, place among them}
+  int4* info;       // [ctas] {unit's request, unit in request, parts, place + 2^16 group}
   unsigned* err;
   float scale_log2;
   int N, B, Hq, heads, group, words, max_new;
@@ -66,73 +69,104 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int r, bool& cu
   if (s.n > 0 && (s.use < s.n || s.len < all)) cut = true;
   return s;
 }
+constexpr int kTreeGroup = 8;  // CTAs of a group at most
+
+// blocks of a request's rows, and the rounds in which a group goes through them
 template <int ROWS>
-__device__ __forceinline__ int tree_units(const TreeArgs& A, const TreeSpan& s) {
-  return (s.use * A.group + ROWS - 1) / ROWS * A.heads;
+__device__ __forceinline__ int tree_blocks(const TreeArgs& A, const TreeSpan& s) {
+  return (s.use * A.group + ROWS - 1) / ROWS;
 }
 template <int TILE>
 __device__ __forceinline__ int tree_tiles(const TreeSpan& s) {
   return max(1, (s.len - s.first + TILE - 1) / TILE);
 }
 
-// A CTA's range, walked part by part: tiles [t0, t1) of the nt of unit x of
-// request b.  Every role of a CTA keeps one.
+// Where this CTA's range begins, in shared memory
+struct TreeStart {
+  long long left, end, total;
+  int b, x, t, groups;
+  int size, place;  // CTAs of a group, this one's place in it
+};
+
+// A CTA's range, walked part by part: tiles [t0, t1) of the nt of unit x (kv head
+// and round) of request b, this CTA's block of it.  Every role of a CTA keeps one.
 template <int ROWS, int TILE, int END>
 struct TreeWalk {
   TreeSpan s;
-  int b, x, t, nt, units;
+  int b, x, t, nt, rounds, blocks;
   long long left, end;  // places from here on; the range's end, counted over all units
-  int t0, t1;
+  int t0, t1, size, place;
 
+  __device__ __forceinline__ int head() const { return x / rounds; }
+  __device__ __forceinline__ int block() const { return x % rounds * size + place; }
   __device__ __forceinline__ void enter(const TreeArgs& A, int request) {
     bool cut = false;
     for (b = request; b < A.B; ++b) {
       s = tree_span(A, b, cut);
-      units = tree_units<ROWS>(A, s);
-      if (units > 0) break;
+      blocks = tree_blocks<ROWS>(A, s);
+      if (blocks > 0) break;
     }
+    rounds = (blocks + size - 1) / size;
     nt = tree_tiles<TILE>(s);
     x = 0;
     t = 0;
   }
-  // the next part; false at the range's end.  `at` is its unit (s, b, x, nt)
-  __device__ __forceinline__ bool next(const TreeArgs& A, TreeWalk& at) {
-    if (left <= 0) return false;
-    at = *this;
-    at.t0 = t;
-    at.t1 = static_cast<int>(min(static_cast<long long>(nt), t + left));
-    left -= at.t1 - t;
-    if (at.t1 < nt) {
-      left = 0;
-      return true;
-    }
-    left -= END;
+  __device__ __forceinline__ void skip(const TreeArgs& A) {
     t = 0;
-    if (left > 0 && ++x >= units) enter(A, b + 1);
-    return true;
+    if (left > 0 && ++x >= rounds * A.heads) enter(A, b + 1);
+  }
+  // the next part; false at the range's end.  `at` is its unit
+  __device__ __forceinline__ bool next(const TreeArgs& A, TreeWalk& at) {
+    while (left > 0) {
+      at = *this;
+      at.t0 = t;
+      at.t1 = static_cast<int>(min(static_cast<long long>(nt), t + left));
+      left -= at.t1 - t;
+      if (at.t1 < nt) {
+        left = 0;
+      } else {
+        left -= END;
+        skip(A);
+      }
+      if (at.block() < at.blocks) return true;  // else there is none for this CTA
+    }
+    return false;
   }
 };
 
-// Where this CTA's range begins.  Every thread of the CTA (a multiple of 32, at
-// most 1024) calls it; the result is in shared memory.  total: of all units.
-struct TreeStart {
-  long long left, end, total;
-  int b, x, t, ctas;
-};
+// Every thread of the CTA (a multiple of 32, at most 1024) calls it; out and sums
+// (33 of them) are in shared memory
 template <int ROWS, int TILE, int END>
 __device__ __forceinline__ void tree_begin(const TreeArgs& A, TreeStart* out, long long* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int threads = blockDim.x, nw = threads >> 5;
   bool cut = false;
-  auto places = [&](const TreeSpan& s) {
-    return static_cast<long long>(tree_units<ROWS>(A, s)) * (tree_tiles<TILE>(s) + END);
-  };
   const int per = (A.B - 1) / threads + 1;
   const int b0 = static_cast<int>(min(static_cast<long long>(A.B),
                                       static_cast<long long>(threadIdx.x) * per));
   const int b1 = b0 + min(per, A.B - b0);
+  // the size of a group: the most blocks that a request has
+  TreeSpan s;
+  int most = 0;
+  for (int b = b0; b < b1; ++b) {
+    s = tree_span(A, b, cut);
+    most = max(most, tree_blocks<ROWS>(A, s));
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) sums[warp] = most;
+  __syncthreads();
+  for (int w = 0; w < nw; ++w) most = max(most, static_cast<int>(sums[w]));
+  const int size = max(1, min(min(most, kTreeGroup), static_cast<int>(gridDim.x)));
+  __syncthreads();
+  auto places = [&](const TreeSpan& s) {
+    return static_cast<long long>((tree_blocks<ROWS>(A, s) + size - 1) / size) * A.heads *
+           (tree_tiles<TILE>(s) + END);
+  };
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += places(tree_span(A, b, cut));
+  for (int b = b0; b < b1; ++b) {
+    if (per > 1) s = tree_span(A, b, cut);
+    mine += places(s);
+  }
   long long incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -147,24 +181,23 @@ __device__ __forceinline__ void tree_begin(const TreeArgs& A, TreeStart* out, lo
     total += sums[w];
   }
   if (cut && A.err && blockIdx.x == 0) atomicOr(A.err, MOE_DEVERR_NO_SPACE);
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  const int cta = blockIdx.x;
+  const int groups = static_cast<int>(min(static_cast<long long>(gridDim.x / size), total));
+  const int g = blockIdx.x / size;
   if (threadIdx.x == 0) {
-    A.info[cta] = make_int4(0, 0, 0, 0);
-    if (cta >= ctas) {
-      out->left = 0;
-      out->ctas = ctas;
-      out->total = total;
-    }
+    A.info[blockIdx.x] = make_int4(0, 0, 0, 0);
+    out->groups = groups;
+    out->size = size;
+    out->place = blockIdx.x % size;
+    out->total = total;
+    if (g >= groups) out->left = 0;
   }
-  if (cta < ctas) {
-    const long long begin = cta * total / ctas, end = (cta + 1) * total / ctas;
+  if (g < groups) {
+    const long long begin = g * total / groups, end = (g + 1) * total / groups;
     const long long lo = before + incl - mine, hi = before + incl;
     if (begin >= lo && begin < hi) {
       long long at = lo;
       int b = b0;
-      TreeSpan s;
-      for (;; ++b) {
+      for (; per > 1; ++b) {
         s = tree_span(A, b, cut);
         const long long n = places(s);
         if (begin < at + n) break;
@@ -176,8 +209,6 @@ __device__ __forceinline__ void tree_begin(const TreeArgs& A, TreeStart* out, lo
       out->t = static_cast<int>(begin - at - static_cast<long long>(out->x) * one);
       out->left = end - begin;
       out->end = end;
-      out->total = total;
-      out->ctas = ctas;
     }
   }
   __syncthreads();
@@ -188,14 +219,15 @@ __device__ __forceinline__ TreeWalk<ROWS, TILE, END> tree_walk(const TreeArgs& A
   TreeWalk<ROWS, TILE, END> k;
   k.left = w.left;
   k.end = w.end;
+  k.size = w.size;
+  k.place = w.place;
   if (k.left <= 0) return k;
   k.enter(A, w.b);
   k.x = w.x;
   k.t = w.t;
   if (k.t >= k.nt) {  // the range begins with a unit's end: on to the next
     k.left -= k.nt + END - k.t;
-    k.t = 0;
-    if (k.left > 0 && ++k.x >= k.units) k.enter(A, k.b + 1);
+    k.skip(A);
   }
   return k;
 }
@@ -206,10 +238,10 @@ __device__ __forceinline__ void tree_record(const TreeArgs& A, const TreeStart& 
                                             const TreeWalk<ROWS, TILE, END>& at) {
   // at: as `next` left it, its `left` counted from t0 on
   const long long from = at.end - at.left - at.t0, to = from + at.nt - 1;
-  const int c0 = static_cast<int>(((from + 1) * w.ctas - 1) / w.total);
-  const int c1 = static_cast<int>(((to + 1) * w.ctas - 1) / w.total);
-  A.info[blockIdx.x] =
-      make_int4(at.b, at.x, c1 - c0 + 1, static_cast<int>(blockIdx.x) - c0);
+  const int g0 = static_cast<int>(((from + 1) * w.groups - 1) / w.total);
+  const int g1 = static_cast<int>(((to + 1) * w.groups - 1) / w.total);
+  const int mine = static_cast<int>(blockIdx.x) / w.size;
+  A.info[blockIdx.x] = make_int4(at.b, at.x, g1 - g0 + 1, (mine - g0) | w.size << 16);
 }
 
 // ------------------------------------------------------------ what a row attends
@@ -303,16 +335,16 @@ __device__ __forceinline__ void tree_store4(void* out, long long at, float a, fl
         make_uint2(tree_bf16x2(a, b), tree_bf16x2(c, d));
 }
 
-// R rows of a unit, joined by a warp from its parts in CTAs cta, cta + 1, ...: the
+// R rows of a unit, joined by a warp from its parts in CTAs cta, cta + size, ...: the
 // loads of all of them, and of some parts at a time, are under way together.
 template <int KV, int DP, int ROWS, int R>
 __device__ __forceinline__ void tree_join_rows(const TreeArgs& A, const TreeSpan& s, int cta,
-                                               int parts, int kvh, int r0, int r, int rows,
-                                               int lane) {
+                                               int size, int parts, int kvh, int r0, int r,
+                                               int rows, int lane) {
   constexpr int VL = DP / 32;  // columns per lane
   constexpr int AHEAD = R == 1 ? 8 : 2;
   auto at = [&](int p, int u) {
-    return (2ll * (cta + p) + (p == 0 ? 0 : 1)) * ROWS + min(r + u, rows - 1);
+    return (2ll * (cta + p * size) + (p == 0 ? 0 : 1)) * ROWS + min(r + u, rows - 1);
   };
   float top[R], sum[R], o[R][VL];
 #pragma unroll
@@ -389,8 +421,8 @@ __device__ __forceinline__ void tree_join_rows(const TreeArgs& A, const TreeSpan
 }
 
 // Joins the parts of the units that range borders cut.  A unit that begins in CTA
-// c and does not end there has c's first slot, then the second slots of the next
-// CTAs.  The kTreeJoinBlocks blocks of each CTA that it does not end in deal its
+// c and does not end there has c's first slot, then the second slots of the CTAs
+// at its place in the next groups.  The kTreeJoinBlocks blocks of each CTA that it does not end in deal its
 // rows out: four a warp where there are few parts, else one.  (One block for each
 // of those CTAs, a row a warp: 40 us more for 64 requests of 16 nodes.)
 constexpr int kTreeJoinWarps = 8, kTreeJoinBlocks = 8, kTreeFewParts = 8;
@@ -398,23 +430,24 @@ template <int KV, int DP, int ROWS>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const TreeArgs A) {
   pdl_wait();
   const int4 unit = A.info[blockIdx.x];
-  const int parts = unit.z, cta = blockIdx.x - unit.w;
+  const int parts = unit.z, place = unit.w & 0xffff, size = unit.w >> 16;
   if (parts == 0) return;
+  const int cta = blockIdx.x - place * size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool cut = false;
   const TreeSpan s = tree_span(A, unit.x, cut);
-  const int blocks = (s.use * A.group + ROWS - 1) / ROWS;
-  const int kvh = unit.y / blocks, r0 = unit.y % blocks * ROWS;
+  const int rounds = (tree_blocks<ROWS>(A, s) + size - 1) / size;
+  const int kvh = unit.y / rounds, r0 = (unit.y % rounds * size + cta % size) * ROWS;
   const int rows = min(ROWS, s.use * A.group - r0);
-  const int first = (unit.w * kTreeJoinBlocks + blockIdx.y) * kTreeJoinWarps + warp;
+  const int first = (place * kTreeJoinBlocks + blockIdx.y) * kTreeJoinWarps + warp;
   const int warps = (parts - 1) * kTreeJoinBlocks * kTreeJoinWarps;
   if (parts <= kTreeFewParts) {
     constexpr int R = DP == 256 ? 2 : 4;
     for (int r = R * first; r < rows; r += R * warps)
-      tree_join_rows<KV, DP, ROWS, R>(A, s, cta, parts, kvh, r0, r, rows, lane);
+      tree_join_rows<KV, DP, ROWS, R>(A, s, cta, size, parts, kvh, r0, r, rows, lane);
   } else {
     for (int r = first; r < rows; r += warps)
-      tree_join_rows<KV, DP, ROWS, 1>(A, s, cta, parts, kvh, r0, r, rows, lane);
+      tree_join_rows<KV, DP, ROWS, 1>(A, s, cta, size, parts, kvh, r0, r, rows, lane);
   }
 }
 

@@ -5,15 +5,15 @@
 
 namespace moe {
 
-constexpr int kTcThreads = 480;  // 16 warps' registers: 128 a thread
+constexpr int kTcThreads = 256;
 constexpr int kTcShared = 1024;  // bytes beside the tiles
 
 template <int DP>
 struct TcCfg {
-  static constexpr int LANES = DP == 256 ? 1 : 2;
-  static constexpr int ROWS = 128 * LANES;
-  static constexpr int TILE = DP == 256 ? 64 : 128;
-  static constexpr int END = 2;  // what a unit's end costs, in tiles
+  static constexpr int ROWS = 128;
+  static constexpr int TILE = 64;
+  static constexpr int CTAS = DP == 256 ? 1 : 2;  // per SM
+  static constexpr int END = 4;                   // what a unit's end costs, in tiles
 };
 
 // bf16 and e4m3 caches; ctas of a single wave
