@@ -83,6 +83,13 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
 // A tile whose 64-column panels hold 128 bytes of each token, for a product over
 // tokens: columns are the contiguous axis.  `panel`: bytes from one to the next
 __device__ __forceinline__ uint64_t tc_desc_tokens(uint32_t saddr, uint32_t panel) {
@@ -199,7 +206,7 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
   bool bad_page = false, ok = true, more = walk.next(A, at);
   uint32_t n = 0;  // tiles asked for
   int slot = 0;
-  const int boxes = TILE / A.box;
+  const int box_shift = 31 - __clz(A.box), boxes = TILE >> box_shift;
   const int bytes = A.box * S::LAND * S::LAND_ROW;
   struct Place {
     int page, row;  // of this lane's box
@@ -257,11 +264,15 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
         // which tokens there are, 32 a word
         const uint32_t there = __ballot_sync(0xffffffffu, now.live);
         if (lane < CH) {
-          uint32_t w = 0;
           const int from = 32 * lane;
-          for (int b = from / A.box; b * A.box < from + 32; ++b)
-            if (there >> b & 1u)
-              w |= A.box >= 32 ? ~0u : ((1u << A.box) - 1) << (b * A.box - from);
+          uint32_t w = 0;
+          if (A.box >= 32) {
+            w = there >> (from >> box_shift) & 1u ? ~0u : 0u;
+          } else {
+#pragma unroll
+            for (int b = 0; b < 32; b += 8)
+              if (there >> (from + b >> box_shift) & 1u) w |= 0xffu << b;
+          }
           const int left = at.s.len - (at.s.first + t * TILE + from);
           if (left < 32) w = left <= 0 ? 0 : w & ((1u << left) - 1);
           sh.live[slot][lane] = w;
@@ -500,7 +511,9 @@ __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, u
   }
 }
 
-// ------------------------------------------------------------ products (one thread)
+// ------------------------------------------------------------ products
+// The whole warp keeps step, so that descriptors are the warp's and not a lane's,
+// and one lane issues.
 template <int KV, int DP>
 __device__ __forceinline__ void tc_mma_role(const TreeArgs& A, TcShared& sh, uint32_t qs,
                                             uint32_t ring) {
@@ -510,56 +523,69 @@ __device__ __forceinline__ void tc_mma_role(const TreeArgs& A, TcShared& sh, uin
   constexpr uint32_t kO = idesc_make(S::FMT, 128, DP) | (1u << 16);  // V: columns contiguous
   auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
   auto at = walk;
-  const uint32_t tmem = sh.tmem;
-  uint32_t n = 0, q = 0, parts = 0;  // tiles of the ring, of weights, and parts before
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+  const uint64_t qd = sdesc_sw128(qs), kd = sdesc_sw128(ring), vd = tc_desc_tokens(ring, S::PANEL);
+  const uint32_t full = smem_u32(sh.full), empty = smem_u32(sh.empty), s_full = smem_u32(sh.s_full),
+                 p_full = smem_u32(sh.p_full), o_full = smem_u32(sh.o_full);
+  uint32_t buf = 0, turn = 0;  // the ring's next tile, and how often the ring has gone round
+  uint32_t q = 0, parts = 0;   // tiles of weights, and parts before
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t phase) {
-    ok = ok && mbar_wait(smem_u32(bar), phase & 1, kTreeWaitNs, &sh.abort);
+  auto wait = [&](uint32_t bar, uint32_t phase) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, kTreeWaitNs, &sh.abort));
     return ok;
   };
-  // S of the i-th tile from q on; the ring's next tile is its keys
-  auto issue_s = [&](uint32_t i) {
-    const uint32_t b = i & 1;
-    const int buf = static_cast<int>(n % S::RING);
-    if (!wait(&sh.full[buf], n / S::RING)) return;
-    // this S holds the weights of the tile before last: used up
-    if (i >= 2 && !wait(&sh.o_full[b], i / 2 - 1)) return;
-    tc_fence_after();
-    const uint32_t ka = ring + buf * S::BUF;
-#pragma unroll
-    for (int ks = 0; ks < DP / 16; ++ks)
-      mma_issue<1>(tmem + b * TILE, sdesc_sw128(qs + ks / 4 * 16384 + ks % 4 * 32),
-                   sdesc_sw128(ka + ks / 4 * S::PANEL + ks % 4 * 32), kS, ks > 0);
-    mma_commit(smem_u32(&sh.s_full[b]));
-    mma_commit(smem_u32(&sh.empty[buf]));
-    ++n;
+  auto used = [&] {  // the tile at buf
+    if (++buf == S::RING) {
+      buf = 0;
+      ++turn;
+    }
   };
   while (ok && walk.next(A, at)) {
     const uint32_t tiles = at.t1 - at.t0;
-    if (!wait(&sh.q_full, parts++)) break;
+    if (!wait(smem_u32(&sh.q_full), parts++)) break;
     // t: S of tile t, then O with the weights of the one before
     for (uint32_t t = 0; ok && t <= tiles; ++t) {
-      if (t < tiles) issue_s(q + t);
-      if (t == 0 || !ok) continue;
-      const uint32_t i = q + t - 1, b = i & 1;
-      const int buf = static_cast<int>(n % S::RING);
-      if (!wait(&sh.p_full[b], i / 2) || !wait(&sh.full[buf], n / S::RING)) break;
-      tc_fence_after();
-      const uint32_t va = ring + buf * S::BUF;
+      if (t < tiles) {
+        const uint32_t i = q + t, b = i & 1;
+        // this S holds the weights of the tile before last: used up
+        if (i >= 2 && !wait(o_full + 8 * b, i / 2 - 1)) break;
+        if (!wait(full + 8 * buf, turn)) break;
+        tc_fence_after();
+        const uint64_t k = kd + (buf * S::BUF >> 4);
+        if (tc_elect()) {
 #pragma unroll
-      for (int ks = 0; ks < TILE / 16; ++ks)
-        tc_mma_ts(tmem + S::O, tmem + b * TILE + 8 * ks, tc_desc_tokens(va + ks * 2048, S::PANEL),
-                  kO, t > 1 || ks > 0);
-      mma_commit(smem_u32(&sh.o_full[b]));
-      mma_commit(smem_u32(&sh.empty[buf]));
-      ++n;
+          for (int ks = 0; ks < DP / 16; ++ks)
+            mma_issue<1>(tmem + b * TILE, qd + (ks / 4 * 16384 + ks % 4 * 32 >> 4),
+                         k + (ks / 4 * S::PANEL + ks % 4 * 32 >> 4), kS, ks > 0);
+          mma_commit(s_full + 8 * b);
+          mma_commit(empty + 8 * buf);
+        }
+        __syncwarp();
+        used();
+      }
+      if (t == 0) continue;
+      const uint32_t i = q + t - 1, b = i & 1;
+      if (!wait(full + 8 * buf, turn) || !wait(p_full + 8 * b, i / 2)) break;
+      tc_fence_after();
+      const uint64_t v = vd + (buf * S::BUF >> 4);
+      if (tc_elect()) {
+#pragma unroll
+        for (int ks = 0; ks < TILE / 16; ++ks)
+          tc_mma_ts(tmem + S::O, tmem + b * TILE + 8 * ks, v + (ks * 2048 >> 4), kO,
+                    t > 1 || ks > 0);
+        mma_commit(o_full + 8 * b);
+        mma_commit(empty + 8 * buf);
+      }
+      __syncwarp();
+      used();
     }
     q += tiles;
   }
   if (!ok) {
     atomicExch(&sh.abort, 1);
     // nothing of this CTA's may be under way when its memory goes
-    mma_commit(smem_u32(&sh.drain));
+    if (tc_elect()) mma_commit(smem_u32(&sh.drain));
+    __syncwarp();
     int never = 0;
     mbar_wait(smem_u32(&sh.drain), 0, kTreeWaitNs, &never);
   }
@@ -865,7 +891,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<DP>::CTAS)
     else tc_load_role<KV, DP>(A, sh, ring, lane);
   } else if (warp >= kReadyWarp) {
     tc_ready_role<KV, DP>(A, sh, ring, warp - kReadyWarp, lane);
-  } else if (lane == 0) {
+  } else {
     tc_mma_role<KV, DP>(A, sh, qs, ring);
   }
   __syncwarp();
