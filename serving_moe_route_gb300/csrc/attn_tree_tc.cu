@@ -36,8 +36,8 @@
 namespace moe {
 
 constexpr uint64_t kTreeWaitNs = 2000000000ull;
-constexpr int kLoadWarp = 4, kMmaWarp = 5, kReadyWarp = 6, kReadyWarps = 2;
-static_assert(kTcThreads == 32 * (kReadyWarp + kReadyWarps), "warps of a CTA");
+constexpr int kLoadWarp = 4, kMmaWarp = 5, kReadyWarp = 6;  // and one more
+static_assert(kTcThreads == 32 * (kReadyWarp + 2), "warps of a CTA");
 
 template <int KV, int DP>
 struct TcShape {
@@ -49,6 +49,8 @@ struct TcShape {
   static constexpr int TMEM = DP == 256 ? 512 : 256;  // columns
   static constexpr int O = TMEM / 2;               // first of O's; S: from 0 and TILE on
   static constexpr int ES = kv_esize(KV);
+  // warps that make ready: e4m3 tiles are work for two; else one of them loads values
+  static constexpr int READY = KV == MOE_KV_E4M3 ? 2 : 1;
   static constexpr int CPR = DP * ES / 16;         // 16-byte chunks of a cached row
   static constexpr float LIFT = KV == MOE_KV_E4M3 ? kTreeLift : 0.0f;
   static constexpr float LAG = KV == MOE_KV_E4M3 ? 2.0f : 8.0f;
@@ -192,19 +194,20 @@ __device__ __forceinline__ bool tc_masked(const TreeArgs& A, const TreeSpan& s, 
 }
 
 // ------------------------------------------------------------ loads
-// By TMA, one warp: a box is A.box tokens of a page and 64 columns, a lane has a
-// box (or two panels of it) of each tile.  The page ids of a tile are asked for a
-// tile ahead.
+// By TMA: a box is A.box tokens of a page and 64 columns, a lane has a box (all
+// panels of it) of each tile.  The page ids of a tile are asked for a tile ahead.
+// A warp takes 0.6 us to ask for a tile of four boxes: keys and values have one each
+// where there is one to spare (keys, values: which this warp has).
 template <int KV, int DP>
 __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap* k_map,
                                             const CUtensorMap* v_map, TcShared& sh, uint32_t ring,
-                                            int lane) {
+                                            int lane, bool keys, bool values) {
   using S = TcShape<KV, DP>;
   constexpr int TILE = S::C::TILE, CH = TILE / 32;
   auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
   auto at = walk;
   bool bad_page = false, ok = true, more = walk.next(A, at);
-  uint32_t n = 0;  // tiles asked for
+  uint32_t n = 0;  // tiles of the ring so far
   int slot = 0;
   const int box_shift = 31 - __clz(A.box), boxes = TILE >> box_shift;
   const int bytes = A.box * S::LAND * S::LAND_ROW;
@@ -225,13 +228,13 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
   };
   auto ask = [&](bool kv, const Place& p, int kvh) {
     const int buf = static_cast<int>(n % S::RING);
+    const uint32_t base = ring + buf * S::BUF, bar = smem_u32(&sh.landed[buf]);
     if (n >= S::RING && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&sh.empty[buf]),
                                                            (n / S::RING - 1) & 1, kTreeWaitNs,
                                                            &sh.abort))) {
       atomicExch(&sh.abort, 1);
       return false;
     }
-    const uint32_t base = ring + buf * S::BUF, bar = smem_u32(&sh.landed[buf]);
     const int count = __popc(__ballot_sync(0xffffffffu, p.live));
     if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
     __syncwarp();
@@ -243,7 +246,6 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
                                           : (j + S::RAW) * S::PANEL + r * 128),
                 kv ? v_map : k_map, bar, j * (S::LAND_ROW / S::ES), p.row, kvh, p.page);
     }
-    ++n;
     return true;
   };
   Place next = {0, 0, false};
@@ -261,33 +263,39 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
           bad_page = true;
           now.live = false;
         }
-        // which tokens there are, 32 a word
-        const uint32_t there = __ballot_sync(0xffffffffu, now.live);
-        if (lane < CH) {
-          const int from = 32 * lane;
-          uint32_t w = 0;
-          if (A.box >= 32) {
-            w = there >> (from >> box_shift) & 1u ? ~0u : 0u;
-          } else {
-#pragma unroll
-            for (int b = 0; b < 32; b += 8)
-              if (there >> (from + b >> box_shift) & 1u) w |= 0xffu << b;
-          }
-          const int left = at.s.len - (at.s.first + t * TILE + from);
-          if (left < 32) w = left <= 0 ? 0 : w & ((1u << left) - 1);
-          sh.live[slot][lane] = w;
-        }
-        slot = (slot + 1) % kSlots;
-        __syncwarp();
         if (t + 1 < at.t1) {
           next = want(at, t + 1);
         } else {
           goes_on = walk.next(A, after);
           if (goes_on) next = want(after, after.t0);
         }
-        ok = ask(false, now, kvh);
+        if (keys) {
+          // which tokens there are, 32 a word
+          const uint32_t there = __ballot_sync(0xffffffffu, now.live);
+          if (lane < CH) {
+            const int from = 32 * lane;
+            uint32_t w = 0;
+            if (A.box >= 32) {
+              w = there >> (from >> box_shift) & 1u ? ~0u : 0u;
+            } else {
+#pragma unroll
+              for (int b = 0; b < 32; b += 8)
+                if (there >> (from + b >> box_shift) & 1u) w |= 0xffu << b;
+            }
+            const int left = at.s.len - (at.s.first + t * TILE + from);
+            if (left < 32) w = left <= 0 ? 0 : w & ((1u << left) - 1);
+            sh.live[slot][lane] = w;
+          }
+          slot = (slot + 1) % kSlots;
+          __syncwarp();
+          ok = ask(false, now, kvh);
+        }
+        ++n;
       }
-      if (ok && t > at.t0) ok = ask(true, before, kvh);
+      if (t > at.t0) {
+        if (ok && values) ok = ask(true, before, kvh);
+        ++n;
+      }
     }
     at = after;
     more = goes_on;
@@ -407,8 +415,7 @@ template <int KV, int DP>
 __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, uint32_t ring,
                                               int warp, int lane) {
   using S = TcShape<KV, DP>;
-  constexpr int TILE = S::C::TILE, TPW = TILE / kReadyWarps;  // 32: a word of live
-  static_assert(TPW == 32, "a word of tokens a warp");
+  constexpr int TILE = S::C::TILE, TPW = TILE / S::READY, WORDS = TPW / 32;
   constexpr int CPR = S::CPR, RPI = 32 / CPR;
   auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
   auto at = walk;
@@ -424,10 +431,16 @@ __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, u
     }
     const uint32_t base = ring + buf * S::BUF;
     const bool tame = kv && tc_masked<TILE>(A, at.s, at.s.first + t * TILE);
-    uint32_t wild_rows = 0;
+    uint32_t wild_rows[WORDS] = {};
     // tokens that are not there: whatever lies in their rows must not count as values
-    const uint32_t there = kv ? *reinterpret_cast<const volatile uint32_t*>(&sh.live[slot][warp]) : ~0u;
-    const bool gaps = there != ~0u;
+    uint32_t there[WORDS];
+    bool gaps = false;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      there[i] = kv ? *reinterpret_cast<const volatile uint32_t*>(&sh.live[slot][warp * WORDS + i])
+                    : ~0u;
+      gaps = gaps || there[i] != ~0u;
+    }
     const bool care = tame || gaps;
     if constexpr (KV == MOE_KV_E4M3) {
       uint4 raw[TPW / RPI];
@@ -435,65 +448,50 @@ __device__ __forceinline__ void tc_ready_role(const TreeArgs& A, TcShared& sh, u
       for (int j = 0; j < TPW / RPI; ++j)
         raw[j] = tc_lds4(base + tc_land<KV, DP>(warp * TPW + j * RPI + row0, chunk));
       __syncwarp();  // the codes lie where the warp's rows are written
-      if (!care) {
-#pragma unroll
-        for (int j = 0; j < TPW / RPI; ++j) {
-          const int r = warp * TPW + j * RPI + row0;
-          uint4 lo, hi;
-          tc_widen(raw[j].x, lo.x, lo.y);
-          tc_widen(raw[j].y, lo.z, lo.w);
-          tc_widen(raw[j].z, hi.x, hi.y);
-          tc_widen(raw[j].w, hi.z, hi.w);
-          tc_sts4(base + tc_chunk(r, 2 * chunk, S::PANEL), lo);
-          tc_sts4(base + tc_chunk(r, 2 * chunk + 1, S::PANEL), hi);
-        }
-      }
 #pragma unroll
       for (int j = 0; j < TPW / RPI; ++j) {
-        if (!care) break;
         const int r = warp * TPW + j * RPI + row0;
         uint4 lo, hi;
         tc_widen(raw[j].x, lo.x, lo.y);
         tc_widen(raw[j].y, lo.z, lo.w);
         tc_widen(raw[j].z, hi.x, hi.y);
         tc_widen(raw[j].w, hi.z, hi.w);
-        if (gaps && !(there >> (j * RPI + row0) & 1u)) lo = hi = make_uint4(0, 0, 0, 0);
-        if (tame) {
-          bool wild = false;
-          uint32_t* const w[2] = {&lo.x, &hi.x};
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[h][e] = tc_tame<0x7c00u>(w[h][e], wild);
-          if (wild) wild_rows |= 1u << (j * RPI + row0);
-        }
         tc_sts4(base + tc_chunk(r, 2 * chunk, S::PANEL), lo);
         tc_sts4(base + tc_chunk(r, 2 * chunk + 1, S::PANEL), hi);
       }
-    } else if (care) {
-#pragma unroll
-      for (int j = 0; j < TPW / RPI; ++j) {
-        const uint32_t to = base + tc_chunk(warp * TPW + j * RPI + row0, chunk, S::PANEL);
-        if (!(there >> (j * RPI + row0) & 1u)) {
+    }
+    if (care) {  // a few tiles of a unit: a short program rather than a fast one
+      constexpr int PER = KV == MOE_KV_E4M3 ? 2 : 1;  // chunks of this lane in a row
+#pragma unroll 1
+      for (int j = 0; j < TPW / RPI * PER; ++j) {
+        const int in = j / PER * RPI + row0;
+        const uint32_t to = base + tc_chunk(warp * TPW + in, chunk * PER + j % PER, S::PANEL);
+        const uint32_t bit = 1u << (in & 31);
+        if (!((WORDS > 1 && in >= 32 ? there[WORDS - 1] : there[0]) & bit)) {
           tc_sts4(to, make_uint4(0, 0, 0, 0));
           continue;
         }
         if (!tame) continue;
+        constexpr uint32_t EXP = KV == MOE_KV_E4M3 ? 0x7c00u : 0x7f80u;
         uint4 v = tc_lds4(to);
         bool wild = false;
-        v.x = tc_tame<0x7f80u>(v.x, wild);
-        v.y = tc_tame<0x7f80u>(v.y, wild);
-        v.z = tc_tame<0x7f80u>(v.z, wild);
-        v.w = tc_tame<0x7f80u>(v.w, wild);
+        v.x = tc_tame<EXP>(v.x, wild);
+        v.y = tc_tame<EXP>(v.y, wild);
+        v.z = tc_tame<EXP>(v.z, wild);
+        v.w = tc_tame<EXP>(v.w, wild);
         if (wild) {
-          wild_rows |= 1u << (j * RPI + row0);
+          if (WORDS > 1 && in >= 32) wild_rows[WORDS - 1] |= bit;
+          else wild_rows[0] |= bit;
           tc_sts4(to, v);
         }
       }
     }
     if (tame) {
-      wild_rows = __reduce_or_sync(0xffffffffu, wild_rows);
-      if (lane == 0) sh.wild[slot][warp] = wild_rows;
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        const uint32_t w = __reduce_or_sync(0xffffffffu, wild_rows[i]);
+        if (lane == 0) sh.wild[slot][warp * WORDS + i] = w;
+      }
     }
     if (kv) slot = (slot + 1) % kSlots;
     // (what TMA has written needs none)
@@ -867,7 +865,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<DP>::CTAS)
   if (tid == 0) {
     for (int i = 0; i < S::RING; ++i) {
       mbar_init(smem_u32(&sh.landed[i]), A.box ? 1 : 33);
-      mbar_init(smem_u32(&sh.full[i]), kReadyWarps);
+      mbar_init(smem_u32(&sh.full[i]), S::READY);
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -886,13 +884,15 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<DP>::CTAS)
   tc_fence_after();
   if (warp < kLoadWarp) {
     tc_softmax_role<KV, DP>(A, sh, qs, warp, lane);
-  } else if (warp == kLoadWarp) {
-    if (A.box) tc_tma_role<KV, DP>(A, &k_map, &v_map, sh, ring, lane);
-    else tc_load_role<KV, DP>(A, sh, ring, lane);
-  } else if (warp >= kReadyWarp) {
-    tc_ready_role<KV, DP>(A, sh, ring, warp - kReadyWarp, lane);
-  } else {
+  } else if (warp == kMmaWarp) {
     tc_mma_role<KV, DP>(A, sh, qs, ring);
+  } else if (warp >= kReadyWarp + 2 - S::READY) {
+    tc_ready_role<KV, DP>(A, sh, ring, warp - (kReadyWarp + 2 - S::READY), lane);
+  } else if (A.box) {
+    tc_tma_role<KV, DP>(A, &k_map, &v_map, sh, ring, lane, warp == kLoadWarp,
+                        S::READY == 2 || warp == kReadyWarp);
+  } else if (warp == kLoadWarp) {
+    tc_load_role<KV, DP>(A, sh, ring, lane);
   }
   __syncwarp();
   tc_fence_before();

@@ -13,7 +13,7 @@ struct TcCfg {
   static constexpr int ROWS = 128;
   static constexpr int TILE = 64;
   static constexpr int CTAS = DP == 256 ? 1 : 2;  // per SM
-  static constexpr int END = 4;                   // what a unit's end costs, in tiles
+  static constexpr int END = 10;                   // what a unit's end costs, in tiles
 };
 
 // bf16 and e4m3 caches; ctas of a single wave
