@@ -335,99 +335,16 @@ __device__ __forceinline__ void tree_store4(void* out, long long at, float a, fl
         make_uint2(tree_bf16x2(a, b), tree_bf16x2(c, d));
 }
 
-// R rows of a unit, joined by a warp from its parts in CTAs cta, cta + size, ...: the
-// loads of all of them, and of some parts at a time, are under way together.
-template <int KV, int DP, int ROWS, int R>
-__device__ __forceinline__ void tree_join_rows(const TreeArgs& A, const TreeSpan& s, int cta,
-                                               int size, int parts, int kvh, int r0, int r,
-                                               int rows, int lane) {
-  constexpr int VL = DP / 32;  // columns per lane
-  constexpr int AHEAD = R == 1 ? 8 : 2;
-  auto at = [&](int p, int u) {
-    return (2ll * (cta + p * size) + (p == 0 ? 0 : 1)) * ROWS + min(r + u, rows - 1);
-  };
-  float top[R], sum[R], o[R][VL];
-#pragma unroll
-  for (int u = 0; u < R; ++u) {
-    top[u] = -INFINITY;
-    for (int p = lane; p < parts; p += 32) top[u] = fmaxf(top[u], A.part_ml[at(p, u)].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], off));
-    sum[u] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VL; ++j) o[u][j] = 0.0f;
-  }
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    float f[R], fl[R];
-#pragma unroll
-    for (int u = 0; u < R; ++u) {
-      const float2 ml =
-          p0 + lane < parts ? A.part_ml[at(p0 + lane, u)] : make_float2(-INFINITY, 0.0f);
-      f[u] = top[u] == -INFINITY ? 1.0f : tree_ex2(ml.x - top[u]);
-      fl[u] = f[u] * ml.y;
-    }
-    const int n = min(32, parts - p0);
-    for (int p = 0; p < n; p += AHEAD) {
-      float v[AHEAD][R][VL];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-          const float* const x = A.part_o + at(p0 + min(p + i, n - 1), u) * DP + lane * VL;
-          if constexpr (VL >= 4) {
-#pragma unroll
-            for (int j = 0; j < VL; j += 4)
-              *reinterpret_cast<float4*>(v[i][u] + j) = *reinterpret_cast<const float4*>(x + j);
-          } else {
-            *reinterpret_cast<float2*>(v[i][u]) = *reinterpret_cast<const float2*>(x);
-          }
-        }
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        if (p + i >= n) break;
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-          const float g = __shfl_sync(0xffffffffu, f[u], p + i);
-          sum[u] += __shfl_sync(0xffffffffu, fl[u], p + i);
-#pragma unroll
-          for (int j = 0; j < VL; ++j) o[u][j] += g * v[i][u][j];
-        }
-      }
-    }
-  }
-  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
-#pragma unroll
-  for (int u = 0; u < R; ++u) {
-    if (r + u >= rows) break;
-    const float inv = top[u] == -INFINITY ? 0.0f : mul / sum[u];
-    const int place = r0 + r + u, node = place / A.group, h = kvh * A.group + place - node * A.group;
-    const long long row = s.row0 + node, to = row * A.o_n + h * A.o_h;
-#pragma unroll
-    for (int j = 0; j < VL; ++j) o[u][j] *= inv;
-    if constexpr (VL >= 4) {
-#pragma unroll
-      for (int j = 0; j < VL; j += 4)
-        if (lane * VL + j < A.dim)
-          tree_store4<KV>(A.out, to + lane * VL + j, o[u][j], o[u][j + 1], o[u][j + 2], o[u][j + 3]);
-    } else {  // two lanes' columns together
-      const float a = __shfl_down_sync(0xffffffffu, o[u][0], 1);
-      const float b = __shfl_down_sync(0xffffffffu, o[u][1], 1);
-      if (lane % 2 == 0 && lane * VL < A.dim)
-        tree_store4<KV>(A.out, to + lane * VL, o[u][0], o[u][1], a, b);
-    }
-    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse<KV>(top[u], sum[u]);
-  }
-}
-
 // Joins the parts of the units that range borders cut.  A unit that begins in CTA
 // c and does not end there has c's first slot, then the second slots of the CTAs
-// at its place in the next groups.  The kTreeJoinBlocks blocks of each CTA that it does not end in deal its
-// rows out: four a warp where there are few parts, else one.  (One block for each
-// of those CTAs, a row a warp: 40 us more for 64 requests of 16 nodes.)
-constexpr int kTreeJoinWarps = 8, kTreeJoinBlocks = 8, kTreeFewParts = 8;
+// at its place in the next groups.  The kTreeJoinBlocks blocks of each CTA that it
+// does not end in deal its rows out, a row a warp.  kTreeAhead parts are loaded
+// along with their maxima and rescaled to the warp's reference so far, in order.
+constexpr int kTreeJoinWarps = 8, kTreeJoinBlocks = 4, kTreeAhead = 4;
 template <int KV, int DP, int ROWS>
-__global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const TreeArgs A) {
+__global__ void __launch_bounds__(32 * kTreeJoinWarps)
+    tree_join_kernel(const __grid_constant__ TreeArgs A) {
+  constexpr int VL = DP / 32;  // columns per lane
   pdl_wait();
   const int4 unit = A.info[blockIdx.x];
   const int parts = unit.z, place = unit.w & 0xffff, size = unit.w >> 16;
@@ -439,15 +356,63 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(const Tr
   const int rounds = (tree_blocks<ROWS>(A, s) + size - 1) / size;
   const int kvh = unit.y / rounds, r0 = (unit.y % rounds * size + cta % size) * ROWS;
   const int rows = min(ROWS, s.use * A.group - r0);
-  const int first = (place * kTreeJoinBlocks + blockIdx.y) * kTreeJoinWarps + warp;
-  const int warps = (parts - 1) * kTreeJoinBlocks * kTreeJoinWarps;
-  if (parts <= kTreeFewParts) {
-    constexpr int R = DP == 256 ? 2 : 4;
-    for (int r = R * first; r < rows; r += R * warps)
-      tree_join_rows<KV, DP, ROWS, R>(A, s, cta, size, parts, kvh, r0, r, rows, lane);
-  } else {
-    for (int r = first; r < rows; r += warps)
-      tree_join_rows<KV, DP, ROWS, 1>(A, s, cta, size, parts, kvh, r0, r, rows, lane);
+  const float mul = KV == MOE_KV_E4M3 ? A.v_scale[kvh] : 1.0f;
+#pragma unroll 1
+  for (int r = (place * kTreeJoinBlocks + blockIdx.y) * kTreeJoinWarps + warp; r < rows;
+       r += (parts - 1) * kTreeJoinBlocks * kTreeJoinWarps) {
+    float top = -INFINITY, sum = 0.0f, o[VL] = {};
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += kTreeAhead) {
+      float2 ml[kTreeAhead];
+      float v[kTreeAhead][VL], t = top;
+#pragma unroll
+      for (int i = 0; i < kTreeAhead; ++i) {
+        const int p = min(p0 + i, parts - 1);
+        const long long at = (2ll * (cta + p * size) + (p == 0 ? 0 : 1)) * ROWS + r;
+        ml[i] = A.part_ml[at];
+        const float* const x = A.part_o + at * DP + lane * VL;
+        if constexpr (VL >= 4) {
+#pragma unroll
+          for (int j = 0; j < VL; j += 4)
+            *reinterpret_cast<float4*>(v[i] + j) = *reinterpret_cast<const float4*>(x + j);
+        } else {
+          *reinterpret_cast<float2*>(v[i]) = *reinterpret_cast<const float2*>(x);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTreeAhead; ++i) t = fmaxf(t, ml[i].x);
+      const float g = t == -INFINITY ? 1.0f : tree_ex2(top - t);
+      top = t;
+      sum *= g;
+#pragma unroll
+      for (int j = 0; j < VL; ++j) o[j] *= g;
+#pragma unroll
+      for (int i = 0; i < kTreeAhead; ++i) {
+        if (p0 + i >= parts) break;
+        const float f = t == -INFINITY ? 1.0f : tree_ex2(ml[i].x - t);
+        sum += f * ml[i].y;
+#pragma unroll
+        for (int j = 0; j < VL; ++j) o[j] += f * v[i][j];
+      }
+    }
+    const float inv = top == -INFINITY ? 0.0f : mul / sum;
+    const int place_in = r0 + r, node = place_in / A.group;
+    const int h = kvh * A.group + place_in - node * A.group;
+    const long long row = s.row0 + node, to = row * A.o_n + h * A.o_h;
+#pragma unroll
+    for (int j = 0; j < VL; ++j) o[j] *= inv;
+    if constexpr (VL >= 4) {
+#pragma unroll
+      for (int j = 0; j < VL; j += 4)
+        if (lane * VL + j < A.dim)
+          tree_store4<KV>(A.out, to + lane * VL + j, o[j], o[j + 1], o[j + 2], o[j + 3]);
+    } else {  // two lanes' columns together
+      const float a = __shfl_down_sync(0xffffffffu, o[0], 1);
+      const float b = __shfl_down_sync(0xffffffffu, o[1], 1);
+      if (lane % 2 == 0 && lane * VL < A.dim)
+        tree_store4<KV>(A.out, to + lane * VL, o[0], o[1], a, b);
+    }
+    if (A.lse && lane == 0) A.lse[row * A.Hq + h] = tree_lse<KV>(top, sum);
   }
 }
 

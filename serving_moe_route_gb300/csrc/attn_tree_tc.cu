@@ -846,13 +846,17 @@ out:
 
 template <int KV, int DP>
 __global__ void __launch_bounds__(kTcThreads, TcCfg<DP>::CTAS)
-    tree_tc_kernel(const TreeArgs A, const __grid_constant__ CUtensorMap k_map,
+    tree_tc_kernel(const __grid_constant__ TreeArgs A, const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map) {
   using S = TcShape<KV, DP>;
   extern __shared__ __align__(1024) uint8_t tc_smem[];
   const uint32_t qs = smem_u32(tc_smem), ring = qs + S::QBLOCK;
   TcShared& sh = *reinterpret_cast<TcShared*>(tc_smem + S::QBLOCK + S::RING * S::BUF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0 && A.box) {
+    prefetch_tmap(&k_map);
+    prefetch_tmap(&v_map);
+  }
   pdl_wait();
   if (qs & 1023) {  // (a CTA's shared memory begins at a multiple of that)
     if (tid == 0 && A.err) atomicOr(A.err, MOE_DEVERR_TIMEOUT);
