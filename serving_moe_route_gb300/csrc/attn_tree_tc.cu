@@ -146,6 +146,32 @@ __device__ __forceinline__ uint32_t tc_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// two f32 operations an instruction
+__device__ __forceinline__ uint64_t tc_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 tc_unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t tc_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t tc_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float tc_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // four e4m3 codes as two pairs of f16: exact
 __device__ __forceinline__ void tc_widen(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
@@ -708,9 +734,13 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       }
       float x[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
 #pragma unroll
-      for (int j = 2; j < 32; ++j) {
-        x[j & 1] = fmaxf(x[j & 1], v[0][j]);
-        x[2 + (j & 1)] = fmaxf(x[2 + (j & 1)], v[1][j]);
+      for (int j = 2; j < 32; j += 4) {
+        x[0] = tc_max3(x[0], v[0][j], v[0][j + 1]);
+        x[2] = tc_max3(x[2], v[1][j], v[1][j + 1]);
+        if (j + 2 < 32) {
+          x[1] = tc_max3(x[1], v[0][j + 2], v[0][j + 3]);
+          x[3] = tc_max3(x[3], v[1][j + 2], v[1][j + 3]);
+        }
       }
       float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       top = top == -INFINITY ? top : top * f;
@@ -725,20 +755,23 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       // from here on the row has tokens, if only of logits -inf: m says so
       if (any) m = fmaxf(m, -FLT_MAX);
       const float ref = m == -INFINITY ? 0.0f : m;
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const uint64_t f2 = tc_pack(f, f), ref2 = tc_pack(-ref, -ref);
+      uint64_t part[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t p[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float a = tree_ex2(fmaf(v[c][2 * j], f, -ref));
-          const float e = tree_ex2(fmaf(v[c][2 * j + 1], f, -ref));
-          part[j & 3] += a + e;
-          p[j] = KV == MOE_KV_E4M3 ? tc_f16x2(a, e) : tree_bf16x2(a, e);
+          float2 w = tc_unpack(tc_fma2(tc_pack(v[c][2 * j], v[c][2 * j + 1]), f2, ref2));
+          w.x = tree_ex2(w.x);
+          w.y = tree_ex2(w.y);
+          part[j & 1] = tc_add2(part[j & 1], tc_pack(w.x, w.y));
+          p[j] = KV == MOE_KV_E4M3 ? tc_f16x2(w.x, w.y) : tree_bf16x2(w.x, w.y);
         }
         tc_st16(t_s + 16 * c, p);
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      const float2 added = tc_unpack(tc_add2(part[0], part[1]));
+      sum += added.x + added.y;
       if (i > 0 && __any_sync(0xffffffffu, grow)) {
         if (!wait_o(q - 1)) goto out;
         tc_fence_after();
