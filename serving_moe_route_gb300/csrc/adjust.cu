@@ -1,17 +1,17 @@
 // adjust.cu -- penalties for repeated tokens, biases and allowed tokens applied
 // to logits before a token is drawn (moe_adjust_logits).
 //
-// One pass over the logits: each is read once and written once.  What a token's
-// logit needs to know of the request's history is a word in shared memory, bit
-// 31: it occurs, below: how often in the answer.  A row's words are spread over
-// the CTAs of a cluster, each of which holds a slice of the vocabulary; they deal
-// the history out among themselves, so that it is read once a row, and add to
-// the words of whichever CTA holds the token.  Counts are whole numbers: the
-// order of additions does not show.
+// One pass over the logits: each is read once and written once.  A CTA has a slice
+// of a row.  What a token's logit needs to know of the request's history is a word
+// in shared memory, bit 31: it occurs, below: how often in the answer; every CTA
+// of a row reads the history for itself and counts the tokens of its slice, while
+// its logits are on their way.  (The CTAs of a row as a cluster that deals the
+// history out and counts in each other's memory: 205 us for 512 rows of 131072,
+// f32; a text's frequent tokens make remote additions queue up.)  Counts are
+// whole numbers: the order of additions does not show.
 //
-// Bound by the logits' bytes for large batches (512 rows of 131072, f32: 202 us,
-// 2.7 TB/s), by the cluster's two barriers and the chain from lengths to tokens
-// to counts for few rows.
+// Bound by the logits' bytes for large batches, by the chain from lengths to
+// tokens to counts for few rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,8 +26,8 @@
 
 namespace moe {
 
-constexpr int kAdjustThreads = 512;
-constexpr int kAdjustCtas = 8;  // of a cluster: every GPU of this kind takes 8
+constexpr int kAdjustThreads = 256;
+constexpr int kAdjustSlice = 8192;  // tokens of a CTA at most
 
 struct AdjustArgs {
   const char* x;
@@ -70,9 +70,10 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 
 // PAST: a history with penalties; BIAS: a list of biases
 template <typename T, bool PAST, bool BIAS>
-__global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs A) {
+__global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustArgs A) {
   extern __shared__ uint4 adjust_smem[];
   constexpr int VE = 16 / sizeof(T);
+  constexpr int U = kAdjustSlice / kAdjustThreads / VE;  // vectors of a thread
   pdl_wait();
   const int tid = threadIdx.x;
   const int row = blockIdx.y, lo = blockIdx.x * A.slice;
@@ -86,6 +87,15 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
   uint16_t* const listed = reinterpret_cast<uint16_t*>(
                                reinterpret_cast<uint32_t*>(adjust_smem) + (PAST ? A.slice + VE : 0)) +
                            skew;
+  // the logits are asked for before anything else: they arrive while the history
+  // is counted
+  const int head = min(n, (VE - skew) % VE), vecs = (n - head) / VE, tail = head + vecs * VE;
+  uint4 raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = u * kAdjustThreads + tid;
+    if (i < vecs) raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + head + i * VE));
+  }
   int req = A.rows ? A.rows[row] : row;
   if (req < 0 || req >= A.R) {
     if (A.err && blockIdx.x == 0 && tid == 0) atomicOr(A.err, MOE_DEVERR_BAD_ID);
@@ -96,8 +106,8 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
     const int w16 = ((PAST ? A.slice + VE : 0) * 4 + (BIAS ? A.slice + VE : 0) * 2 + 15) / 16;
     for (int i = tid; i < w16; i += kAdjustThreads) adjust_smem[i] = make_uint4(0, 0, 0, 0);
   }
+  if constexpr (PAST || BIAS) __syncthreads();
   if constexpr (PAST) {
-    cluster_sync();
     if (req >= 0) {
       if (A.repetition) rep = A.repetition[req];
       if (A.presence) pres = A.presence[req];
@@ -105,32 +115,33 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
       const int len = max(0, min(A.history_lens[req], A.max_history));
       const int prompt = A.prompt_lens ? A.prompt_lens[req] : 0;
       const int* const h = A.history + req * A.history_stride;
-      const uint32_t mine = smem_u32(words);  // in all CTAs: slices are multiples of a vector
-      for (long long i = static_cast<long long>(blockIdx.x) * kAdjustThreads + tid; i < len;
-           i += static_cast<long long>(gridDim.x) * kAdjustThreads) {
-        const int t = __ldg(h + i);
-        if (t < 0 || t >= A.V) continue;
-        const unsigned to = static_cast<unsigned>(t) / A.slice;
-        const uint32_t at = mapa_shared(mine + (t - to * A.slice) * 4, to);
-        if (i < prompt)
-          asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(at),
-                       "r"(0x80000000u)
-                       : "memory");
-        else
-          asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(1u)
-                       : "memory");
+      constexpr int AT_ONCE = 8;
+      for (long long i0 = tid; i0 < len; i0 += AT_ONCE * kAdjustThreads) {
+        int t[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          const long long i = i0 + u * kAdjustThreads;
+          t[u] = i < len ? __ldg(h + i) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          const long long i = i0 + u * kAdjustThreads;
+          if (t[u] < lo || t[u] - lo >= n) continue;
+          if (i < prompt) atomicOr(words + (t[u] - lo), 0x80000000u);
+          else atomicAdd(words + (t[u] - lo), 1u);
+        }
       }
     }
   }
   const float* bias = nullptr;
   if constexpr (BIAS) {
-    if constexpr (!PAST) __syncthreads();
     if (req >= 0) {
       bias = A.bias + static_cast<long long>(req) * A.n_bias;
       const int* const ids = A.bias_ids + static_cast<long long>(req) * A.n_bias;
       for (int j = tid; j < A.n_bias; j += kAdjustThreads) {
-        const int t = __ldg(ids + j) - lo;
-        if (t < 0 || t >= n) continue;
+        const int id = __ldg(ids + j);
+        if (id < lo || id - lo >= n) continue;
+        const int t = id - lo;
         // the last of equal ids counts: the largest place in the list, by
         // comparing words that hold two tokens' places
         uint16_t* const at = listed + t;
@@ -146,8 +157,7 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
       }
     }
   }
-  if constexpr (PAST) cluster_sync();
-  else if constexpr (BIAS) __syncthreads();
+  if constexpr (PAST || BIAS) __syncthreads();
 
   const unsigned* const allowed = A.allowed ? A.allowed + row * A.allowed_stride : nullptr;
   auto adjust = [&](float v, uint32_t word, unsigned place, bool ok) {
@@ -168,40 +178,44 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
     const bool ok = !allowed || (__ldg(allowed + (lo + t) / 32) >> ((lo + t) & 31) & 1u);
     out[t] = from_f32<T>(adjust(v, PAST ? words[t] : 0u, BIAS ? listed[t] : 0u, ok));
   };
-  const int head = min(n, (VE - skew) % VE), vecs = (n - head) / VE, tail = head + vecs * VE;
   const bool same = reinterpret_cast<uintptr_t>(out) / sizeof(T) % VE == static_cast<unsigned>(skew);
   if (tid < head) one(tid);
   if (tail + tid < n) one(tail + tid);
-  for (int i = tid; i < vecs; i += kAdjustThreads) {
-    const int t = head + i * VE;
-    uint4 raw = *reinterpret_cast<const uint4*>(x + t);
-    T* const v = reinterpret_cast<T*>(&raw);
-    uint32_t w[VE];
-    uint16_t p[VE];
-    if constexpr (PAST) {
+  {
 #pragma unroll
-      for (int j = 0; j < VE; j += 4)
-        *reinterpret_cast<uint4*>(w + j) = *reinterpret_cast<const uint4*>(words + t + j);
-    }
-    if constexpr (BIAS) {
+    for (int u = 0; u < U; ++u) {
+      const int i = u * kAdjustThreads + tid;
+      if (i >= vecs) break;
+      const int t = head + i * VE;
+      T* const v = reinterpret_cast<T*>(raw + u);
+      uint32_t w[VE];
+      uint16_t p[VE];
+      if constexpr (PAST) {
 #pragma unroll
-      for (int j = 0; j < VE; j += 4)
-        *reinterpret_cast<uint2*>(p + j) = *reinterpret_cast<const uint2*>(listed + t + j);
-    }
-    unsigned bits = ~0u;
-    if (allowed) {  // VE tokens may lie in two words
-      const int k = (lo + t) / 32, s = (lo + t) & 31;
-      bits = __ldg(allowed + k) >> s;
-      if (s > 32 - VE) bits |= __ldg(allowed + k + 1) << (32 - s);
-    }
+        for (int j = 0; j < VE; j += 4)
+          *reinterpret_cast<uint4*>(w + j) = *reinterpret_cast<const uint4*>(words + t + j);
+      }
+      if constexpr (BIAS) {
 #pragma unroll
-    for (int j = 0; j < VE; ++j)
-      v[j] = from_f32<T>(adjust(as_f32<T>(v[j]), PAST ? w[j] : 0u, BIAS ? p[j] : 0u, bits >> j & 1u));
-    if (same) {
-      *reinterpret_cast<uint4*>(out + t) = raw;
-    } else {
+        for (int j = 0; j < VE; j += 4)
+          *reinterpret_cast<uint2*>(p + j) = *reinterpret_cast<const uint2*>(listed + t + j);
+      }
+      unsigned bits = ~0u;
+      if (allowed) {  // VE tokens may lie in two words
+        const int k = (lo + t) / 32, s = (lo + t) & 31;
+        bits = __ldg(allowed + k) >> s;
+        if (s > 32 - VE) bits |= __ldg(allowed + k + 1) << (32 - s);
+      }
 #pragma unroll
-      for (int j = 0; j < VE; ++j) out[t + j] = v[j];
+      for (int j = 0; j < VE; ++j)
+        v[j] =
+            from_f32<T>(adjust(as_f32<T>(v[j]), PAST ? w[j] : 0u, BIAS ? p[j] : 0u, bits >> j & 1u));
+      if (same) {
+        __stcs(reinterpret_cast<uint4*>(out + t), raw[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) out[t + j] = v[j];
+      }
     }
   }
 }
@@ -210,20 +224,18 @@ template <typename T, bool PAST, bool BIAS>
 static cudaError_t launch_adjust(AdjustArgs a, cudaStream_t st) {
   auto* kern = adjust_kernel<T, PAST, BIAS>;
   const int ve = 16 / sizeof(T);
-  int ctas = kAdjustCtas;
-  a.slice = ((a.V + ctas - 1) / ctas + 31) / 32 * 32;
-  if (!PAST) {  // no cluster: slices of any number
-    a.slice = a.slice < 8192 ? a.slice : 8192;
-    ctas = (a.V + a.slice - 1) / a.slice;
-  }
+  // few rows: smaller slices, until every SM has one
+  a.slice = kAdjustSlice;
+  while (a.slice > 1024 && static_cast<long long>(a.N) * ((a.V - 1) / a.slice + 1) < sm_count())
+    a.slice /= 2;
   const int smem = (PAST ? a.slice + ve : 0) * 4 + (BIAS ? a.slice + ve : 0) * 2 + 16;
   static std::atomic<uint64_t> done{0};
-  if (PAST) {
+  if (smem > 32 * 1024) {
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern),
-                                     ((1 << 18) / kAdjustCtas + ve) * (BIAS ? 6 : 4) + 16, done);
+                                     (kAdjustSlice + ve) * (BIAS ? 6 : 4) + 16, done);
     if (e != cudaSuccess) return e;
   }
-  return launch_cluster(kern, dim3(ctas, a.N), dim3(kAdjustThreads), PAST ? ctas : 1, smem, st, a);
+  return launch_chained(kern, dim3((a.V - 1) / a.slice + 1, a.N), dim3(kAdjustThreads), smem, st, a);
 }
 
 template <typename T>
