@@ -765,10 +765,12 @@ int moe_kv_trim(const int32_t* keep_lens, const int32_t* seq_lens, int B, int32_
  *   history_lens   device int32 [requests]; prompt_lens NULL: 0
  *   repetition, presence, frequency  device f32 [requests] (1, 0 and 0)
  *   bias_ids, bias device int32 and f32 [requests, n_bias]; ids outside the
- *                  vocabulary (-1 pads a list) count for nothing; n_bias <= 65535
+ *                  vocabulary (-1 pads a list) count for nothing; n_bias <=
+ *                  MOE_ADJUST_MAX_BIAS
  *   allowed        device int32 [N, >= ceil(V/32)], rows allowed_stride apart:
  *                  token v is allowed if bit v%32 of word v/32 is set
  */
+#define MOE_ADJUST_MAX_BIAS 1024
 typedef struct moe_adjust {
   int32_t requests, max_history, n_bias, reserved0;
   int64_t history_stride, allowed_stride;

@@ -28,6 +28,7 @@ namespace moe {
 
 constexpr int kAdjustThreads = 256;
 constexpr int kAdjustSlice = 8192;  // tokens of a CTA at most
+constexpr int kAdjustBias = MOE_ADJUST_MAX_BIAS;
 
 struct AdjustArgs {
   const char* x;
@@ -84,9 +85,6 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
   // are shifted so that a vector of logits has a vector of words
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % VE);
   uint32_t* const words = reinterpret_cast<uint32_t*>(adjust_smem) + skew;
-  uint16_t* const listed = reinterpret_cast<uint16_t*>(
-                               reinterpret_cast<uint32_t*>(adjust_smem) + (PAST ? A.slice + VE : 0)) +
-                           skew;
   // the logits are asked for before anything else: they arrive while the history
   // is counted
   const int head = min(n, (VE - skew) % VE), vecs = (n - head) / VE, tail = head + vecs * VE;
@@ -101,66 +99,83 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
     if (A.err && blockIdx.x == 0 && tid == 0) atomicOr(A.err, MOE_DEVERR_BAD_ID);
     req = -1;
   }
+  // the slice's words of allowed tokens and the list of biased ones go to shared
+  // memory; asked for here as well
+  __shared__ uint32_t s_allowed[kAdjustSlice / 32];
+  __shared__ int s_ids[BIAS ? kAdjustBias : 1];
+  static_assert(kAdjustSlice / 32 == kAdjustThreads, "a word a thread");
+  const unsigned* const allowed = A.allowed ? A.allowed + row * A.allowed_stride : nullptr;
+  uint32_t my_allowed = ~0u;
+  if (allowed && 32 * tid < n) my_allowed = __ldg(allowed + lo / 32 + tid);
+  constexpr int K = BIAS ? kAdjustBias / kAdjustThreads : 1;  // biases of a thread at most
+  const int n_bias = BIAS && req >= 0 ? A.n_bias : 0;
+  int id[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int j = k * kAdjustThreads + tid;
+    id[k] = -1;
+    if (j < n_bias) id[k] = __ldg(A.bias_ids + static_cast<long long>(req) * A.n_bias + j);
+  }
   float rep = 1.0f, freq = 0.0f, pres = 0.0f;
-  if constexpr (PAST || BIAS) {
-    const int w16 = ((PAST ? A.slice + VE : 0) * 4 + (BIAS ? A.slice + VE : 0) * 2 + 15) / 16;
+  constexpr int AT_ONCE = 8;  // tokens of the history that a thread asks for
+  int len = 0, prompt = 0, past[AT_ONCE];
+  const int* h = nullptr;
+  auto ask = [&](long long i0) {
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const long long i = i0 + u * kAdjustThreads;
+      past[u] = i < len ? __ldg(h + i) : -1;
+    }
+  };
+  if (PAST && req >= 0) {
+    if (A.repetition) rep = A.repetition[req];
+    if (A.presence) pres = A.presence[req];
+    if (A.frequency) freq = A.frequency[req];
+    len = max(0, min(A.history_lens[req], A.max_history));
+    prompt = A.prompt_lens ? A.prompt_lens[req] : 0;
+    h = A.history + req * A.history_stride;
+    ask(tid);
+  }
+  if constexpr (PAST) {
+    const int w16 = (A.slice + VE) / 4;
     for (int i = tid; i < w16; i += kAdjustThreads) adjust_smem[i] = make_uint4(0, 0, 0, 0);
   }
-  if constexpr (PAST || BIAS) __syncthreads();
+  s_allowed[tid] = my_allowed;
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) s_ids[k * kAdjustThreads + tid] = id[k];
+  }
+  __syncthreads();
   if constexpr (PAST) {
-    if (req >= 0) {
-      if (A.repetition) rep = A.repetition[req];
-      if (A.presence) pres = A.presence[req];
-      if (A.frequency) freq = A.frequency[req];
-      const int len = max(0, min(A.history_lens[req], A.max_history));
-      const int prompt = A.prompt_lens ? A.prompt_lens[req] : 0;
-      const int* const h = A.history + req * A.history_stride;
-      constexpr int AT_ONCE = 8;
-      for (long long i0 = tid; i0 < len; i0 += AT_ONCE * kAdjustThreads) {
-        int t[AT_ONCE];
+    for (long long i0 = tid; i0 < len; i0 += AT_ONCE * kAdjustThreads) {
+      if (i0 > tid) ask(i0);
 #pragma unroll
-        for (int u = 0; u < AT_ONCE; ++u) {
-          const long long i = i0 + u * kAdjustThreads;
-          t[u] = i < len ? __ldg(h + i) : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < AT_ONCE; ++u) {
-          const long long i = i0 + u * kAdjustThreads;
-          if (t[u] < lo || t[u] - lo >= n) continue;
-          if (i < prompt) atomicOr(words + (t[u] - lo), 0x80000000u);
-          else atomicAdd(words + (t[u] - lo), 1u);
-        }
+      for (int u = 0; u < AT_ONCE; ++u) {
+        if (past[u] < lo || past[u] - lo >= n) continue;
+        if (i0 + u * kAdjustThreads < prompt) atomicOr(words + (past[u] - lo), 0x80000000u);
+        else atomicAdd(words + (past[u] - lo), 1u);
       }
     }
   }
-  const float* bias = nullptr;
+  // a biased token of the slice: its logit and its bias, for later.  Of equal ids the
+  // last counts
+  float biased[K], more[K];
   if constexpr (BIAS) {
-    if (req >= 0) {
-      bias = A.bias + static_cast<long long>(req) * A.n_bias;
-      const int* const ids = A.bias_ids + static_cast<long long>(req) * A.n_bias;
-      for (int j = tid; j < A.n_bias; j += kAdjustThreads) {
-        const int id = __ldg(ids + j);
-        if (id < lo || id - lo >= n) continue;
-        const int t = id - lo;
-        // the last of equal ids counts: the largest place in the list, by
-        // comparing words that hold two tokens' places
-        uint16_t* const at = listed + t;
-        uint32_t* const word = reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(at) & ~3ull);
-        const int shift = (reinterpret_cast<uintptr_t>(at) & 2) * 8;
-        uint32_t seen = *reinterpret_cast<volatile uint32_t*>(word);
-        while (static_cast<int>(seen >> shift & 0xffffu) < j + 1) {
-          const uint32_t want = (seen & ~(0xffffu << shift)) | static_cast<uint32_t>(j + 1) << shift;
-          const uint32_t got = atomicCAS(word, seen, want);
-          if (got == seen) break;
-          seen = got;
-        }
-      }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int j = k * kAdjustThreads + tid;
+      if (id[k] < lo || id[k] - lo >= n) id[k] = -1;
+      if (id[k] < 0) continue;
+      for (int i = j + 1; i < n_bias; ++i)
+        if (s_ids[i] == id[k]) id[k] = -1;
+      if (id[k] < 0) continue;
+      biased[k] = as_f32<T>(x[id[k] - lo]);
+      more[k] = __ldg(A.bias + static_cast<long long>(req) * A.n_bias + j);
     }
   }
   if constexpr (PAST || BIAS) __syncthreads();
 
-  const unsigned* const allowed = A.allowed ? A.allowed + row * A.allowed_stride : nullptr;
-  auto adjust = [&](float v, uint32_t word, unsigned place, bool ok) {
+  auto adjust = [&](float v, uint32_t word, float add, bool ok) {
     if constexpr (PAST) {
       if (word) {
         v = v > 0.0f ? v / rep : v * rep;
@@ -169,14 +184,13 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
         if (c) v -= pres;
       }
     }
-    if constexpr (BIAS)
-      if (place) v += __ldg(bias + place - 1);
+    if constexpr (BIAS) v += add;
     return ok ? v : -INFINITY;
   };
   auto one = [&](int t) {
     const float v = as_f32<T>(x[t]);
-    const bool ok = !allowed || (__ldg(allowed + (lo + t) / 32) >> ((lo + t) & 31) & 1u);
-    out[t] = from_f32<T>(adjust(v, PAST ? words[t] : 0u, BIAS ? listed[t] : 0u, ok));
+    const bool ok = s_allowed[t / 32] >> (t & 31) & 1u;
+    out[t] = from_f32<T>(adjust(v, PAST ? words[t] : 0u, 0.0f, ok));
   };
   const bool same = reinterpret_cast<uintptr_t>(out) / sizeof(T) % VE == static_cast<unsigned>(skew);
   if (tid < head) one(tid);
@@ -188,34 +202,50 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
       if (i >= vecs) break;
       const int t = head + i * VE;
       T* const v = reinterpret_cast<T*>(raw + u);
-      uint32_t w[VE];
-      uint16_t p[VE];
-      if constexpr (PAST) {
+      constexpr unsigned ALL = (1u << VE) - 1;
+      auto bits_of = [&](const uint32_t* map) {  // VE tokens may lie in two words
+        const int k = t / 32, s = t & 31;
+        unsigned bits = map[k] >> s;
+        if (s > 32 - VE) bits |= map[k + 1] << (32 - s);
+        return bits & ALL;
+      };
+      const unsigned ok = allowed ? bits_of(s_allowed) : ALL;
+      uint4 w[VE / 4];
+      uint32_t touched = 0;
 #pragma unroll
-        for (int j = 0; j < VE; j += 4)
-          *reinterpret_cast<uint4*>(w + j) = *reinterpret_cast<const uint4*>(words + t + j);
+      for (int j = 0; j < VE / 4; ++j) {
+        w[j] = make_uint4(0, 0, 0, 0);
+        if constexpr (PAST) w[j] = *reinterpret_cast<const uint4*>(words + t + 4 * j);
+        touched |= w[j].x | w[j].y | w[j].z | w[j].w;
       }
-      if constexpr (BIAS) {
+      if (touched) {  // few are
 #pragma unroll
-        for (int j = 0; j < VE; j += 4)
-          *reinterpret_cast<uint2*>(p + j) = *reinterpret_cast<const uint2*>(listed + t + j);
-      }
-      unsigned bits = ~0u;
-      if (allowed) {  // VE tokens may lie in two words
-        const int k = (lo + t) / 32, s = (lo + t) & 31;
-        bits = __ldg(allowed + k) >> s;
-        if (s > 32 - VE) bits |= __ldg(allowed + k + 1) << (32 - s);
-      }
+        for (int j = 0; j < VE; ++j) {
+          const uint4 a = w[j / 4];
+          const uint32_t word = j % 4 == 0 ? a.x : j % 4 == 1 ? a.y : j % 4 == 2 ? a.z : a.w;
+          v[j] = from_f32<T>(adjust(as_f32<T>(v[j]), word, 0.0f, ok >> j & 1u));
+        }
+      } else if (ok != ALL) {
 #pragma unroll
-      for (int j = 0; j < VE; ++j)
-        v[j] =
-            from_f32<T>(adjust(as_f32<T>(v[j]), PAST ? w[j] : 0u, BIAS ? p[j] : 0u, bits >> j & 1u));
+        for (int j = 0; j < VE; ++j)
+          if (!(ok >> j & 1u)) v[j] = from_f32<T>(-INFINITY);
+      }
       if (same) {
         __stcs(reinterpret_cast<uint4*>(out + t), raw[u]);
       } else {
 #pragma unroll
         for (int j = 0; j < VE; ++j) out[t + j] = v[j];
       }
+    }
+  }
+  if constexpr (BIAS) {  // the biased ones once more
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (id[k] < 0) continue;
+      const int t = id[k] - lo;
+      const bool ok = s_allowed[t / 32] >> (t & 31) & 1u;
+      out[t] = from_f32<T>(adjust(biased[k], PAST ? words[t] : 0u, more[k], ok));
     }
   }
 }
@@ -228,11 +258,11 @@ static cudaError_t launch_adjust(AdjustArgs a, cudaStream_t st) {
   a.slice = kAdjustSlice;
   while (a.slice > 1024 && static_cast<long long>(a.N) * ((a.V - 1) / a.slice + 1) < sm_count())
     a.slice /= 2;
-  const int smem = (PAST ? a.slice + ve : 0) * 4 + (BIAS ? a.slice + ve : 0) * 2 + 16;
+  const int smem = PAST ? (a.slice + ve) * 4 : 0;
   static std::atomic<uint64_t> done{0};
-  if (smem > 32 * 1024) {
+  if (smem > 0) {
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern),
-                                     (kAdjustSlice + ve) * (BIAS ? 6 : 4) + 16, done);
+                                     (kAdjustSlice + ve) * 4, done);
     if (e != cudaSuccess) return e;
   }
   return launch_chained(kern, dim3((a.V - 1) / a.slice + 1, a.N), dim3(kAdjustThreads), smem, st, a);
@@ -254,7 +284,7 @@ extern "C" int moe_adjust_logits(const moe_adjust_t* s, const void* logits, int 
                                  uint32_t* err, void* stream) {
   if (!s || N < 0 || N > 65535 || V < 1 || V > (1 << 18) || row_stride < 0 ||
       (logits_dtype != MOE_LOGITS_F32 && logits_dtype != MOE_LOGITS_BF16) || s->requests < 0 ||
-      s->max_history < 0 || s->n_bias < 0 || s->n_bias > 65535 || s->history_stride < 0 ||
+      s->max_history < 0 || s->n_bias < 0 || s->n_bias > MOE_ADJUST_MAX_BIAS || s->history_stride < 0 ||
       s->allowed_stride < 0)
     return MOE_ERR_INVALID_ARG;
   if (!s->rows && s->requests < N) return MOE_ERR_INVALID_ARG;

@@ -171,7 +171,7 @@ def adjust(settings=(), **kw):
     (dict(out=FAKE, out_stride=200), BAD), (dict(out=FAKE - 4), BAD),
     (dict(settings=dict(requests=-1)), BAD), (dict(settings=dict(requests=1)), BAD),
     (dict(settings=dict(max_history=-1)), BAD), (dict(settings=dict(n_bias=-1)), BAD),
-    (dict(settings=dict(n_bias=65536)), BAD), (dict(settings=dict(history_lens=0)), BAD),
+    (dict(settings=dict(n_bias=1025)), BAD), (dict(settings=dict(history_lens=0)), BAD),
     (dict(settings=dict(bias=0)), BAD), (dict(settings=dict(bias_ids=0)), BAD),
     (dict(settings=dict(history_stride=-1)), BAD), (dict(settings=dict(allowed_stride=-1)), BAD),
     (dict(N=0, x=0, out=0), OK)])
