@@ -741,7 +741,7 @@ int moe_kv_copy_pages(const moe_kv_cache_t* cache, const int32_t* src_pages,
  * An entry outside the pool becomes -1; one other than -1 sets
  * MOE_DEVERR_BAD_PAGE.  Pages that do not fit free_capacity are dropped with
  * MOE_DEVERR_NO_SPACE.
- * Errors: MOE_ERR_INVALID_ARG (also B * max_pages >= 2^31 - 1024), MOE_ERR_CUDA.
+ * Errors: MOE_ERR_INVALID_ARG (also B * max_pages >= 2^31 - 8193), MOE_ERR_CUDA.
  */
 int moe_kv_trim(const int32_t* keep_lens, const int32_t* seq_lens, int B, int32_t* block_table,
                 int max_pages, long long table_stride, int32_t* free_pages, int free_capacity,

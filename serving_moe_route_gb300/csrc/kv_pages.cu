@@ -125,44 +125,64 @@ __global__ void __launch_bounds__(kPageThreads) kv_trim_kernel(const TrimArgs A)
   }
   __syncthreads();
   // this CTA's entries
-  const int each = (entries - 1) / ctas + 1;
-  const int lo = min(static_cast<long long>(entries), static_cast<long long>(each) * blockIdx.x);
-  const int hi = min(static_cast<long long>(entries), static_cast<long long>(lo) + each);
+  const int share = (entries - 1) / ctas + 1;
+  const int lo = min(static_cast<long long>(entries), static_cast<long long>(share) * blockIdx.x);
+  const int hi = min(static_cast<long long>(entries), static_cast<long long>(lo) + share);
   auto entry = [&](int e) {
     const int r = row_of(base, A.B, e);
     return A.table + r * A.table_stride + pages_of(A.keep[r], A.page, A.max_pages) + (e - base[r]);
   };
   auto inside = [&](int pg) { return pg >= 0 && pg < A.num_pages; };
-  if (A.refs) {
-    for (int e = lo + tid; e < hi; e += kPageThreads) {
-      const int pg = *entry(e);
-      if (inside(pg)) atomicSub(A.refs + pg, 1);
-    }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
-    for (int e = lo + tid; e < hi; e += kPageThreads) {
-      const int pg = *entry(e);
-      if (inside(pg) && __ldcg(A.refs + pg) < 0) atomicMin(A.refs + pg, INT_MIN + e);
-    }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
+  // a thread's first entries are looked up once; any others in each pass
+  constexpr int HOLD = 4;
+  int* held[HOLD];
+  int pages[HOLD];
+#pragma unroll
+  for (int k = 0; k < HOLD; ++k) {
+    const int e = lo + k * kPageThreads + tid;
+    held[k] = e < hi ? entry(e) : nullptr;
+    pages[k] = e < hi ? *held[k] : -1;
   }
-  auto frees = [&](int pg, int e) {
-    return inside(pg) && (!A.refs || __ldcg(A.refs + pg) == INT_MIN + e);
+  auto each = [&](auto f) {  // f(entry, its page)
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k)
+      if (inside(pages[k])) f(lo + k * kPageThreads + tid, pages[k]);
+    for (int e = lo + HOLD * kPageThreads + tid; e < hi; e += kPageThreads) {
+      const int pg = *entry(e);
+      if (inside(pg)) f(e, pg);
+    }
   };
-  int mine = 0;
-  for (int e = lo + tid; e < hi; e += kPageThreads) mine += frees(*entry(e), e);
+  auto all_done = [&] {
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+  };
+  if (A.refs) {
+    each([&](int, int pg) { atomicSub(A.refs + pg, 1); });
+    all_done();
+    each([&](int e, int pg) {
+      if (__ldcg(A.refs + pg) < 0) atomicMin(A.refs + pg, INT_MIN + e);
+    });
+    all_done();
+  }
+  auto frees = [&](int e, int pg) { return !A.refs || __ldcg(A.refs + pg) == INT_MIN + e; };
+  int mine = 0, mask = 0;  // of the held entries: which free their page
+  each([&](int e, int pg) {
+    const bool out = frees(e, pg);
+    mine += out;
+    const int k = (e - lo) / kPageThreads;
+    if (out && k < HOLD) mask |= 1 << k;
+  });
   int count, total;
   scan1(mine, sums, count);
   long long at = old + static_cast<long long>(over_cluster(count, inbox, ctas, total));
-  for (int e0 = lo; e0 < hi; e0 += kPageThreads) {
-    const int e = e0 + tid;
+  for (int k = 0; lo + k * kPageThreads < hi; ++k) {
+    const int e = lo + k * kPageThreads + tid;
     int pg = -1;
     bool out = false;
     if (e < hi) {
       int* const w = entry(e);
       pg = *w;
-      out = frees(pg, e);
+      out = k < HOLD ? mask >> k & 1 : inside(pg) && frees(e, pg);
       *w = -1;
       if (pg != -1 && !inside(pg)) bad |= MOE_DEVERR_BAD_PAGE;
     }
@@ -476,7 +496,7 @@ int moe_kv_trim(const int32_t* keep_lens, const int32_t* seq_lens, int B, int32_
                 void* stream) {
   if (!table_ok(B, max_pages, table_stride) || free_capacity < 0 || num_pages < 1 || page_size < 1 ||
       static_cast<long long>(num_pages) * page_size > INT_MAX ||
-      static_cast<long long>(B) * max_pages >= INT_MAX - kPageThreads)
+      static_cast<long long>(B) * max_pages >= INT_MAX - 8 * kPageThreads)
     return MOE_ERR_INVALID_ARG;
   if (B == 0) return MOE_OK;
   if (!keep_lens || !seq_lens || !block_table || !n_free || (free_capacity > 0 && !free_pages))
