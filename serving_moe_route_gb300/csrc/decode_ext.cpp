@@ -261,10 +261,13 @@ PyObject* entry(Py_ssize_t n, Py_ssize_t want, F f) {
   return nullptr;
 }
 
-// n elements of a buffer, from `at` on, as a tensor of its own
-Tensor cut(const Tensor& buffer, int64_t at, int64_t n) {
-  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()),
-                                                      buffer.key_set(), buffer.dtype());
+// n elements of a buffer, from `at` on, as a tensor of its own (of that type, the
+// buffer's by default; `at` counts elements of it)
+Tensor cut(const Tensor& buffer, int64_t at, int64_t n,
+           at::ScalarType type = at::ScalarType::Undefined) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(buffer.storage()), buffer.key_set(),
+      type == at::ScalarType::Undefined ? buffer.dtype() : c10::scalarTypeToTypeMeta(type));
   t.unsafeGetTensorImpl()->set_storage_offset(at);
   t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
   return t;
@@ -515,7 +518,10 @@ PyObject* tree_masks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     vec(lens, at::kInt, B, "seq_lens", dev);
     const long long max_new = nodes_of(a[3], "max_new");
     if (B == 0 && N > 0) refuse("rows of no requests: starts holds one number");
-    const Tensor masks = at_.make({N, (max_new + 63) / 64}, at::kLong), pos = at_.make({N}, at::kInt);
+    const int64_t words = (max_new + 63) / 64;
+    const Tensor all = at_.make({N * (2 * words + 1)}, at::kInt);
+    const Tensor masks = cut(all, 0, N * words, at::kLong), pos = cut(all, 2 * N * words, N);
+    masks.unsafeGetTensorImpl()->set_sizes_contiguous({N, words});
     check(moe_tree_masks(i32(parents), static_cast<int>(N), i32(starts), i32(lens),
                          static_cast<int>(B), static_cast<int>(max_new),
                          static_cast<int64_t*>(masks.data_ptr()), i32(pos), error_word(a[4], dev),
