@@ -1,0 +1,108 @@
+"""The example's speculative loop on the GPU: the calls on drafted tokens, shared
+pages and adjusted logits together, against the same model computed densely in 64
+bits (no cache, no pages, one token after the other)."""
+import importlib.util
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import serving_moe_route_gb300 as moe
+from test_gpu_decode_loop import _dense_logits
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PROMPTS = [[1, 2, 3, 1, 2, 3, 1], list(range(10, 31)), [7], [100, 200], [5] * 12, [9, 8, 9, 8, 9]]
+
+
+@pytest.fixture(scope="module")
+def loop():
+    spec = importlib.util.spec_from_file_location(
+        "speculative_loop", os.path.join(ROOT, "examples", "speculative_loop.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def _follows(model, prompt, answer, repetition=None, banned=()):
+    """Every token of a greedy answer is the best there is, as far as the kernels'
+    products of TF32 operands can tell (the decode loop's bound)."""
+    logits = _dense_logits(model, prompt + answer)[len(prompt) - 1:-1]
+    for i, (row, token) in enumerate(zip(logits, answer)):
+        near = 0.02 * np.abs(row).max()
+        if repetition:
+            for t in set(prompt + answer[:i]):
+                row[t] = row[t] / repetition if row[t] > 0 else row[t] * repetition
+        row[list(banned)] = -np.inf
+        assert row[token] >= row.max() - near
+
+
+@pytest.mark.parametrize("max_new,page,width", [(1, 5, 1), (8, 5, 2), (16, 16, 3)])
+def test_greedy_tokens_follow_the_dense_model(loop, max_new, page, width):
+    model = loop.TreeDecoder(dtype=moe.F32, num_pages=60, page_size=page)
+    answers, left, steps = loop.generate(model, PROMPTS, 9, batch=3, max_new=max_new, width=width,
+                                         max_pages=16, temperature=0.0)
+    assert left == model.num_pages               # every page came back
+    for p, (a,) in zip(PROMPTS, answers):
+        assert len(a) == 9
+        _follows(model, p, a)
+
+
+def test_drafts_are_accepted_where_the_text_repeats(loop):
+    # a model that repeats itself: its greedy text is the best draft, fed as a prompt
+    model = loop.TreeDecoder(dtype=moe.F32, num_pages=60, page_size=5)
+    prompt = [3, 4]
+    (plain,), _, slow = loop.generate(model, [prompt], 20, max_new=1, max_pages=16, temperature=0.0)
+    (fast,), _, steps = loop.generate(model, [prompt], 20, max_new=8, max_pages=16, temperature=0.0)
+    _follows(model, prompt, plain[0])
+    _follows(model, prompt, fast[0])
+    assert slow == len(prompt) + 19 and steps <= slow
+
+
+def test_answers_fork_from_one_prompt(loop):
+    # greedily all are the same one; the pages that they share come back
+    model = loop.TreeDecoder(dtype=moe.F32, num_pages=80, page_size=5)
+    answers, left, _ = loop.generate(model, PROMPTS, 7, samples=3, batch=6, max_new=8, max_pages=16,
+                                     temperature=0.0)
+    assert left == model.num_pages
+    for p, three in zip(PROMPTS, answers):
+        for a in three:
+            _follows(model, p, a)
+
+
+def test_penalties_and_banned_tokens(loop):
+    # one node a request: a drafted token's own ancestors are not in its history
+    model = loop.TreeDecoder(dtype=moe.F32, num_pages=60, page_size=5)
+    banned = (31, 32, 999)
+    answers, left, _ = loop.generate(model, PROMPTS, 8, batch=4, max_new=1, max_pages=16,
+                                     temperature=0.0, repetition=1.5, banned=banned)
+    for p, (a,) in zip(PROMPTS, answers):
+        _follows(model, p, a, repetition=1.5, banned=banned)
+
+
+@pytest.mark.parametrize("kv", [torch.bfloat16, torch.float8_e4m3fn])
+def test_sampling_runs_and_repeats(loop, kv):
+    model = loop.TreeDecoder(kv_dtype=kv, num_pages=60)
+    kw = dict(samples=2, batch=4, temperature=0.7, top_k=5, top_p=0.9, repetition=1.1, banned=(4,))
+    answers, left, _ = loop.generate(model, PROMPTS, 8, **kw)
+    again, _, _ = loop.generate(model, PROMPTS, 8, **kw)
+    assert left == model.num_pages and answers == again
+    assert all(len(a) == 8 and all(0 <= t < model.V and t != 4 for t in a)
+               for two in answers for a in two)
+
+
+def test_a_pool_that_runs_out_is_reported(loop):
+    model = loop.TreeDecoder(num_pages=1)
+    with pytest.raises(moe.MoeError):
+        loop.generate(model, [[1] * 20], 4, batch=1, temperature=0.0)
+
+
+def test_trees_and_drafts_on_the_host(loop):
+    assert loop.draft([1, 2, 3, 1, 2], 2, 3) == [[3, 1, 2]]
+    assert loop.draft([5], 3, 3) == []
+    tokens, parents = loop.tree_of(9, [[1, 2], [1, 3], [4]], 5)
+    assert tokens == [9, 1, 2, 3, 4] and parents == [-1, 0, 1, 1, 0]
+    assert loop.tree_of(9, [[1, 2, 3]], 2) == ([9, 1], [-1, 0])
+    with pytest.raises(ValueError, match="empty"):
+        loop.generate(None, [[]], 3)
