@@ -288,9 +288,13 @@ __device__ __forceinline__ uint32_t tree_bits(const TreeSpan& s, const TreeMask&
 // first context token that its node attends
 __device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, const TreeMask& t) {
   if (A.window <= 0) return 0;
+  const int lim = min(s.n, s.len - s.ctx);
   int c = 0;
 #pragma unroll
-  for (int j = 0; j < MOE_TREE_MAX; j += 32) c += __popc(tree_bits(s, t, j));
+  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
+    const int k = lim - 64 * w;
+    c += __popcll(k <= 0 ? 0 : k >= 64 ? t.m[w] : t.m[w] & ((1ull << k) - 1));
+  }
   return max(0, s.ctx - max(0, A.window - c));
 }
 // which of the 32 tokens from pos on its node attends (by its mask and window alone)
@@ -338,13 +342,14 @@ __device__ __forceinline__ void tree_store4(void* out, long long at, float a, fl
 // Joins the parts of the units that range borders cut.  A unit that begins in CTA
 // c and does not end there has c's first slot, then the second slots of the CTAs
 // at its place in the next groups.  The kTreeJoinBlocks blocks of each CTA that it
-// does not end in deal its rows out, a row a warp.  kTreeAhead parts are loaded
+// does not end in deal its rows out, a row a warp.  A few parts at a time are loaded
 // along with their maxima and rescaled to the warp's reference so far, in order.
-constexpr int kTreeJoinWarps = 8, kTreeJoinBlocks = 4, kTreeAhead = 4;
+constexpr int kTreeJoinWarps = 8, kTreeJoinBlocks = 4;
 template <int KV, int DP, int ROWS>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps)
     tree_join_kernel(const __grid_constant__ TreeArgs A) {
   constexpr int VL = DP / 32;  // columns per lane
+  constexpr int kTreeAhead = 4;
   pdl_wait();
   const int4 unit = A.info[blockIdx.x];
   const int parts = unit.z, place = unit.w & 0xffff, size = unit.w >> 16;
@@ -367,7 +372,9 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps)
       float v[kTreeAhead][VL], t = top;
 #pragma unroll
       for (int i = 0; i < kTreeAhead; ++i) {
-        const int p = min(p0 + i, parts - 1);
+        const int p = p0 + i;
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        if (p >= parts) break;
         const long long at = (2ll * (cta + p * size) + (p == 0 ? 0 : 1)) * ROWS + r;
         ml[i] = A.part_ml[at];
         const float* const x = A.part_o + at * DP + lane * VL;
@@ -380,7 +387,8 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps)
         }
       }
 #pragma unroll
-      for (int i = 0; i < kTreeAhead; ++i) t = fmaxf(t, ml[i].x);
+      for (int i = 0; i < kTreeAhead; ++i)
+        if (p0 + i < parts) t = fmaxf(t, ml[i].x);
       const float g = t == -INFINITY ? 1.0f : tree_ex2(top - t);
       top = t;
       sum *= g;
