@@ -638,11 +638,13 @@ int moe_tree_accept(const int32_t* tokens, const int32_t* draws, const int32_t* 
  *   starts     device int32 [B+1]
  *   max_new    rows of a request at most: those past it are left out, with
  *              MOE_DEVERR_NO_SPACE
- *   ws         moe_attn_tree_workspace(...) bytes, 256-byte aligned
+ *   ws         moe_attn_tree_workspace(...) bytes, 256-byte aligned; calls that
+ *              may overlap (on two streams, in two graphs) need one each
  * A row that attends nothing gets out 0 and lse -inf.  What a row does not
  * attend has no part in its result, whatever its bits.  NaN and infinities that
  * it attends, bad pages, lengths past max_pages and the order of sums are as for
- * moe_attn_decode, but that in an E4M3 cache too an infinite logit may leave NaN.
+ * moe_attn_decode.  A wait inside the kernel that runs out (after 2 s; it never
+ * should) ends the call with MOE_DEVERR_TIMEOUT and no valid output.
  * Requires 1 <= max_new <= MOE_TREE_MAX, N * Hq < 2^31.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
  * MOE_ERR_CUDA.

@@ -62,8 +62,8 @@ struct TcShape {
   static constexpr int LAND_ROW = KV == MOE_KV_E4M3 && DP == 64 ? 64 : 128;  // bytes of a row
   static constexpr uint32_t FMT = KV == MOE_KV_E4M3 ? 0 : 1;  // f16, bf16
 };
-// a logit's factor is not 0, so that -inf stays -inf
-constexpr float kTcLeast = 1e-37f;
+// a logit's factor is not 0, so that a masked one's -inf stays that
+constexpr float kTcLeast = 1.4e-45f;
 constexpr int kSlots = 8;  // tiles whose live and non-finite tokens are kept
 
 // What lies behind the tiles in shared memory
@@ -700,7 +700,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       fence_proxy_async_shared();
       mbar_arrive(smem_u32(&sh.q_full));
     }
-    const float f = fmaxf(fabsf(sl) * mul, kTcLeast);  // of logits, in base 2
+    const float f0 = fabsf(sl) * mul, f = f0 < kTcLeast ? kTcLeast : f0;  // of logits, in base 2
     const int low = tree_low(A, s, mask);
     const uint32_t tiles = at.t1 - at.t0;
     float m = -INFINITY, sum = 0.0f;
@@ -892,6 +892,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<DP>::CTAS)
   }
   pdl_wait();
   if (qs & 1023) {  // (a CTA's shared memory begins at a multiple of that)
+    if (tid == 0) A.info[blockIdx.x] = make_int4(0, 0, 0, 0);
     if (tid == 0 && A.err) atomicOr(A.err, MOE_DEVERR_TIMEOUT);
     return;
   }

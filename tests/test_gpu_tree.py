@@ -402,3 +402,76 @@ def test_two_streams_two_graphs_and_one_call_are_the_same():
             graphs[i][0].replay()
             torch.cuda.synchronize()
             assert all(torch.equal(x, y) for x, y in zip(graphs[i][1], want[i]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_of_an_8_bit_cache_that_are_odd(D):
+    # negative ones turn logits and values round, 0 makes weights alike, NaN is NaN
+    c = _case(17, [100, 3], [9, 2], 4, 2, D, 16, "e4m3")
+    for k, v in ((-0.03, 0.02), (0.0, -0.5), (1e-42, 1.0)):
+        c["sc"] = dict(k_scale=torch.tensor([0.02, k], device=DEV),
+                       v_scale=torch.tensor([0.03, v], device=DEV))
+        _check(c, *_attend(c))
+    c["sc"]["k_scale"][1] = float("nan")
+    out, lse = _attend(c)
+    assert out[:, 2:].isnan().all() and out[:, :2].isfinite().all()
+    c["sc"] = dict(k_scale=torch.tensor([0.02, 0.02], device=DEV),
+                   v_scale=torch.tensor([0.03, float("nan")], device=DEV))
+    out, lse = _attend(c)
+    assert out[:, 2:].isnan().all() and out[:, :2].isfinite().all() and lse.isfinite().all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "f32"])
+def test_a_scale_of_zero(kv):
+    c = _case(18, [70, 0], [5, 3], 4, 2, 64, 16, kv)
+    out, lse = _attend(c, scale=0.0)
+    _check(c, out, lse, scale=0.0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 80, 128, 192, 256])
+@pytest.mark.parametrize("page", [1, 5, 8, 24, 48, 96, 256])
+def test_pages_of_any_size(kv, D, page):
+    c = _case(page, [200, 7, 130], [20, 3, 1], 6, 2, D, page, kv, "head" if page % 2 else "token")
+    _check(c, *_attend(c))
+    _check(c, *_attend(c, window=50), window=50)
+
+
+def test_a_cache_that_overlaps_may_be_read():
+    # all kv heads on one memory: no box fits, the copies do
+    c = _case(19, [90], [6], 8, 1, 64, 16, "bf16")
+    one = _attend(c)
+    c["kc"], c["vc"] = (t.expand(-1, -1, 4, -1) for t in (c["kc"], c["vc"]))
+    four = _attend(c)
+    torch.testing.assert_close(four[0], one[0], rtol=2.0 ** -7, atol=2.0 ** -9)
+    torch.testing.assert_close(four[1], one[1], rtol=2.0 ** -20, atol=2.0 ** -19)
+
+
+def test_outputs_are_cut_off_and_out_has_a_new_version():
+    c = _case(20, [9], [3], 2, 1, 64, 16, "f32")
+    c["q"].requires_grad_(True)
+    out, lse = _attend(c)
+    assert not out.requires_grad and not lse.requires_grad
+    to = torch.empty_like(out)
+    before = to._version
+    _attend(c, out=to)
+    assert to._version > before and torch.equal(to, out)
+    with torch.inference_mode():
+        _attend(c, out=torch.empty(3, 2, 64, device=DEV))
+
+
+def test_refusals_of_the_wrapper():
+    c = _case(21, [9, 4], [3, 2], 4, 2, 64, 16, "bf16")
+
+    def call(**kw):
+        d = dict(c, **kw)
+        return moe.attn_tree(d["q"], d["kc"], d["vc"], d["table"], d["starts"], d["lens"], d["masks"],
+                             max_new=d["max_new"])
+
+    for kw, what in ((dict(max_new=0), "max_new"), (dict(max_new=257), "max_new"),
+                     (dict(masks=c["masks"].int()), "masks"), (dict(masks=c["masks"][:2]), "masks"),
+                     (dict(max_new=65), "masks"), (dict(starts=c["starts"][:0]), "starts"),
+                     (dict(lens=c["lens"][:1]), "seq_lens"), (dict(q=c["q"].float()), "q"),
+                     (dict(q=c["q"][:, :3]), "multiple"), (dict(table=c["table"][:1]), "block_table")):
+        with pytest.raises(ValueError, match=what):
+            call(**kw)
