@@ -10,8 +10,15 @@
 // f32; a text's frequent tokens make remote additions queue up.)  Counts are
 // whole numbers: the order of additions does not show.
 //
-// Bound by the logits' bytes for large batches, by the chain from lengths to
-// tokens to counts for few rows.
+// Biases are few: their tokens are adjusted once more behind the pass, from logits
+// that were set aside before it.  (A place in the list for every token of the slice
+// in shared memory: 139 us for the same rows.)
+//
+// Bound by the logits' bytes without a history (512 rows of 131072, f32: 78 us, 6.9
+// TB/s, as long as a copy takes); with histories of up to 8192 tokens, a hundred
+// biases and masks 121 us, 4.5 TB/s: the chain from lengths to tokens to counts,
+// and each CTA's own pass over the history, are longer than its loads take.  64
+// rows of 50257, bf16: 9.6 us, that chain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -26,7 +26,10 @@ __device__ __forceinline__ void tree_cp16(uint32_t dst, const void* src, bool re
 // S = Q K^T, the running softmax and O += P V on tiles in shared memory, 2 rows
 // by TILE / 16 tokens and by DP / 16 columns a thread, all in fp32: nothing is
 // split or rounded.  A value that a row does not attend is skipped, not
-// multiplied by 0.
+// multiplied by 0.  (Tensor cores would take f32 operands as pairs of tf32 terms,
+// three products each, and split them again for every block of rows.)  Bound by
+// latency for small calls, 24.5 us for 5 requests of up to 13 nodes, 3 heads on
+// each of 2 of 80, window 1000; by the fp32 units for large ones.
 template <int DP>
 __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
     tree_simt_kernel(const TreeArgs A) {

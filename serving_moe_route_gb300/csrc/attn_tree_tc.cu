@@ -26,6 +26,23 @@
 // Two CTAs an SM, so that one's products and softmax run under the other's unit
 // ends: Q's loads, the last tile's chain of steps and the output take 7 us.
 //
+// Bound by shared memory's bandwidth in long units: a tile of 64 tokens moves 96 KB
+// of operands for 128 rows of 128 (S: 48, O: 16, its own arrival 32), 750 cycles,
+// where its products take 512; measured 890.  Loads and stores to memory share that
+// path.  By the units' ends in short ones, and by latency in small calls.  Measured
+// on a GB300, 32 query heads on 4 of 128, bf16: one request of 61 nodes at 131089
+// tokens 127 us, 1030 TFLOP/s (53% of cuBLAS's rate); 64 requests of 64 nodes up to
+// 8192: 219 us, 800 TFLOP/s; of up to 16 nodes, up to 4096: 56 us, 3.1 TB/s; one of
+// 8 nodes at 700: 16 us.  e4m3, 128 requests of 8 nodes up to 8192: 135 us, 2.5 TB/s:
+// the widening moves another 32 KB a tile.
+//
+// Tried: one CTA an SM with two blocks of rows in turn (the unit ends uncovered: 85 us
+// for the batch of 16 nodes); four warps of cp.async instead of TMA, and the fence
+// between proxies by the warps that load, which then wait for all their copies (110);
+// loops over a tile's columns unrolled (406 instead of 317 for the batch of 64: the
+// program is fetched again and again); the next part's Q before the last one's output,
+// output through shared memory, one warp that walks for all: no gain.
+//
 // Every wait has a limit; a role that runs into it sets MOE_DEVERR_TIMEOUT, and
 // all leave.
 #include <cuda_fp16.h>
