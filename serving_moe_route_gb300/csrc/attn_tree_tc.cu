@@ -251,6 +251,7 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
   auto at = walk;
   bool bad_page = false, ok = true, more = walk.next(A, at);
   uint32_t n = 0;  // tiles of the ring so far
+  uint32_t asked = 0, phases = 0;  // bits by tile of the ring: this warp asked last, in which turn
   int slot = 0;
   const int box_shift = 31 - __clz(A.box), boxes = TILE >> box_shift;
   const int bytes = A.box * S::LAND * S::LAND_ROW;
@@ -281,6 +282,8 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
     const int count = __popc(__ballot_sync(0xffffffffu, p.live));
     if (lane == 0) mbar_arrive_expect_tx(bar, count * bytes);
     __syncwarp();
+    asked |= 1u << buf;
+    phases = (phases & ~(1u << buf)) | (n / S::RING & 1) << buf;
     if (p.live) {
       const int r = lane * A.box;
 #pragma unroll
@@ -332,17 +335,24 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
           slot = (slot + 1) % kSlots;
           __syncwarp();
           ok = ask(false, now, kvh);
+        } else {
+          asked &= ~(1u << n % S::RING);  // the other warp has it from here on
         }
         ++n;
       }
       if (t > at.t0) {
         if (ok && values) ok = ask(true, before, kvh);
+        if (!values) asked &= ~(1u << n % S::RING);
         ++n;
       }
     }
     at = after;
     more = goes_on;
   }
+  // nothing may be on its way to memory that the CTA gives up
+  int never = 0;
+  for (int i = 0; i < S::RING; ++i)
+    if (asked >> i & 1u) mbar_wait(smem_u32(&sh.landed[i]), phases >> i & 1, kTreeWaitNs, &never);
   if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
 }
 
