@@ -687,7 +687,9 @@ int moe_kv_compact(const moe_kv_cache_t* cache, const int32_t* path, int max_pat
  * many rows hold it beyond the first: 0 for a page of one row, or of none, so
  * moe_kv_step needs no word of it.  It starts as zeros.  A shared page must not
  * be written: moe_kv_fork gives every fork a page of its own for the tokens to
- * come.
+ * come.  A request that is trimmed back into a page that it shares can go on in
+ * another row only, as a fork of its own.  Rows that share pages give them back by
+ * moe_kv_trim; moe_kv_release does not know of page_refs.
  *
  * moe_kv_fork -- let rows of the block table go on from other rows: row
  * dst_rows[i] gets the full pages of row src_rows[i] (page_refs + 1 each) and,
@@ -704,10 +706,10 @@ int moe_kv_compact(const moe_kv_cache_t* cache, const int32_t* path, int max_pat
  *                  -1, -1, 0 for a fork that needs no copy
  * A fork is refused if a row lies outside the table (MOE_DEVERR_BAD_ID), if it
  * breaks the rules above (MOE_DEVERR_DUP_ID), if there is no free page or its
- * length does not fit max_pages (MOE_DEVERR_NO_SPACE), or if its partial page
- * lies outside the pool (MOE_DEVERR_BAD_PAGE): its row and its length stay as
- * they were and its pair is -1, -1, 0.  A shared page outside the pool becomes -1
- * in the destination, with MOE_DEVERR_BAD_PAGE.
+ * length does not fit max_pages (MOE_DEVERR_NO_SPACE), or if its partial page or
+ * the one in its place lies outside the pool (MOE_DEVERR_BAD_PAGE): its row and
+ * its length stay as they were and its pair is -1, -1, 0.  A shared page outside
+ * the pool becomes -1 in the destination, with MOE_DEVERR_BAD_PAGE.
  * Errors: MOE_ERR_INVALID_ARG (also F * max_pages >= 2^31), MOE_ERR_CUDA.
  */
 int moe_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int F, int32_t* ctx_lens, int B,
@@ -722,7 +724,8 @@ int moe_kv_fork(const int32_t* src_rows, const int32_t* dst_rows, int F, int32_t
  * page outside the cache too, with MOE_DEVERR_BAD_PAGE): the first tokens[i] of
  * the page (device int32 [n]), or all of it where tokens is NULL.  A page that is
  * written must stand in the call once, and must not be read by another pair.
- * Vectors move bit for bit; the cache's scales may be NULL.  The cache must not overlap itself (see moe_kv_append).
+ * Vectors move bit for bit; the cache's scales may be NULL.  The cache must not
+ * overlap itself (see moe_kv_append).
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
  */
 int moe_kv_copy_pages(const moe_kv_cache_t* cache, const int32_t* src_pages,
@@ -790,7 +793,7 @@ typedef struct moe_adjust {
 
 /*   logits  device [N, V] (MOE_LOGITS_*), rows row_stride elements apart
  *   out     the same type, rows out_stride >= V apart: the logits themselves,
- *           or memory that they do not overlap
+ *           or memory before or behind all of them
  * Requires 1 <= V <= 2^18, N <= 65535.  Errors: MOE_ERR_INVALID_ARG,
  * MOE_ERR_CUDA. */
 int moe_adjust_logits(const moe_adjust_t* settings, const void* logits, int logits_dtype, int N,

@@ -256,17 +256,23 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_kernel(const ForkArgs A)
         }
       }
     }
+    int from = -1, to = -1;
+    if (ok && part) {  // before a free page is dealt to it, which would be lost
+      from = A.table[s * A.table_stride + full];
+      if (from < 0 || from >= A.num_pages) {
+        bad |= MOE_DEVERR_BAD_PAGE;
+        ok = false;
+      }
+    }
     int all;
     const int rank = taken + scan1(ok && part, sums, all);
     taken += all;
-    int from = -1, to = -1;
     if (ok && part) {
       if (rank < n_free) to = __ldg(A.free_pages + (n_free - 1 - rank));
-      from = A.table[s * A.table_stride + full];
       if (rank >= n_free) {
         bad |= MOE_DEVERR_NO_SPACE;
         ok = false;
-      } else if (to < 0 || to >= A.num_pages || from < 0 || from >= A.num_pages) {
+      } else if (to < 0 || to >= A.num_pages) {
         bad |= MOE_DEVERR_BAD_PAGE;
         ok = false;
       }

@@ -40,7 +40,9 @@ node 0 follows the context, packed by request like any new tokens::
 
 Requests may share pages: ``kv_fork`` lets rows go on from another one's pages,
 ``kv_copy_pages`` copies the partial ones, and ``kv_trim`` with the same
-``page_refs`` gives a page back when its last holder does.
+``page_refs`` gives a page back when its last holder does (``kv_release`` does not
+look at them).  A request that was trimmed back into a page that it shares goes on
+in another row, as a fork of its own: its next token would be written to that page.
 
 ``err`` is an int32 tensor of one zero that collects error bits
 (``MOE_DEVERR_*``) on the device; ``check_word`` reads and clears it.  Every
@@ -273,7 +275,8 @@ def adjust_logits(logits, *, rows=None, history=None, history_lens=None, prompt_
     subtracted; ``bias[r, j]`` is added to token ``bias_ids[r, j]`` (-1 pads; of
     several for one token the last counts); tokens whose bit in ``allowed`` (int32
     [N, ceil(V / 32)], one row per row of logits) is not set become -inf.
-    ``out`` may be ``logits`` itself; by default the result is a new tensor."""
+    ``out`` may be ``logits`` itself, or lie before or behind all of them; by default
+    the result is a new tensor."""
     return _ext().adjust_logits(logits, rows, history, history_lens, prompt_lens, repetition,
                                 presence, frequency, bias_ids, bias, allowed, out, err,
                                 _handle(stream))

@@ -88,6 +88,29 @@ def test_fork_refusals():
     _fork([], [], *args)
 
 
+def test_bad_source_page_takes_no_free_page():
+    ctx, table = np.array([6, 6, 0, 0]), np.full((4, 3), -1)
+    table[0, :2], table[1, :2] = (0, 9), (1, 2)          # pages of 4, a pool of 9
+    pairs, *_, n_free, bits = _fork([0, 1], [2, 3], ctx, table, np.zeros(9, int), np.array([7, 8]), 2,
+                                    4, 9)
+    assert bits == R.BAD_PAGE and n_free == 1
+    np.testing.assert_array_equal(pairs, [(-1, -1, 0), (2, 8, 2)])
+
+
+def test_row_cut_inside_a_shared_page_goes_on_as_a_fork():
+    ctx, table = np.array([10, 0, 0]), np.full((3, 3), -1)
+    table[0] = 0, 1, 2                                   # pages of 4, a pool of 6
+    lst = np.array([3, 4, 5, -1, -1, -1])
+    _, ctx, table, refs, n_free, _ = _fork([0], [1], ctx, table, np.zeros(6, int), lst, 3, 4, 6)
+    keep = np.array([10, 6, 0])                          # page 1 is shared: row 1 may not go on in it
+    table, lst, n_free, refs, _ = _trim(keep, ctx, table, lst, n_free, 4, 6, refs)
+    pairs, ctx, table, refs, n_free, bits = _fork([1], [2], keep, table, refs, lst, n_free, 4, 6)
+    assert bits == 0 and pairs[0][0] == 1 and pairs[0][2] == 2
+    table, lst, n_free, refs, _ = _trim(np.array([10, 0, 6]), ctx, table, lst, n_free, 4, 6, refs)
+    np.testing.assert_array_equal(refs, [1, 0, 0, 0, 0, 0])
+    np.testing.assert_array_equal(table, [[0, 1, 2], [-1, -1, -1], [0, pairs[0][1], -1]])
+
+
 @pytest.mark.parametrize("shared", [False, True])
 def test_trim_shortage_and_bad_entries(shared):
     rng = np.random.default_rng(2)

@@ -147,12 +147,16 @@ def fork(src, dst, ctx, table, refs, free, n_free, page, num_pages):
             bits |= NO_SPACE
             continue
         if part:
+            a = old_table[s, full]
+            if not 0 <= a < num_pages:  # no free page is taken for it
+                bits |= BAD_PAGE
+                continue
             left -= 1
             if left < 0:
                 bits |= NO_SPACE
                 continue
-            a, b = old_table[s, full], free[left]
-            if not (0 <= a < num_pages and 0 <= b < num_pages):
+            b = free[left]
+            if not 0 <= b < num_pages:
                 bits |= BAD_PAGE
                 continue
             table[d, full] = b
