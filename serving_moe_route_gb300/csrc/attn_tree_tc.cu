@@ -26,22 +26,28 @@
 // Two CTAs an SM, so that one's products and softmax run under the other's unit
 // ends: Q's loads, the last tile's chain of steps and the output take 7 us.
 //
-// Bound by shared memory's bandwidth in long units: a tile of 64 tokens moves 96 KB
-// of operands for 128 rows of 128 (S: 48, O: 16, its own arrival 32), 750 cycles,
-// where its products take 512; measured 890.  Loads and stores to memory share that
-// path.  By the units' ends in short ones, and by latency in small calls.  Measured
-// on a GB300, 32 query heads on 4 of 128, bf16: one request of 61 nodes at 131089
-// tokens 127 us, 1030 TFLOP/s (53% of cuBLAS's rate); 64 requests of 64 nodes up to
-// 8192: 219 us, 800 TFLOP/s; of up to 16 nodes, up to 4096: 56 us, 3.1 TB/s; one of
-// 8 nodes at 700: 16 us.  e4m3, 128 requests of 8 nodes up to 8192: 135 us, 2.5 TB/s:
-// the widening moves another 32 KB a tile.
+// Bound by the softmax's chain in long units: a warp takes 1340 cycles for a tile of
+// 64 tokens (reading S 260, maximum 360, weights 530, storing them the rest) and then
+// waits 260 for the next S, two CTAs at a time; their products take 1024 for the two,
+// shared memory 1500 (a tile moves 96 KB: S 48, O 16, its own arrival 32).  By the
+// units' ends in short ones, and by latency in small calls.  Measured on a GB300, 32
+// query heads on 4 of 128, bf16: one request of 61 nodes at 131089 tokens 128 us, 1020
+// TFLOP/s (53% of cuBLAS's rate); 64 requests of 64 nodes up to 8192: 209 to 219 us,
+// 800 to 830 TFLOP/s; of up to 16 nodes, up to 4096: 56 us, 3.1 TB/s; one of 8 nodes
+// at 700: 16 us.  e4m3, 128 requests of 8 nodes up to 8192: 135 us, 2.5 TB/s: there a
+// tile takes the softmax 2030 beside the warps that widen.
 //
 // Tried: one CTA an SM with two blocks of rows in turn (the unit ends uncovered: 85 us
 // for the batch of 16 nodes); four warps of cp.async instead of TMA, and the fence
 // between proxies by the warps that load, which then wait for all their copies (110);
 // loops over a tile's columns unrolled (406 instead of 317 for the batch of 64: the
 // program is fetched again and again); the next part's Q before the last one's output,
-// output through shared memory, one warp that walks for all: no gain.
+// output through shared memory, one warp that walks for all: no gain.  Q in tensor
+// memory with one S (128 us become 146, 209 become 234), or its half there with S tiles
+// that overlap by half (within 4% either way); weights from the last maximum while the
+// next is taken, and again where it grew (211 become 225; e4m3 136 become 158); the
+// second half of S read under the first one's maximum (233 instead of 220 for heads
+// of 64).
 //
 // Every wait has a limit; a role that runs into it sets MOE_DEVERR_TIMEOUT, and
 // all leave.
