@@ -64,7 +64,8 @@ __device__ __forceinline__ int pages_of(int tokens, int page, int width) {
 }
 
 // this CTA's value `mine` as the sum over the cluster's CTAs before it, and
-// over all of them.  `inbox`: kPageCtas words of this CTA that the others write
+// over all of them.  `inbox`: kPageCtas words of this CTA that the others write, so
+// all of the cluster must have passed a barrier before
 __device__ __forceinline__ int over_cluster(int mine, int* inbox, int ctas, int& total) {
   if (ctas == 1) {
     total = mine;
@@ -108,8 +109,9 @@ __global__ void __launch_bounds__(kPageThreads) kv_trim_kernel(const TrimArgs A)
   extern __shared__ int base[];  // [B] the first entry that a row gives back
   __shared__ int sums[33];
   __shared__ int inbox[kPageCtas];
-  pdl_wait();
   const int tid = threadIdx.x, ctas = gridDim.x;
+  if (ctas > 1) cluster_arrive();  // waited for before the first write into another CTA
+  pdl_wait();
   const int old = max(0, min(*A.n_free, A.free_cap));
   unsigned bad = 0;
   int entries = 0;
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_trim_kernel(const TrimArgs A)
     if (r < A.B) base[r] = entries + before;
     entries += all;
   }
+  if (ctas > 1) cluster_wait();
   __syncthreads();
   // this CTA's entries
   const int share = (entries - 1) / ctas + 1;

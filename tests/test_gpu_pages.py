@@ -289,3 +289,21 @@ def test_versions_and_a_captured_step():
     assert f.src_pages.tolist() == [1] and f.dst_pages.tolist() == [3] and f.tokens.tolist() == [2]
     assert int(n_free) == 2 and not refs.any() and free[:2].tolist() == [2, 3]
     assert torch.equal(kc[3, :2].view(torch.int16), kc[1, :2].view(torch.int16))
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,width,page", [(1, 1025, 1), (64, 40, 16), (600, 220, 3), (8192, 9, 2)])
+def test_trim_of_large_tables(B, width, page, shared):
+    # more entries than one CTA takes, and (600 x 220) than its threads hold
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, width * page + 1, B)
+    lens[0] = width * page
+    table, free, pool = _pool(rng, lens, page, width, 3)
+    lst = np.full(pool, -1)
+    lst[:len(free)] = free
+    refs = np.zeros(pool, int) if shared else None
+    keep = np.where(rng.random(B) < 0.3, 0, (lens * rng.random(B)).astype(int))
+    table, lst, n_free, refs, bits = _trim(keep, lens, table, lst, len(free), page, pool, refs)
+    assert bits == 0 and n_free > len(free)
+    table, lst, n_free, refs, bits = _trim(np.zeros(B, int), keep, table, lst, n_free, page, pool, refs)
+    assert bits == 0 and sorted(lst) == list(range(pool)) and n_free == pool and (table == -1).all()
