@@ -625,10 +625,12 @@ int moe_tree_accept(const int32_t* tokens, const int32_t* draws, const int32_t* 
  * moe_attn_tree -- moe_attn_decode for several new tokens per request.  Request
  * r has n = starts[r+1] - starts[r] rows and len = seq_lens[r] tokens in the
  * cache, its new ones last: ctx = max(0, len - n).  Row i attends
- *   the tokens t < ctx (window > 0: with t >= ctx - max(0, window - c), c the
- *     number of new tokens that it attends), and
  *   of the new tokens ctx + j, j < min(n, len - ctx), those whose bit j is set
- *     in its mask (masks NULL: those with j <= i, a chain).
+ *     in its mask (masks NULL: those with j <= i, a chain; window > 0: of these
+ *     the last `window`), and
+ *   the tokens t < ctx (window > 0: with t >= ctx - (window - c), c the number of
+ *     new tokens that it attends).
+ * For a path from the root that is the sliding window of moe_attn_decode.
  * Arguments as for moe_attn_decode, but for
  *   q, out     device [N, Hq, head_dim], packed by request; rows of no request
  *              are not read, and left as they are

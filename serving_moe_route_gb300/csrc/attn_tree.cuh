@@ -245,10 +245,32 @@ __device__ __forceinline__ void tree_record(const TreeArgs& A, const TreeStart& 
 }
 
 // ------------------------------------------------------------ what a row attends
-// A node's mask, in registers
+// A node's mask, in registers: the new tokens that count
 struct TreeMask {
   unsigned long long m[MOE_TREE_MAX / 64];
 };
+// of more new tokens than the window the highest, which for a path from the root are
+// the last
+__device__ __forceinline__ void tree_cut(const TreeArgs& A, const TreeSpan& s, TreeMask& t) {
+  const int lim = min(s.n, s.len - s.ctx);
+  int extra = -A.window;
+#pragma unroll
+  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
+    const int k = lim - 64 * w;
+    t.m[w] = k <= 0 ? 0 : k >= 64 ? t.m[w] : t.m[w] & ((1ull << k) - 1);
+    extra += __popcll(t.m[w]);
+  }
+#pragma unroll
+  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
+    const int c = __popcll(t.m[w]);
+    if (extra >= c) {
+      t.m[w] = 0;
+    } else {
+      for (int i = 0; i < extra; ++i) t.m[w] &= t.m[w] - 1;
+    }
+    extra -= c;
+  }
+}
 __device__ __forceinline__ TreeMask tree_mask(const TreeArgs& A, const TreeSpan& s, int i) {
   TreeMask t;
 #pragma unroll
@@ -262,6 +284,7 @@ __device__ __forceinline__ TreeMask tree_mask(const TreeArgs& A, const TreeSpan&
       t.m[w] = n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
     }
   }
+  if (A.window > 0) tree_cut(A, s, t);
   return t;
 }
 // 32 bits of it from new token j on (j may be negative), of the tokens there are
@@ -288,14 +311,10 @@ __device__ __forceinline__ uint32_t tree_bits(const TreeSpan& s, const TreeMask&
 // first context token that its node attends
 __device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, const TreeMask& t) {
   if (A.window <= 0) return 0;
-  const int lim = min(s.n, s.len - s.ctx);
   int c = 0;
 #pragma unroll
-  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
-    const int k = lim - 64 * w;
-    c += __popcll(k <= 0 ? 0 : k >= 64 ? t.m[w] : t.m[w] & ((1ull << k) - 1));
-  }
-  return max(0, s.ctx - max(0, A.window - c));
+  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) c += __popcll(t.m[w]);
+  return max(0, s.ctx - (A.window - c));
 }
 // which of the 32 tokens from pos on its node attends (by its mask and window alone)
 __device__ __forceinline__ uint32_t tree_attends(const TreeSpan& s, const TreeMask& t, int low,

@@ -200,10 +200,10 @@ def attn_tree(q, k_cache, v_cache, block_table, starts, seq_lens, masks=None, *,
     """Attention of several new tokens per request: q ``[N, Hq, head_dim]`` packed
     by request.  A row attends its request's context and the new tokens whose bits
     are set in its mask (``tree_masks``), by default those up to itself.  With a
-    ``window``, a row that attends c new tokens attends the last ``window - c`` of
-    the context.  Otherwise as ``attn_decode``: returns out, or (out, lse) with lse
-    ``[N, Hq]``; a row that attends nothing gets zeros and -inf, rows of no request
-    are left as they are.  ``workspace`` is a uint8 tensor of
+    ``window``, it attends the last ``window`` of these, and where they are fewer, c,
+    the last ``window - c`` of the context.  Otherwise as ``attn_decode``: returns out,
+    or (out, lse) with lse ``[N, Hq]``; a row that attends nothing gets zeros and -inf,
+    rows of no request are left as they are.  ``workspace`` is a uint8 tensor of
     ``attn_tree_workspace(...)`` bytes (by default one is allocated)."""
     return _ext().attn_tree(q, k_cache, v_cache, block_table, starts, seq_lens, masks, max_new,
                             scale, window, k_scale, v_scale, out, return_lse, workspace, err,

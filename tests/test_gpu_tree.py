@@ -475,3 +475,33 @@ def test_refusals_of_the_wrapper():
                      (dict(q=c["q"][:, :3]), "multiple"), (dict(table=c["table"][:1]), "block_table")):
         with pytest.raises(ValueError, match=what):
             call(**kw)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("window", [1, 4, 40, 64, 100])
+def test_a_chain_longer_than_the_window_is_decode_token_by_token(kv, window):
+    c = _case(23, [3, 0, 200, 31], [6, 40, 170, 1], 4, 2, 64, 16, kv, kind="chain")
+    starts, lens = c["starts"].tolist(), c["lens"].tolist()
+    of = [r for r in range(4) for _ in range(starts[r + 1] - starts[r])]
+    upto = [lens[r] - starts[r + 1] + i + 1 for i, r in enumerate(of)]
+    one, one_lse = moe.attn_decode(c["q"], c["kc"], c["vc"], c["table"][of], _i32(upto), window=window,
+                                   return_lse=True, **c["sc"])
+    for masks in (False, True):
+        out, lse = _attend(c, masks=masks, window=window)
+        _, _, tol, lse_tol = _bounds(c, masks=masks, window=window)
+        assert (np.abs(D64.f64(out) - D64.f64(one)) <= 2 * tol).all()
+        assert (np.abs(D64.f64(lse) - D64.f64(one_lse)) <= 2 * lse_tol).all()
+        _check(c, out, lse, masks=masks, window=window)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 3, 65, 130])
+def test_of_more_new_tokens_than_the_window_the_last_count(kv, window):
+    # masks of any bits over four words; a table that cuts the last request's nodes off
+    c = _case(24, [0, 90, 20], [250, 4, 200], 2, 1, 64, 16, kv, max_new=256)
+    c["bits"] = np.random.default_rng(2).random(c["bits"].shape) < 0.6
+    c["bits"][[3, 251]] = False
+    c["masks"] = torch.as_tensor(R.packed(c["bits"]), device=DEV)
+    _check(c, *_attend(c, window=window), window=window)
+    c["table"] = c["table"][:, :9].contiguous()
+    _check(c, *_attend(c, window=window), window=window)

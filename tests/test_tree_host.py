@@ -3,10 +3,13 @@ of them made on the host before anything is launched (no GPU here), and of their
 Python wrappers for CPU tensors."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
+import decode_reference as D64
 import serving_moe_route_gb300 as moe
+import tree_reference as R
 from serving_moe_route_gb300 import _binding as B
 from test_decode_host import BAD, BAD_CACHES, FAKE, OK, UNSUPPORTED, cache
 
@@ -218,3 +221,18 @@ def test_wrappers_refuse_cpu_tensors():
         moe.kv_trim(i, i, t, i, i[:1], page_size=4, num_pages=2)
     with pytest.raises(ValueError, match="CUDA"):
         moe.adjust_logits(torch.zeros(2, 8))
+
+
+@pytest.mark.parametrize("window", [1, 2, 4, 9, 30])
+def test_plain_form_of_a_window_is_that_of_one_token_at_a_time(window):
+    rng = np.random.default_rng(window)
+    ctx, sizes, page = [3, 0, 20], [6, 15, 2], 4
+    lens, starts = np.add(ctx, sizes), np.concatenate([[0], np.cumsum(sizes)])
+    table = rng.permutation(30).reshape(3, 10)
+    k, v, q = (rng.standard_normal(s) for s in ((30, page, 2, 8), (30, page, 2, 8), (sum(sizes), 4, 8)))
+    of = [r for r, n in enumerate(sizes) for _ in range(n)]
+    upto = [ctx[r] + i - starts[r] + 1 for i, r in enumerate(of)]
+    want = D64.attend(q, k, v, table[of], upto, 0.3, window)
+    got = R.attend(q, k, v, table, starts, lens, None, 15, 0.3, window)
+    for a, b in zip(got, want):
+        np.testing.assert_allclose(a, b, rtol=1e-12)

@@ -71,7 +71,9 @@ def attend(q, k, v, table, starts, lens, bits, max_new, scale, window=0, k_scale
         for i in range(min(n, max_new)):
             drafted = [j for j in range(min(n, length - ctx))
                        if (j <= i if bits is None else j < bits.shape[1] and bits[lo + i, j])]
-            first = max(0, ctx - max(0, window - len(drafted))) if window else 0
+            if window:  # the last of them count, and of the context what is left
+                drafted = drafted[-window:]
+            first = max(0, ctx - (window - len(drafted))) if window else 0
             pos = np.array(list(range(first, min(ctx, length))) + [ctx + j for j in drafted], int)
             pg = table[r, pos // page].astype(np.int64)
             ok = (pg >= 0) & (pg < pages)
