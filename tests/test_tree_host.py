@@ -234,5 +234,7 @@ def test_plain_form_of_a_window_is_that_of_one_token_at_a_time(window):
     upto = [ctx[r] + i - starts[r] + 1 for i, r in enumerate(of)]
     want = D64.attend(q, k, v, table[of], upto, 0.3, window)
     got = R.attend(q, k, v, table, starts, lens, None, 15, 0.3, window)
+    # either form: logits of 8 products that add up to 40 at most, so off by 8 x 40 x 2^-53;
+    # values below 5, their weights off by twice that, sums of 30: 5 (640 + 30) 2^-53
     for a, b in zip(got, want):
-        np.testing.assert_allclose(a, b, rtol=1e-12)
+        np.testing.assert_allclose(a, b, rtol=1e-12, atol=2 * 5 * 670 * 2.0 ** -53)
