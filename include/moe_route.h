@@ -645,8 +645,10 @@ int moe_tree_accept(const int32_t* tokens, const int32_t* draws, const int32_t* 
  * A row that attends nothing gets out 0 and lse -inf.  What a row does not
  * attend has no part in its result, whatever its bits.  NaN and infinities that
  * it attends, bad pages, lengths past max_pages and the order of sums are as for
- * moe_attn_decode.  A wait inside the kernel that runs out (after 2 s; it never
- * should) ends the call with MOE_DEVERR_TIMEOUT and no valid output.
+ * moe_attn_decode; pages that lie behind the window of all of a request's rows may
+ * be gone (table entries of any value).  A wait inside the kernel that runs out
+ * (after 2 s; it never should) ends the call with MOE_DEVERR_TIMEOUT and no valid
+ * output.
  * Requires 1 <= max_new <= MOE_TREE_MAX, N * Hq < 2^31.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
  * MOE_ERR_CUDA.

@@ -65,8 +65,6 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
         const int id = __ldg(A.table + at.b * A.table_stride + p);
         if (id >= 0 && id < A.num_pages)
           off = id * A.s_page + (pos - p * A.page) * A.s_token + kvh * A.s_head;
-        else
-          bad_page = true;
       }
       s_off[buf][tid] = off;
     };
@@ -98,7 +96,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
     for (int e = 0; e < 2; ++e) {
       node[e] = (r0 + min(2 * ty + e, rows - 1)) / A.group;
       mask[e] = tree_mask(A, s, node[e]);
-      low[e] = tree_low(A, s, mask[e]);
+      low[e] = tree_low(A, s, mask[e], node[e]);
     }
     __syncthreads();
     load(A.k, ks, KP, 0);
@@ -128,7 +126,11 @@ __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
         for (int j = 0; j < NK; ++j) {
           const int c = tx + 16 * j;
           const uint32_t bits = tree_attends(s, mask[e], low[e], pos0 + (c & ~31));
-          const bool on = (bits >> (c & 31) & 1u) && s_off[buf][c] >= 0;
+          bool on = bits >> (c & 31) & 1u;
+          if (on && s_off[buf][c] < 0) {
+            bad_page = true;
+            on = false;
+          }
           live |= static_cast<unsigned>(on) << j;
           x[e][j] *= f;
           if (on) top = fmaxf(top, x[e][j]);

@@ -245,32 +245,10 @@ __device__ __forceinline__ void tree_record(const TreeArgs& A, const TreeStart& 
 }
 
 // ------------------------------------------------------------ what a row attends
-// A node's mask, in registers: the new tokens that count
+// A node's mask, in registers
 struct TreeMask {
   unsigned long long m[MOE_TREE_MAX / 64];
 };
-// of more new tokens than the window the highest, which for a path from the root are
-// the last
-__device__ __forceinline__ void tree_cut(const TreeArgs& A, const TreeSpan& s, TreeMask& t) {
-  const int lim = min(s.n, s.len - s.ctx);
-  int extra = -A.window;
-#pragma unroll
-  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
-    const int k = lim - 64 * w;
-    t.m[w] = k <= 0 ? 0 : k >= 64 ? t.m[w] : t.m[w] & ((1ull << k) - 1);
-    extra += __popcll(t.m[w]);
-  }
-#pragma unroll
-  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
-    const int c = __popcll(t.m[w]);
-    if (extra >= c) {
-      t.m[w] = 0;
-    } else {
-      for (int i = 0; i < extra; ++i) t.m[w] &= t.m[w] - 1;
-    }
-    extra -= c;
-  }
-}
 __device__ __forceinline__ TreeMask tree_mask(const TreeArgs& A, const TreeSpan& s, int i) {
   TreeMask t;
 #pragma unroll
@@ -284,7 +262,6 @@ __device__ __forceinline__ TreeMask tree_mask(const TreeArgs& A, const TreeSpan&
       t.m[w] = n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
     }
   }
-  if (A.window > 0) tree_cut(A, s, t);
   return t;
 }
 // 32 bits of it from new token j on (j may be negative), of the tokens there are
@@ -308,25 +285,39 @@ __device__ __forceinline__ uint32_t tree_bits(const TreeSpan& s, const TreeMask&
   if (lim - j < 32) bits &= (1u << (lim - j)) - 1;
   return bits;
 }
-// first context token that its node attends
-__device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, const TreeMask& t) {
+// first token that node i, whose mask t is, attends: of more new tokens than the window
+// the highest count, which for a path from the root are the last
+__device__ __forceinline__ int tree_low(const TreeArgs& A, const TreeSpan& s, const TreeMask& t,
+                                        int i) {
   if (A.window <= 0) return 0;
+  const int lim = min(s.n, s.len - s.ctx);
   int c = 0;
 #pragma unroll
-  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) c += __popcll(t.m[w]);
-  return max(0, s.ctx - (A.window - c));
+  for (int w = 0; w < MOE_TREE_MAX / 64; ++w) {
+    const int k = lim - 64 * w;
+    c += __popcll(k <= 0 ? 0 : k >= 64 ? t.m[w] : t.m[w] & ((1ull << k) - 1));
+  }
+  int low = max(0, s.ctx + c - A.window);
+  if (c > A.window && A.masks) {  // (a short program: the mask is read again)
+    low = s.ctx;
+    int extra = c - A.window;
+#pragma unroll 1
+    for (int w = 0; extra > 0; ++w) {
+      unsigned long long m = __ldg(A.masks + static_cast<long long>(s.row0 + i) * A.words + w);
+#pragma unroll 1
+      for (; extra > 0 && m; --extra, m &= m - 1)
+        low = s.ctx + 64 * w + __ffsll(static_cast<long long>(m));
+    }
+  }
+  return low;
 }
 // which of the 32 tokens from pos on its node attends (by its mask and window alone)
 __device__ __forceinline__ uint32_t tree_attends(const TreeSpan& s, const TreeMask& t, int low,
                                                  int pos) {
-  uint32_t bits = 0;
   const int end = min(s.ctx, s.len);
-  if (pos < end && pos + 32 > low) {
-    bits = ~0u;
-    if (end - pos < 32) bits &= (1u << (end - pos)) - 1;
-    if (low > pos) bits &= ~0u << (low - pos);
-  }
-  return bits | tree_bits(s, t, pos - s.ctx);
+  uint32_t bits = pos >= end ? 0 : end - pos < 32 ? (1u << (end - pos)) - 1 : ~0u;
+  bits |= tree_bits(s, t, pos - s.ctx);
+  return low <= pos ? bits : low - pos < 32 ? bits & (~0u << (low - pos)) : 0;
 }
 
 __device__ __forceinline__ float tree_ex2(float x) {

@@ -255,7 +255,7 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
   constexpr int TILE = S::C::TILE, CH = TILE / 32;
   auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
   auto at = walk;
-  bool bad_page = false, ok = true, more = walk.next(A, at);
+  bool ok = true, more = walk.next(A, at);
   uint32_t n = 0;  // tiles of the ring so far
   uint32_t asked = 0, phases = 0;  // bits by tile of the ring: this warp asked last, in which turn
   int slot = 0;
@@ -311,10 +311,7 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
       before = now;
       if (t < at.t1) {
         now = next;
-        if (now.live && (now.page < 0 || now.page >= A.num_pages)) {
-          bad_page = true;
-          now.live = false;
-        }
+        now.live = now.live && now.page >= 0 && now.page < A.num_pages;
         if (t + 1 < at.t1) {
           next = want(at, t + 1);
         } else {
@@ -359,7 +356,6 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
   int never = 0;
   for (int i = 0; i < S::RING; ++i)
     if (asked >> i & 1u) mbar_wait(smem_u32(&sh.landed[i]), phases >> i & 1, kTreeWaitNs, &never);
-  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
 }
 
 // By cp.async, for pages that no box of eight tokens or more divides.  (A warp has
@@ -372,7 +368,7 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
   constexpr int CPR = S::CPR, RPI = 32 / CPR;  // rows at a time
   auto walk = tree_walk<S::C::ROWS, TILE, S::C::END>(A, sh.start);
   auto at = walk;
-  bool bad_page = false, ok = true, more = walk.next(A, at);
+  bool ok = true, more = walk.next(A, at);
   uint32_t n = 0;  // tiles asked for
   int slot = 0;
   const int row0 = lane / CPR, chunk = lane % CPR;  // of this lane, of the first rows
@@ -441,7 +437,6 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
         for (int i = 0; i < NW; ++i) {
           const bool in = next.page[i] >= 0 && next.page[i] < A.num_pages;
           const bool live = next.row[i] >= 0 && in;
-          bad_page |= next.row[i] >= 0 && !in;
           now.off[i] = live ? next.page[i] * A.s_page + next.row[i] * A.s_token + kvh * A.s_head : 0;
           now.mask[i] = __ballot_sync(0xffffffffu, live);
           if (lane == 0) sh.live[slot][i] = now.mask[i];
@@ -462,7 +457,6 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
     more = goes_on;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if (bad_page && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
 }
 
 // What has landed is made ready for the products: e4m3 codes are widened, values
@@ -734,7 +728,7 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       mbar_arrive(smem_u32(&sh.q_full));
     }
     const float f0 = fabsf(sl) * mul, f = f0 < kTcLeast ? kTcLeast : f0;  // of logits, in base 2
-    const int low = tree_low(A, s, mask);
+    const int low = tree_low(A, s, mask, node);
     const uint32_t tiles = at.t1 - at.t0;
     float m = -INFINITY, sum = 0.0f;
     for (uint32_t i = 0; i < tiles; ++i) {
@@ -759,7 +753,11 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       if (!all) {  // logits that do not count become -inf
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          word[c] &= tree_attends(s, mask, low, pos + 32 * c);
+          const uint32_t want = tree_attends(s, mask, low, pos + 32 * c);
+          // told of here, where it is known that a row attends the token: pages that all
+          // rows have left behind may be gone
+          if ((want & ~word[c]) && A.err) atomicOr(A.err, MOE_DEVERR_BAD_PAGE);
+          word[c] &= want;
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[c][j] = word[c] >> j & 1u ? v[c][j] : -INFINITY;
         }

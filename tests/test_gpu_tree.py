@@ -505,3 +505,48 @@ def test_of_more_new_tokens_than_the_window_the_last_count(kv, window):
     _check(c, *_attend(c, window=window), window=window)
     c["table"] = c["table"][:, :9].contiguous()
     _check(c, *_attend(c, window=window), window=window)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("page", [1, 4, 8, 16, 64])
+@pytest.mark.parametrize("window", [1, 30, 64, 200])
+def test_pages_behind_the_window_may_be_gone(kv, page, window):
+    # a server gives pages back once every token to come has left them behind
+    c = _case(25, [500, 130, 700, 9], [5, 20, 1, 3], 4, 2, 64, page, kv)
+    lens, starts = c["lens"].tolist(), c["starts"].tolist()
+    first = [max(0, lens[r] - starts[r + 1] + starts[r] + 1 - window) for r in range(4)]
+    whole = _attend(c, window=window)
+    gone = c["table"].clone()
+    for r in range(4):
+        gone[r, :first[r] // page] = torch.tensor([-1, c["kc"].shape[0], -9], device=DEV).repeat(
+            gone.shape[1])[:first[r] // page]
+    err = _word()
+    cut = _attend(dict(c, table=gone), window=window, err=err)
+    assert moe.check_word(err) == (0, 0)
+    assert torch.equal(cut[0], whole[0]) and torch.equal(cut[1], whole[1])
+    one = _attend(dict(c, table=gone), masks=False, window=window, err=err)
+    assert moe.check_word(err) == (0, 0) and one[0].isfinite().all()
+    for r in range(4):                                   # the page of the first token is needed
+        less = gone.clone()
+        less[r, first[r] // page] = -1
+        _attend(dict(c, table=less), window=window, err=err)
+        assert moe.check_word(err) == (-5, R.BAD_PAGE)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [1, 8])
+def test_what_lies_behind_the_window_goes_by_the_rows_masks(kv, page):
+    # the row with the fewest new tokens reaches farthest back
+    window, ctx = 16, 64
+    for least in (0, 1, 3):
+        c = _case(26, [ctx], [7], 2, 1, 64, page, kv)
+        c["bits"][:] = False
+        for i, n in enumerate([3, 4, 5, least, 6, 3, 4]):
+            c["bits"][i, :n] = True
+        c["masks"] = torch.as_tensor(R.packed(c["bits"]), device=DEV)
+        first, err = ctx - window + least, _word()
+        for at, bits in ((first // page, R.BAD_PAGE), (first // page - 1, 0)):
+            gone = c["table"].clone()
+            gone[0, :at + 1] = -1
+            _attend(dict(c, table=gone), window=window, err=err)
+            assert moe.check_word(err)[1] == bits
