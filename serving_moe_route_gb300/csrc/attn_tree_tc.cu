@@ -786,7 +786,9 @@ __device__ __forceinline__ void tc_softmax_role(const TreeArgs& A, TcShared& sh,
       // from here on the row has tokens, if only of logits -inf: m says so
       if (any) m = fmaxf(m, -FLT_MAX);
       const float ref = m == -INFINITY ? 0.0f : m;
-      const uint64_t f2 = tc_pack(f, f), ref2 = tc_pack(-ref, -ref);
+      // (nothing attended: -inf stays that, whatever the scale, a NaN of e4m3 among them)
+      const float by = KV == MOE_KV_E4M3 && !any ? 1.0f : f;
+      const uint64_t f2 = tc_pack(by, by), ref2 = tc_pack(-ref, -ref);
       uint64_t part[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {

@@ -550,3 +550,23 @@ def test_what_lies_behind_the_window_goes_by_the_rows_masks(kv, page):
             gone[0, :at + 1] = -1
             _attend(dict(c, table=gone), window=window, err=err)
             assert moe.check_word(err)[1] == bits
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_row_that_attends_nothing_under_a_nan_scale(D):
+    c = _case(27, [0, 0, 40], [200, 3, 5], 4, 2, D, 16, "e4m3", max_new=256)
+    rng = np.random.default_rng(3)
+    c["bits"] = rng.random(c["bits"].shape) < 0.2
+    none = [0, 7, 64, 130, 199, 201]
+    c["bits"][none] = False
+    c["masks"] = torch.as_tensor(R.packed(c["bits"]), device=DEV)
+    starts = c["starts"].tolist()
+    few = [i for r, ctx in enumerate((0, 0, 40)) for i in range(starts[r], starts[r + 1])
+           if ctx == 0 and not c["bits"][i, :starts[r + 1] - starts[r]].any()]
+    assert set(none) <= set(few)
+    c["sc"]["k_scale"][1] = float("nan")
+    out, lse = _attend(c)
+    assert (out[few] == 0).all() and (lse[few] == -float("inf")).all()
+    some = torch.ones(len(out), dtype=torch.bool, device=DEV)
+    some[few] = False
+    assert out[some][:, 2:].isnan().all() and out[:, :2].isfinite().all()
