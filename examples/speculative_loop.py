@@ -73,11 +73,12 @@ def tree_of(root, branches, limit):
 
 
 def generate(model, prompts, new_tokens, *, samples=1, batch=4, max_new=8, max_pages=8, width=2,
-             seed=0, repetition=None, banned=(), **sampling):
+             seed=0, repetition=None, frequency=None, banned=(), **sampling):
     """`samples` answers of `new_tokens` tokens to each prompt, on `batch` rows.
-    `repetition`: a penalty for repeated tokens; `banned`: tokens that are never
-    drawn; `sampling`: numbers for temperature, top_k, top_p, min_p.  Returns the
-    answers, the free pages at the end, and how many steps were taken."""
+    `repetition`, `frequency`: penalties for repeated tokens, the prompt's among them;
+    `banned`: tokens that are never drawn; `sampling`: numbers for temperature, top_k,
+    top_p, min_p.  Returns the answers, the free pages at the end, and how many steps
+    were taken."""
     for i, p in enumerate(prompts):
         if not p:
             raise ValueError(f"prompt {i} is empty")
@@ -138,9 +139,11 @@ def generate(model, prompts, new_tokens, *, samples=1, batch=4, max_new=8, max_p
         tree = moe.tree_masks(parents, step.starts, step.seq_lens, max_new=max_new, err=err)
         logits = model.tree_logits(tokens, step, tree.masks, table, max_new, err=err)
         past = {}
-        if repetition:
-            past = dict(history=torch.tensor(history, **i32), repetition=torch.full(
-                (batch,), repetition, **f32), history_lens=torch.full((batch,), longest, **i32))
+        if repetition or frequency:   # a drafted token's ancestors are text as well
+            past = dict(history=torch.tensor(history, **i32), tokens=tokens, masks=tree.masks,
+                        starts=step.starts, history_lens=torch.full((batch,), longest, **i32))
+            past.update((name, torch.full((batch,), v, **f32)) for name, v in
+                        (("repetition", repetition), ("frequency", frequency)) if v)
         logits = moe.adjust_logits(logits, rows=row_of, allowed=allowed, out=logits, err=err, **past)
         ids, _ = moe.sample_tokens(logits, torch.rand(N, generator=rand, device="cuda"), **per_row)
         draws = torch.where(forced >= 0, forced, ids)

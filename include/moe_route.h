@@ -760,12 +760,13 @@ int moe_kv_trim(const int32_t* keep_lens, const int32_t* seq_lens, int B, int32_
 /*
  * moe_adjust_logits -- what a request asks of its logits before a token is
  * drawn.  For row i of request r (rows[i], or i), token v with logit x:
- *   1. if v occurs in r's history: x = x > 0 ? x / repetition : x * repetition
+ *   1. if v occurs in the row's text: x = x > 0 ? x / repetition : x * repetition
  *   2. x -= frequency * c, and x -= presence if c > 0, where c is how often v
- *      occurs in the history from prompt_lens[r] on
+ *      occurs in the history from prompt_lens[r] on and on the path
  *   3. x += the bias listed for v (of several for one token the last counts)
  *   4. x = -inf if v is not allowed in row i
- * computed in f32 and rounded once.  NULL leaves a part out.
+ * computed in f32 and rounded once.  NULL leaves a part out.  The text is r's
+ * history and, at a node of a tree, the drafted tokens on its path behind it.
  *   rows           device int32 [N]: the request of each row; outside
  *                  [0, requests) it is of none (only step 4 is done), with
  *                  MOE_DEVERR_BAD_ID
@@ -778,10 +779,17 @@ int moe_kv_trim(const int32_t* keep_lens, const int32_t* seq_lens, int B, int32_
  *                  MOE_ADJUST_MAX_BIAS
  *   allowed        device int32 [N, >= ceil(V/32)], rows allowed_stride apart:
  *                  token v is allowed if bit v%32 of word v/32 is set
+ *   tokens, masks, starts  device int32 [N], int64 [N, mask_words] and int32
+ *                  [requests + 1]: drafted tokens, what a row attends of them and
+ *                  where a request's rows are, as for moe_attn_tree; mask_words at
+ *                  most MOE_TREE_MAX / 64.  The tokens of the nodes that a row
+ *                  attends are part of its text, but for node 0's, which is the
+ *                  last of the history.  mask_words 0: none, and the three are not
+ *                  looked at
  */
 #define MOE_ADJUST_MAX_BIAS 1024
 typedef struct moe_adjust {
-  int32_t requests, max_history, n_bias, reserved0;
+  int32_t requests, max_history, n_bias, mask_words;
   int64_t history_stride, allowed_stride;
   const int32_t* rows;
   const int32_t* history;
@@ -793,6 +801,9 @@ typedef struct moe_adjust {
   const int32_t* bias_ids;
   const float* bias;
   const int32_t* allowed;
+  const int32_t* tokens;
+  const int64_t* masks;
+  const int32_t* starts;
 } moe_adjust_t;
 
 /*   logits  device [N, V] (MOE_LOGITS_*), rows row_stride elements apart

@@ -72,11 +72,11 @@ class MoeKvCache(ctypes.Structure):
 
 class MoeAdjust(ctypes.Structure):
     """Mirror of ``moe_adjust_t``."""
-    _fields_ = [(n, c_i32) for n in ("requests", "max_history", "n_bias", "reserved0")]
+    _fields_ = [(n, c_i32) for n in ("requests", "max_history", "n_bias", "mask_words")]
     _fields_ += [(n, c_i64) for n in ("history_stride", "allowed_stride")]
     _fields_ += [(n, c_void_p) for n in (
         "rows", "history", "history_lens", "prompt_lens", "repetition", "presence", "frequency",
-        "bias_ids", "bias", "allowed")]
+        "bias_ids", "bias", "allowed", "tokens", "masks", "starts")]
 
 
 class MoeError(RuntimeError):

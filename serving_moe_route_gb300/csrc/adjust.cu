@@ -8,7 +8,8 @@
 // its logits are on their way.  (The CTAs of a row as a cluster that deals the
 // history out and counts in each other's memory: 205 us for 512 rows of 131072,
 // f32; a text's frequent tokens make remote additions queue up.)  Counts are
-// whole numbers: the order of additions does not show.
+// whole numbers: the order of additions does not show.  At a node of a tree the
+// drafted tokens on its path count too, a node a thread.
 //
 // Biases are few: their tokens are adjusted once more behind the pass, from logits
 // that were set aside before it.  (A place in the list for every token of the slice
@@ -50,8 +51,11 @@ struct AdjustArgs {
   const float* bias;
   const unsigned* allowed;
   long long allowed_stride;  // words
+  const int* tokens;         // NULL: no drafted tokens
+  const unsigned long long* masks;
+  const int* starts;
   unsigned* err;
-  int N, V, R, max_history, n_bias;
+  int N, V, R, max_history, n_bias, mask_words;
   int slice;  // tokens of a CTA, a multiple of 32
 };
 
@@ -76,7 +80,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// PAST: a history with penalties; BIAS: a list of biases
+// PAST: a history (or drafted tokens) with penalties; BIAS: a list of biases
 template <typename T, bool PAST, bool BIAS>
 __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustArgs A) {
   extern __shared__ uint4 adjust_smem[];
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
   }
   float rep = 1.0f, freq = 0.0f, pres = 0.0f;
   constexpr int AT_ONCE = 8;  // tokens of the history that a thread asks for
-  int len = 0, prompt = 0, past[AT_ONCE];
+  int len = 0, prompt = 0, past[AT_ONCE], drafted = -1;
   const int* h = nullptr;
   auto ask = [&](long long i0) {
 #pragma unroll
@@ -138,10 +142,17 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
     if (A.repetition) rep = A.repetition[req];
     if (A.presence) pres = A.presence[req];
     if (A.frequency) freq = A.frequency[req];
-    len = max(0, min(A.history_lens[req], A.max_history));
+    if (A.max_history > 0) len = max(0, min(A.history_lens[req], A.max_history));
     prompt = A.prompt_lens ? A.prompt_lens[req] : 0;
     h = A.history + req * A.history_stride;
     ask(tid);
+    if (A.tokens && tid > 0) {  // node tid, if the row attends it
+      static_assert(MOE_TREE_MAX <= kAdjustThreads, "a node a thread");
+      const int row0 = max(0, min(A.starts[req], A.N)), end = min(A.starts[req + 1], A.N);
+      if (row >= row0 && row < end && row0 + tid < end && tid < 64 * A.mask_words &&
+          A.masks[static_cast<long long>(row) * A.mask_words + tid / 64] >> (tid % 64) & 1)
+        drafted = A.tokens[row0 + tid];
+    }
   }
   if constexpr (PAST) {
     const int w16 = (A.slice + VE) / 4;
@@ -163,6 +174,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustA
         else atomicAdd(words + (past[u] - lo), 1u);
       }
     }
+    if (drafted >= lo && drafted - lo < n) atomicAdd(words + (drafted - lo), 1u);
   }
   // a biased token of the slice: its logit and its bias, for later.  Of equal ids the
   // last counts
@@ -277,7 +289,7 @@ static cudaError_t launch_adjust(AdjustArgs a, cudaStream_t st) {
 
 template <typename T>
 static cudaError_t launch_type(const AdjustArgs& a, cudaStream_t st) {
-  const bool past = a.history && a.max_history > 0;
+  const bool past = a.max_history > 0 || a.tokens;
   if (past) return a.n_bias > 0 ? launch_adjust<T, true, true>(a, st) : launch_adjust<T, true, false>(a, st);
   return a.n_bias > 0 ? launch_adjust<T, false, true>(a, st) : launch_adjust<T, false, false>(a, st);
 }
@@ -302,6 +314,9 @@ extern "C" int moe_adjust_logits(const moe_adjust_t* s, const void* logits, int 
     return MOE_ERR_INVALID_ARG;
   if (s->history && s->max_history > 0 && !s->history_lens) return MOE_ERR_INVALID_ARG;
   if (s->n_bias > 0 && (!s->bias_ids || !s->bias)) return MOE_ERR_INVALID_ARG;
+  if (s->mask_words < 0 || s->mask_words > MOE_TREE_MAX / 64 ||
+      (s->mask_words > 0 && (!s->tokens || !s->masks || !s->starts)))
+    return MOE_ERR_INVALID_ARG;
   // the logits themselves may be the output; anything else must not overlap them
   const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), o0 = reinterpret_cast<uintptr_t>(out);
   const uintptr_t x1 = x0 + (static_cast<uintptr_t>(N - 1) * row_stride + V) * es;
@@ -329,7 +344,13 @@ extern "C" int moe_adjust_logits(const moe_adjust_t* s, const void* logits, int 
   a.N = N;
   a.V = V;
   a.R = s->requests;
-  a.max_history = s->max_history;
+  a.max_history = s->history ? s->max_history : 0;
+  if (s->mask_words > 0) {
+    a.tokens = s->tokens;
+    a.masks = reinterpret_cast<const unsigned long long*>(s->masks);
+    a.starts = s->starts;
+    a.mask_words = s->mask_words;
+  }
   a.n_bias = s->n_bias;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_dtype == MOE_LOGITS_F32 ? launch_type<float>(a, st)

@@ -767,11 +767,11 @@ void logits_of(const Tensor& x, const char* name) {
 }
 
 // (logits, rows, history, history_lens, prompt_lens, repetition, presence,
-//  frequency, bias_ids, bias, allowed, out, err, stream)
+//  frequency, bias_ids, bias, allowed, tokens, masks, starts, out, err, stream)
 PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return entry(n, 14, [&]() -> PyObject* {
+  return entry(n, 17, [&]() -> PyObject* {
     const Tensor& x = tensor(a[0], "logits");
-    const Place at_(x, "logits", a[13]);
+    const Place at_(x, "logits", a[16]);
     const int dev = at_.dev;
     logits_of(x, "logits");
     const int64_t N = x.size(0), V = x.size(1);
@@ -805,6 +805,7 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
       for (int i = 3; i < 8; ++i)
         if (a[i] != Py_None)
           refuse("history_lens, prompt_lens and penalties are only used with a history");
+      if (a[11] != Py_None) refuse("drafted tokens are only used with a history");
     }
     s.history_lens = static_cast<const int32_t*>(optional_vec(a[3], at::kInt, R, "history_lens", dev));
     s.prompt_lens = static_cast<const int32_t*>(optional_vec(a[4], at::kInt, R, "prompt_lens", dev));
@@ -835,11 +836,24 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
       s.allowed = i32(w);
       s.allowed_stride = N > 1 ? w.stride(0) : w.size(1);
     }
+    if ((a[11] == Py_None) != (a[12] == Py_None) || (a[11] == Py_None) != (a[13] == Py_None))
+      refuse("tokens, masks and starts come together");
+    if (a[11] != Py_None) {
+      const Tensor& m = tensor(a[12], "masks");
+      const int64_t words = matrix(m, at::kLong, N, "masks", dev);
+      if (words < 1 || words > MOE_TREE_MAX / 64)
+        refuse("masks must have a word for every 64 nodes, " + std::to_string(MOE_TREE_MAX / 64) +
+               " at most");
+      s.mask_words = static_cast<int32_t>(words);
+      s.masks = static_cast<const int64_t*>(m.data_ptr());
+      s.tokens = static_cast<const int32_t*>(optional_vec(a[11], at::kInt, N, "tokens", dev));
+      s.starts = static_cast<const int32_t*>(optional_vec(a[13], at::kInt, R + 1, "starts", dev));
+    }
     Tensor out;
-    if (a[11] == Py_None) {
+    if (a[14] == Py_None) {
       out = at_.make({N, V}, x.scalar_type());
     } else {
-      out = tensor(a[11], "out");
+      out = tensor(a[14], "out");
       on_device(out, "out", dev);
       logits_of(out, "out");
       if (out.scalar_type() != x.scalar_type() || out.sizes() != x.sizes())
@@ -848,13 +862,13 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(moe_adjust_logits(&s, x.data_ptr(),
                             x.scalar_type() == at::kFloat ? MOE_LOGITS_F32 : MOE_LOGITS_BF16,
                             static_cast<int>(N), static_cast<int>(V), N > 1 ? x.stride(0) : V,
-                            out.data_ptr(), N > 1 ? out.stride(0) : V, error_word(a[12], dev),
+                            out.data_ptr(), N > 1 ? out.stride(0) : V, error_word(a[15], dev),
                             at_.stream),
           "moe_adjust_logits");
-    if (a[11] == Py_None) return THPVariable_Wrap(out);
+    if (a[14] == Py_None) return THPVariable_Wrap(out);
     written(out);
-    Py_INCREF(a[11]);
-    return a[11];
+    Py_INCREF(a[14]);
+    return a[14];
   });
 }
 

@@ -30,7 +30,8 @@ node 0 follows the context, packed by request like any new tokens::
         out = attn_tree(q, k_cache, v_cache, block_table, step.starts, step.seq_lens,
                         tree.masks, max_new=M, err=err)
         ...
-    logits = adjust_logits(logits, rows=request_of_row, history=..., allowed=..., err=err)
+    logits = adjust_logits(logits, rows=request_of_row, history=..., allowed=..., tokens=tokens,
+                           masks=tree.masks, starts=step.starts, err=err)
     draws, _ = sample_tokens(logits, u, temperature=t)
     walk = tree_accept(tokens, draws, parents, step.starts, ctx_lens, max_path=M, err=err)
     for each layer:
@@ -265,7 +266,8 @@ def kv_trim(keep_lens, seq_lens, block_table, free_pages, n_free, *, page_size, 
 
 def adjust_logits(logits, *, rows=None, history=None, history_lens=None, prompt_lens=None,
                   repetition=None, presence=None, frequency=None, bias_ids=None, bias=None,
-                  allowed=None, out=None, err=None, stream=None):
+                  allowed=None, tokens=None, masks=None, starts=None, out=None, err=None,
+                  stream=None):
     """Logits [N, V] (float32 or bfloat16) with penalties, biases and a grammar's
     mask applied, before ``sample_tokens``.  Row i belongs to request ``rows[i]``
     (int32 [N]; by default i).  In this order: the logits of tokens in
@@ -275,11 +277,14 @@ def adjust_logits(logits, *, rows=None, history=None, history_lens=None, prompt_
     subtracted; ``bias[r, j]`` is added to token ``bias_ids[r, j]`` (-1 pads; of
     several for one token the last counts); tokens whose bit in ``allowed`` (int32
     [N, ceil(V / 32)], one row per row of logits) is not set become -inf.
+    At the nodes of trees the drafted tokens on a node's path count as the end of its
+    request's history: give ``tokens`` (int32 [N], as for ``tree_accept``), ``masks``
+    (``tree_masks``) and ``starts``.  Node 0's token is the last of the history.
     ``out`` may be ``logits`` itself, or lie before or behind all of them; by default
     the result is a new tensor."""
     return _ext().adjust_logits(logits, rows, history, history_lens, prompt_lens, repetition,
-                                presence, frequency, bias_ids, bias, allowed, out, err,
-                                _handle(stream))
+                                presence, frequency, bias_ids, bias, allowed, tokens, masks, starts,
+                                out, err, _handle(stream))
 
 
 def check_word(err, stream=None):

@@ -164,3 +164,94 @@ def test_a_captured_call_and_another_stream():
         out.zero_()
         g.replay()
         assert torch.equal(out, want)
+
+
+def _trees(rng, sizes, pad, V, words):
+    """Random trees' tokens (of a few words, so that paths repeat them), what their nodes
+    attend, and where requests begin."""
+    starts = np.concatenate([[0], np.cumsum(sizes)]).astype(int)
+    parents = np.concatenate([[-1] + [rng.integers(max(0, j - 3), j) for j in range(1, n)]
+                              for n in sizes if n] + [np.zeros(pad, int)]).astype(int)
+    N = sum(sizes) + pad
+    bits = R.masks(parents, starts, sizes, 64 * words, N)[0]
+    return dict(tokens=rng.integers(0, min(V, 40), N), bits=bits, starts=starts)
+
+
+def _tree_args(t):
+    return dict(tokens=_i32(t["tokens"]), starts=_i32(t["starts"]),
+                masks=torch.as_tensor(R.packed(t["bits"]), device=DEV))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes,pad,V,L,words,n_bias", [
+    ([1], 0, 5, 3, 1, 0), ([7, 0, 4], 2, 1000, 30, 1, 5), ([64, 3, 20], 0, 50257, 2000, 1, 0),
+    ([256, 1], 3, 9001, 100, 4, 9), ([100, 130], 0, 300, 10, 2, 0)])
+def test_tokens_on_a_nodes_path_are_text(dtype, sizes, pad, V, L, words, n_bias):
+    rng = np.random.default_rng(V)
+    t = _trees(rng, sizes, pad, V, words)
+    N = sum(sizes) + pad
+    s = _settings(V, N, V, R_=len(sizes), L=L, n_bias=n_bias, grammar=True)
+    s["rows"] = np.array([r for r, n in enumerate(sizes) for _ in range(n)] + [0] * pad)
+    t["tokens"][rng.random(N) < 0.05] = -1               # not a token
+    s["tokens"] = t["tokens"]
+    x = torch.randn(N, V, device=DEV).mul_(3).to(DT[dtype])
+    g = _gpu({k: v for k, v in s.items() if k != "tokens"})
+    err = _word()
+    out = moe.adjust_logits(x, err=err, **g, **_tree_args(t))
+    assert moe.check_word(err) == (0, 0)
+    _check(x, dict(s, bits=t["bits"], starts=t["starts"]), out, out.dtype)
+    # the same bits as with a history a row that ends with the path
+    longer = np.full((N, L + 64 * words), -1)
+    lens, of = np.zeros(N, int), s["rows"]
+    for i in range(N):
+        n, lo = int(s["history_lens"][of[i]]), t["starts"][of[i]]
+        path = [t["tokens"][lo + j] for j in range(1, 64 * words) if i < sum(sizes) and t["bits"][i, j]]
+        longer[i, :n] = s["history"][of[i], :n]
+        longer[i, n:n + len(path)] = path
+        lens[i] = n + len(path)
+    each = {k: v[of] for k, v in s.items() if k in ("prompt_lens", "repetition", "presence", "frequency",
+                                                   "bias_ids", "bias")}
+    # (a path is never the prompt's)
+    each["prompt_lens"] = np.minimum(each["prompt_lens"], s["history_lens"][of])
+    want = moe.adjust_logits(x, **_gpu(dict(each, history=longer, history_lens=lens,
+                                            allowed=s["allowed"])))
+    assert torch.equal(out, want)
+
+
+def test_drafted_tokens_without_a_text_before_them():
+    x = torch.zeros(3, 9, device=DEV)
+    bits = np.zeros((3, 64), bool)
+    bits[0, 0], bits[1, :2], bits[2, [0, 1, 2]] = True, True, True
+    t = dict(tokens=np.array([4, 5, 5]), bits=bits, starts=np.array([0, 3]))
+    kw = dict(rows=_i32([0, 0, 0]), history_lens=_i32([0]), frequency=_f32([2.0]), presence=_f32([0.5]))
+    for history in (torch.zeros(1, 0, dtype=torch.int32, device=DEV), _i32([[7]])):
+        out = moe.adjust_logits(x, history=history, **kw, **_tree_args(t))
+        want = torch.zeros(3, 9)
+        want[1, 5], want[2, 5] = -2.5, -4.5
+        assert torch.equal(out.cpu(), want)
+
+
+def test_starts_that_do_not_rise_add_nothing_outside():
+    # what rows get is not said, but nothing outside the arrays is looked at
+    x = torch.zeros(6, 50, device=DEV)
+    t = dict(tokens=np.zeros(6, int), bits=np.ones((6, 256), bool), starts=np.zeros(3, int))
+    for starts in ([5, 2, 9], [-4, 100, 3], [0, 4, 2 ** 31 - 1], [4, 4, 4], [3, -2 ** 31, 2 ** 31 - 1]):
+        t["starts"] = np.array(starts)
+        out = moe.adjust_logits(x, rows=_i32([0, 0, 1, 1, 0, 1]), history=_i32([[1], [1]]),
+                                history_lens=_i32([1, 1]), frequency=_f32([1.0, 1.0]), **_tree_args(t))
+        assert (out[:, 1] == -1).all() and (out[:, 2:] == 0).all()
+
+
+def test_refusals_of_drafted_tokens():
+    x = torch.zeros(3, 9, device=DEV)
+    t = _tree_args(dict(tokens=np.zeros(3, int), bits=np.ones((3, 64), bool), starts=np.array([0, 3])))
+    past = dict(rows=_i32([0, 0, 0]), history=_i32([[1]]), history_lens=_i32([1]))
+    for kw, what in ((dict(t, tokens=None), "together"), (dict(t, masks=None), "together"),
+                     (dict(t, starts=None), "together"), (dict(t, starts=_i32([0, 1, 3])), "starts"),
+                     (dict(t, tokens=_i32([0, 0])), "tokens"), (dict(t, masks=t["masks"][:2]), "masks"),
+                     (dict(t, masks=t["masks"].int()), "masks"),
+                     (dict(t, masks=t["masks"].repeat(1, 5)), "masks")):
+        with pytest.raises(ValueError, match=what):
+            moe.adjust_logits(x, **past, **kw)
+    with pytest.raises(ValueError, match="history"):
+        moe.adjust_logits(x, rows=past["rows"], **t)

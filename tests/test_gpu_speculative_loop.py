@@ -106,3 +106,37 @@ def test_trees_and_drafts_on_the_host(loop):
     assert loop.tree_of(9, [[1, 2, 3]], 2) == ([9, 1], [-1, 0])
     with pytest.raises(ValueError, match="empty"):
         loop.generate(None, [[]], 3)
+
+
+def _right_drafts(prompts, answers):
+    """Drafts that know the answers: a wrong sibling first, so that accepted nodes' keys
+    and values have to move, and then the answer's next tokens."""
+    def draft(text, width, depth):
+        for p, (a,) in zip(prompts, answers):
+            known = p + a
+            if known[:len(text)] == text and depth > 0:
+                right = known[len(text):len(text) + depth]
+                return [[(right[0] + 1) % 1000], right] if right else []
+        return []
+    return draft
+
+
+def test_tokens_on_a_nodes_path_are_penalised(loop, monkeypatch):
+    # long paths are accepted, and every token is the best after the penalties of the text
+    # before it, the step's own drafted tokens included
+    model = loop.TreeDecoder(dtype=moe.F32, num_pages=60, page_size=5)
+    prompts = [[1, 2, 3], [7], [5] * 4]
+    kw = dict(batch=3, max_pages=16, temperature=0.0, repetition=1.2, frequency=0.6)
+    plain, _, slow = loop.generate(model, prompts, 20, max_new=1, **kw)
+    monkeypatch.setattr(loop, "draft", _right_drafts(prompts, plain))
+    fast, left, steps = loop.generate(model, prompts, 20, max_new=8, **kw)
+    assert left == model.num_pages and steps < slow
+    for p, (a,) in zip(prompts, fast):
+        logits = _dense_logits(model, p + a)[len(p) - 1:-1]
+        for i, (row, token) in enumerate(zip(logits, a)):
+            near = 0.02 * np.abs(row).max()
+            text = p + a[:i]
+            for t in set(text):
+                row[t] = (row[t] / 1.2 if row[t] > 0 else row[t] * 1.2) - 0.6 * text.count(t)
+            assert row[token] >= row.max() - near
+    assert fast == plain and steps <= 1 + -(-19 // 7)

@@ -238,3 +238,30 @@ def test_plain_form_of_a_window_is_that_of_one_token_at_a_time(window):
     # values below 5, their weights off by twice that, sums of 30: 5 (640 + 30) 2^-53
     for a, b in zip(got, want):
         np.testing.assert_allclose(a, b, rtol=1e-12, atol=2 * 5 * 670 * 2.0 ** -53)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(mask_words=-1), BAD), (dict(mask_words=5), BAD), (dict(mask_words=1), BAD),
+    (dict(mask_words=1, tokens=FAKE, masks=FAKE), BAD), (dict(mask_words=4, tokens=FAKE, starts=FAKE), BAD),
+    (dict(mask_words=4, masks=FAKE, starts=FAKE), BAD)])
+def test_adjust_of_drafted_tokens(kw, code):
+    assert adjust(settings=kw) == code
+
+
+def test_where_the_struct_has_drafted_tokens(tmp_path):
+    import os
+    import subprocess
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "moe_route.h"\n'
+                   'int main(void){printf("%zu %zu %zu %zu\\n", offsetof(moe_adjust_t, mask_words),'
+                   " offsetof(moe_adjust_t, tokens), offsetof(moe_adjust_t, masks),"
+                   " offsetof(moe_adjust_t, starts)); return 0;}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    A = B.MoeAdjust
+    assert got == [A.mask_words.offset, A.tokens.offset, A.masks.offset, A.starts.offset]

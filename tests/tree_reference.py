@@ -210,9 +210,11 @@ def trim(keep, lens, table, free, n_free, page, num_pages, refs=None):
 
 
 def adjust(x, rows=None, history=None, history_lens=None, prompt_lens=None, repetition=None,
-           presence=None, frequency=None, bias_ids=None, bias=None, allowed=None):
-    """x [N, V] float64; returns what the definition gives in 64 bits, and the sum
-    of the magnitudes that were added up (for error bounds)."""
+           presence=None, frequency=None, bias_ids=None, bias=None, allowed=None, tokens=None,
+           bits=None, starts=None):
+    """x [N, V] float64, bits [N, >= nodes] truth values (``masks``); returns what the
+    definition gives in 64 bits, and the sum of the magnitudes that were added up (for
+    error bounds)."""
     x = x.copy()
     size = np.abs(x)
     N, V = x.shape
@@ -222,7 +224,11 @@ def adjust(x, rows=None, history=None, history_lens=None, prompt_lens=None, repe
         if some and 0 <= r < len(some[0]):
             if history is not None:
                 h = history[r, :min(max(0, int(history_lens[r])), history.shape[1])]
-                p = 0 if prompt_lens is None else max(0, int(prompt_lens[r]))
+                p = 0 if prompt_lens is None else min(max(0, int(prompt_lens[r])), len(h))
+                if tokens is not None and starts[r] <= i < starts[r + 1]:
+                    path = [j for j in range(1, min(starts[r + 1] - starts[r], bits.shape[1]))
+                            if bits[i, j]]
+                    h = np.concatenate([h, [tokens[starts[r] + j] for j in path]]).astype(int)
                 for t in set(int(t) for t in h if 0 <= t < V):
                     if repetition is not None:
                         x[i, t] = (x[i, t] / repetition[r] if x[i, t] > 0 else x[i, t] * repetition[r])
