@@ -140,3 +140,22 @@ def test_tokens_on_a_nodes_path_are_penalised(loop, monkeypatch):
                 row[t] = (row[t] / 1.2 if row[t] > 0 else row[t] * 1.2) - 0.6 * text.count(t)
             assert row[token] >= row.max() - near
     assert fast == plain and steps <= 1 + -(-19 // 7)
+
+
+def test_right_drafts_are_accepted_and_their_vectors_move(loop, monkeypatch):
+    model = loop.TreeDecoder(dtype=moe.F32, num_pages=60, page_size=5)
+    prompts = [[3, 4], [9]]
+    kw = dict(batch=2, max_pages=16, temperature=0.0)
+    plain, _, slow = loop.generate(model, prompts, 20, max_new=1, **kw)
+    monkeypatch.setattr(loop, "draft", _right_drafts(prompts, plain))
+    walks, accept = [], moe.tree_accept
+    monkeypatch.setattr(moe, "tree_accept", lambda *a, **k: walks.append(accept(*a, **k)) or walks[-1])
+    fast, left, steps = loop.generate(model, prompts, 20, max_new=8, **kw)
+    # seven tokens a step: the root, the wrong sibling, six of the answer, and the one drawn
+    assert slow == 21 and steps <= 1 + -(-19 // 7) and left == model.num_pages
+    moved = [int((w.path[r, :n] != torch.arange(n, device="cuda")).sum())
+             for w in walks for r, n in enumerate(w.accepted.tolist())]
+    assert max(moved) == 6
+    for p, (a,) in zip(prompts, fast):
+        assert len(a) == 20
+        _follows(model, p, a)
