@@ -6,9 +6,9 @@ and penalties: drafted tokens are checked as a tree in one pass.
 Drafts come from the request's own text (what followed the last tokens where they
 occurred before), so nothing but the decoder is needed; a prompt goes through the
 cache in chunks as a chain whose tokens are all accepted.  When a prompt is in the
-cache, further answers fork from its row: they share its pages, and the last one is
-copied.  The host reads the accepted nodes once a step; nothing else leaves the
-GPU.
+cache, further answers fork from its row, each with a first token of its own: they
+share its pages, and the last one is copied.  The host reads the accepted nodes once a
+step, and what is drawn for such answers; nothing else leaves the GPU.
 """
 from __future__ import annotations
 
@@ -125,7 +125,9 @@ def generate(model, prompts, new_tokens, *, samples=1, batch=4, max_new=8, max_p
                 known += [-1] * (len(t) - len(known))
             else:
                 left = new_tokens - len(answers[r[0]][r[1]])
-                t, p = tree_of(text[-1], draft(text, width, min(left - 1, max_new - 1)), max_new)
+                # (answers part at the first token: what forks has no drafts behind it)
+                t, p = tree_of(text[-1], [] if samples > 1 and fed[i] < len(prompts[r[0]]) else
+                               draft(text, width, min(left - 1, max_new - 1)), max_new)
                 known = [-1] * len(t)
             tokens, parents, forced = tokens + t, parents + p, forced + known
             sizes.append(len(t))
@@ -152,7 +154,7 @@ def generate(model, prompts, new_tokens, *, samples=1, batch=4, max_new=8, max_p
             moe.kv_compact(walk.path, walk.accepted, ctx, table, b["k_cache"], b["v_cache"], err=err)
         steps += 1
 
-        keep, forks = walk.seq_lens.clone(), []
+        keep, forks, firsts = walk.seq_lens.clone(), [], []
         read = torch.cat([walk.path, walk.accepted[:, None], walk.next_ids[:, None]], 1).tolist()
         host = tokens.tolist()
         at = 0
@@ -173,8 +175,14 @@ def generate(model, prompts, new_tokens, *, samples=1, batch=4, max_new=8, max_p
                 others = [j for j, x in enumerate(rows) if x is None][:samples - 1]
                 for s, j in enumerate(others, 1):
                     rows[j], fed[j] = (r[0], s), fed[i]
-                    answers[r[0]][s] += text
+                    firsts.append((lo + path[accepted - 1], answers[r[0]][s]))
                     forks.append((i, j))
+        if firsts:   # drawn from the logits at the prompt's end
+            ids, _ = moe.sample_tokens(logits[[row for row, _ in firsts]],
+                                       torch.rand(len(firsts), generator=rand, device="cuda"),
+                                       **{k: v[:len(firsts)] for k, v in per_row.items()})
+            for (_, text), token in zip(firsts, ids.tolist()):
+                text.append(token)
         done = [i for i, r in enumerate(rows) if r and len(answers[r[0]][r[1]]) == new_tokens]
         if forks:
             moe.kv_trim(keep, step.seq_lens, table, free, n_free, page_refs=refs, err=err, **pages)

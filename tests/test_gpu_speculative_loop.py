@@ -159,3 +159,16 @@ def test_right_drafts_are_accepted_and_their_vectors_move(loop, monkeypatch):
     for p, (a,) in zip(prompts, fast):
         assert len(a) == 20
         _follows(model, p, a)
+
+
+@pytest.mark.parametrize("max_new", [1, 3, 8])
+def test_answers_to_a_prompt_part_at_their_first_token(loop, max_new):
+    model = loop.TreeDecoder(num_pages=80)
+    answers, left, _ = loop.generate(model, PROMPTS, 5, samples=4, batch=8, max_new=max_new,
+                                     temperature=5.0)
+    assert left == model.num_pages
+    for four in answers:
+        assert all(len(a) == 5 for a in four)
+        assert len({a[0] for a in four}) > 1             # of a thousand nearly as likely ones
+    one, _, _ = loop.generate(model, PROMPTS, 1, samples=4, batch=4, max_new=max_new, temperature=5.0)
+    assert all(len(a) == 1 for four in one for a in four)
