@@ -611,7 +611,7 @@ int moe_tree_masks(const int32_t* parents, int N, const int32_t* starts, const i
  *   accepted   device int32 [B] out: how many; 0 for a request without nodes
  *   next_ids   device int32 [B] out: the token drawn at the last of them (the
  *              next step's node 0); -1 for a request without nodes
- *   seq_lens   device int32 [B] out: ctx + accepted
+ *   seq_lens   device int32 [B] out: ctx + accepted (2^31 - 1 at most)
  * A walk ends after max_path nodes.  Nodes past MOE_TREE_MAX are not looked at
  * and set MOE_DEVERR_NO_SPACE.  Requires 1 <= max_path <= MOE_TREE_MAX.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.

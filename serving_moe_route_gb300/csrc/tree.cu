@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_masks_kernel(const MaskArgs
     at ^= 1;
     __syncthreads();
   }
-  const int ctx = max(0, A.lens[r] - (rows.y - rows.x));
+  const int ctx = max(0, max(0, A.lens[r]) - (rows.y - rows.x));
   for (int j = tid; j < rows.y - rows.x; j += kTreeThreads) {
     int depth = 0;
     for (int w = 0; w < A.words; ++w) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_accept_kernel(const AcceptA
     }
     A.accepted[r] = count;
     A.next[r] = last >= 0 ? A.draws[rows.x + last] : -1;
-    A.lens[r] = max(0, A.ctx[r]) + count;
+    A.lens[r] = min(max(0, A.ctx[r]), INT_MAX - count) + count;
     s_child[0] = count;  // (the walk is over)
   }
   __syncthreads();

@@ -570,3 +570,13 @@ def test_a_row_that_attends_nothing_under_a_nan_scale(D):
     some = torch.ones(len(out), dtype=torch.bool, device=DEV)
     some[few] = False
     assert out[some][:, 2:].isnan().all() and out[:, :2].isfinite().all()
+
+
+def test_lengths_at_the_ends_of_32_bits():
+    starts, lens = _i32([0, 3, 5, 8]), _i32([-2 ** 31, 1, 2 ** 31 - 1])
+    parents, tokens = _i32([-1, 0, 1, -1, 0, -1, 0, 1]), _i32([1] * 8)
+    got = moe.tree_masks(parents, starts, lens, max_new=3)
+    assert got.positions.tolist() == [0, 1, 2, 0, 1, 2 ** 31 - 4, 2 ** 31 - 3, 2 ** 31 - 2]
+    walk = moe.tree_accept(tokens, tokens, parents, starts, lens, max_path=3)
+    assert walk.accepted.tolist() == [3, 2, 3]
+    assert walk.seq_lens.tolist() == [3, 3, 2 ** 31 - 1]
