@@ -63,6 +63,14 @@ __device__ __forceinline__ int pages_of(int tokens, int page, int width) {
   return min((tokens - 1) / page + 1, width);
 }
 
+// the two halves of cluster_sync
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // this CTA's value `mine` as the sum over the cluster's CTAs before it, and
 // over all of them.  `inbox`: kPageCtas words of this CTA that the others write, so
 // all of the cluster must have passed a barrier before

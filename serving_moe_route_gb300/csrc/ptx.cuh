@@ -412,16 +412,12 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
   return r;
 }
 
-// all threads of the cluster; orders shared-memory and barrier state
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// all threads of both CTAs; orders shared-memory and barrier state
 __device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
 }
 
 // shared::cluster address of the object at shared::cta address `a` in the
