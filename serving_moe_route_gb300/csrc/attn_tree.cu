@@ -17,19 +17,14 @@ struct SimtCfg {
   static constexpr int CTAS = 2;  // per SM
 };
 
-__device__ __forceinline__ void tree_cp16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
-
 // S = Q K^T, the running softmax and O += P V on tiles in shared memory, 2 rows
 // by TILE / 16 tokens and by DP / 16 columns a thread, all in fp32: nothing is
 // split or rounded.  A value that a row does not attend is skipped, not
 // multiplied by 0.  (Tensor cores would take f32 operands as pairs of tf32 terms,
 // three products each, and split them again for every block of rows.)  Bound by
-// latency for small calls, 24.5 us for 5 requests of up to 13 nodes, 3 heads on
-// each of 2 of 80, window 1000; by the fp32 units for large ones.
+// latency for small calls, 25 us for 5 requests of up to 13 nodes, 3 heads on
+// each of 2 of 80, window 1000; by the fp32 units for large ones, 839 us for 64 of up
+// to 16 nodes, 8 heads on each of 4 of 128, up to 4096 tokens.
 template <int DP>
 __global__ void __launch_bounds__(kSimtThreads, SimtCfg<DP>::CTAS)
     tree_simt_kernel(const TreeArgs A) {

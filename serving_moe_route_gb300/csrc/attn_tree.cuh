@@ -5,11 +5,11 @@
 // of that kv head), nodes in order.  Its tokens form tiles of TILE; it counts its
 // tiles and END more for its end.  CTAs work in groups of as many as the largest
 // request has blocks (8 at most), one block each, on the same tokens at the same
-// time, so that all but one find them in L2.  The counts of all (request, kv head),
-// in order, are cut into equal contiguous ranges, one per group of a single wave,
-// so that ragged lengths and one long request balance alike.  A range may begin
-// and end inside a unit; the unit's parts go to the workspace and a second kernel
-// joins them in order.
+// time, so that all but one find them in L2; a request of fewer blocks leaves the
+// rest of the group idle.  The counts of all (request, kv head), in order, are cut
+// into equal contiguous ranges, one per group of a single wave, so that ragged
+// lengths and one long request balance alike.  A range may begin and end inside a
+// unit; the unit's parts go to the workspace and a second kernel joins them in order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -69,9 +69,15 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeArgs& A, int r, bool& cu
   if (s.n > 0 && (s.use < s.n || s.len < all)) cut = true;
   return s;
 }
+// 16 bytes to shared memory; zeros, and nothing is read, where they are not real
+__device__ __forceinline__ void tree_cp16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
 constexpr int kTreeGroup = 8;  // CTAs of a group at most
 
-// blocks of a request's rows, and the rounds in which a group goes through them
+// blocks of a request's rows
 template <int ROWS>
 __device__ __forceinline__ int tree_blocks(const TreeArgs& A, const TreeSpan& s) {
   return (s.use * A.group + ROWS - 1) / ROWS;

@@ -17,8 +17,10 @@
 //            l of a row in fp32 (base 2); O is rescaled only when a logit lies LAG
 //            above the one that m was taken from.  P is rounded to bf16 (f16 for
 //            e4m3 caches) into the columns of S that it has been read from; l adds
-//            the weights before that.  f16 weights are lifted to 2^LIFT, which
-//            keeps 11 bits down to 2^-27 of the largest.
+//            the weights before that.  bf16 weights leave outputs 1.1 to 1.4 times
+//            as far off as their own rounding does; pairs of bf16 mend that and cost
+//            2 to 29% (127 us become 164 for the long request below).  f16 weights
+//            are lifted to 2^LIFT, which keeps 11 bits down to 2^-27 of the largest.
 //   masks    Only tiles that some row does not wholly attend look at masks.  Their
 //            weights are 0, but 0 times a value that is not finite is not: such
 //            values are replaced by 0 in the tile, and added to O for the rows
@@ -33,7 +35,7 @@
 // units' ends in short ones, and by latency in small calls.  Measured on a GB300, 32
 // query heads on 4 of 128, bf16: one request of 61 nodes at 131089 tokens 128 us, 1020
 // TFLOP/s (53% of cuBLAS's rate); 64 requests of 64 nodes up to 8192: 209 to 219 us,
-// 800 to 830 TFLOP/s; of up to 16 nodes, up to 4096: 56 us, 3.1 TB/s; one of 8 nodes
+// 800 to 830 TFLOP/s; of up to 16 nodes, up to 4096: 55 us, 3.2 TB/s; one of 8 nodes
 // at 700: 16 us.  e4m3, 128 requests of 8 nodes up to 8192: 135 us, 2.5 TB/s: there a
 // tile takes the softmax 2030 beside the warps that widen.
 //
@@ -145,12 +147,6 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const float (&v)[32]) {
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_cp16(uint32_t dst, const void* src, bool real) {
-  // a chunk that is not real is filled with zeros and nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
 }
 __device__ __forceinline__ uint4 tc_lds4(uint32_t addr) {
   uint4 v;
@@ -359,7 +355,8 @@ __device__ __forceinline__ void tc_tma_role(const TreeArgs& A, const CUtensorMap
 }
 
 // By cp.async, for pages that no box of eight tokens or more divides.  (A warp has
-// few copies under way at a time: 1.6 us for 16 KB.)
+// few copies under way at a time: 1.6 us for 16 KB; the batch of 16 nodes takes 84 us
+// in pages of 1, 4 or 5, bf16 and e4m3, and 64 in pages of 16, caches cold.)
 template <int KV, int DP>
 __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, uint32_t ring,
                                              int lane) {
@@ -414,7 +411,7 @@ __device__ __forceinline__ void tc_load_role(const TreeArgs& A, TcShared& sh, ui
       const int r = j * RPI + row0;
       const long long o = __shfl_sync(0xffffffffu, p.off[j * RPI / 32], r & 31);
       const bool real = (p.mask[j * RPI / 32] >> (r & 31) & 1u) && real_chunk;
-      tc_cp16(base + tc_land<KV, DP>(r, chunk), real ? from + o : A.k, real);
+      tree_cp16(base + tc_land<KV, DP>(r, chunk), real ? from + o : A.k, real);
     }
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                      smem_u32(&sh.landed[buf]))

@@ -1,5 +1,5 @@
 // decode_internal.cuh -- shared by the translation units of the decode-step
-// operators (kv_cache.cu, attn_decode.cu, sample.cu).
+// operators: cache and pages, attention, trees, adjusted logits, sampling.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -49,6 +49,17 @@ inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// last index r with a[r] <= i (a ascending, a[0] == 0 <= i)
+__device__ __forceinline__ int last_at_most(const int* a, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 // Launch `kern` in clusters of `cluster` CTAs (1: none) such that it may

@@ -73,17 +73,6 @@ __device__ __forceinline__ int cut_int(long long v) {
   return v > INT_MAX ? INT_MAX : static_cast<int>(v);
 }
 
-// last index r with a[r] <= i (a ascending, a[0] == 0 <= i)
-__device__ __forceinline__ int last_at_most(const int* a, int n, int i) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= i) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // Every CTA scans the requests' new tokens and new pages for itself (two
 // exclusive sums, at most 8 steps of 1024 requests) and keeps them in shared
 // memory; then the token rows and the new table entries are dealt out over

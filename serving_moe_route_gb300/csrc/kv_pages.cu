@@ -47,17 +47,6 @@ __device__ __forceinline__ int scan1(int v, int* sums, int& total) {
   return before;
 }
 
-// last r with a[r] <= i (a ascending, a[0] == 0 <= i)
-__device__ __forceinline__ int row_of(const int* a, int n, int i) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= i) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 __device__ __forceinline__ int pages_of(int tokens, int page, int width) {
   if (tokens <= 0) return 0;
   return min((tokens - 1) / page + 1, width);
@@ -141,7 +130,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_trim_kernel(const TrimArgs A)
   const int lo = min(static_cast<long long>(entries), static_cast<long long>(share) * blockIdx.x);
   const int hi = min(static_cast<long long>(entries), static_cast<long long>(lo) + share);
   auto entry = [&](int e) {
-    const int r = row_of(base, A.B, e);
+    const int r = last_at_most(base, A.B, e);
     return A.table + r * A.table_stride + pages_of(A.keep[r], A.page, A.max_pages) + (e - base[r]);
   };
   auto inside = [&](int pg) { return pg >= 0 && pg < A.num_pages; };
@@ -307,7 +296,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_kernel(const ForkArgs A)
   if (ctas > 1) cluster_sync();  // all have read n_free, and the lengths
   for (long long e = blockIdx.x * kPageThreads + tid; e < shared;
        e += static_cast<long long>(ctas) * kPageThreads) {
-    const int i = row_of(base, A.F, static_cast<int>(e));
+    const int i = last_at_most(base, A.F, static_cast<int>(e));
     const long long col = e - base[i];
     int pg = A.table[A.src[i] * A.table_stride + col];
     if (pg < 0 || pg >= A.num_pages) {
